@@ -75,7 +75,19 @@ typedef struct dkv_cache dkv_cache; /* opaque; tagged so a stale handle is rejec
  * in section 6, When it's worth it; not part of DirectKV's pages).  New
  * rows are the fp32 projection sums rounded once to E4M3 (to nearest, ties
  * to even, saturating); decode only, bf16 activations only. */
-typedef enum { DKV_KV_NATIVE = 0, DKV_KV_E4M3 = 1 } dkv_kv_format;
+typedef enum {
+    DKV_KV_NATIVE = 0,
+    DKV_KV_E4M3 = 1,
+    /* 4-bit E2M1 codes (OCP FP4: 0, .5, 1, 1.5, 2, 3, 4, 6 with a sign) with one
+     * E4M3 scale per 16 elements: 9/16 byte an element.  Paged caches only, pages
+     * of 16 to 4096 tokens, both dtypes.  A page of one KV head is one run of
+     * bytes: page_tokens rows of head_dim/2 code bytes (element 2i in the low
+     * four bits of byte i), then page_tokens rows of head_dim/16 scale bytes;
+     * a pool is [num_pages][n_kv_heads][page_tokens * head_dim * 9 / 16].  Served by
+     * dkv_qkv_append and dkv_paged_attend; the calls that project, decode or
+     * prefill through the cache handle return UNSUPPORTED for it. */
+    DKV_KV_E2M1 = 2
+} dkv_kv_format;
 
 /* Everything a cache can be: dense (page_tokens 0), paged (page_tokens > 0,
  * one layer), layered (layers > 1, dense), in either element format.
@@ -121,7 +133,8 @@ dkv_status dkv_cache_alloc(dkv_cache** out, int batch, int n_kv_heads, int head_
  * (its host views hold uint8 E4M3 bits); dkv_prefill, dkv_decode_staged,
  * dkv_prefill_staged and dkv_attend_naive return UNSUPPORTED for it.  Errors: as the three
  * allocators, plus INVALID_ARG for an unknown format, UNSUPPORTED for E4M3
- * with fp16 activations or a paged cache of several layers. */
+ * with fp16 activations, for E2M1 in a cache that is not paged or has pages of
+ * fewer than 16 tokens, or for a paged cache of several layers. */
 dkv_status dkv_cache_alloc_ex(dkv_cache** out, const dkv_cache_desc_t* desc);
 
 /* A layered cache: one pinned allocation each for K and V holding `layers`
@@ -437,6 +450,141 @@ dkv_status dkv_decode_noalloc_status(void* stream);
  * that the consumers' bounded wait expires after about a second; the call's
  * outputs are NaN and dkv_decode_noalloc_status reports DKV_ERR_TIMEOUT. */
 dkv_status dkv_decode_noalloc_debug_withhold(int enable);
+
+/* ---- the device-side step over a 4-bit paged cache ------------------------ */
+
+/* A decoder that normalises and rotates its queries and keys cannot use the
+ * fused projection of dkv_decode / dkv_prefill.  These three calls serve it on
+ * caller-owned buffers, with lengths, page tables and slots that live on the
+ * device, so that a whole step (plan, append, attend for each layer) can be captured
+ * in a CUDA graph and replayed without the host knowing a length:
+ *
+ *   dkv_step_plan      lengths and new-token counts -> pages, row starts,
+ *                      positions and slots
+ *   dkv_qkv_append     head norms and rotation of q and k; k and v into the
+ *                      slots of an E2M1 pool
+ *   dkv_paged_attend   softmax attention of ragged query rows over the pool
+ *
+ * A step has `rows` token rows: sequence b's new tokens are rows row_start[b] ..
+ * row_start[b+1]-1, and rows behind the last sequence are padding (slot -1):
+ * nothing of them is written.  Pools are device-accessible pointers: HBM, or
+ * the mapped alias of pinned host memory (dkv_cache_device_ptrs of a
+ * DKV_KV_E2M1 cache), which is then read across the host link.
+ * Nothing here allocates, synchronises or keeps state between calls; errors
+ * return before anything is enqueued.  Calls that may overlap on the GPU need
+ * outputs and workspaces of their own. */
+
+#define DKV_MAX_STEP_BATCH 1024 /* sequences of a step */
+
+/* Plan one step on the GPU.  All pointers are device memory of int32.
+ *   lengths    [batch]  cached rows per sequence
+ *   new_tokens [batch]  rows the step adds (0: none); below 0: the sequence has
+ *                       ended, its pages go back and its length becomes 0
+ *   page_table [batch][max_pages]  pool pages of each sequence's rows; the
+ *                       entries of newly taken pages are written (entries past a
+ *                       sequence's length are never read)
+ *   free_pages [num_pages]  stack of unused pages, free_count[0] of them valid.
+ *                       Pages released are pushed in order of sequence and
+ *                       page; the k-th page taken, in that order too, is the k-th
+ *                       from the top.
+ * Written: row_start [batch + 1]; row_pos, row_slot [max_rows] (position and slot
+ * = page * page_tokens + offset of each row; 0 and -1 behind the last);
+ * kv_len [batch], the lengths with the new rows; free_left [1]; report [4] =
+ * {status, rows, pages taken, longest kv_len}.
+ * All or nothing: where the pages, the rows (max_rows) or a sequence's table
+ * (max_pages) do not suffice, report[0] is DKV_ERR_CAPACITY, every row is padding,
+ * kv_len = lengths, free_left = free_count, and table and stack stay as they were.
+ * kv_len may be `lengths` and free_left may be `free_count` (update in place); other
+ * buffers must not overlap.
+ * Errors: INVALID_ARG (null pointer; batch outside [1, DKV_MAX_STEP_BATCH];
+ * page_tokens not a power of two in [1, 4096]; max_pages, num_pages or max_rows not
+ * positive, or above 2^30 rows), CUDA. */
+dkv_status dkv_step_plan(const int32_t* lengths, const int32_t* new_tokens, int32_t* page_table,
+                         int32_t* free_pages, const int32_t* free_count, int batch, int max_pages,
+                         int page_tokens, int num_pages, int max_rows, int32_t* row_start,
+                         int32_t* row_pos, int32_t* row_slot, int32_t* kv_len, int32_t* free_left,
+                         int32_t* report, void* stream);
+
+/* Norm, rotation and append of one step's projected rows.
+ *   q [rows][n_q_heads][head_dim], k and v [rows][n_kv_heads][head_dim], `dtype`;
+ *     consecutive rows lie *_stride elements apart (one projection's output
+ *     holds all three), heads of a row are contiguous.  q may be null (keys and
+ *     values only), or k and v (queries only).
+ *   q_gamma, k_gamma [head_dim], `dtype`, or null: RMS norm of each head's row,
+ *     x / sqrt(mean x^2 + eps) * gamma.  Values are never normalised.
+ *   cos_sin [max_positions][rotary_dim] fp32, or null: rotary_dim/2 cosines, then
+ *     rotary_dim/2 sines of each position; positions [rows] int32.  Pairs are
+ *     (i, i + rotary_dim/2), or (2i, 2i + 1) with `interleaved`; elements from
+ *     rotary_dim on are not rotated.  A position outside the table makes the
+ *     row's q and k NaN.
+ *   slots [rows] int32: where the row's k and v go in the pools (page * page_tokens
+ *     + offset).  A slot outside [0, num_pages * page_tokens) marks padding:
+ *     nothing of the row is written, q_out included.  Two rows of a call must not
+ *     have the same slot.  Null slots and pools: no append, k_out and v_out
+ *     take the rows rounded to `dtype`.
+ *   k_scale, v_scale: the pools hold k / k_scale and v / v_scale.
+ *   q_out [rows][n_q_heads][head_dim] (may be q if q is contiguous); k_out, v_out
+ *     [rows][n_kv_heads][head_dim] or null: with pools, the values that the cache
+ *     now holds (times the scale, rounded to `dtype`).
+ * Arithmetic is fp32, each operation rounded once, the key norm's sum of squares in
+ * two words.  A block of 16 takes the scale e4m3(max|y| / 6), saturating at 448, and
+ * the codes e2m1(y / scale), both to nearest even, saturating; a block with a NaN
+ * or an infinity gets a NaN scale and reads back as NaN.
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim not 64 or 128), CUDA. */
+typedef struct {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;
+    const void *q_gamma, *k_gamma;
+    const float* cos_sin;
+    const int32_t *positions, *slots;
+    void *k_pool, *v_pool;
+    void *q_out, *k_out, *v_out;
+    int rows, n_q_heads, n_kv_heads, head_dim;
+    dkv_dtype dtype;
+    int rotary_dim, max_positions, interleaved;
+    int page_tokens, num_pages;
+    float eps, k_scale, v_scale;
+} dkv_append_t;
+dkv_status dkv_qkv_append(const dkv_append_t* args, void* stream);
+
+/* Attention of a step's query rows over an E2M1 pool: row i of sequence b (n_b =
+ * row_start[b+1] - row_start[b] rows) attends to keys 0 .. kv_len[b] - n_b + i of its
+ * sequence, through page_table [batch][max_pages]:
+ *   o = v_scale * softmax(scale * q . k) . v
+ * A null row_start means one row per sequence (a decode step).  kv_len counts the
+ * rows' own keys, appended before.  A row that sees no key is zero with lse -infinity.
+ * out [rows][n_q_heads][head_dim] in `dtype`; lse [rows][n_q_heads] fp32, or null:
+ * the natural log of the sum of exp(scale * q . k).  Rows of no sequence are left as
+ * they were.
+ * max_rows: no sequence has more rows than this; it chooses the kernel, any lengths
+ * on the device are then served.  Lengths above max_pages * page_tokens are cut to
+ * that; a page index outside [0, num_pages) counts as a page without keys.  K's
+ * scale (dkv_append_t.k_scale) belongs into `scale`.
+ * A NaN in a key or value reaches the rows that see it and no others.
+ * q, k.v products run on fp16 tensor operands (cache values and fp16 queries exactly;
+ * bf16 queries scaled by a power of two per row; weights rounded to fp16), sums and
+ * softmax statistics in fp32.  The result does not depend on timing.
+ * workspace: device memory of dkv_paged_attend_workspace bytes (0 for arguments
+ * that dkv_paged_attend refuses), on a 256-byte boundary; its contents do not matter
+ * before and after a call.
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim not 64 or 128), CUDA. */
+typedef struct {
+    const void* q;
+    long long q_stride;
+    const void *k_pool, *v_pool;
+    const int32_t *page_table, *kv_len, *row_start;
+    void* out;
+    float* lse;
+    void* workspace;
+    size_t workspace_bytes;
+    int batch, rows, max_rows, n_q_heads, n_kv_heads, head_dim;
+    dkv_dtype dtype;
+    int page_tokens, num_pages, max_pages;
+    float scale, v_scale;
+} dkv_attend_t;
+dkv_status dkv_paged_attend(const dkv_attend_t* args, void* stream);
+size_t dkv_paged_attend_workspace(int batch, int n_q_heads, int n_kv_heads, int head_dim,
+                                  int max_rows);
 
 /* Number of kernel launches the last dkv_decode / dkv_prefill enqueued. */
 int dkv_last_launch_count(void);

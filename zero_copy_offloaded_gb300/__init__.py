@@ -28,6 +28,8 @@ __all__ = [
     "dkv_prefill_layer", "dkv_step_graph_capture", "dkv_step_graph_launch",
     "dkv_cache_alloc_ex", "KV_FORMATS", "dkv_decode_noalloc", "dkv_decode_noalloc_status",
     "dkv_decode_noalloc_debug_withhold", "dkv_pci_numa_node", "dkv_numa_probe",
+    "dkv_step_plan", "dkv_qkv_append", "dkv_paged_attend", "dkv_paged_attend_workspace",
+    "rope_table", "MAX_STEP_BATCH",
 ]
 
 BF16 = 0
@@ -71,7 +73,32 @@ class _CacheDesc(ctypes.Structure):
                 ("max_pages_per_seq", ctypes.c_int)]
 
 
-KV_FORMATS = {"native": 0, "e4m3": 1}
+class _Append(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v")]
+                + [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride")]
+                + [(n, ctypes.c_void_p) for n in (
+                    "q_gamma", "k_gamma", "cos_sin", "positions", "slots", "k_pool", "v_pool",
+                    "q_out", "k_out", "v_out")]
+                + [(n, ctypes.c_int) for n in (
+                    "rows", "n_q_heads", "n_kv_heads", "head_dim", "dtype", "rotary_dim",
+                    "max_positions", "interleaved", "page_tokens", "num_pages")]
+                + [(n, ctypes.c_float) for n in ("eps", "k_scale", "v_scale")])
+
+
+class _Attend(ctypes.Structure):
+    _fields_ = ([("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in (
+                    "k_pool", "v_pool", "page_table", "kv_len", "row_start", "out", "lse",
+                    "workspace")]
+                + [("workspace_bytes", ctypes.c_size_t)]
+                + [(n, ctypes.c_int) for n in (
+                    "batch", "rows", "max_rows", "n_q_heads", "n_kv_heads", "head_dim", "dtype",
+                    "page_tokens", "num_pages", "max_pages")]
+                + [(n, ctypes.c_float) for n in ("scale", "v_scale")])
+
+
+KV_FORMATS = {"native": 0, "e4m3": 1, "e2m1": 2}
+MAX_STEP_BATCH = 1024
 
 
 _lib = None
@@ -125,6 +152,9 @@ def lib(build_if_missing: bool = False):
         "dkv_decode_noalloc": [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P],
         "dkv_decode_noalloc_status": [P],
         "dkv_decode_noalloc_debug_withhold": [I],
+        "dkv_step_plan": [P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P],
+        "dkv_qkv_append": [ctypes.POINTER(_Append), P],
+        "dkv_paged_attend": [ctypes.POINTER(_Attend), P],
         "dkv_project": [P, P, P, I, I, I, I, P],
         "dkv_cache_debug_withhold": [P, I],
     }
@@ -140,6 +170,8 @@ def lib(build_if_missing: bool = False):
     L.dkv_last_launch_count.restype = ctypes.c_int
     L.dkv_pci_numa_node.argtypes = [ctypes.c_char_p, ctypes.c_char_p]
     L.dkv_pci_numa_node.restype = ctypes.c_int
+    L.dkv_paged_attend_workspace.argtypes = [I] * 5
+    L.dkv_paged_attend_workspace.restype = ctypes.c_size_t
     L.dkv_numa_probe.argtypes = [ctypes.c_int]
     L.dkv_numa_probe.restype = ctypes.c_int
     _lib = L
@@ -398,6 +430,187 @@ def dkv_decode_noalloc_debug_withhold(enable=True):
            "dkv_decode_noalloc_debug_withhold")
 
 
+# ---- the device-side step over a 4-bit paged cache -----------------------------------
+
+def _arg(t, what, dtype, device, shape=None, strided=False):
+    """Device pointer of a CUDA tensor of this dtype, device and shape; None stays None."""
+    if t is None:
+        return None
+    if t.dtype != dtype:
+        raise ValueError(f"{what} is {t.dtype}, not {dtype}")
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, not on {device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
+    if not strided and not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows(t, what, dtype, device, heads=None, D=None):
+    """Pointer and token stride of [rows, heads, D] whose heads are contiguous in each row."""
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (D is not None and t.shape[2] != D):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}: [rows, {heads or 'heads'}, {D or 'head_dim'}] is wanted")
+    n, h, d = t.shape
+    st = t.stride()
+    if st[2] != 1 or (h > 1 and st[1] != d):
+        raise ValueError(f"the heads of a row of {what} must be contiguous")
+    return _arg(t, what, dtype, device, strided=True), (st[0] if n > 1 else max(st[0], h * d))
+
+
+def _pool(t, what, device, D):
+    """Pointer and (num_pages, n_kv_heads, page_tokens) of an E2M1 pool: CUDA, or pinned host memory."""
+    import torch
+    if t.dtype != torch.uint8 or t.dim() != 3 or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous uint8 [num_pages, n_kv_heads, page bytes]")
+    if t.device != device and not (t.device.type == "cpu" and t.is_pinned()):
+        raise ValueError(f"{what} is neither on {device} nor in pinned host memory")
+    per = D * 9 // 16
+    if t.shape[2] % per:
+        raise ValueError(f"{what}: a page of {t.shape[2]} bytes does not hold rows of {per}")
+    return t.data_ptr(), (t.shape[0], t.shape[1], t.shape[2] // per)
+
+
+def _launch(device, stream):
+    """The stream to launch on; the tensors must be on the current device, as the library launches there."""
+    import torch
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {device}, not on the current CUDA device")
+    return _stream(stream)
+
+
+def rope_table(max_positions, rotary_dim, base=10000.0, device="cuda"):
+    """fp32 [max_positions, rotary_dim]: the cosines, then the sines, of position * base^(-2i/rotary_dim),
+    from angles in 64 bits."""
+    import torch
+    i = torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device)
+    a = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * base ** (-i / rotary_dim)
+    return torch.cat((a.cos(), a.sin()), -1).to(torch.float32)
+
+
+def dkv_step_plan(lengths, new_tokens, page_table, free_pages, free_count, page_tokens, row_start,
+                  row_pos, row_slot, kv_len, free_left, report, stream=None):
+    """Pages, row starts, positions and slots of a step from its lengths, on the GPU (see
+    include/dkv.h).  All tensors are int32 and CUDA; page_table [batch, max_pages], row_pos and
+    row_slot [max_rows], report [4]."""
+    import torch
+    dev, i32 = page_table.device, torch.int32
+    if page_table.dim() != 2 or row_pos.dim() != 1 or free_pages.dim() != 1:
+        raise ValueError("page_table is [batch, max_pages], row_pos [max_rows], free_pages [num_pages]")
+    B, max_pages = page_table.shape
+    n, pages = row_pos.shape[0], free_pages.shape[0]
+    one = (1,)
+    _check(lib().dkv_step_plan(
+        _arg(lengths, "lengths", i32, dev, (B,)), _arg(new_tokens, "new_tokens", i32, dev, (B,)),
+        _arg(page_table, "page_table", i32, dev), _arg(free_pages, "free_pages", i32, dev),
+        _arg(free_count, "free_count", i32, dev, one), B, max_pages, page_tokens, pages, n,
+        _arg(row_start, "row_start", i32, dev, (B + 1,)), _arg(row_pos, "row_pos", i32, dev),
+        _arg(row_slot, "row_slot", i32, dev, (n,)), _arg(kv_len, "kv_len", i32, dev, (B,)),
+        _arg(free_left, "free_left", i32, dev, one), _arg(report, "report", i32, dev, (4,)),
+        _launch(dev, stream)), "dkv_step_plan")
+
+
+def _dtype_of(t):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return BF16
+    if t.dtype == torch.float16:
+        return FP16
+    raise ValueError(f"{t.dtype} is neither bfloat16 nor float16")
+
+
+def dkv_qkv_append(q, k, v, positions=None, slots=None, k_pool=None, v_pool=None, q_out=None,
+                   k_out=None, v_out=None, q_gamma=None, k_gamma=None, eps=1e-6, cos_sin=None,
+                   interleaved=False, k_scale=1.0, v_scale=1.0, stream=None):
+    """Head norms and rotation of q and k, append of k and v to an E2M1 pool (see include/dkv.h).
+    q [rows, n_q_heads, D] and k, v [rows, n_kv_heads, D] may be slices of one projection's output."""
+    import torch
+    some = q if q is not None else k
+    if some is None:
+        raise ValueError("neither queries nor keys")
+    dev, dt = some.device, some.dtype
+    a = _Append(dtype=_dtype_of(some), rows=some.shape[0], eps=eps, k_scale=k_scale, v_scale=v_scale,
+                interleaved=int(bool(interleaved)))
+    n, D = some.shape[0], some.shape[-1]
+    a.head_dim = D
+    if q is not None:
+        a.q, a.q_stride = _rows(q, "q", dt, dev)
+        a.n_q_heads = q.shape[1]
+        a.q_out = _arg(q_out, "q_out", dt, dev, tuple(q.shape))
+        a.q_gamma = _arg(q_gamma, "q_gamma", dt, dev, (D,))
+    if k is not None:
+        if v is None or v.shape != k.shape or k.shape[0] != n:
+            raise ValueError("k and v are [rows, n_kv_heads, D], with q's rows")
+        a.k, a.k_stride = _rows(k, "k", dt, dev, D=D)
+        a.v, a.v_stride = _rows(v, "v", dt, dev)
+        a.n_kv_heads = k.shape[1]
+        a.k_out = _arg(k_out, "k_out", dt, dev, tuple(k.shape))
+        a.v_out = _arg(v_out, "v_out", dt, dev, tuple(k.shape))
+        a.k_gamma = _arg(k_gamma, "k_gamma", dt, dev, (D,))
+    elif v is not None:
+        raise ValueError("keys and values come together")
+    if k_pool is not None:
+        if v_pool is None or k is None:
+            raise ValueError("both pools and the keys come together")
+        a.k_pool, shape = _pool(k_pool, "k_pool", dev, D)
+        a.v_pool, other = _pool(v_pool, "v_pool", dev, D)
+        if shape != other or shape[1] != k.shape[1]:
+            raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens) for {k.shape[1]} heads")
+        a.num_pages, a.page_tokens = shape[0], shape[2]
+    a.slots = _arg(slots, "slots", torch.int32, dev, (n,))
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin is [max_positions, rotary_dim]")
+        a.cos_sin = _arg(cos_sin, "cos_sin", torch.float32, dev)
+        a.max_positions, a.rotary_dim = cos_sin.shape
+        a.positions = _arg(positions, "positions", torch.int32, dev, (n,))
+    _check(lib().dkv_qkv_append(a, _launch(dev, stream)), "dkv_qkv_append")
+
+
+def dkv_paged_attend_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_rows=1) -> int:
+    """Bytes of device memory that dkv_paged_attend needs (0 for arguments that it refuses)."""
+    return lib().dkv_paged_attend_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_rows)
+
+
+def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None, max_rows=1,
+                     scale=None, v_scale=1.0, lse=None, workspace=None, stream=None):
+    """Attention of q [rows, n_q_heads, D] over an E2M1 pool (see include/dkv.h); scale None is
+    1/sqrt(D).  Without a workspace (uint8, dkv_paged_attend_workspace bytes) one is taken from
+    torch's allocator on the launching stream."""
+    import torch
+    dev, dt, i32 = q.device, q.dtype, torch.int32
+    s = _launch(dev, stream)
+    a = _Attend(dtype=_dtype_of(q), v_scale=v_scale, max_rows=max_rows)
+    a.q, a.q_stride = _rows(q, "q", dt, dev)
+    n, hq, D = q.shape
+    a.rows, a.n_q_heads, a.head_dim = n, hq, D
+    a.scale = D ** -0.5 if scale is None else scale
+    a.k_pool, shape = _pool(k_pool, "k_pool", dev, D)
+    a.v_pool, other = _pool(v_pool, "v_pool", dev, D)
+    if shape != other:
+        raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens)")
+    a.num_pages, a.n_kv_heads, a.page_tokens = shape
+    if page_table.dim() != 2:
+        raise ValueError("page_table is [batch, max_pages]")
+    B, a.max_pages = page_table.shape
+    a.batch = B
+    a.page_table = _arg(page_table, "page_table", i32, dev)
+    a.kv_len = _arg(kv_len, "kv_len", i32, dev, (B,))
+    a.row_start = _arg(row_start, "row_start", i32, dev, (B + 1,))
+    a.out = _arg(out, "out", dt, dev, (n, hq, D))
+    a.lse = _arg(lse, "lse", torch.float32, dev, (n, hq))
+    if workspace is None:
+        need = max(1, lib().dkv_paged_attend_workspace(B, hq, a.n_kv_heads, D, max_rows))
+        if stream is None:
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+        else:  # owned by the launching stream, so that it is not handed out again before it ran
+            with torch.cuda.stream(torch.cuda.ExternalStream(s, device=dev)):
+                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+    a.workspace = _arg(workspace, "workspace", torch.uint8, dev)
+    a.workspace_bytes = workspace.numel()
+    _check(lib().dkv_paged_attend(a, s), "dkv_paged_attend")
+
+
 class KVCache:
     """Owner of one dkv_cache handle, with numpy views of the pinned caches."""
 
@@ -411,7 +624,7 @@ class KVCache:
     def _views(self, shape):
         kp, vp = dkv_cache_host_ptrs(self.h)
         n = int(np.prod(shape))
-        el = ctypes.c_uint8 if self.kv_format == "e4m3" else ctypes.c_uint16
+        el = ctypes.c_uint16 if self.kv_format == "native" else ctypes.c_uint8
         self.k_host = np.ctypeslib.as_array((el * n).from_address(kp)).reshape(shape)
         self.v_host = np.ctypeslib.as_array((el * n).from_address(vp)).reshape(shape)
 
@@ -445,7 +658,11 @@ class KVCache:
 
 class PagedKVCache(KVCache):
     """A paged cache: numpy views of the K and V page pools
-    ([num_pages, Hkv, page_tokens, D] uint16 each) and the page table."""
+    ([num_pages, Hkv, page_tokens, D] uint16 each) and the page table.
+
+    kv_format "e2m1": 4-bit pools ([num_pages, Hkv, page_tokens * D * 9 // 16] uint8) for
+    ``append`` and ``attend``, whose lengths, page table and slots are device tensors
+    (dkv_step_plan); ``k_pool`` and ``v_pool`` are the pools as pinned torch tensors."""
 
     def __init__(self, batch, n_kv_heads, head_dim, page_tokens, num_pages, max_pages_per_seq,
                  dtype="bf16", kv_format="native"):
@@ -455,8 +672,25 @@ class PagedKVCache(KVCache):
         self.dtype, self.kv_format = dtype, kv_format
         self.h = dkv_cache_alloc_ex(batch, n_kv_heads, head_dim, 0, dtype, kv_format, 1,
                                     page_tokens, num_pages, max_pages_per_seq)
-        self._views((num_pages, n_kv_heads, page_tokens, head_dim))
+        if kv_format == "e2m1":
+            import torch
+            self._views((num_pages, n_kv_heads, page_tokens * head_dim * 9 // 16))
+            self.k_pool, self.v_pool = torch.from_numpy(self.k_host), torch.from_numpy(self.v_host)
+        else:
+            self._views((num_pages, n_kv_heads, page_tokens, head_dim))
         self.table = np.full((batch, max_pages_per_seq), -1, np.int32)
+
+    def append(self, q, k, v, positions, slots, q_out, **more):
+        """dkv_qkv_append into this E2M1 cache."""
+        dkv_qkv_append(q, k, v, positions, slots, self.k_pool, self.v_pool, q_out, **more)
+
+    def attend(self, q, page_table, kv_len, out, **more):
+        """dkv_paged_attend over this E2M1 cache."""
+        dkv_paged_attend(q, self.k_pool, self.v_pool, page_table, kv_len, out, **more)
+
+    def free(self):
+        self.k_pool = self.v_pool = None
+        super().free()
 
     def set_page_table(self, table):
         dkv_cache_set_page_table(self.h, table)

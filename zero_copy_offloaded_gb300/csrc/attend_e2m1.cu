@@ -1,0 +1,685 @@
+// dkv_paged_attend: softmax attention of ragged query rows over a paged cache
+// held in 4 bits (E2M1 codes, an E4M3 scale per 16 elements).
+//
+// For query row i of sequence b (n_b rows, len_b cached keys, the rows' own keys
+// among them), query head h:
+//   s_j = scale * q . k_j   for keys j <= len_b - n_b + i,  o = sum_j softmax(s)_j v_j
+// in one pass over the keys with the running maximum and sum of the softmax.
+//
+// Work: an item is (sequence, KV head, R query rows of that head's group, rows
+// counted token-major over the G heads); its keys are cut into tiles of 128.
+// All tiles of all items form one line that is dealt to the CTAs in equal
+// contiguous ranges, whatever the lengths are, from the lengths on the device
+// (no host copy, so a captured graph serves any lengths).  A CTA that holds a whole
+// item writes its rows; an item cut between CTAs leaves fp32 partials, which a
+// second kernel joins in CTA order.
+//
+// Inside a CTA each of 8 warps takes 16 keys of every tile through its own
+// cp.async ring, with no barrier between warps until the item ends.  Per 16 keys:
+//   S^T[16 keys, 8 rows] = K Q^T  and  O^T[D, 8 rows] += V^T P^T  as m16n8k16 MMAs,
+// keys (then dims) in the M = 16 slot, so that a group of up to 8 query heads of a
+// single token fills the N = 8 slot.  The contraction order inside an MMA is free:
+// each thread uses its codes in the order in which its wide shared-memory load
+// brings them, and q, the key order of P and the dims of O follow.  Codes become
+// fp16 in registers; code x scale is exact in fp16 (6 significant bits), so the
+// MMA operands carry no rounding of the cache.  bf16 queries are brought to fp16's
+// range by a power of two per row (exact, undone on the scores; an element below
+// 2^-27 of its row's largest may lose bits).  P is rounded to fp16 (2^-11
+// relative, as the tensor operand must be 16 bits); scores, maxima, sums and
+// outputs stay in fp32.
+#include <float.h>
+#include <math.h>
+#include <stdio.h>
+
+#include "attend_e2m1.cuh"
+#include "tc_common.cuh"
+
+namespace dkv {
+void set_last_error(dkv_status s, const char* msg);
+}
+
+namespace {
+
+using namespace dkv;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kStep = 16;               // keys of one warp step
+constexpr int kTile = kStep * kWarps;   // keys of one tile
+constexpr float kLazy = 8.0f;  // the running maximum moves only when passed by 2^8
+
+template <int D, int NT>
+struct Cfg {
+  static constexpr int R = 8 * NT;                   // query rows per item
+  static constexpr int kC = kStep * e2m1::code_bytes(D);
+  static constexpr int kS = kStep * e2m1::scale_bytes(D);
+  static constexpr int kStage = 2 * (kC + kS);
+  static constexpr int kStages = D == 128 ? 4 : 6;
+  static constexpr int kRing = kStages * kStage;     // per warp
+  static constexpr int kMerge = kWarps * 8 * D * 4;  // one 8-row round of every warp's O
+  static constexpr int kOffMerge = kWarps * kRing;
+  static constexpr int kOffMl = kOffMerge + kMerge;          // [2][kWarps][R] floats
+  static constexpr int kOffBatch = kOffMl + 2 * kWarps * R * 4;
+};
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Where a CTA is on the line of tiles.
+struct Pos {
+  int b, item, tile;  // item: KV head * qtiles + query tile, inside sequence b
+  int items, tiles;   // of sequence b
+};
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const AttendParams p) {
+  using C = Cfg<D, NT>;
+  constexpr int R = C::R, J = D / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, c = lane & 3;
+  uint8_t* ring = smem + warp * C::kRing;
+  float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+  float* s_m = reinterpret_cast<float*>(smem + C::kOffMl);
+  float* s_l = s_m + kWarps * R;
+  long long* s_pre = reinterpret_cast<long long*>(smem + C::kOffBatch);  // [B + 1]
+  int* s_kv = reinterpret_cast<int*>(s_pre + p.B + 1);                   // [B]
+  int* s_row = s_kv + p.B;                                               // [B]
+  int* s_n = s_row + p.B;                                                // [B]
+  const int G = p.G;
+
+  // the line of tiles: lengths, row counts, and the prefix of tile counts
+  for (int b = threadIdx.x; b < p.B; b += kThreads) {
+    int kv, row, n;
+    batch_entry(p, b, kv, row, n);
+    s_kv[b] = kv;
+    s_row[b] = row;
+    s_n[b] = n;
+    s_pre[b + 1] = (long long)p.Hkv * ((n * G + R - 1) / R) * max(1, (kv + kTile - 1) / kTile);
+  }
+  if (threadIdx.x == 0) s_pre[0] = 0;
+  __syncthreads();
+  if (warp == 0) {
+    long long carry = 0;
+    for (int base = 0; base < p.B; base += 32) {
+      long long v = base + lane < p.B ? s_pre[base + lane + 1] : 0;
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(~0u, v, d);
+        if (lane >= d) v += o;
+      }
+      v += carry;
+      if (base + lane < p.B) s_pre[base + lane + 1] = v;
+      carry = __shfl_sync(~0u, v, 31);
+    }
+  }
+  __syncthreads();
+  const long long total = s_pre[p.B];
+  // with fewer tiles than CTAs the first `total` CTAs take one each, so that an
+  // item's pieces always lie in consecutive CTAs
+  const long long ctas = min(total, (long long)gridDim.x);
+  if (threadIdx.x < 2) p.desc[2 * blockIdx.x + threadIdx.x].valid = 0;
+  if ((long long)blockIdx.x >= ctas) return;
+  const long long g0 = total * blockIdx.x / ctas, g1 = total * (blockIdx.x + 1) / ctas;
+
+  auto enter = [&](Pos& at, int b) {
+    at.b = b;
+    at.items = p.Hkv * ((s_n[b] * G + R - 1) / R);
+    at.tiles = max(1, (s_kv[b] + kTile - 1) / kTile);
+  };
+  auto next_tile = [&](Pos& at) {
+    if (++at.tile < at.tiles) return;
+    at.tile = 0;
+    if (++at.item < at.items) return;
+    at.item = 0;
+    int b = at.b + 1;
+    while (b < p.B && s_n[b] == 0) ++b;
+    if (b < p.B) enter(at, b);
+  };
+  Pos cons;
+  {
+    int lo = 0, hi = p.B;  // s_pre[lo] <= g0 < s_pre[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_pre[mid] <= g0) lo = mid; else hi = mid;
+    }
+    enter(cons, lo);
+    const long long rem = g0 - s_pre[lo];
+    cons.item = (int)(rem / cons.tiles);
+    cons.tile = (int)(rem - (long long)cons.item * cons.tiles);
+  }
+
+  // ---- producer side: this warp's next step to fetch -------------------------
+  Pos prod = cons;
+  long long left = g1 - g0;  // steps not yet issued
+  int page = -1;             // pool page of prod's step (-1: nothing to fetch)
+  uint32_t have = 0;         // bit s: stage s holds keys
+  auto find_page = [&]() {
+    page = -1;
+    if (left <= 0) return;
+    const int t0 = prod.tile * kTile + warp * kStep;
+    if (t0 < s_kv[prod.b]) page = __ldg(p.table + (size_t)prod.b * p.max_pages + (t0 >> p.page_shift));
+  };
+  int st_in = 0;
+  auto issue = [&]() {
+    const bool ok = page >= 0 && page < p.num_pages;
+    have = ok ? have | (1u << st_in) : have & ~(1u << st_in);
+    if (ok) {
+      const int in_page = (prod.tile * kTile + warp * kStep) & ((1 << p.page_shift) - 1);
+      const int qtiles = prod.items / p.Hkv;
+      const size_t base = ((size_t)page * p.Hkv + prod.item / qtiles) * p.page_bytes;
+      const size_t codes = base + (size_t)in_page * e2m1::code_bytes(D);
+      const size_t scales = base + ((size_t)e2m1::code_bytes(D) << p.page_shift) +
+                            (size_t)in_page * e2m1::scale_bytes(D);
+      uint8_t* st = ring + st_in * C::kStage;
+      constexpr int CPR = e2m1::code_bytes(D) / 16;  // 16-byte chunks per row
+#pragma unroll
+      for (int i = 0; i < C::kC / 512; ++i) {
+        const int ch = lane + 32 * i, t = ch / CPR, part = ch % CPR;
+        // K: row of key t in MMA order; V: in key order, chunks of keys 2, 3 mod 4 swapped in pairs
+        const int r = ((t & 3) << 1) | ((t >> 2) & 1) | (t & 8);
+        cp_async16(st + r * e2m1::code_bytes(D) + part * 16, p.k_pool + codes + ch * 16, 16);
+        const int vp = D == 128 ? part ^ (t & 2) : part;
+        cp_async16(st + C::kC + C::kS + t * e2m1::code_bytes(D) + vp * 16, p.v_pool + codes + ch * 16, 16);
+      }
+      constexpr int SCH = C::kS / 16;  // chunks of one scale block: 8 or 4
+      if (lane < SCH)
+        cp_async16(st + C::kC + lane * 16, p.k_pool + scales + lane * 16, 16);
+      else if (lane < 2 * SCH)
+        cp_async16(st + 2 * C::kC + C::kS + (lane - SCH) * 16, p.v_pool + scales + (lane - SCH) * 16, 16);
+    }
+    cp_async_commit();
+    st_in = st_in + 1 == C::kStages ? 0 : st_in + 1;
+    if (left > 0) {
+      --left;
+      next_tile(prod);
+      find_page();
+    }
+  };
+  find_page();
+#pragma unroll 1
+  for (int i = 0; i < C::kStages - 1; ++i) issue();
+
+  // ---- consumer side -----------------------------------------------------------
+  int st_out = 0;
+  long long at = g0;
+  while (at < g1) {
+    const int b = cons.b, qtiles = cons.items / p.Hkv, h = cons.item / qtiles, qt = cons.item % qtiles;
+    const int kv = s_kv[b], n = s_n[b], row0 = s_row[b];
+    const int tile0 = cons.tile;
+    const int tile1 = (int)min((long long)cons.tiles, tile0 + (g1 - at));
+    const int last = min((qt + 1) * R, n * G) - 1;  // last packed row of the item
+    const int minvis = max(0, kv - n + (qt * R) / G + 1), maxvis = max(0, kv - n + last / G + 1);
+
+    uint32_t qf[NT][2 * J];
+    float sl[NT][2];
+    int vis[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int pr = qt * R + nt * 8 + g;
+      float unscale = 1.0f;
+      if (pr <= last) {
+        const int t = pr / G;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const T*>(p.q) + (size_t)(row0 + t) * p.q_stride + (size_t)(h * G + pr - t * G) * D +
+            c * (D / 4));
+#pragma unroll
+        for (int i = 0; i < J / 2; ++i) {
+          const uint4 w = __ldg(src + i);
+          qf[nt][4 * i] = w.x; qf[nt][4 * i + 1] = w.y; qf[nt][4 * i + 2] = w.z; qf[nt][4 * i + 3] = w.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 2 * J; ++i) qf[nt][i] = 0;
+      }
+      if constexpr (DT<T>::code == DKV_BF16) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * J; ++i) {
+          const float2 f = DT<T>::to_f2(qf[nt][i]);
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        // largest element to [2^13, 2^14)
+        int e = (int)(__float_as_uint(top) >> 23) - 127;
+        e = top > 0.f && top <= FLT_MAX ? max(e, -113) : 13;
+        const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+        unscale = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+#pragma unroll
+        for (int i = 0; i < 2 * J; ++i) {
+          const float2 f = DT<T>::to_f2(qf[nt][i]);
+          qf[nt][i] = tc::pack2<__half>(f.x * up, f.y * up);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        sl[nt][u] = p.scale_log2 * __shfl_sync(~0u, unscale, (2 * c + u) * 4);
+        const int pc = qt * R + nt * 8 + 2 * c + u;
+        vis[nt][u] = pc <= last ? max(0, kv - n + pc / G + 1) : 0;
+      }
+    }
+
+    float m[NT][2], l[NT][2], o[NT][J][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      m[nt][0] = m[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < J; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+    }
+
+#pragma unroll 1
+    for (int tile = tile0; tile < tile1; ++tile) {
+      issue();
+      cp_async_wait_group<C::kStages - 1>();
+      __syncwarp();
+      const uint8_t* st = ring + st_out * C::kStage;
+      const bool full = (have >> st_out) & 1;
+      st_out = st_out + 1 == C::kStages ? 0 : st_out + 1;
+      const int t0 = tile * kTile + warp * kStep;
+      if (full && t0 < maxvis) {
+        // scores
+        float s[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+        {
+          constexpr int W = D / 32;  // code words of a thread per key
+          uint32_t kw[2][W];
+          uint32_t ks[2][2];
+#pragma unroll
+          for (int rr = 0; rr < 2; ++rr) {
+            const uint8_t* row = st + (g + 8 * rr) * e2m1::code_bytes(D) + c * (D / 8);
+            if constexpr (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(row);
+              kw[rr][0] = w.x; kw[rr][1] = w.y; kw[rr][2] = w.z; kw[rr][3] = w.w;
+            } else {
+              const uint2 w = *reinterpret_cast<const uint2*>(row);
+              kw[rr][0] = w.x; kw[rr][1] = w.y;
+            }
+            const int t = (g >> 1) + 4 * (g & 1) + 8 * rr;
+            const uint8_t* sp = st + C::kC + t * e2m1::scale_bytes(D) + c * (D / 64);
+            if constexpr (D == 128) {
+              const uint32_t s2 = e2m1::scales_to_h2(*reinterpret_cast<const uint16_t*>(sp));
+              ks[rr][0] = __byte_perm(s2, 0, 0x1010);
+              ks[rr][1] = __byte_perm(s2, 0, 0x3232);
+            } else {
+              ks[rr][0] = ks[rr][1] = __byte_perm(e2m1::scales_to_h2(*sp), 0, 0x1010);
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const int blk = D == 128 ? j / 4 : 0;
+            uint32_t a[4];
+#pragma unroll
+            for (int rr = 0; rr < 2; ++rr) {
+              const uint32_t w = kw[rr][j / 2] >> (16 * (j & 1));
+              a[rr] = hmul2(e2m1::codes_to_h2(w & 0xff), ks[rr][blk]);
+              a[rr + 2] = hmul2(e2m1::codes_to_h2((w >> 8) & 0xff), ks[rr][blk]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[nt][2 * j], qf[nt][2 * j + 1]);
+          }
+        }
+        const bool edge = t0 + kStep > minvis;
+        const int tok = t0 + (g >> 1) + 4 * (g & 1);
+        bool up = false;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            s[nt][u] *= sl[nt][u & 1];
+            if (edge && tok + 8 * (u >> 1) >= vis[nt][u & 1]) s[nt][u] = -INFINITY;
+            up |= s[nt][u] > m[nt][u & 1] + kLazy;
+          }
+        }
+        if (__any_sync(~0u, up)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              float x = fmaxf(s[nt][u], s[nt][u + 2]);
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+              x = fmaxf(x, m[nt][u]);
+              f[u] = x == m[nt][u] ? 1.0f : exp2f(m[nt][u] - x);
+              m[nt][u] = x;
+              l[nt][u] *= f[u];
+            }
+#pragma unroll
+            for (int i = 0; i < J; ++i) {
+              o[nt][i][0] *= f[0]; o[nt][i][1] *= f[1];
+              o[nt][i][2] *= f[0]; o[nt][i][3] *= f[1];
+            }
+          }
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+          const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+          const float p0 = tc::ex2_approx(s[nt][0] - m0), p1 = tc::ex2_approx(s[nt][1] - m1);
+          const float p2 = tc::ex2_approx(s[nt][2] - m0), p3 = tc::ex2_approx(s[nt][3] - m1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          pb[nt][0] = transpose8x8(tc::pack2<__half>(p0, p1));
+          pb[nt][1] = transpose8x8(tc::pack2<__half>(p2, p3));
+        }
+        // values: keys c, c+4, c+8, c+12 of the step, dims [g * D/8, (g + 1) * D/8)
+        {
+          constexpr int W = D / 64;
+          uint32_t vw[4][W], vs[4];
+          const uint8_t* sv = st + 2 * C::kC + C::kS + (D == 128 ? g : g >> 1);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int t = c + 4 * k;
+            const uint8_t* row = st + C::kC + C::kS + t * e2m1::code_bytes(D);
+            if constexpr (D == 128) {
+              const uint2 w = *reinterpret_cast<const uint2*>(row + (((g >> 1) ^ (t & 2)) * 16 + (g & 1) * 8));
+              vw[k][0] = w.x; vw[k][1] = w.y;
+            } else {
+              vw[k][0] = *reinterpret_cast<const uint32_t*>(row + g * 4);
+            }
+            uint32_t sb = sv[t * e2m1::scale_bytes(D)];
+            // nobody sees this key, or its NaN is dealt out below
+            if (edge && (t0 + t >= maxvis || (sb & 0x7f) == 0x7f)) sb = 0;
+            vs[k] = __byte_perm(e2m1::scales_to_h2(sb), 0, 0x1010);
+          }
+#pragma unroll
+          for (int i = 0; i < J; ++i) {
+            uint32_t x[4], a[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              x[k] = hmul2(e2m1::codes_to_h2((vw[k][i / 4] >> (8 * (i & 3))) & 0xff), vs[k]);
+            a[0] = __byte_perm(x[0], x[1], 0x5410);
+            a[1] = __byte_perm(x[0], x[1], 0x7632);
+            a[2] = __byte_perm(x[2], x[3], 0x5410);
+            a[3] = __byte_perm(x[2], x[3], 0x7632);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a, pb[nt][0], pb[nt][1]);
+          }
+          if (edge) {
+            // A NaN block of V reaches the rows that see its key, and no others (a
+            // zero weight times NaN would reach them all).
+#pragma unroll 1
+            for (int t = 0; t < kStep; ++t)
+              if ((sv[t * e2m1::scale_bytes(D)] & 0x7f) == 0x7f) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int i = 0; i < J; ++i)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                      if (t0 + t < vis[nt][u & 1]) o[nt][i][u] = __int_as_float(0x7fc00000);
+              }
+          }
+        }
+      }
+      __syncwarp();
+    }
+
+    // ---- the item's end: join the warps --------------------------------------
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        float x = l[nt][u];
+        x += __shfl_xor_sync(~0u, x, 4);
+        x += __shfl_xor_sync(~0u, x, 8);
+        x += __shfl_xor_sync(~0u, x, 16);
+        if (lane < 4) {
+          s_m[warp * R + nt * 8 + 2 * c + u] = m[nt][u];
+          s_l[warp * R + nt * 8 + 2 * c + u] = x;
+        }
+      }
+    const bool starts = tile0 == 0, ends = tile1 == cons.tiles;
+    const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
+#pragma unroll 1
+    for (int nt = 0; nt < NT; ++nt) {
+      __syncthreads();
+      // this warp's rows against the CTA's maximum
+      float f[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = nt * 8 + 2 * c + u;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * R + r]);
+        const float mine = s_m[warp * R + r];
+        f[u] = mine == top ? 1.0f : exp2f(mine - top);
+      }
+#pragma unroll
+      for (int n2 = 0; n2 < NT; ++n2)
+        if (n2 == nt) {
+#pragma unroll
+          for (int i = 0; i < J; ++i)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+              *reinterpret_cast<float2*>(merge + (warp * 8 + 2 * c + u) * D + g * (D / 8) + 2 * i) =
+                  make_float2(o[n2][i][u] * f[u], o[n2][i][u + 2] * f[u]);
+        }
+      __syncthreads();
+      {
+        constexpr int V = D / 32;
+        const int r = threadIdx.x >> 5, d0 = lane * V, pr = qt * R + nt * 8 + r;
+        float acc[V], top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * R + nt * 8 + r]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = s_m[w * R + nt * 8 + r];
+          sum += s_l[w * R + nt * 8 + r] * (mw == top ? 1.0f : exp2f(mw - top));
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[e] += merge[(w * 8 + r) * D + d0 + e];
+        }
+        if (starts && ends) {
+          if (pr <= last) store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, top, sum, lane == 0);
+        } else {
+          float* po = p.part_o + ((size_t)slot * R + nt * 8 + r) * D + d0;
+#pragma unroll
+          for (int e = 0; e < V; ++e) po[e] = acc[e];
+          if (lane == 0) {
+            p.part_ml[((size_t)slot * R + nt * 8 + r) * 2] = top;
+            p.part_ml[((size_t)slot * R + nt * 8 + r) * 2 + 1] = sum;
+          }
+        }
+      }
+    }
+    if (!(starts && ends) && threadIdx.x == 0) {
+      AttendDesc d;
+      d.valid = 1; d.ends = ends; d.row0 = row0; d.first = qt * R; d.last = last; d.head0 = h * G;
+      p.desc[slot] = d;
+    }
+    __syncthreads();  // s_m, s_l and merge are free for the next item
+    at += tile1 - tile0;
+    cons.tile = tile1 - 1;
+    next_tile(cons);
+  }
+  cp_async_wait_all();
+}
+
+// Joins the partials of each cut item: block c takes the item whose first piece
+// CTA c left unfinished, whose further pieces CTAs c+1, c+2, ... hold.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, int R, int ctas) {
+  griddep_wait();
+  const AttendDesc d = p.desc[2 * blockIdx.x + 1];
+  if (!d.valid || d.ends) return;
+  constexpr int V = D / 32;
+  const int lane = threadIdx.x & 31;
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < R; r += gridDim.y * 8) {
+    const int pr = d.first + r;
+    if (pr > d.last) continue;
+    float top = -INFINITY, sum = 0.f, acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    int slot = 2 * blockIdx.x + 1;
+    bool more = true;
+    while (more) {
+      const size_t at = (size_t)slot * R + r;
+      const float m = p.part_ml[2 * at], l = p.part_ml[2 * at + 1];
+      const float nt = fmaxf(top, m);
+      const float fa = top == nt ? 1.0f : exp2f(top - nt), fb = m == nt ? 1.0f : exp2f(m - nt);
+      sum = sum * fa + l * fb;
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = acc[e] * fa + p.part_o[at * D + lane * V + e] * fb;
+      top = nt;
+      more = !p.desc[slot].ends;
+      slot = (slot | 1) + 1;
+      if (slot >= 2 * ctas) break;
+    }
+    store_row<T, V>(p, d.row0 + pr / p.G, d.head0 + pr % p.G, D, lane * V, acc, top, sum, lane == 0);
+  }
+}
+
+dkv_status refuse(dkv_status s, const char* msg) {
+  set_last_error(s, msg);
+  return s;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+constexpr int kMaxCtas = 304;  // two CTAs on each of 152 SMs
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+// Workspace: descriptors | partial (max, sum) | partial o, two slots per CTA.
+size_t ws_desc() { return align256(2 * kMaxCtas * sizeof(AttendDesc)); }
+size_t ws_ml(int R) { return align256((size_t)2 * kMaxCtas * R * 2 * 4); }
+size_t ws_o(int R, int D) { return align256((size_t)2 * kMaxCtas * R * D * 4); }
+
+// Query rows per item: the smallest of 8, 16 and 32 that holds a sequence's rows.
+int rows_per_item(int G, int max_rows) {
+  const long long rows = (long long)G * max_rows;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+
+template <typename T, int D, int NT>
+cudaError_t launch(const AttendParams& p, cudaStream_t s) {
+  using C = Cfg<D, NT>;
+  const int smem = C::kOffBatch + (p.B + 1) * 8 + 3 * p.B * 4;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(attend_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             C::kOffBatch + (DKV_MAX_STEP_BATCH + 1) * 20);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set[dev] = true;
+  }
+  const int per_sm = NT <= 2 && 2 * (smem + 1024) <= 228 * 1024 ? 2 : 1;
+  const int grid = 152 * per_sm;
+  attend_kernel<T, D, NT><<<grid, kThreads, smem, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, NT);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p, C::R, grid);
+}
+
+template <typename T, int D>
+cudaError_t launch_rows(const AttendParams& p, int R, cudaStream_t s) {
+  return R == 8 ? launch<T, D, 1>(p, s) : R == 16 ? launch<T, D, 2>(p, s) : launch<T, D, 4>(p, s);
+}
+
+}  // namespace
+
+extern "C" size_t dkv_paged_attend_workspace(int batch, int n_q_heads, int n_kv_heads, int head_dim,
+                                             int max_rows) {
+  if (batch <= 0 || n_kv_heads <= 0 || n_q_heads <= 0 || n_q_heads % n_kv_heads || max_rows <= 0 ||
+      (head_dim != 64 && head_dim != 128))
+    return 0;
+  const int R = rows_per_item(n_q_heads / n_kv_heads, max_rows);
+  return ws_desc() + ws_ml(R) + ws_o(R, head_dim);
+}
+
+extern "C" dkv_status dkv_paged_attend(const dkv_attend_t* a, void* stream) {
+  if (!a) return refuse(DKV_ERR_INVALID_ARG, "null description");
+  if (!a->q || !a->k_pool || !a->v_pool || !a->page_table || !a->kv_len || !a->out || !a->workspace)
+    return refuse(DKV_ERR_INVALID_ARG, "null pointer argument");
+  if (a->batch <= 0 || a->batch > DKV_MAX_STEP_BATCH)
+    return refuse(DKV_ERR_INVALID_ARG, "batch outside [1, DKV_MAX_STEP_BATCH]");
+  if (a->rows <= 0 || a->rows > (1 << 30) || a->max_rows <= 0)
+    return refuse(DKV_ERR_INVALID_ARG, "rows outside [1, 2^30] or max_rows not positive");
+  if (!a->row_start && (a->rows != a->batch || a->max_rows != 1))
+    return refuse(DKV_ERR_INVALID_ARG, "without row_start there is one row per sequence");
+  if (a->dtype != DKV_BF16 && a->dtype != DKV_FP16)
+    return refuse(DKV_ERR_INVALID_ARG, "dtype is not bf16 (0) or fp16 (1)");
+  if (a->head_dim != 64 && a->head_dim != 128)
+    return refuse(DKV_ERR_UNSUPPORTED, "head_dim (supported: 64, 128)");
+  if (a->n_kv_heads <= 0 || a->n_q_heads <= 0 || a->n_q_heads % a->n_kv_heads || a->n_q_heads > 65536)
+    return refuse(DKV_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of n_kv_heads");
+  if (a->q_stride < (long long)a->n_q_heads * a->head_dim || a->q_stride % 8)
+    return refuse(DKV_ERR_INVALID_ARG, "q_stride must hold the heads and be a multiple of 8");
+  if (a->page_tokens < e2m1::kMinPageTokens || a->page_tokens > 4096 ||
+      (a->page_tokens & (a->page_tokens - 1)))
+    return refuse(DKV_ERR_INVALID_ARG, "page_tokens must be a power of two in [16, 4096]");
+  if (a->num_pages <= 0 || (long long)a->num_pages * a->page_tokens > (1LL << 30))
+    return refuse(DKV_ERR_INVALID_ARG, "num_pages must be positive, num_pages * page_tokens at most 2^30");
+  if (a->max_pages <= 0 || (long long)a->max_pages * a->page_tokens > (1LL << 30))
+    return refuse(DKV_ERR_INVALID_ARG, "max_pages must be positive, max_pages * page_tokens at most 2^30");
+  if (!aligned16(a->q) || !aligned16(a->k_pool) || !aligned16(a->v_pool) || !aligned16(a->out) ||
+      (reinterpret_cast<uintptr_t>(a->workspace) & 255))
+    return refuse(DKV_ERR_INVALID_ARG, "tensors must start on 16-byte boundaries, the workspace on 256");
+  if (!(fabsf(a->scale) <= FLT_MAX) || !(fabsf(a->v_scale) <= FLT_MAX))
+    return refuse(DKV_ERR_INVALID_ARG, "scale and v_scale must be finite");
+  const int G = a->n_q_heads / a->n_kv_heads, D = a->head_dim;
+  if ((long long)a->rows * G > (1LL << 30))
+    return refuse(DKV_ERR_INVALID_ARG, "rows times heads per KV head above 2^30");
+  const int R = rows_per_item(G, a->max_rows);
+  if (a->workspace_bytes < ws_desc() + ws_ml(R) + ws_o(R, D))
+    return refuse(DKV_ERR_INVALID_ARG, "workspace smaller than dkv_paged_attend_workspace says");
+  AttendParams p;
+  char* w = static_cast<char*>(a->workspace);
+  p.desc = reinterpret_cast<AttendDesc*>(w);
+  p.part_ml = reinterpret_cast<float*>(w + ws_desc());
+  p.part_o = reinterpret_cast<float*>(w + ws_desc() + ws_ml(R));
+  p.q = a->q; p.k_pool = static_cast<const uint8_t*>(a->k_pool); p.v_pool = static_cast<const uint8_t*>(a->v_pool);
+  p.table = a->page_table; p.kv_len = a->kv_len; p.row_start = a->row_start;
+  p.out = a->out; p.lse = a->lse; p.q_stride = a->q_stride;
+  p.B = a->batch; p.N = a->rows; p.Hq = a->n_q_heads; p.Hkv = a->n_kv_heads; p.G = G;
+  p.num_pages = a->num_pages; p.max_pages = a->max_pages;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < a->page_tokens) ++p.page_shift;
+  p.page_bytes = e2m1::page_bytes(D, a->page_tokens);
+  p.scale_log2 = (float)(1.4426950408889634 * (double)a->scale);
+  p.v_scale = a->v_scale;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (a->dtype == DKV_BF16)
+    e = D == 64 ? launch_rows<__nv_bfloat16, 64>(p, R, s) : launch_rows<__nv_bfloat16, 128>(p, R, s);
+  else
+    e = D == 64 ? launch_rows<__half, 64>(p, R, s) : launch_rows<__half, 128>(p, R, s);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return refuse(DKV_ERR_CUDA, cudaGetErrorString(e));
+  }
+  return DKV_OK;
+}

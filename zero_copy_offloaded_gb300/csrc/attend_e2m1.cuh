@@ -1,0 +1,71 @@
+// What the kernels of the 4-bit paged attention share.
+#pragma once
+
+#include <math.h>
+
+#include "e2m1.cuh"
+
+namespace dkv {
+
+// A piece of an item that its CTA could not finish or did not start.
+struct AttendDesc {
+  int valid, ends;      // ends: the item's last piece
+  int row0;             // first query row of the sequence
+  int first, last;      // packed rows (token-major over the group's heads) of the item
+  int head0;            // first query head of the group
+  int pad[2];
+};
+
+struct AttendParams {
+  const void* q;
+  const uint8_t* k_pool;
+  const uint8_t* v_pool;
+  const int* table;      // [B][max_pages]
+  const int* kv_len;     // [B]
+  const int* row_start;  // [B + 1], or null: row b is sequence b's only one
+  void* out;
+  float* lse;
+  AttendDesc* desc;
+  float* part_ml;
+  float* part_o;
+  long long q_stride;
+  size_t page_bytes;
+  int B, N, Hq, Hkv, G;
+  int num_pages, max_pages, page_shift;
+  float scale_log2, v_scale;
+};
+
+// Sequence b's cached keys, first row and rows, held inside what the buffers have.
+__device__ __forceinline__ void batch_entry(const AttendParams& p, int b, int& kv, int& row, int& n) {
+  kv = min(max(p.kv_len[b], 0), p.max_pages << p.page_shift);
+  if (p.row_start) {
+    row = min(max(p.row_start[b], 0), p.N);
+    n = min(max(p.row_start[b + 1], row), p.N) - row;
+  } else {
+    row = b;
+    n = 1;
+  }
+}
+
+// Rows are normalised and rounded once; a row that saw no key is zero, its lse -infinity.
+// A NaN sum or output stays NaN.
+template <typename T, int V>
+__device__ __forceinline__ void store_row(const AttendParams& p, int row, int head, int D, int d0,
+                                          const float (&acc)[V], float top, float sum, bool lead) {
+  const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
+  T* o = static_cast<T*>(p.out) + ((size_t)row * p.Hq + head) * D + d0;
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int i = 0; i < V / 2; ++i) {
+    const T a = DT<T>::from_f(acc[2 * i] * inv), b = DT<T>::from_f(acc[2 * i + 1] * inv);
+    w[i] = (uint32_t)(*reinterpret_cast<const uint16_t*>(&a)) |
+           ((uint32_t)(*reinterpret_cast<const uint16_t*>(&b)) << 16);
+  }
+  if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(o) = w[0];
+  if (lead && p.lse)
+    p.lse[(size_t)row * p.Hq + head] =
+        sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+}  // namespace dkv

@@ -192,6 +192,8 @@ dkv_status choose_decode(dkv_cache* c, int G, DecodeChoice* ch) {
 dkv_status check_call(dkv_cache* c, const void* x, const void* wq, const void* wk,
                       const void* wv, int hidden, int n_q_heads, const void* out, int T) {
   if (!valid(c)) return fail(DKV_ERR_INVALID_ARG, "invalid cache handle");
+  if (c->kv_format == DKV_KV_E2M1)
+    return fail(DKV_ERR_UNSUPPORTED, "an E2M1 cache takes dkv_qkv_append and dkv_paged_attend");
   if (!x || !wq || !wk || !wv || !out) return fail(DKV_ERR_INVALID_ARG, "null tensor pointer");
   if (hidden <= 0 || hidden % 16 != 0)
     return fail(DKV_ERR_INVALID_ARG, "hidden=%d must be a positive multiple of 16", hidden);
@@ -219,6 +221,11 @@ dkv_status check_call(dkv_cache* c, const void* x, const void* wq, const void* w
 size_t pool_rows(const dkv_cache* c) {
   return c->page_tokens ? (size_t)c->num_pages * c->Hkv * c->page_tokens
                         : (size_t)c->B * c->Hkv * c->max_tokens;
+}
+
+// Bytes of `rows` cache rows of D elements: 2, 1 or (E2M1) 9/16 an element.
+size_t cache_bytes(size_t rows, int D, int kv_format) {
+  return kv_format == DKV_KV_E2M1 ? rows * (D * 9 / 16) : rows * D * (kv_format == DKV_KV_E4M3 ? 1 : 2);
 }
 
 CacheLayout layout_of(const dkv_cache* c) {
@@ -365,12 +372,12 @@ static dkv_status alloc_common(dkv_cache** out, int batch, int n_kv_heads, int h
   cudaDeviceGetAttribute(&can_map, cudaDevAttrCanMapHostMemory, dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (!can_map) return fail(DKV_ERR_NO_MAPPED_MEMORY, "device %d cannot map host memory", dev);
-  if (kv_format != DKV_KV_NATIVE && kv_format != DKV_KV_E4M3)
-    return fail(DKV_ERR_INVALID_ARG, "kv_format=%d is not native (0) or E4M3 (1)", kv_format);
+  if (kv_format != DKV_KV_NATIVE && kv_format != DKV_KV_E4M3 && kv_format != DKV_KV_E2M1)
+    return fail(DKV_ERR_INVALID_ARG, "kv_format=%d is not native (0), E4M3 (1) or E2M1 (2)", kv_format);
   if (kv_format == DKV_KV_E4M3 && dtype != DKV_BF16)
     return fail(DKV_ERR_UNSUPPORTED, "E4M3 caches take bf16 activations");
-  const int kv_eb = kv_format == DKV_KV_E4M3 ? 1 : 2;
-  const size_t bytes = rows * head_dim * kv_eb * layers;
+  const int kv_eb = kv_format == DKV_KV_NATIVE ? 2 : 1;
+  const size_t bytes = cache_bytes(rows * layers, head_dim, kv_format);
   void* kh = nullptr;
   void* vh = nullptr;
   // pinned on the host NUMA node attached to this GPU, where known
@@ -503,6 +510,8 @@ dkv_status dkv_cache_alloc_ex(dkv_cache** out, const dkv_cache_desc_t* d) {
     return fail(DKV_ERR_INVALID_ARG, "batch=%d must be in [1, %d]", d->batch, kMaxBatch);
   if (d->n_kv_heads <= 0)
     return fail(DKV_ERR_INVALID_ARG, "n_kv_heads=%d must be positive", d->n_kv_heads);
+  if (d->kv_format == DKV_KV_E2M1 && d->page_tokens < 16)
+    return fail(DKV_ERR_UNSUPPORTED, "E2M1 caches are paged, with pages of 16 tokens or more");
   if (d->page_tokens) {
     if (layers != 1) return fail(DKV_ERR_UNSUPPORTED, "paged caches hold one layer");
     if (d->page_tokens < 1 || d->page_tokens > 4096 || (d->page_tokens & (d->page_tokens - 1)))
@@ -627,7 +636,7 @@ dkv_status dkv_cache_get_lengths(const dkv_cache* c, int32_t* len) {
 
 dkv_status dkv_cache_info(const dkv_cache* c, dkv_cache_info_t* info) {
   if (!valid(c) || !info) return fail(DKV_ERR_INVALID_ARG, "invalid argument");
-  info->host_pinned_bytes = 2 * pool_rows(c) * c->D * c->kv_eb * c->layers;
+  info->host_pinned_bytes = 2 * cache_bytes(pool_rows(c) * c->layers, c->D, c->kv_format);
   info->device_workspace_bytes = c->ws.bytes + sizeof(DeviceStatus) +
                                  c->pages.size() * sizeof(int32_t);
   info->device_staging_bytes = 0;
@@ -661,6 +670,8 @@ dkv_status dkv_cache_set_tuning(dkv_cache* c, int splits, int tile_n, int stages
 dkv_status dkv_cache_reserve(dkv_cache* c, int n_q_heads, int max_new_tokens) {
   if (!valid(c) || n_q_heads <= 0 || max_new_tokens <= 0 || n_q_heads % c->Hkv)
     return fail(DKV_ERR_INVALID_ARG, "invalid argument");
+  if (c->kv_format == DKV_KV_E2M1)
+    return fail(DKV_ERR_UNSUPPORTED, "the calls on an E2M1 cache use no workspace of the cache");
   std::lock_guard<std::mutex> lk(c->mu);
   dkv_status st = set_device(c);
   if (st != DKV_OK) return st;

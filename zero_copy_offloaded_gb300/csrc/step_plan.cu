@@ -1,0 +1,232 @@
+// dkv_step_plan: lengths and new-token counts of a batch become pages, row
+// starts, positions and slots, on the GPU.
+//
+// For sequence b with len_b cached rows and new_b >= 0 new ones, pages of P rows:
+//   held_b = ceil(len_b / P),  need_b = ceil((len_b + new_b) / P) - held_b,
+// new_b < 0 releases the sequence (its held_b pages go back, its length is 0).
+// Released pages are pushed on the free stack in order of (sequence, page);
+// then the k-th page taken, in the same order, is the k-th from the top.  The
+// three exclusive scans (need, released, rows) give every sequence its place.
+// The new token t of sequence b has position len_b + t and slot
+// table[b][pos / P] * P + pos % P.
+//
+// It moves a few KB, so what bounds it is latency.  One CTA does the scans with
+// a sequence per thread (inputs are all read before anything is written, so that
+// lengths and the free count may be updated in place); the pages are then moved
+// a warp per sequence.
+#include <stdio.h>
+
+#include "dkv_internal.cuh"
+
+namespace dkv {
+void set_last_error(dkv_status s, const char* msg);
+}
+
+namespace {
+
+using namespace dkv;
+
+constexpr int kPlanThreads = 1024;
+
+struct PlanParams {
+  const int* lengths;
+  const int* new_tokens;
+  int* table;
+  int* free_pages;
+  const int* free_count;
+  int* row_start;
+  int* row_pos;
+  int* row_slot;
+  int* kv_len;
+  int* free_left;
+  int* report;
+  int B, max_pages, shift, num_pages, max_rows;
+};
+
+struct Sums {
+  long long need, back, rows;
+};
+
+__device__ __forceinline__ Sums add(const Sums& a, const Sums& b) {
+  return {a.need + b.need, a.back + b.back, a.rows + b.rows};
+}
+
+__device__ __forceinline__ Sums shfl_up(const Sums& v, int d) {
+  return {__shfl_up_sync(~0u, v.need, d), __shfl_up_sync(~0u, v.back, d),
+          __shfl_up_sync(~0u, v.rows, d)};
+}
+
+// Positions and slots of rows [first, last) with `stride` threads: the sequence
+// of a row is found by bisection of the row starts.
+__device__ __forceinline__ void fill_rows(const PlanParams& p, const int* start, const int* kv,
+                                          int first, int stride) {
+  const int total = start[p.B];
+  for (int r = first; r < p.max_rows; r += stride) {
+    int pos = 0, slot = -1;
+    if (r < total) {
+      int lo = 0, hi = p.B;  // start[lo] <= r < start[hi]
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= r) lo = mid; else hi = mid;
+      }
+      pos = kv[lo] - (start[lo + 1] - r);
+      const int page = p.table[(size_t)lo * p.max_pages + (pos >> p.shift)];
+      slot = (page << p.shift) + (pos & ((1 << p.shift) - 1));
+    }
+    p.row_pos[r] = pos;
+    p.row_slot[r] = slot;
+  }
+}
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p, int fill) {
+  __shared__ int s_start[kPlanThreads + 1], s_kv[kPlanThreads], s_held[kPlanThreads];
+  __shared__ int s_need[kPlanThreads + 1], s_back[kPlanThreads + 1];
+  __shared__ Sums s_warp[32];
+  __shared__ int s_max;
+  const int b = threadIdx.x, lane = b & 31, warp = b >> 5, warps = blockDim.x >> 5;
+  const long long cap = (long long)p.max_pages << p.shift;
+  const int free_count = min(max(*p.free_count, 0), p.num_pages);
+  if (b == 0) s_max = 0;
+  int len = 0, kv = 0, held = 0;
+  Sums own = {0, 0, 0};
+  bool bad = false;
+  if (b < p.B) {
+    len = max(p.lengths[b], 0);
+    const int nw = p.new_tokens[b];
+    bad = len > cap || (nw > 0 && (long long)len + nw > cap);
+    if (!bad) {
+      held = (int)(((long long)len + (1 << p.shift) - 1) >> p.shift);
+      if (nw < 0) {
+        own.back = held;
+      } else {
+        kv = len + nw;
+        own.need = (((long long)kv + (1 << p.shift) - 1) >> p.shift) - held;
+        own.rows = nw;
+      }
+    }
+  }
+  Sums inc = own;
+  for (int d = 1; d < 32; d <<= 1) {
+    const Sums o = shfl_up(inc, d);
+    if (lane >= d) inc = add(inc, o);
+  }
+  if (lane == 31) s_warp[warp] = inc;
+  bad = __syncthreads_or(bad);
+  if (warp == 0) {
+    Sums w = lane < warps ? s_warp[lane] : Sums{0, 0, 0};
+    for (int d = 1; d < 32; d <<= 1) {
+      const Sums o = shfl_up(w, d);
+      if (lane >= d) w = add(w, o);
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  if (warp > 0) inc = add(inc, s_warp[warp - 1]);
+  const Sums all = s_warp[warps - 1];
+  const long long stack = (long long)free_count + all.back;
+  const bool ok = !bad && all.need <= stack && all.rows <= p.max_rows && stack <= p.num_pages;
+  if (b < p.B) {
+    s_start[b] = ok ? (int)(inc.rows - own.rows) : 0;
+    s_kv[b] = ok ? kv : len;
+    s_held[b] = held;
+    s_need[b] = ok ? (int)(inc.need - own.need) : 0;
+    s_back[b] = ok ? (int)(inc.back - own.back) : 0;
+    p.kv_len[b] = ok ? kv : len;
+    atomicMax(&s_max, ok ? kv : len);
+  }
+  if (b == 0) {
+    s_start[p.B] = ok ? (int)all.rows : 0;
+    s_need[p.B] = ok ? (int)all.need : 0;
+    s_back[p.B] = ok ? (int)all.back : 0;
+  }
+  __syncthreads();
+  for (int i = b; i <= p.B; i += blockDim.x) p.row_start[i] = s_start[i];
+  if (b == 0) {
+    *p.free_left = ok ? (int)(stack - all.need) : free_count;
+    p.report[0] = ok ? DKV_OK : DKV_ERR_CAPACITY;
+    p.report[1] = s_start[p.B];
+    p.report[2] = s_need[p.B];
+    p.report[3] = s_max;
+  }
+  // released pages onto the stack, a warp per sequence
+  if (s_back[p.B] > 0)
+    for (int s = warp; s < p.B; s += warps) {
+      const int at = s_back[s], n = s_back[s + 1] - at;
+      for (int i = lane; i < n; i += 32)
+        p.free_pages[free_count + at + i] = p.table[(size_t)s * p.max_pages + i];
+    }
+  __syncthreads();
+  // pages taken, from the top of the stack
+  if (s_need[p.B] > 0)
+    for (int s = warp; s < p.B; s += warps) {
+      const int at = s_need[s], n = s_need[s + 1] - at, h = s_held[s];
+      for (int i = lane; i < n; i += 32)
+        p.table[(size_t)s * p.max_pages + h + i] = p.free_pages[stack - 1 - at - i];
+    }
+  if (fill) {
+    __syncthreads();
+    fill_rows(p, s_start, s_kv, b, blockDim.x);
+  }
+}
+
+// The rows of a long step, over the whole GPU.
+__global__ void __launch_bounds__(256) plan_rows_kernel(const PlanParams p) {
+  extern __shared__ int s_plan[];
+  int* s_start = s_plan;
+  int* s_kv = s_plan + p.B + 1;
+  for (int i = threadIdx.x; i <= p.B; i += blockDim.x) {
+    s_start[i] = p.row_start[i];
+    if (i < p.B) s_kv[i] = p.kv_len[i];
+  }
+  __syncthreads();
+  fill_rows(p, s_start, s_kv, blockIdx.x * blockDim.x + threadIdx.x, gridDim.x * blockDim.x);
+}
+
+// Up to here the planning CTA fills the rows itself.
+constexpr int kFillRows = 4096;
+
+dkv_status refuse(dkv_status s, const char* msg) {
+  set_last_error(s, msg);
+  return s;
+}
+
+}  // namespace
+
+extern "C" dkv_status dkv_step_plan(const int32_t* lengths, const int32_t* new_tokens,
+                                    int32_t* page_table, int32_t* free_pages,
+                                    const int32_t* free_count, int batch, int max_pages,
+                                    int page_tokens, int num_pages, int max_rows,
+                                    int32_t* row_start, int32_t* row_pos, int32_t* row_slot,
+                                    int32_t* kv_len, int32_t* free_left, int32_t* report,
+                                    void* stream) {
+  if (!lengths || !new_tokens || !page_table || !free_pages || !free_count || !row_start ||
+      !row_pos || !row_slot || !kv_len || !free_left || !report)
+    return refuse(DKV_ERR_INVALID_ARG, "null pointer argument");
+  if (batch <= 0 || batch > DKV_MAX_STEP_BATCH)
+    return refuse(DKV_ERR_INVALID_ARG, "batch outside [1, DKV_MAX_STEP_BATCH]");
+  if (page_tokens < 1 || page_tokens > 4096 || (page_tokens & (page_tokens - 1)))
+    return refuse(DKV_ERR_INVALID_ARG, "page_tokens must be a power of two in [1, 4096]");
+  if (max_pages <= 0 || (long long)max_pages * page_tokens > (1LL << 30))
+    return refuse(DKV_ERR_INVALID_ARG, "max_pages must be positive, max_pages * page_tokens at most 2^30");
+  if (num_pages <= 0 || (long long)num_pages * page_tokens > (1LL << 30))
+    return refuse(DKV_ERR_INVALID_ARG, "num_pages must be positive, num_pages * page_tokens at most 2^30");
+  if (max_rows <= 0 || max_rows > (1 << 30))
+    return refuse(DKV_ERR_INVALID_ARG, "max_rows outside [1, 2^30]");
+  PlanParams p;
+  p.lengths = lengths; p.new_tokens = new_tokens; p.table = page_table;
+  p.free_pages = free_pages; p.free_count = free_count;
+  p.row_start = row_start; p.row_pos = row_pos; p.row_slot = row_slot;
+  p.kv_len = kv_len; p.free_left = free_left; p.report = report;
+  p.B = batch; p.max_pages = max_pages; p.num_pages = num_pages; p.max_rows = max_rows;
+  p.shift = 0;
+  while ((1 << p.shift) < page_tokens) ++p.shift;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool fill = max_rows <= kFillRows;
+  plan_kernel<<<1, kPlanThreads, 0, s>>>(p, fill);
+  if (!fill) {
+    const int blocks = max_rows / 1024 < 152 ? max_rows / 1024 : 152;
+    plan_rows_kernel<<<blocks, 256, (2 * batch + 1) * sizeof(int), s>>>(p);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? DKV_OK : refuse(DKV_ERR_CUDA, cudaGetErrorString(e));
+}
