@@ -272,10 +272,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) 
         }
         if (out) {  // what the cache now holds
           const float mul = kind == 1 ? p.k_scale : p.v_scale;
+          uint32_t hh[4];
+          e2m1::codes_to_h2(code, hh);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const uint32_t hh = e2m1::codes_to_h2((code >> (8 * e)) & 0xff);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh[e]));
             x[2 * e] = __fmul_rn(__fmul_rn(f.x, sf), mul);
             x[2 * e + 1] = __fmul_rn(__fmul_rn(f.y, sf), mul);
           }

@@ -84,8 +84,8 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 
 // Where a CTA is on the line of tiles.
 struct Pos {
-  int b, item, tile;  // item: KV head * qtiles + query tile, inside sequence b
-  int items, tiles;   // of sequence b
+  int b, h, qt, tile;  // sequence, KV head, query tile, key tile
+  int qtiles, tiles;   // of sequence b
 };
 
 template <typename T, int D, int NT>
@@ -140,14 +140,16 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
 
   auto enter = [&](Pos& at, int b) {
     at.b = b;
-    at.items = p.Hkv * ((s_n[b] * G + R - 1) / R);
+    at.qtiles = (s_n[b] * G + R - 1) / R;
     at.tiles = max(1, (s_kv[b] + kTile - 1) / kTile);
   };
   auto next_tile = [&](Pos& at) {
     if (++at.tile < at.tiles) return;
     at.tile = 0;
-    if (++at.item < at.items) return;
-    at.item = 0;
+    if (++at.qt < at.qtiles) return;
+    at.qt = 0;
+    if (++at.h < p.Hkv) return;
+    at.h = 0;
     int b = at.b + 1;
     while (b < p.B && s_n[b] == 0) ++b;
     if (b < p.B) enter(at, b);
@@ -161,8 +163,10 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
     }
     enter(cons, lo);
     const long long rem = g0 - s_pre[lo];
-    cons.item = (int)(rem / cons.tiles);
-    cons.tile = (int)(rem - (long long)cons.item * cons.tiles);
+    const long long item = rem / cons.tiles;
+    cons.tile = (int)(rem - item * cons.tiles);
+    cons.h = (int)(item / cons.qtiles);
+    cons.qt = (int)(item - (long long)cons.h * cons.qtiles);
   }
 
   // ---- producer side: this warp's next step to fetch -------------------------
@@ -182,8 +186,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
     have = ok ? have | (1u << st_in) : have & ~(1u << st_in);
     if (ok) {
       const int in_page = (prod.tile * kTile + warp * kStep) & ((1 << p.page_shift) - 1);
-      const int qtiles = prod.items / p.Hkv;
-      const size_t base = ((size_t)page * p.Hkv + prod.item / qtiles) * p.page_bytes;
+      const size_t base = ((size_t)page * p.Hkv + prod.h) * p.page_bytes;
       const size_t codes = base + (size_t)in_page * e2m1::code_bytes(D);
       const size_t scales = base + ((size_t)e2m1::code_bytes(D) << p.page_shift) +
                             (size_t)in_page * e2m1::scale_bytes(D);
@@ -220,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
   int st_out = 0;
   long long at = g0;
   while (at < g1) {
-    const int b = cons.b, qtiles = cons.items / p.Hkv, h = cons.item / qtiles, qt = cons.item % qtiles;
+    const int b = cons.b, h = cons.h, qt = cons.qt;
     const int kv = s_kv[b], n = s_n[b], row0 = s_row[b];
     const int tile0 = cons.tile;
     const int tile1 = (int)min((long long)cons.tiles, tile0 + (g1 - at));
@@ -324,17 +327,22 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
             }
           }
 #pragma unroll
-          for (int j = 0; j < J; ++j) {
-            const int blk = D == 128 ? j / 4 : 0;
-            uint32_t a[4];
+          for (int w = 0; w < W; ++w) {
+            uint32_t x[2][4];
+            e2m1::codes_to_h2(kw[0][w], x[0]);
+            e2m1::codes_to_h2(kw[1][w], x[1]);
 #pragma unroll
-            for (int rr = 0; rr < 2; ++rr) {
-              const uint32_t w = kw[rr][j / 2] >> (16 * (j & 1));
-              a[rr] = hmul2(e2m1::codes_to_h2(w & 0xff), ks[rr][blk]);
-              a[rr + 2] = hmul2(e2m1::codes_to_h2((w >> 8) & 0xff), ks[rr][blk]);
+            for (int jj = 0; jj < 2; ++jj) {
+              const int j = 2 * w + jj;
+              uint32_t a[4];
+#pragma unroll
+              for (int rr = 0; rr < 2; ++rr) {
+                a[rr] = hmul2(x[rr][2 * jj], ks[rr][D == 128 ? w / 2 : 0]);
+                a[rr + 2] = hmul2(x[rr][2 * jj + 1], ks[rr][D == 128 ? w / 2 : 0]);
+              }
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[nt][2 * j], qf[nt][2 * j + 1]);
             }
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[nt][2 * j], qf[nt][2 * j + 1]);
           }
         }
         const bool edge = t0 + kStep > minvis;
@@ -386,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
         // values: keys c, c+4, c+8, c+12 of the step, dims [g * D/8, (g + 1) * D/8)
         {
           constexpr int W = D / 64;
-          uint32_t vw[4][W], vs[4];
+          uint32_t vw[4][W], sb[4];
           const uint8_t* sv = st + 2 * C::kC + C::kS + (D == 128 ? g : g >> 1);
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -398,23 +406,29 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
             } else {
               vw[k][0] = *reinterpret_cast<const uint32_t*>(row + g * 4);
             }
-            uint32_t sb = sv[t * e2m1::scale_bytes(D)];
+            sb[k] = sv[t * e2m1::scale_bytes(D)];
             // nobody sees this key, or its NaN is dealt out below
-            if (edge && (t0 + t >= maxvis || (sb & 0x7f) == 0x7f)) sb = 0;
-            vs[k] = __byte_perm(e2m1::scales_to_h2(sb), 0, 0x1010);
+            if (edge && (t0 + t >= maxvis || (sb[k] & 0x7f) == 0x7f)) sb[k] = 0;
           }
+          const uint32_t vs[2] = {e2m1::scales_to_h2(sb[0] | (sb[1] << 8)),
+                                  e2m1::scales_to_h2(sb[2] | (sb[3] << 8))};
 #pragma unroll
-          for (int i = 0; i < J; ++i) {
-            uint32_t x[4], a[4];
+          for (int w = 0; w < W; ++w) {
+            // bytes that pair one dim of two keys: even dims, odd dims
+            uint32_t ev[2][4], od[2][4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              x[k] = hmul2(e2m1::codes_to_h2((vw[k][i / 4] >> (8 * (i & 3))) & 0xff), vs[k]);
-            a[0] = __byte_perm(x[0], x[1], 0x5410);
-            a[1] = __byte_perm(x[0], x[1], 0x7632);
-            a[2] = __byte_perm(x[2], x[3], 0x5410);
-            a[3] = __byte_perm(x[2], x[3], 0x7632);
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t lo = vw[2 * k][w], hi = vw[2 * k + 1][w];
+              e2m1::codes_to_h2((lo & 0x0F0F0F0Fu) | ((hi << 4) & 0xF0F0F0F0u), ev[k]);
+              e2m1::codes_to_h2(((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), od[k]);
+            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][i], a, pb[nt][0], pb[nt][1]);
+            for (int ii = 0; ii < 4; ++ii) {
+              const uint32_t a[4] = {hmul2(ev[0][ii], vs[0]), hmul2(od[0][ii], vs[0]),
+                                     hmul2(ev[1][ii], vs[1]), hmul2(od[1][ii], vs[1])};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * w + ii], a, pb[nt][0], pb[nt][1]);
+            }
           }
           if (edge) {
             // A NaN block of V reaches the rows that see its key, and no others (a

@@ -25,16 +25,26 @@ __host__ __device__ constexpr size_t page_bytes(int D, int page_tokens) {
   return (size_t)page_tokens * (code_bytes(D) + scale_bytes(D));
 }
 
-// Two codes (the low byte of `b`) as two fp16 numbers, the low code in the low half.
-__device__ __forceinline__ uint32_t codes_to_h2(uint32_t b) {
-  const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)b, __NV_E2M1);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// The eight codes of a word as four fp16 pairs; pair i holds byte i's two codes, the
+// low one in its low half.  One conversion instruction a pair, straight from the byte.
+__device__ __forceinline__ void codes_to_h2(uint32_t w, uint32_t (&x)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+      : "r"(w));
 }
 
 // Two E4M3 scales (the low 16 bits of `s`) as two fp16 numbers.
 __device__ __forceinline__ uint32_t scales_to_h2(uint32_t s) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)s, __NV_E4M3);
-  return (uint32_t)h.x | ((uint32_t)h.y << 16);
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+      : "=r"(r)
+      : "r"(s));
+  return r;
 }
 
 }  // namespace e2m1
