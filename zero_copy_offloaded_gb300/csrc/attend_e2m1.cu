@@ -14,7 +14,7 @@
 // item writes its rows; an item cut between CTAs leaves fp32 partials, which a
 // second kernel joins in CTA order.
 //
-// Inside a CTA each of 8 warps takes 16 keys of every tile through its own
+// Inside a CTA each of 4 warps takes 32 keys of every tile through its own
 // cp.async ring, with no barrier between warps until the item ends.  Per 16 keys:
 //   S^T[16 keys, 8 rows] = K Q^T  and  O^T[D, 8 rows] += V^T P^T  as m16n8k16 MMAs,
 // keys (then dims) in the M = 16 slot, so that a group of up to 8 query heads of a
@@ -42,24 +42,28 @@ namespace {
 
 using namespace dkv;
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStep = 16;               // keys of one warp step
+constexpr int kSub = 16;                // keys of one MMA, one ring slot
+constexpr int kStep = 2 * kSub;         // keys of one warp step
 constexpr int kTile = kStep * kWarps;   // keys of one tile
+constexpr int kSlots = 4;               // ring slots per warp
 constexpr float kLazy = 8.0f;  // the running maximum moves only when passed by 2^8
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int R = 8 * NT;                   // query rows per item
-  static constexpr int kC = kStep * e2m1::code_bytes(D);
-  static constexpr int kS = kStep * e2m1::scale_bytes(D);
-  static constexpr int kStage = 2 * (kC + kS);
-  static constexpr int kStages = D == 128 ? 4 : 6;
-  static constexpr int kRing = kStages * kStage;     // per warp
+  static constexpr int kC = kSub * e2m1::code_bytes(D);
+  static constexpr int kS = kSub * e2m1::scale_bytes(D);
+  static constexpr int kSlot = 2 * (kC + kS);        // K codes | K scales | V codes | V scales
+  static constexpr int kRing = kSlots * kSlot;       // per warp
   static constexpr int kMerge = kWarps * 8 * D * 4;  // one 8-row round of every warp's O
   static constexpr int kOffMerge = kWarps * kRing;
   static constexpr int kOffMl = kOffMerge + kMerge;          // [2][kWarps][R] floats
   static constexpr int kOffBatch = kOffMl + 2 * kWarps * R * 4;
+  // resident CTAs per SM, by registers: o takes 4 NT D/16, q 2 NT D/16
+  static constexpr int kPerSm = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int kBoth = NT == 1 ? 2 : 1;  // subs whose scores are held at once
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
@@ -89,7 +93,7 @@ struct Pos {
 };
 
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const AttendParams p) {
+__global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(const AttendParams p) {
   using C = Cfg<D, NT>;
   constexpr int R = C::R, J = D / 16;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -172,55 +176,61 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
   // ---- producer side: this warp's next step to fetch -------------------------
   Pos prod = cons;
   long long left = g1 - g0;  // steps not yet issued
-  int page = -1;             // pool page of prod's step (-1: nothing to fetch)
-  uint32_t have = 0;         // bit s: stage s holds keys
-  auto find_page = [&]() {
-    page = -1;
+  int page[2] = {-1, -1};    // pool pages of prod's two subs (-1: nothing to fetch)
+  uint32_t have = 0;         // bit s: slot s holds keys
+  auto find_pages = [&]() {
+    page[0] = page[1] = -1;
     if (left <= 0) return;
-    const int t0 = prod.tile * kTile + warp * kStep;
-    if (t0 < s_kv[prod.b]) page = __ldg(p.table + (size_t)prod.b * p.max_pages + (t0 >> p.page_shift));
+    const int t0 = prod.tile * kTile + warp * kStep, kv = s_kv[prod.b];
+    const int* row = p.table + (size_t)prod.b * p.max_pages;
+    if (t0 < kv) page[0] = __ldg(row + (t0 >> p.page_shift));
+    if (t0 + kSub < kv) page[1] = __ldg(row + ((t0 + kSub) >> p.page_shift));
   };
-  int st_in = 0;
+  int first_in = 0;  // slot of the next step's first sub: 0 or 2
   auto issue = [&]() {
-    const bool ok = page >= 0 && page < p.num_pages;
-    have = ok ? have | (1u << st_in) : have & ~(1u << st_in);
-    if (ok) {
-      const int in_page = (prod.tile * kTile + warp * kStep) & ((1 << p.page_shift) - 1);
-      const size_t base = ((size_t)page * p.Hkv + prod.h) * p.page_bytes;
-      const size_t codes = base + (size_t)in_page * e2m1::code_bytes(D);
-      const size_t scales = base + ((size_t)e2m1::code_bytes(D) << p.page_shift) +
-                            (size_t)in_page * e2m1::scale_bytes(D);
-      uint8_t* st = ring + st_in * C::kStage;
-      constexpr int CPR = e2m1::code_bytes(D) / 16;  // 16-byte chunks per row
 #pragma unroll
-      for (int i = 0; i < C::kC / 512; ++i) {
-        const int ch = lane + 32 * i, t = ch / CPR, part = ch % CPR;
-        // K: row of key t in MMA order; V: in key order, chunks of keys 2, 3 mod 4 swapped in pairs
-        const int r = ((t & 3) << 1) | ((t >> 2) & 1) | (t & 8);
-        cp_async16(st + r * e2m1::code_bytes(D) + part * 16, p.k_pool + codes + ch * 16, 16);
-        const int vp = D == 128 ? part ^ (t & 2) : part;
-        cp_async16(st + C::kC + C::kS + t * e2m1::code_bytes(D) + vp * 16, p.v_pool + codes + ch * 16, 16);
+    for (int sub = 0; sub < 2; ++sub) {
+      const int slot = first_in + sub;
+      const bool ok = page[sub] >= 0 && page[sub] < p.num_pages;
+      have = ok ? have | (1u << slot) : have & ~(1u << slot);
+      if (ok) {
+        const int in_page = (prod.tile * kTile + warp * kStep + sub * kSub) & ((1 << p.page_shift) - 1);
+        const size_t base = ((size_t)page[sub] * p.Hkv + prod.h) * p.page_bytes;
+        const size_t codes = base + (size_t)in_page * e2m1::code_bytes(D);
+        const size_t scales = base + ((size_t)e2m1::code_bytes(D) << p.page_shift) +
+                              (size_t)in_page * e2m1::scale_bytes(D);
+        uint8_t* st = ring + slot * C::kSlot;
+        constexpr int CPR = e2m1::code_bytes(D) / 16;  // 16-byte chunks per row
+#pragma unroll
+        for (int i = 0; i < C::kC / 512; ++i) {
+          const int ch = lane + 32 * i, t = ch / CPR, part = ch % CPR;
+          // K: row of key t in MMA order; V: in key order, chunks of keys 2, 3 mod 4 swapped in pairs
+          const int r = ((t & 3) << 1) | ((t >> 2) & 1) | (t & 8);
+          cp_async16(st + r * e2m1::code_bytes(D) + part * 16, p.k_pool + codes + ch * 16, 16);
+          const int vp = D == 128 ? part ^ (t & 2) : part;
+          cp_async16(st + C::kC + C::kS + t * e2m1::code_bytes(D) + vp * 16, p.v_pool + codes + ch * 16, 16);
+        }
+        constexpr int SCH = C::kS / 16;  // chunks of one scale block: 8 or 4
+        if (lane < SCH)
+          cp_async16(st + C::kC + lane * 16, p.k_pool + scales + lane * 16, 16);
+        else if (lane < 2 * SCH)
+          cp_async16(st + 2 * C::kC + C::kS + (lane - SCH) * 16, p.v_pool + scales + (lane - SCH) * 16, 16);
       }
-      constexpr int SCH = C::kS / 16;  // chunks of one scale block: 8 or 4
-      if (lane < SCH)
-        cp_async16(st + C::kC + lane * 16, p.k_pool + scales + lane * 16, 16);
-      else if (lane < 2 * SCH)
-        cp_async16(st + 2 * C::kC + C::kS + (lane - SCH) * 16, p.v_pool + scales + (lane - SCH) * 16, 16);
     }
     cp_async_commit();
-    st_in = st_in + 1 == C::kStages ? 0 : st_in + 1;
+    first_in ^= 2;
     if (left > 0) {
       --left;
       next_tile(prod);
-      find_page();
+      find_pages();
     }
   };
-  find_page();
-#pragma unroll 1
-  for (int i = 0; i < C::kStages - 1; ++i) issue();
+  find_pages();
+  issue();
+  issue();
 
   // ---- consumer side -----------------------------------------------------------
-  int st_out = 0;
+  int first_out = 0;
   long long at = g0;
   while (at < g1) {
     const int b = cons.b, h = cons.h, qt = cons.qt;
@@ -288,74 +298,153 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
       for (int i = 0; i < J; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
 
-#pragma unroll 1
-    for (int tile = tile0; tile < tile1; ++tile) {
-      issue();
-      cp_async_wait_group<C::kStages - 1>();
-      __syncwarp();
-      const uint8_t* st = ring + st_out * C::kStage;
-      const bool full = (have >> st_out) & 1;
-      st_out = st_out + 1 == C::kStages ? 0 : st_out + 1;
-      const int t0 = tile * kTile + warp * kStep;
-      if (full && t0 < maxvis) {
-        // scores
-        float s[NT][4];
+    // scores of one sub, scaled to base 2, masked; whether one passes its lazy maximum
+    auto scores = [&](const uint8_t* st, int t0, bool edge, float (&s)[NT][4]) -> bool {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
-        {
-          constexpr int W = D / 32;  // code words of a thread per key
-          uint32_t kw[2][W];
-          uint32_t ks[2][2];
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+      constexpr int W = D / 32;  // code words of a thread per key
+      uint32_t kw[2][W], ks[2][2];
+#pragma unroll
+      for (int rr = 0; rr < 2; ++rr) {
+        const uint8_t* row = st + (g + 8 * rr) * e2m1::code_bytes(D) + c * (D / 8);
+        if constexpr (D == 128) {
+          const uint4 w = *reinterpret_cast<const uint4*>(row);
+          kw[rr][0] = w.x; kw[rr][1] = w.y; kw[rr][2] = w.z; kw[rr][3] = w.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(row);
+          kw[rr][0] = w.x; kw[rr][1] = w.y;
+        }
+        const int t = (g >> 1) + 4 * (g & 1) + 8 * rr;
+        const uint8_t* sp = st + C::kC + t * e2m1::scale_bytes(D) + c * (D / 64);
+        if constexpr (D == 128) {
+          const uint32_t s2 = e2m1::scales_to_h2(*reinterpret_cast<const uint16_t*>(sp));
+          ks[rr][0] = __byte_perm(s2, 0, 0x1010);
+          ks[rr][1] = __byte_perm(s2, 0, 0x3232);
+        } else {
+          ks[rr][0] = ks[rr][1] = __byte_perm(e2m1::scales_to_h2(*sp), 0, 0x1010);
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        uint32_t x[2][4];
+        e2m1::codes_to_h2(kw[0][w], x[0]);
+        e2m1::codes_to_h2(kw[1][w], x[1]);
+#pragma unroll
+        for (int jj = 0; jj < 2; ++jj) {
+          const int j = 2 * w + jj;
+          uint32_t a[4];
 #pragma unroll
           for (int rr = 0; rr < 2; ++rr) {
-            const uint8_t* row = st + (g + 8 * rr) * e2m1::code_bytes(D) + c * (D / 8);
-            if constexpr (D == 128) {
-              const uint4 w = *reinterpret_cast<const uint4*>(row);
-              kw[rr][0] = w.x; kw[rr][1] = w.y; kw[rr][2] = w.z; kw[rr][3] = w.w;
-            } else {
-              const uint2 w = *reinterpret_cast<const uint2*>(row);
-              kw[rr][0] = w.x; kw[rr][1] = w.y;
-            }
-            const int t = (g >> 1) + 4 * (g & 1) + 8 * rr;
-            const uint8_t* sp = st + C::kC + t * e2m1::scale_bytes(D) + c * (D / 64);
-            if constexpr (D == 128) {
-              const uint32_t s2 = e2m1::scales_to_h2(*reinterpret_cast<const uint16_t*>(sp));
-              ks[rr][0] = __byte_perm(s2, 0, 0x1010);
-              ks[rr][1] = __byte_perm(s2, 0, 0x3232);
-            } else {
-              ks[rr][0] = ks[rr][1] = __byte_perm(e2m1::scales_to_h2(*sp), 0, 0x1010);
-            }
+            a[rr] = hmul2(x[rr][2 * jj], ks[rr][D == 128 ? w / 2 : 0]);
+            a[rr + 2] = hmul2(x[rr][2 * jj + 1], ks[rr][D == 128 ? w / 2 : 0]);
           }
 #pragma unroll
-          for (int w = 0; w < W; ++w) {
-            uint32_t x[2][4];
-            e2m1::codes_to_h2(kw[0][w], x[0]);
-            e2m1::codes_to_h2(kw[1][w], x[1]);
-#pragma unroll
-            for (int jj = 0; jj < 2; ++jj) {
-              const int j = 2 * w + jj;
-              uint32_t a[4];
-#pragma unroll
-              for (int rr = 0; rr < 2; ++rr) {
-                a[rr] = hmul2(x[rr][2 * jj], ks[rr][D == 128 ? w / 2 : 0]);
-                a[rr + 2] = hmul2(x[rr][2 * jj + 1], ks[rr][D == 128 ? w / 2 : 0]);
-              }
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[nt][2 * j], qf[nt][2 * j + 1]);
-            }
-          }
+          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[nt][2 * j], qf[nt][2 * j + 1]);
         }
-        const bool edge = t0 + kStep > minvis;
-        const int tok = t0 + (g >> 1) + 4 * (g & 1);
-        bool up = false;
+      }
+      const int tok = t0 + (g >> 1) + 4 * (g & 1);
+      bool up = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            s[nt][u] *= sl[nt][u & 1];
-            if (edge && tok + 8 * (u >> 1) >= vis[nt][u & 1]) s[nt][u] = -INFINITY;
-            up |= s[nt][u] > m[nt][u & 1] + kLazy;
+        for (int u = 0; u < 4; ++u) s[nt][u] *= sl[nt][u & 1];
+        if (edge) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            if (tok + 8 * (u >> 1) >= vis[nt][u & 1]) s[nt][u] = -INFINITY;
+        }
+        up |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + kLazy;
+        up |= fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + kLazy;
+      }
+      return up;
+    };
+
+    // weights of one sub, then o += V^T P^T
+    auto values = [&](const uint8_t* st, int t0, bool edge, const float (&s)[NT][4]) {
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
+        const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+        const float p0 = tc::ex2_approx(s[nt][0] - m0), p1 = tc::ex2_approx(s[nt][1] - m1);
+        const float p2 = tc::ex2_approx(s[nt][2] - m0), p3 = tc::ex2_approx(s[nt][3] - m1);
+        l[nt][0] += p0 + p2;
+        l[nt][1] += p1 + p3;
+        pb[nt][0] = transpose8x8(tc::pack2<__half>(p0, p1));
+        pb[nt][1] = transpose8x8(tc::pack2<__half>(p2, p3));
+      }
+      // keys c, c+4, c+8, c+12 of the sub, dims [g * D/8, (g + 1) * D/8)
+      constexpr int W = D / 64;
+      uint32_t vw[4][W], sb[4];
+      const uint8_t* sv = st + 2 * C::kC + C::kS + (D == 128 ? g : g >> 1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int t = c + 4 * k;
+        const uint8_t* row = st + C::kC + C::kS + t * e2m1::code_bytes(D);
+        if constexpr (D == 128) {
+          const uint2 w = *reinterpret_cast<const uint2*>(row + (((g >> 1) ^ (t & 2)) * 16 + (g & 1) * 8));
+          vw[k][0] = w.x; vw[k][1] = w.y;
+        } else {
+          vw[k][0] = *reinterpret_cast<const uint32_t*>(row + g * 4);
+        }
+        sb[k] = sv[t * e2m1::scale_bytes(D)];
+      }
+      if (edge) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)  // nobody sees this key, or its NaN is dealt out below
+          if (t0 + c + 4 * k >= maxvis || (sb[k] & 0x7f) == 0x7f) sb[k] = 0;
+      }
+      const uint32_t vs[2] = {e2m1::scales_to_h2(sb[0] | (sb[1] << 8)),
+                              e2m1::scales_to_h2(sb[2] | (sb[3] << 8))};
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        // bytes that pair one dim of two keys: even dims, odd dims
+        uint32_t ev[2][4], od[2][4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint32_t lo = vw[2 * k][w], hi = vw[2 * k + 1][w];
+          e2m1::codes_to_h2((lo & 0x0F0F0F0Fu) | ((hi << 4) & 0xF0F0F0F0u), ev[k]);
+          e2m1::codes_to_h2(((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), od[k]);
+        }
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          const uint32_t a[4] = {hmul2(ev[0][ii], vs[0]), hmul2(od[0][ii], vs[0]),
+                                 hmul2(ev[1][ii], vs[1]), hmul2(od[1][ii], vs[1])};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * w + ii], a, pb[nt][0], pb[nt][1]);
+        }
+      }
+      if (edge) {
+        // A NaN block of V reaches the rows that see its key, and no others (a
+        // zero weight times NaN would reach them all).
+#pragma unroll 1
+        for (int t = 0; t < kSub; ++t)
+          if ((sv[t * e2m1::scale_bytes(D)] & 0x7f) == 0x7f) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < J; ++i)
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                  if (t0 + t < vis[nt][u & 1]) o[nt][i][u] = __int_as_float(0x7fc00000);
           }
+      }
+    };
+
+#pragma unroll 1
+    for (int tile = tile0; tile < tile1; ++tile) {
+      cp_async_wait_group<1>();
+      __syncwarp();
+      const int t0 = tile * kTile + warp * kStep;
+#pragma unroll
+      for (int s0 = 0; s0 < 2; s0 += C::kBoth) {
+        float s[C::kBoth][NT][4];
+        bool up = false, on[C::kBoth];
+#pragma unroll
+        for (int k = 0; k < C::kBoth; ++k) {
+          const int slot = first_out + s0 + k, ts = t0 + (s0 + k) * kSub;
+          on[k] = ((have >> slot) & 1) && ts < maxvis;
+          if (on[k]) up |= scores(ring + slot * C::kSlot, ts, ts + kSub > minvis, s[k]);
         }
         if (__any_sync(~0u, up)) {
 #pragma unroll
@@ -363,7 +452,10 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
             float f[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              float x = fmaxf(s[nt][u], s[nt][u + 2]);
+              float x = -INFINITY;
+#pragma unroll
+              for (int k = 0; k < C::kBoth; ++k)
+                if (on[k]) x = fmaxf(x, fmaxf(s[k][nt][u], s[k][nt][u + 2]));
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
@@ -379,75 +471,15 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
             }
           }
         }
-        uint32_t pb[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-          const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-          const float p0 = tc::ex2_approx(s[nt][0] - m0), p1 = tc::ex2_approx(s[nt][1] - m1);
-          const float p2 = tc::ex2_approx(s[nt][2] - m0), p3 = tc::ex2_approx(s[nt][3] - m1);
-          l[nt][0] += p0 + p2;
-          l[nt][1] += p1 + p3;
-          pb[nt][0] = transpose8x8(tc::pack2<__half>(p0, p1));
-          pb[nt][1] = transpose8x8(tc::pack2<__half>(p2, p3));
-        }
-        // values: keys c, c+4, c+8, c+12 of the step, dims [g * D/8, (g + 1) * D/8)
-        {
-          constexpr int W = D / 64;
-          uint32_t vw[4][W], sb[4];
-          const uint8_t* sv = st + 2 * C::kC + C::kS + (D == 128 ? g : g >> 1);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int t = c + 4 * k;
-            const uint8_t* row = st + C::kC + C::kS + t * e2m1::code_bytes(D);
-            if constexpr (D == 128) {
-              const uint2 w = *reinterpret_cast<const uint2*>(row + (((g >> 1) ^ (t & 2)) * 16 + (g & 1) * 8));
-              vw[k][0] = w.x; vw[k][1] = w.y;
-            } else {
-              vw[k][0] = *reinterpret_cast<const uint32_t*>(row + g * 4);
-            }
-            sb[k] = sv[t * e2m1::scale_bytes(D)];
-            // nobody sees this key, or its NaN is dealt out below
-            if (edge && (t0 + t >= maxvis || (sb[k] & 0x7f) == 0x7f)) sb[k] = 0;
-          }
-          const uint32_t vs[2] = {e2m1::scales_to_h2(sb[0] | (sb[1] << 8)),
-                                  e2m1::scales_to_h2(sb[2] | (sb[3] << 8))};
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            // bytes that pair one dim of two keys: even dims, odd dims
-            uint32_t ev[2][4], od[2][4];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const uint32_t lo = vw[2 * k][w], hi = vw[2 * k + 1][w];
-              e2m1::codes_to_h2((lo & 0x0F0F0F0Fu) | ((hi << 4) & 0xF0F0F0F0u), ev[k]);
-              e2m1::codes_to_h2(((lo >> 4) & 0x0F0F0F0Fu) | (hi & 0xF0F0F0F0u), od[k]);
-            }
-#pragma unroll
-            for (int ii = 0; ii < 4; ++ii) {
-              const uint32_t a[4] = {hmul2(ev[0][ii], vs[0]), hmul2(od[0][ii], vs[0]),
-                                     hmul2(ev[1][ii], vs[1]), hmul2(od[1][ii], vs[1])};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * w + ii], a, pb[nt][0], pb[nt][1]);
-            }
-          }
-          if (edge) {
-            // A NaN block of V reaches the rows that see its key, and no others (a
-            // zero weight times NaN would reach them all).
-#pragma unroll 1
-            for (int t = 0; t < kStep; ++t)
-              if ((sv[t * e2m1::scale_bytes(D)] & 0x7f) == 0x7f) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                  for (int i = 0; i < J; ++i)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                      if (t0 + t < vis[nt][u & 1]) o[nt][i][u] = __int_as_float(0x7fc00000);
-              }
-          }
+        for (int k = 0; k < C::kBoth; ++k) {
+          const int slot = first_out + s0 + k, ts = t0 + (s0 + k) * kSub;
+          if (on[k]) values(ring + slot * C::kSlot, ts, ts + kSub > minvis, s[k]);
         }
       }
+      first_out ^= 2;
       __syncwarp();
+      issue();
     }
 
     // ---- the item's end: join the warps --------------------------------------
@@ -493,28 +525,31 @@ __global__ void __launch_bounds__(kThreads, NT <= 2 ? 2 : 1) attend_kernel(const
       __syncthreads();
       {
         constexpr int V = D / 32;
-        const int r = threadIdx.x >> 5, d0 = lane * V, pr = qt * R + nt * 8 + r;
-        float acc[V], top = -INFINITY, sum = 0.f;
+        const int d0 = lane * V;
+        for (int r = warp; r < 8; r += kWarps) {
+          const int pr = qt * R + nt * 8 + r;
+          float acc[V], top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+          for (int e = 0; e < V; ++e) acc[e] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * R + nt * 8 + r]);
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * R + nt * 8 + r]);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float mw = s_m[w * R + nt * 8 + r];
-          sum += s_l[w * R + nt * 8 + r] * (mw == top ? 1.0f : exp2f(mw - top));
+          for (int w = 0; w < kWarps; ++w) {
+            const float mw = s_m[w * R + nt * 8 + r];
+            sum += s_l[w * R + nt * 8 + r] * (mw == top ? 1.0f : exp2f(mw - top));
 #pragma unroll
-          for (int e = 0; e < V; ++e) acc[e] += merge[(w * 8 + r) * D + d0 + e];
-        }
-        if (starts && ends) {
-          if (pr <= last) store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, top, sum, lane == 0);
-        } else {
-          float* po = p.part_o + ((size_t)slot * R + nt * 8 + r) * D + d0;
+            for (int e = 0; e < V; ++e) acc[e] += merge[(w * 8 + r) * D + d0 + e];
+          }
+          if (starts && ends) {
+            if (pr <= last) store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, top, sum, lane == 0);
+          } else {
+            float* po = p.part_o + ((size_t)slot * R + nt * 8 + r) * D + d0;
 #pragma unroll
-          for (int e = 0; e < V; ++e) po[e] = acc[e];
-          if (lane == 0) {
-            p.part_ml[((size_t)slot * R + nt * 8 + r) * 2] = top;
-            p.part_ml[((size_t)slot * R + nt * 8 + r) * 2 + 1] = sum;
+            for (int e = 0; e < V; ++e) po[e] = acc[e];
+            if (lane == 0) {
+              p.part_ml[((size_t)slot * R + nt * 8 + r) * 2] = top;
+              p.part_ml[((size_t)slot * R + nt * 8 + r) * 2 + 1] = sum;
+            }
           }
         }
       }
@@ -573,7 +608,8 @@ dkv_status refuse(dkv_status s, const char* msg) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-constexpr int kMaxCtas = 304;  // two CTAs on each of 152 SMs
+constexpr int kSms = 152;
+constexpr int kMaxCtas = 4 * kSms;
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
@@ -582,10 +618,10 @@ size_t ws_desc() { return align256(2 * kMaxCtas * sizeof(AttendDesc)); }
 size_t ws_ml(int R) { return align256((size_t)2 * kMaxCtas * R * 2 * 4); }
 size_t ws_o(int R, int D) { return align256((size_t)2 * kMaxCtas * R * D * 4); }
 
-// Query rows per item: the smallest of 8, 16 and 32 that holds a sequence's rows.
+// Query rows per item: the smallest of 8, 16, 24 and 32 that holds a sequence's rows.
 int rows_per_item(int G, int max_rows) {
   const long long rows = (long long)G * max_rows;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
 }
 
 template <typename T, int D, int NT>
@@ -602,8 +638,8 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     if (dev < 64) attr_set[dev] = true;
   }
-  const int per_sm = NT <= 2 && 2 * (smem + 1024) <= 228 * 1024 ? 2 : 1;
-  const int grid = 152 * per_sm;
+  const int fit = 228 * 1024 / (smem + 1024);
+  const int grid = kSms * (fit < C::kPerSm ? fit : C::kPerSm);
   attend_kernel<T, D, NT><<<grid, kThreads, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -620,7 +656,10 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t launch_rows(const AttendParams& p, int R, cudaStream_t s) {
-  return R == 8 ? launch<T, D, 1>(p, s) : R == 16 ? launch<T, D, 2>(p, s) : launch<T, D, 4>(p, s);
+  return R == 8    ? launch<T, D, 1>(p, s)
+         : R == 16 ? launch<T, D, 2>(p, s)
+         : R == 24 ? launch<T, D, 3>(p, s)
+                   : launch<T, D, 4>(p, s);
 }
 
 }  // namespace
