@@ -48,19 +48,22 @@ constexpr int kSub = 16;                // keys of one MMA, one ring slot
 constexpr int kStep = 2 * kSub;         // keys of one warp step
 constexpr int kTile = kStep * kWarps;   // keys of one tile
 constexpr int kSlots = 4;               // ring slots per warp
-constexpr float kLazy = 8.0f;  // the running maximum moves only when passed by 2^8
+constexpr float kLazy = 8.0f;   // the running maximum moves only when passed by 2^8
+constexpr float kNone = -3e38f;  // the running maximum of a row that has seen no key
 
 template <int D, int NT>
 struct Cfg {
   static constexpr int R = 8 * NT;                   // query rows per item
   static constexpr int kC = kSub * e2m1::code_bytes(D);
   static constexpr int kS = kSub * e2m1::scale_bytes(D);
-  static constexpr int kSlot = 2 * (kC + kS);        // K codes | K scales | V codes | V scales
+  static constexpr int kSlot = 2 * (kC + kS);        // K codes | V codes | K scales | V scales
+  static constexpr int kOffScale = 2 * kC;
   static constexpr int kRing = kSlots * kSlot;       // per warp
   static constexpr int kMerge = kWarps * 8 * D * 4;  // one 8-row round of every warp's O
   static constexpr int kOffMerge = kWarps * kRing;
   static constexpr int kOffMl = kOffMerge + kMerge;          // [2][kWarps][R] floats
-  static constexpr int kOffBatch = kOffMl + 2 * kWarps * R * 4;
+  static constexpr int kOffBar = kOffMl + 2 * kWarps * R * 4;  // a full barrier per warp and step
+  static constexpr int kOffBatch = kOffBar + kWarps * 2 * 8;
   // resident CTAs per SM, by registers: o takes 4 NT D/16, q 2 NT D/16
   static constexpr int kPerSm = NT == 1 ? 4 : NT == 2 ? 3 : 2;
   static constexpr int kBoth = NT == 1 ? 2 : 1;  // subs whose scores are held at once
@@ -86,6 +89,15 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Copies `bytes` (a multiple of 16, both addresses on 16-byte boundaries) to shared memory.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+          smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
 // Where a CTA is on the line of tiles.
 struct Pos {
   int b, h, qt, tile;  // sequence, KV head, query tile, key tile
@@ -99,10 +111,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
+  // MMA row r of a sub is key (r >> 1) for even r, ((r >> 1) ^ 1) + 4 for odd r < 8, and 8 more in
+  // the upper half: two rows that one phase of a 16-byte load reads have different parity, and
+  // so have the keys of neighbouring lanes of V's loads, which keeps both off the same banks
+  // (V: two ways) with keys in their natural order.
+  const int key_g = g & 1 ? ((g >> 1) ^ 1) + 4 : g >> 1;
   uint8_t* ring = smem + warp * C::kRing;
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* s_m = reinterpret_cast<float*>(smem + C::kOffMl);
   float* s_l = s_m + kWarps * R;
+  __shared__ volatile int s_abort;
+  if (threadIdx.x == 0) s_abort = 0;
   long long* s_pre = reinterpret_cast<long long*>(smem + C::kOffBatch);  // [B + 1]
   int* s_kv = reinterpret_cast<int*>(s_pre + p.B + 1);                   // [B]
   int* s_row = s_kv + p.B;                                               // [B]
@@ -174,63 +193,61 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   }
 
   // ---- producer side: this warp's next step to fetch -------------------------
+  // Lanes 0-7 each own one run of bytes of a step: sub (lane >> 2), and K codes, V codes,
+  // K scales or V scales (lane & 3).  A run is one bulk copy; a sub without keys (past the
+  // length, or a page outside the pool) has none.
   Pos prod = cons;
   long long left = g1 - g0;  // steps not yet issued
-  int page[2] = {-1, -1};    // pool pages of prod's two subs (-1: nothing to fetch)
-  uint32_t have = 0;         // bit s: slot s holds keys
-  auto find_pages = [&]() {
-    page[0] = page[1] = -1;
-    if (left <= 0) return;
-    const int t0 = prod.tile * kTile + warp * kStep, kv = s_kv[prod.b];
-    const int* row = p.table + (size_t)prod.b * p.max_pages;
-    if (t0 < kv) page[0] = __ldg(row + (t0 >> p.page_shift));
-    if (t0 + kSub < kv) page[1] = __ldg(row + ((t0 + kSub) >> p.page_shift));
+  int page = -1;             // pool page of this lane's run (-1: nothing to fetch)
+  uint32_t have = 0;         // bit 2 * (step & 1) + sub: the sub holds keys
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + 2 * warp;
+  const bool runner = lane < 8;
+  const int sub_in = (lane >> 2) & 1;
+  const uint8_t* run_pool = (lane & 1) ? p.v_pool : p.k_pool;
+  const int run_bytes = (lane & 2) ? C::kS : C::kC;
+  const int run_row = (lane & 2) ? e2m1::scale_bytes(D) : e2m1::code_bytes(D);
+  const size_t run_off = (lane & 2) ? (size_t)e2m1::code_bytes(D) << p.page_shift : 0;
+  uint8_t* run_dst = ring + sub_in * C::kSlot + ((lane & 2) ? C::kOffScale : 0) + (lane & 1) * run_bytes;
+  auto find_page = [&]() {
+    page = -1;
+    if (left <= 0 || !runner) return;
+    const int t = prod.tile * kTile + warp * kStep + sub_in * kSub;
+    if (t < s_kv[prod.b]) page = __ldg(p.table + (size_t)prod.b * p.max_pages + (t >> p.page_shift));
   };
-  int first_in = 0;  // slot of the next step's first sub: 0 or 2
+  int in = 0;  // the step to issue, modulo 2
   auto issue = [&]() {
-#pragma unroll
-    for (int sub = 0; sub < 2; ++sub) {
-      const int slot = first_in + sub;
-      const bool ok = page[sub] >= 0 && page[sub] < p.num_pages;
-      have = ok ? have | (1u << slot) : have & ~(1u << slot);
-      if (ok) {
-        const int in_page = (prod.tile * kTile + warp * kStep + sub * kSub) & ((1 << p.page_shift) - 1);
-        const size_t base = ((size_t)page[sub] * p.Hkv + prod.h) * p.page_bytes;
-        const size_t codes = base + (size_t)in_page * e2m1::code_bytes(D);
-        const size_t scales = base + ((size_t)e2m1::code_bytes(D) << p.page_shift) +
-                              (size_t)in_page * e2m1::scale_bytes(D);
-        uint8_t* st = ring + slot * C::kSlot;
-        constexpr int CPR = e2m1::code_bytes(D) / 16;  // 16-byte chunks per row
-#pragma unroll
-        for (int i = 0; i < C::kC / 512; ++i) {
-          const int ch = lane + 32 * i, t = ch / CPR, part = ch % CPR;
-          // K: row of key t in MMA order; V: in key order, chunks of keys 2, 3 mod 4 swapped in pairs
-          const int r = ((t & 3) << 1) | ((t >> 2) & 1) | (t & 8);
-          cp_async16(st + r * e2m1::code_bytes(D) + part * 16, p.k_pool + codes + ch * 16, 16);
-          const int vp = D == 128 ? part ^ (t & 2) : part;
-          cp_async16(st + C::kC + C::kS + t * e2m1::code_bytes(D) + vp * 16, p.v_pool + codes + ch * 16, 16);
-        }
-        constexpr int SCH = C::kS / 16;  // chunks of one scale block: 8 or 4
-        if (lane < SCH)
-          cp_async16(st + C::kC + lane * 16, p.k_pool + scales + lane * 16, 16);
-        else if (lane < 2 * SCH)
-          cp_async16(st + 2 * C::kC + C::kS + (lane - SCH) * 16, p.v_pool + scales + (lane - SCH) * 16, 16);
-      }
+    const bool ok = page >= 0 && page < p.num_pages;
+    const uint32_t runs = __ballot_sync(~0u, ok);
+    have = (have & ~(3u << (2 * in))) | ((runs & 1) << (2 * in)) | (((runs >> 4) & 1) << (2 * in + 1));
+    if (lane == 0)
+      tc::mbar_expect_tx(bars + in, (uint32_t)__popc(runs & 0x11) * (uint32_t)C::kSlot);
+    __syncwarp();
+    if (ok) {
+      const int in_page = (prod.tile * kTile + warp * kStep + sub_in * kSub) & ((1 << p.page_shift) - 1);
+      bulk_load(run_dst + in * (2 * C::kSlot),
+                run_pool + ((size_t)page * p.Hkv + prod.h) * p.page_bytes + run_off + (size_t)in_page * run_row,
+                run_bytes, bars + in);
     }
-    cp_async_commit();
-    first_in ^= 2;
+    in ^= 1;
     if (left > 0) {
       --left;
       next_tile(prod);
-      find_pages();
+      find_page();
     }
   };
-  find_pages();
+  if (lane == 0) {
+    mbar_init(bars, 1);
+    mbar_init(bars + 1, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  __syncwarp();
+  find_page();
   issue();
   issue();
+  griddep_launch_dependents();
 
   // ---- consumer side -----------------------------------------------------------
-  int first_out = 0;
+  int first_out = 0, parity = 0;  // slot of the step's first sub; phase of its barrier
   long long at = g0;
   while (at < g1) {
     const int b = cons.b, h = cons.h, qt = cons.qt;
@@ -281,24 +298,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
           qf[nt][i] = tc::pack2<__half>(f.x * up, f.y * up);
         }
       }
+      if (p.scale_log2 < 0.f) {  // the scale's sign goes to the queries
+#pragma unroll
+        for (int i = 0; i < 2 * J; ++i) qf[nt][i] ^= 0x80008000u;
+      }
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        sl[nt][u] = p.scale_log2 * __shfl_sync(~0u, unscale, (2 * c + u) * 4);
+        // positive and finite, so that a masked -infinity stays one
+        sl[nt][u] = fminf(fmaxf(fabsf(p.scale_log2) * __shfl_sync(~0u, unscale, (2 * c + u) * 4), 1e-37f), FLT_MAX);
         const int pc = qt * R + nt * 8 + 2 * c + u;
         vis[nt][u] = pc <= last ? max(0, kv - n + pc / G + 1) : 0;
       }
     }
 
-    float m[NT][2], l[NT][2], o[NT][J][4];
+    // running maximum (base 2, scaled), the raw score that moves it, sum, output
+    float m[NT][2], thr[NT][2], l[NT][2], o[NT][J][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = -INFINITY;
+      m[nt][0] = m[nt][1] = kNone;
+      thr[nt][0] = thr[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < J; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
 
-    // scores of one sub, scaled to base 2, masked; whether one passes its lazy maximum
+    // raw scores of one sub, masked; whether one passes its lazy maximum
     auto scores = [&](const uint8_t* st, int t0, bool edge, float (&s)[NT][4]) -> bool {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
@@ -306,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       uint32_t kw[2][W], ks[2][2];
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
-        const uint8_t* row = st + (g + 8 * rr) * e2m1::code_bytes(D) + c * (D / 8);
+        const uint8_t* row = st + (key_g + 8 * rr) * e2m1::code_bytes(D) + c * (D / 8);
         if constexpr (D == 128) {
           const uint4 w = *reinterpret_cast<const uint4*>(row);
           kw[rr][0] = w.x; kw[rr][1] = w.y; kw[rr][2] = w.z; kw[rr][3] = w.w;
@@ -314,8 +338,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
           const uint2 w = *reinterpret_cast<const uint2*>(row);
           kw[rr][0] = w.x; kw[rr][1] = w.y;
         }
-        const int t = (g >> 1) + 4 * (g & 1) + 8 * rr;
-        const uint8_t* sp = st + C::kC + t * e2m1::scale_bytes(D) + c * (D / 64);
+        const uint8_t* sp = st + C::kOffScale + (key_g + 8 * rr) * e2m1::scale_bytes(D) + c * (D / 64);
         if constexpr (D == 128) {
           const uint32_t s2 = e2m1::scales_to_h2(*reinterpret_cast<const uint16_t*>(sp));
           ks[rr][0] = __byte_perm(s2, 0, 0x1010);
@@ -342,19 +365,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
           for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[nt][2 * j], qf[nt][2 * j + 1]);
         }
       }
-      const int tok = t0 + (g >> 1) + 4 * (g & 1);
+      const int tok = t0 + key_g;
       bool up = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) s[nt][u] *= sl[nt][u & 1];
         if (edge) {
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             if (tok + 8 * (u >> 1) >= vis[nt][u & 1]) s[nt][u] = -INFINITY;
         }
-        up |= fmaxf(s[nt][0], s[nt][2]) > m[nt][0] + kLazy;
-        up |= fmaxf(s[nt][1], s[nt][3]) > m[nt][1] + kLazy;
+        up |= fmaxf(s[nt][0], s[nt][2]) > thr[nt][0];
+        up |= fmaxf(s[nt][1], s[nt][3]) > thr[nt][1];
       }
       return up;
     };
@@ -364,35 +385,35 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-        const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
-        const float p0 = tc::ex2_approx(s[nt][0] - m0), p1 = tc::ex2_approx(s[nt][1] - m1);
-        const float p2 = tc::ex2_approx(s[nt][2] - m0), p3 = tc::ex2_approx(s[nt][3] - m1);
+        const float p0 = tc::ex2_approx(fmaf(s[nt][0], sl[nt][0], -m[nt][0]));
+        const float p1 = tc::ex2_approx(fmaf(s[nt][1], sl[nt][1], -m[nt][1]));
+        const float p2 = tc::ex2_approx(fmaf(s[nt][2], sl[nt][0], -m[nt][0]));
+        const float p3 = tc::ex2_approx(fmaf(s[nt][3], sl[nt][1], -m[nt][1]));
         l[nt][0] += p0 + p2;
         l[nt][1] += p1 + p3;
         pb[nt][0] = transpose8x8(tc::pack2<__half>(p0, p1));
         pb[nt][1] = transpose8x8(tc::pack2<__half>(p2, p3));
       }
-      // keys c, c+4, c+8, c+12 of the sub, dims [g * D/8, (g + 1) * D/8)
+      // keys c, (c^1)+4, c+8, (c^1)+12 of the sub, dims [g * D/8, (g + 1) * D/8)
       constexpr int W = D / 64;
       uint32_t vw[4][W], sb[4];
-      const uint8_t* sv = st + 2 * C::kC + C::kS + (D == 128 ? g : g >> 1);
+      const uint8_t* sv = st + C::kOffScale + C::kS + (D == 128 ? g : g >> 1);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int t = c + 4 * k;
-        const uint8_t* row = st + C::kC + C::kS + t * e2m1::code_bytes(D);
+        const int t = (k & 1 ? c ^ 1 : c) + 4 * k;
+        const uint8_t* row = st + C::kC + t * e2m1::code_bytes(D) + g * (D / 16);
         if constexpr (D == 128) {
-          const uint2 w = *reinterpret_cast<const uint2*>(row + (((g >> 1) ^ (t & 2)) * 16 + (g & 1) * 8));
+          const uint2 w = *reinterpret_cast<const uint2*>(row);
           vw[k][0] = w.x; vw[k][1] = w.y;
         } else {
-          vw[k][0] = *reinterpret_cast<const uint32_t*>(row + g * 4);
+          vw[k][0] = *reinterpret_cast<const uint32_t*>(row);
         }
         sb[k] = sv[t * e2m1::scale_bytes(D)];
       }
       if (edge) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // nobody sees this key, or its NaN is dealt out below
-          if (t0 + c + 4 * k >= maxvis || (sb[k] & 0x7f) == 0x7f) sb[k] = 0;
+          if (t0 + (k & 1 ? c ^ 1 : c) + 4 * k >= maxvis || (sb[k] & 0x7f) == 0x7f) sb[k] = 0;
       }
       const uint32_t vs[2] = {e2m1::scales_to_h2(sb[0] | (sb[1] << 8)),
                               e2m1::scales_to_h2(sb[2] | (sb[3] << 8))};
@@ -433,7 +454,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
 
 #pragma unroll 1
     for (int tile = tile0; tile < tile1; ++tile) {
-      cp_async_wait_group<1>();
+      if (!mbar_wait_bounded(bars + (first_out >> 1), parity, &s_abort)) {
+        s_abort = 1;  // the copies did not land: give up, fetch no more, the rows become NaN
+        left = 0;
+        page = -1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = __int_as_float(0x7fc00000);
+      }
       __syncwarp();
       const int t0 = tile * kTile + warp * kStep;
 #pragma unroll
@@ -459,9 +486,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
               x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-              x = fmaxf(x, m[nt][u]);
+              x = fmaxf(x * sl[nt][u], m[nt][u]);
               f[u] = x == m[nt][u] ? 1.0f : exp2f(m[nt][u] - x);
               m[nt][u] = x;
+              if (x != kNone) thr[nt][u] = __fdividef(x + kLazy, sl[nt][u]);
               l[nt][u] *= f[u];
             }
 #pragma unroll
@@ -478,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
         }
       }
       first_out ^= 2;
+      parity ^= first_out == 0;
       __syncwarp();
       issue();
     }
@@ -564,7 +593,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     cons.tile = tile1 - 1;
     next_tile(cons);
   }
-  cp_async_wait_all();
+  // the steps issued beyond the range carry no bytes: nothing is in flight, unless a wait gave up
+  if (s_abort) {
+    mbar_wait_drain(bars, 0);
+    mbar_wait_drain(bars, 1);
+    mbar_wait_drain(bars + 1, 0);
+    mbar_wait_drain(bars + 1, 1);
+  }
 }
 
 // Joins the partials of each cut item: block c takes the item whose first piece
