@@ -31,6 +31,8 @@
 #include <math.h>
 #include <stdio.h>
 
+#include <type_traits>
+
 #include "attend_e2m1.cuh"
 #include "tc_common.cuh"
 
@@ -66,12 +68,12 @@ struct Cfg {
   static constexpr int kOffBatch = kOffBar + kWarps * 2 * 8;
   // resident CTAs per SM, by registers: o takes 4 NT D/16, q 2 NT D/16
   static constexpr int kPerSm = NT == 1 ? 4 : NT == 2 ? 3 : 2;
-  static constexpr int kBoth = NT == 1 ? 2 : 1;  // subs whose scores are held at once
+  static constexpr int kBoth = NT == 1 ? 2 : 1;  // subs in flight at once
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -80,7 +82,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
@@ -97,6 +99,10 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes,
       "l"(src), "r"(bytes), "r"(smem_u32(bar))
       : "memory");
 }
+
+// Whether a sub's keys are all seen by every row of the item.
+using Inner = std::false_type;
+using Edge = std::true_type;
 
 // Where a CTA is on the line of tiles.
 struct Pos {
@@ -323,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     }
 
     // raw scores of one sub, masked; whether one passes its lazy maximum
-    auto scores = [&](const uint8_t* st, int t0, bool edge, float (&s)[NT][4]) -> bool {
+    auto scores = [&](auto edge, const uint8_t* st, int t0, float (&s)[NT][4]) -> bool {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
       constexpr int W = D / 32;  // code words of a thread per key
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       bool up = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        if (edge) {
+        if constexpr (edge) {
 #pragma unroll
           for (int u = 0; u < 4; ++u)
             if (tok + 8 * (u >> 1) >= vis[nt][u & 1]) s[nt][u] = -INFINITY;
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     };
 
     // weights of one sub, then o += V^T P^T
-    auto values = [&](const uint8_t* st, int t0, bool edge, const float (&s)[NT][4]) {
+    auto values = [&](auto edge, const uint8_t* st, int t0, const float (&s)[NT][4]) {
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
         }
         sb[k] = sv[t * e2m1::scale_bytes(D)];
       }
-      if (edge) {
+      if constexpr (edge) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)  // nobody sees this key, or its NaN is dealt out below
           if (t0 + (k & 1 ? c ^ 1 : c) + 4 * k >= maxvis || (sb[k] & 0x7f) == 0x7f) sb[k] = 0;
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
           for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][4 * w + ii], a, pb[nt][0], pb[nt][1]);
         }
       }
-      if (edge) {
+      if constexpr (edge) {
         // A NaN block of V reaches the rows that see its key, and no others (a
         // zero weight times NaN would reach them all).
 #pragma unroll 1
@@ -452,6 +458,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       }
     };
 
+    // takes these scores into the running maxima and rescales what was summed under the old ones
+    auto raise = [&](const float (&s)[NT][4]) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float f[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          float x = fmaxf(s[nt][u], s[nt][u + 2]);
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+          x = fmaxf(x * sl[nt][u], m[nt][u]);
+          f[u] = x == m[nt][u] ? 1.0f : exp2f(m[nt][u] - x);
+          m[nt][u] = x;
+          if (x != kNone) thr[nt][u] = __fdividef(x + kLazy, sl[nt][u]);
+          l[nt][u] *= f[u];
+        }
+#pragma unroll
+        for (int i = 0; i < J; ++i) {
+          o[nt][i][0] *= f[0]; o[nt][i][1] *= f[1];
+          o[nt][i][2] *= f[0]; o[nt][i][3] *= f[1];
+        }
+      }
+    };
+
 #pragma unroll 1
     for (int tile = tile0; tile < tile1; ++tile) {
       if (!mbar_wait_bounded(bars + (first_out >> 1), parity, &s_abort)) {
@@ -463,46 +494,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       }
       __syncwarp();
       const int t0 = tile * kTile + warp * kStep;
+      const uint8_t* st = ring + first_out * C::kSlot;
+      const uint32_t on = (have >> first_out) & 3;
+      if (on == 3 && t0 + kStep <= minvis) {  // every row sees every key
+        float s[2][NT][4];
+        if constexpr (C::kBoth == 2) {
+          const bool a = scores(Inner(), st, t0, s[0]);
+          const bool b = scores(Inner(), st + C::kSlot, t0 + kSub, s[1]);
+          if (__any_sync(~0u, a | b)) {
+            raise(s[0]);
+            raise(s[1]);
+          }
+          values(Inner(), st, t0, s[0]);
+          values(Inner(), st + C::kSlot, t0 + kSub, s[1]);
+        } else {
 #pragma unroll
-      for (int s0 = 0; s0 < 2; s0 += C::kBoth) {
-        float s[C::kBoth][NT][4];
-        bool up = false, on[C::kBoth];
-#pragma unroll
-        for (int k = 0; k < C::kBoth; ++k) {
-          const int slot = first_out + s0 + k, ts = t0 + (s0 + k) * kSub;
-          on[k] = ((have >> slot) & 1) && ts < maxvis;
-          if (on[k]) up |= scores(ring + slot * C::kSlot, ts, ts + kSub > minvis, s[k]);
-        }
-        if (__any_sync(~0u, up)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float f[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float x = -INFINITY;
-#pragma unroll
-              for (int k = 0; k < C::kBoth; ++k)
-                if (on[k]) x = fmaxf(x, fmaxf(s[k][nt][u], s[k][nt][u + 2]));
-              x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-              x = fmaxf(x * sl[nt][u], m[nt][u]);
-              f[u] = x == m[nt][u] ? 1.0f : exp2f(m[nt][u] - x);
-              m[nt][u] = x;
-              if (x != kNone) thr[nt][u] = __fdividef(x + kLazy, sl[nt][u]);
-              l[nt][u] *= f[u];
-            }
-#pragma unroll
-            for (int i = 0; i < J; ++i) {
-              o[nt][i][0] *= f[0]; o[nt][i][1] *= f[1];
-              o[nt][i][2] *= f[0]; o[nt][i][3] *= f[1];
-            }
+          for (int k = 0; k < 2; ++k) {
+            if (__any_sync(~0u, scores(Inner(), st + k * C::kSlot, t0 + k * kSub, s[0]))) raise(s[0]);
+            values(Inner(), st + k * C::kSlot, t0 + k * kSub, s[0]);
           }
         }
-#pragma unroll
-        for (int k = 0; k < C::kBoth; ++k) {
-          const int slot = first_out + s0 + k, ts = t0 + (s0 + k) * kSub;
-          if (on[k]) values(ring + slot * C::kSlot, ts, ts + kSub > minvis, s[k]);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          const int ts = t0 + k * kSub;
+          if (!((on >> k) & 1) || ts >= maxvis) continue;
+          float s[NT][4];
+          if (__any_sync(~0u, scores(Edge(), st + k * C::kSlot, ts, s))) raise(s);
+          values(Edge(), st + k * C::kSlot, ts, s);
         }
       }
       first_out ^= 2;
