@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   // with fewer tiles than CTAs the first `total` CTAs take one each, so that an
   // item's pieces always lie in consecutive CTAs
   const long long ctas = min(total, (long long)gridDim.x);
-  if (threadIdx.x < 2) p.desc[2 * blockIdx.x + threadIdx.x].valid = 0;
+  if (threadIdx.x == 0) p.desc[blockIdx.x].pieces = 0;
   if ((long long)blockIdx.x >= ctas) return;
   const long long g0 = total * blockIdx.x / ctas, g1 = total * (blockIdx.x + 1) / ctas;
 
@@ -602,10 +602,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
         }
       }
     }
-    if (!(starts && ends) && threadIdx.x == 0) {
+    if (starts && !ends && threadIdx.x == 0) {
       AttendDesc d;
-      d.valid = 1; d.ends = ends; d.row0 = row0; d.first = qt * R; d.last = last; d.head0 = h * G;
-      p.desc[slot] = d;
+      const long long end = at + cons.tiles - 1;  // the item's last tile, and the CTA that holds it
+      d.pieces = (int)(((end + 1) * ctas - 1) / total) - (int)blockIdx.x + 1;
+      d.row0 = row0; d.first = qt * R; d.last = last; d.head0 = h * G;
+      p.desc[blockIdx.x] = d;
     }
     __syncthreads();  // s_m, s_l and merge are free for the next item
     at += tile1 - tile0;
@@ -622,37 +624,56 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
 }
 
 // Joins the partials of each cut item: block c takes the item whose first piece
-// CTA c left unfinished, whose further pieces CTAs c+1, c+2, ... hold.
+// CTA c left unfinished, whose further pieces CTAs c+1, c+2, ... hold.  A warp takes
+// a row: its lanes read the pieces' maxima and sums 32 at a time, then the
+// outputs are read with nothing to wait for between pieces.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, int R, int ctas) {
+__global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, int R) {
   griddep_wait();
-  const AttendDesc d = p.desc[2 * blockIdx.x + 1];
-  if (!d.valid || d.ends) return;
+  const AttendDesc d = p.desc[blockIdx.x];
+  if (d.pieces < 2) return;
   constexpr int V = D / 32;
   const int lane = threadIdx.x & 31;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < R; r += gridDim.y * 8) {
-    const int pr = d.first + r;
-    if (pr > d.last) continue;
-    float top = -INFINITY, sum = 0.f, acc[V];
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int pr = d.first + r;
+  if (r >= R || pr > d.last) return;
+  // piece i lies in slot 2 (c + i), but the first in slot 2 c + 1
+  auto at = [&](int i) { return (size_t)(2 * (blockIdx.x + i) + (i == 0)) * R + r; };
+  float top = -INFINITY;
+  for (int i = lane; i < d.pieces; i += 32) top = fmaxf(top, p.part_ml[2 * at(i)]);
 #pragma unroll
-    for (int e = 0; e < V; ++e) acc[e] = 0.f;
-    int slot = 2 * blockIdx.x + 1;
-    bool more = true;
-    while (more) {
-      const size_t at = (size_t)slot * R + r;
-      const float m = p.part_ml[2 * at], l = p.part_ml[2 * at + 1];
-      const float nt = fmaxf(top, m);
-      const float fa = top == nt ? 1.0f : exp2f(top - nt), fb = m == nt ? 1.0f : exp2f(m - nt);
-      sum = sum * fa + l * fb;
+  for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+  float sum = 0.f, acc[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = acc[e] * fa + p.part_o[at * D + lane * V + e] * fb;
-      top = nt;
-      more = !p.desc[slot].ends;
-      slot = (slot | 1) + 1;
-      if (slot >= 2 * ctas) break;
+  for (int e = 0; e < V; ++e) acc[e] = 0.f;
+  for (int base = 0; base < d.pieces; base += 32) {
+    const int n = min(32, d.pieces - base);
+    float f = 0.f, l = 0.f;
+    if (lane < n) {
+      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at(base + lane));
+      f = ml.x == top ? 1.0f : exp2f(ml.x - top);
+      l = ml.y * f;
     }
-    store_row<T, V>(p, d.row0 + pr / p.G, d.head0 + pr % p.G, D, lane * V, acc, top, sum, lane == 0);
+#pragma unroll
+    for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(~0u, l, w);
+    sum += l;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+      const float fi = __shfl_sync(~0u, f, i);
+      const float* o = p.part_o + at(base + i) * D + lane * V;
+      float v[V];
+      if constexpr (V == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(o);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(o);
+        v[0] = x.x; v[1] = x.y;
+      }
+#pragma unroll
+      for (int e = 0; e < V; ++e) acc[e] = fmaf(v[e], fi, acc[e]);
+    }
   }
+  store_row<T, V>(p, d.row0 + pr / p.G, d.head0 + pr % p.G, D, lane * V, acc, top, sum, lane == 0);
 }
 
 dkv_status refuse(dkv_status s, const char* msg) {
@@ -668,7 +689,7 @@ constexpr int kMaxCtas = 4 * kSms;
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workspace: descriptors | partial (max, sum) | partial o, two slots per CTA.
-size_t ws_desc() { return align256(2 * kMaxCtas * sizeof(AttendDesc)); }
+size_t ws_desc() { return align256(kMaxCtas * sizeof(AttendDesc)); }
 size_t ws_ml(int R) { return align256((size_t)2 * kMaxCtas * R * 2 * 4); }
 size_t ws_o(int R, int D) { return align256((size_t)2 * kMaxCtas * R * D * 4); }
 
@@ -705,7 +726,7 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p, C::R, grid);
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p, C::R);
 }
 
 template <typename T, int D>

@@ -7,13 +7,13 @@
 
 namespace dkv {
 
-// A piece of an item that its CTA could not finish or did not start.
+// The item that a CTA began and left unfinished.
 struct AttendDesc {
-  int valid, ends;      // ends: the item's last piece
+  int pieces;           // how many CTAs hold it, this one first; 0: there is none
   int row0;             // first query row of the sequence
   int first, last;      // packed rows (token-major over the group's heads) of the item
   int head0;            // first query head of the group
-  int pad[2];
+  int pad[3];
 };
 
 struct AttendParams {
