@@ -100,11 +100,46 @@ def test_attention_oracle_closed_forms():
 P16 = 1 << 20  # a 16-byte aligned address that no refused call touches
 
 
+class AppendArgs(ctypes.Structure):
+    """dkv_append_t of include/dkv.h, field by field."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v")]
+                + [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride")]
+                + [(n, ctypes.c_void_p) for n in (
+                    "q_gamma", "k_gamma", "cos_sin", "positions", "slots", "k_pool", "v_pool",
+                    "q_out", "k_out", "v_out")]
+                + [(n, ctypes.c_int) for n in (
+                    "rows", "n_q_heads", "n_kv_heads", "head_dim", "dtype", "rotary_dim",
+                    "max_positions", "interleaved", "page_tokens", "num_pages")]
+                + [(n, ctypes.c_float) for n in ("eps", "k_scale", "v_scale")])
+
+
+class AttendArgs(ctypes.Structure):
+    """dkv_attend_t."""
+    _fields_ = ([("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong)]
+                + [(n, ctypes.c_void_p) for n in (
+                    "k_pool", "v_pool", "page_table", "kv_len", "row_start", "out", "lse",
+                    "workspace")]
+                + [("workspace_bytes", ctypes.c_size_t)]
+                + [(n, ctypes.c_int) for n in (
+                    "batch", "rows", "max_rows", "n_q_heads", "n_kv_heads", "head_dim", "dtype",
+                    "page_tokens", "num_pages", "max_pages")]
+                + [(n, ctypes.c_float) for n in ("scale", "v_scale")])
+
+
+def test_packed_arguments_match_the_structures():
+    # the binding packs every field in order; numbers of their own find a field out of place
+    for packer, cls in ((dkv._APPEND, AppendArgs), (dkv._ATTEND, AttendArgs)):
+        names = [n for n, _ in cls._fields_]
+        raw = packer.pack(*range(1, len(names) + 1))
+        a = cls.from_buffer_copy(raw + bytes(ctypes.sizeof(cls) - len(raw)))
+        assert [getattr(a, n) for n in names] == list(range(1, len(names) + 1))
+
+
 def append_args(**over):
-    a = dkv._Append(q=P16, k=P16, v=P16, q_stride=6144, k_stride=6144, v_stride=6144, positions=P16,
-                    cos_sin=P16, slots=P16, k_pool=P16, v_pool=P16, q_out=P16, rows=4, n_q_heads=32,
-                    n_kv_heads=8, head_dim=128, dtype=0, rotary_dim=128, max_positions=64,
-                    page_tokens=16, num_pages=4, eps=1e-6, k_scale=1.0, v_scale=1.0)
+    a = AppendArgs(q=P16, k=P16, v=P16, q_stride=6144, k_stride=6144, v_stride=6144, positions=P16,
+                   cos_sin=P16, slots=P16, k_pool=P16, v_pool=P16, q_out=P16, rows=4, n_q_heads=32,
+                   n_kv_heads=8, head_dim=128, dtype=0, rotary_dim=128, max_positions=64,
+                   page_tokens=16, num_pages=4, eps=1e-6, k_scale=1.0, v_scale=1.0)
     for k, v in over.items():
         setattr(a, k, v)
     return a
@@ -131,10 +166,10 @@ def test_append_unsupported_head_dim(L):
 
 
 def attend_args(**over):
-    a = dkv._Attend(q=P16, q_stride=4096, k_pool=P16, v_pool=P16, page_table=P16, kv_len=P16,
-                    row_start=P16, out=P16, workspace=P16, workspace_bytes=1 << 30, batch=4, rows=8,
-                    max_rows=2, n_q_heads=32, n_kv_heads=8, head_dim=128, dtype=0, page_tokens=16,
-                    num_pages=64, max_pages=16, scale=0.1, v_scale=1.0)
+    a = AttendArgs(q=P16, q_stride=4096, k_pool=P16, v_pool=P16, page_table=P16, kv_len=P16,
+                   row_start=P16, out=P16, workspace=P16, workspace_bytes=1 << 30, batch=4, rows=8,
+                   max_rows=2, n_q_heads=32, n_kv_heads=8, head_dim=128, dtype=0, page_tokens=16,
+                   num_pages=64, max_pages=16, scale=0.1, v_scale=1.0)
     for k, v in over.items():
         setattr(a, k, v)
     return a

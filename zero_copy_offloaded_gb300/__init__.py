@@ -12,7 +12,9 @@ PyTorch is used only as plumbing for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import numpy as np
 
@@ -73,30 +75,9 @@ class _CacheDesc(ctypes.Structure):
                 ("max_pages_per_seq", ctypes.c_int)]
 
 
-class _Append(ctypes.Structure):
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v")]
-                + [(n, ctypes.c_longlong) for n in ("q_stride", "k_stride", "v_stride")]
-                + [(n, ctypes.c_void_p) for n in (
-                    "q_gamma", "k_gamma", "cos_sin", "positions", "slots", "k_pool", "v_pool",
-                    "q_out", "k_out", "v_out")]
-                + [(n, ctypes.c_int) for n in (
-                    "rows", "n_q_heads", "n_kv_heads", "head_dim", "dtype", "rotary_dim",
-                    "max_positions", "interleaved", "page_tokens", "num_pages")]
-                + [(n, ctypes.c_float) for n in ("eps", "k_scale", "v_scale")])
-
-
-class _Attend(ctypes.Structure):
-    _fields_ = ([("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong)]
-                + [(n, ctypes.c_void_p) for n in (
-                    "k_pool", "v_pool", "page_table", "kv_len", "row_start", "out", "lse",
-                    "workspace")]
-                + [("workspace_bytes", ctypes.c_size_t)]
-                + [(n, ctypes.c_int) for n in (
-                    "batch", "rows", "max_rows", "n_q_heads", "n_kv_heads", "head_dim", "dtype",
-                    "page_tokens", "num_pages", "max_pages")]
-                + [(n, ctypes.c_float) for n in ("scale", "v_scale")])
-
-
+# The argument structures of include/dkv.h, packed in one call (native alignment)
+_APPEND = struct.Struct("@3P3q10P10i3f")
+_ATTEND = struct.Struct("@PqPPPPPPPPN10i2f")
 KV_FORMATS = {"native": 0, "e4m3": 1, "e2m1": 2}
 MAX_STEP_BATCH = 1024
 
@@ -153,8 +134,8 @@ def lib(build_if_missing: bool = False):
         "dkv_decode_noalloc_status": [P],
         "dkv_decode_noalloc_debug_withhold": [I],
         "dkv_step_plan": [P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P],
-        "dkv_qkv_append": [ctypes.POINTER(_Append), P],
-        "dkv_paged_attend": [ctypes.POINTER(_Attend), P],
+        "dkv_qkv_append": [P, P],
+        "dkv_paged_attend": [P, P],
         "dkv_project": [P, P, P, I, I, I, I, P],
         "dkv_cache_debug_withhold": [P, I],
     }
@@ -432,50 +413,59 @@ def dkv_decode_noalloc_debug_withhold(enable=True):
 
 # ---- the device-side step over a 4-bit paged cache -----------------------------------
 
-def _arg(t, what, dtype, device, shape=None, strided=False):
-    """Device pointer of a CUDA tensor of this dtype, device and shape; None stays None."""
-    if t is None:
-        return None
+def _bad(t, what, dtype, index, shape):
     if t.dtype != dtype:
         raise ValueError(f"{what} is {t.dtype}, not {dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, not on {device}")
-    if shape is not None and tuple(t.shape) != shape:
+    if t.get_device() != index:
+        raise ValueError(f"{what} is on {t.device}, not with the others")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, not {shape}")
-    if not strided and not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous")
+    raise ValueError(f"{what} must be contiguous")
+
+
+def _arg(t, what, dtype, index, shape=None):
+    """Address of a contiguous tensor of this dtype, device index and shape; 0 for None."""
+    if t is None:
+        return 0
+    if (t.dtype != dtype or t.get_device() != index or (shape is not None and t.shape != shape)
+            or not t.is_contiguous()):
+        _bad(t, what, dtype, index, shape)
     return t.data_ptr()
 
 
-def _rows(t, what, dtype, device, heads=None, D=None):
-    """Pointer and token stride of [rows, heads, D] whose heads are contiguous in each row."""
-    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (D is not None and t.shape[2] != D):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}: [rows, {heads or 'heads'}, {D or 'head_dim'}] is wanted")
-    n, h, d = t.shape
-    st = t.stride()
-    if st[2] != 1 or (h > 1 and st[1] != d):
+def _rows(t, what, dtype, index, rows, D):
+    """Address, heads and token stride of [rows, heads, D] whose heads are contiguous in each row."""
+    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != D:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}: [{rows}, heads, {D}] is wanted")
+    if t.dtype != dtype or t.get_device() != index:
+        _bad(t, what, dtype, index, None)
+    h, st = t.shape[1], t.stride()
+    if st[2] != 1 or (h > 1 and st[1] != D):
         raise ValueError(f"the heads of a row of {what} must be contiguous")
-    return _arg(t, what, dtype, device, strided=True), (st[0] if n > 1 else max(st[0], h * d))
+    return t.data_ptr(), h, (st[0] if rows > 1 else h * D)
 
 
-def _pool(t, what, device, D):
-    """Pointer and (num_pages, n_kv_heads, page_tokens) of an E2M1 pool: CUDA, or pinned host memory."""
+def _pool(t, what, index, D):
+    """Address and (num_pages, n_kv_heads, page_tokens) of an E2M1 pool: CUDA, or pinned host memory."""
     import torch
     if t.dtype != torch.uint8 or t.dim() != 3 or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous uint8 [num_pages, n_kv_heads, page bytes]")
-    if t.device != device and not (t.device.type == "cpu" and t.is_pinned()):
-        raise ValueError(f"{what} is neither on {device} nor in pinned host memory")
+    if t.get_device() != index and not (t.get_device() < 0 and t.is_pinned()):
+        raise ValueError(f"{what} is neither with the other tensors nor in pinned host memory")
+    pages, heads, nbytes = t.shape
     per = D * 9 // 16
-    if t.shape[2] % per:
-        raise ValueError(f"{what}: a page of {t.shape[2]} bytes does not hold rows of {per}")
-    return t.data_ptr(), (t.shape[0], t.shape[1], t.shape[2] // per)
+    if nbytes % per:
+        raise ValueError(f"{what}: a page of {nbytes} bytes does not hold rows of {per}")
+    return t.data_ptr(), (pages, heads, nbytes // per)
 
 
-def _launch(device, stream):
+def _launch(index, stream):
     """The stream to launch on; the tensors must be on the current device, as the library launches there."""
     import torch
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {device}, not on the current CUDA device")
+    if index < 0 or index != torch.cuda.current_device():
+        raise ValueError("the tensors are not on the current CUDA device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
     return _stream(stream)
 
 
@@ -494,20 +484,22 @@ def dkv_step_plan(lengths, new_tokens, page_table, free_pages, free_count, page_
     include/dkv.h).  All tensors are int32 and CUDA; page_table [batch, max_pages], row_pos and
     row_slot [max_rows], report [4]."""
     import torch
-    dev, i32 = page_table.device, torch.int32
+    i32 = torch.int32
     if page_table.dim() != 2 or row_pos.dim() != 1 or free_pages.dim() != 1:
         raise ValueError("page_table is [batch, max_pages], row_pos [max_rows], free_pages [num_pages]")
     B, max_pages = page_table.shape
-    n, pages = row_pos.shape[0], free_pages.shape[0]
-    one = (1,)
-    _check(lib().dkv_step_plan(
-        _arg(lengths, "lengths", i32, dev, (B,)), _arg(new_tokens, "new_tokens", i32, dev, (B,)),
+    n, pages, dev = row_pos.shape[0], free_pages.shape[0], page_table.get_device()
+    each, one = (B,), (1,)
+    st = lib().dkv_step_plan(
+        _arg(lengths, "lengths", i32, dev, each), _arg(new_tokens, "new_tokens", i32, dev, each),
         _arg(page_table, "page_table", i32, dev), _arg(free_pages, "free_pages", i32, dev),
         _arg(free_count, "free_count", i32, dev, one), B, max_pages, page_tokens, pages, n,
         _arg(row_start, "row_start", i32, dev, (B + 1,)), _arg(row_pos, "row_pos", i32, dev),
-        _arg(row_slot, "row_slot", i32, dev, (n,)), _arg(kv_len, "kv_len", i32, dev, (B,)),
+        _arg(row_slot, "row_slot", i32, dev, (n,)), _arg(kv_len, "kv_len", i32, dev, each),
         _arg(free_left, "free_left", i32, dev, one), _arg(report, "report", i32, dev, (4,)),
-        _launch(dev, stream)), "dkv_step_plan")
+        _launch(dev, stream))
+    if st:
+        _check(st, "dkv_step_plan")
 
 
 def _dtype_of(t):
@@ -528,45 +520,51 @@ def dkv_qkv_append(q, k, v, positions=None, slots=None, k_pool=None, v_pool=None
     some = q if q is not None else k
     if some is None:
         raise ValueError("neither queries nor keys")
-    dev, dt = some.device, some.dtype
-    a = _Append(dtype=_dtype_of(some), rows=some.shape[0], eps=eps, k_scale=k_scale, v_scale=v_scale,
-                interleaved=int(bool(interleaved)))
-    n, D = some.shape[0], some.shape[-1]
-    a.head_dim = D
+    if some.dim() != 3:
+        raise ValueError("q, k and v are [rows, heads, head_dim]")
+    dev, dt, code = some.get_device(), some.dtype, _dtype_of(some)
+    n, _, D = some.shape
+    i32, f32 = torch.int32, torch.float32
+    pq = hq = sq = pqo = pqg = pk = pv = hkv = sk = sv = pko = pvo = pkg = 0
     if q is not None:
-        a.q, a.q_stride = _rows(q, "q", dt, dev)
-        a.n_q_heads = q.shape[1]
-        a.q_out = _arg(q_out, "q_out", dt, dev, tuple(q.shape))
-        a.q_gamma = _arg(q_gamma, "q_gamma", dt, dev, (D,))
+        pq, hq, sq = _rows(q, "q", dt, dev, n, D)
+        pqo = _arg(q_out, "q_out", dt, dev, (n, hq, D))
+        pqg = _arg(q_gamma, "q_gamma", dt, dev, (D,))
     if k is not None:
-        if v is None or v.shape != k.shape or k.shape[0] != n:
-            raise ValueError("k and v are [rows, n_kv_heads, D], with q's rows")
-        a.k, a.k_stride = _rows(k, "k", dt, dev, D=D)
-        a.v, a.v_stride = _rows(v, "v", dt, dev)
-        a.n_kv_heads = k.shape[1]
-        a.k_out = _arg(k_out, "k_out", dt, dev, tuple(k.shape))
-        a.v_out = _arg(v_out, "v_out", dt, dev, tuple(k.shape))
-        a.k_gamma = _arg(k_gamma, "k_gamma", dt, dev, (D,))
+        if v is None or v.shape != k.shape:
+            raise ValueError("k and v are both [rows, n_kv_heads, head_dim]")
+        pk, hkv, sk = _rows(k, "k", dt, dev, n, D)
+        pv, _, sv = _rows(v, "v", dt, dev, n, D)
+        pko = _arg(k_out, "k_out", dt, dev, (n, hkv, D))
+        pvo = _arg(v_out, "v_out", dt, dev, (n, hkv, D))
+        pkg = _arg(k_gamma, "k_gamma", dt, dev, (D,))
     elif v is not None:
         raise ValueError("keys and values come together")
+    pkp = pvp = pages = page_tokens = 0
     if k_pool is not None:
         if v_pool is None or k is None:
             raise ValueError("both pools and the keys come together")
-        a.k_pool, shape = _pool(k_pool, "k_pool", dev, D)
-        a.v_pool, other = _pool(v_pool, "v_pool", dev, D)
-        if shape != other or shape[1] != k.shape[1]:
-            raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens) for {k.shape[1]} heads")
-        a.num_pages, a.page_tokens = shape[0], shape[2]
-    a.slots = _arg(slots, "slots", torch.int32, dev, (n,))
+        pkp, shape = _pool(k_pool, "k_pool", dev, D)
+        pvp, other = _pool(v_pool, "v_pool", dev, D)
+        if shape != other or shape[1] != hkv:
+            raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens) for {hkv} heads")
+        pages, page_tokens = shape[0], shape[2]
+    pcs = pp = max_positions = rotary_dim = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin is [max_positions, rotary_dim]")
-        a.cos_sin = _arg(cos_sin, "cos_sin", torch.float32, dev)
-        a.max_positions, a.rotary_dim = cos_sin.shape
-        a.positions = _arg(positions, "positions", torch.int32, dev, (n,))
-    _check(lib().dkv_qkv_append(a, _launch(dev, stream)), "dkv_qkv_append")
+        pcs = _arg(cos_sin, "cos_sin", f32, dev)
+        max_positions, rotary_dim = cos_sin.shape
+        pp = _arg(positions, "positions", i32, dev, (n,))
+    st = lib().dkv_qkv_append(
+        _APPEND.pack(pq, pk, pv, sq, sk, sv, pqg, pkg, pcs, pp, _arg(slots, "slots", i32, dev, (n,)), pkp, pvp,
+                     pqo, pko, pvo, n, hq, hkv, D, code, rotary_dim, max_positions, bool(interleaved),
+                     page_tokens, pages, eps, k_scale, v_scale), _launch(dev, stream))
+    if st:
+        _check(st, "dkv_qkv_append")
 
 
+@functools.lru_cache(maxsize=256)
 def dkv_paged_attend_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_rows=1) -> int:
     """Bytes of device memory that dkv_paged_attend needs (0 for arguments that it refuses)."""
     return lib().dkv_paged_attend_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_rows)
@@ -578,37 +576,34 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
     1/sqrt(D).  Without a workspace (uint8, dkv_paged_attend_workspace bytes) one is taken from
     torch's allocator on the launching stream."""
     import torch
-    dev, dt, i32 = q.device, q.dtype, torch.int32
+    if q.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("q is [rows, n_q_heads, head_dim], page_table [batch, max_pages]")
+    dev, dt, i32 = q.get_device(), q.dtype, torch.int32
+    code = _dtype_of(q)
     s = _launch(dev, stream)
-    a = _Attend(dtype=_dtype_of(q), v_scale=v_scale, max_rows=max_rows)
-    a.q, a.q_stride = _rows(q, "q", dt, dev)
-    n, hq, D = q.shape
-    a.rows, a.n_q_heads, a.head_dim = n, hq, D
-    a.scale = D ** -0.5 if scale is None else scale
-    a.k_pool, shape = _pool(k_pool, "k_pool", dev, D)
-    a.v_pool, other = _pool(v_pool, "v_pool", dev, D)
+    n, _, D = q.shape
+    pq, hq, sq = _rows(q, "q", dt, dev, n, D)
+    pkp, shape = _pool(k_pool, "k_pool", dev, D)
+    pvp, other = _pool(v_pool, "v_pool", dev, D)
     if shape != other:
         raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens)")
-    a.num_pages, a.n_kv_heads, a.page_tokens = shape
-    if page_table.dim() != 2:
-        raise ValueError("page_table is [batch, max_pages]")
-    B, a.max_pages = page_table.shape
-    a.batch = B
-    a.page_table = _arg(page_table, "page_table", i32, dev)
-    a.kv_len = _arg(kv_len, "kv_len", i32, dev, (B,))
-    a.row_start = _arg(row_start, "row_start", i32, dev, (B + 1,))
-    a.out = _arg(out, "out", dt, dev, (n, hq, D))
-    a.lse = _arg(lse, "lse", torch.float32, dev, (n, hq))
+    pages, hkv, page_tokens = shape
+    B, max_pages = page_table.shape
     if workspace is None:
-        need = max(1, lib().dkv_paged_attend_workspace(B, hq, a.n_kv_heads, D, max_rows))
+        need = max(1, dkv_paged_attend_workspace(B, hq, hkv, D, max_rows))
         if stream is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
+            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
         else:  # owned by the launching stream, so that it is not handed out again before it ran
-            with torch.cuda.stream(torch.cuda.ExternalStream(s, device=dev)):
-                workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-    a.workspace = _arg(workspace, "workspace", torch.uint8, dev)
-    a.workspace_bytes = workspace.numel()
-    _check(lib().dkv_paged_attend(a, s), "dkv_paged_attend")
+            with torch.cuda.stream(torch.cuda.ExternalStream(s, device=q.device)):
+                workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
+    st = lib().dkv_paged_attend(
+        _ATTEND.pack(pq, sq, pkp, pvp, _arg(page_table, "page_table", i32, dev), _arg(kv_len, "kv_len", i32, dev, (B,)),
+                     _arg(row_start, "row_start", i32, dev, (B + 1,)), _arg(out, "out", dt, dev, (n, hq, D)),
+                     _arg(lse, "lse", torch.float32, dev, (n, hq)), _arg(workspace, "workspace", torch.uint8, dev),
+                     workspace.numel(), B, n, max_rows, hq, hkv, D, code, page_tokens, pages, max_pages,
+                     D ** -0.5 if scale is None else scale, v_scale), s)
+    if st:
+        _check(st, "dkv_paged_attend")
 
 
 class KVCache:
