@@ -482,6 +482,119 @@ def test_attend_bad_tables_and_lengths():
     torch.cuda.synchronize()
 
 
+# ---- attention for many rows (tiles of 128 and 256 packed rows) -----------------------------
+
+@pytest.mark.parametrize("Hq,Hkv,D,dtype,P,rows,cached", [
+    (8, 1, 128, "bf16", 16, [300, 1, 0, 40], [2000, 500, 9, 0]), (4, 2, 64, "fp16", 32, [700, 129], [0, 3000]),
+    (8, 8, 128, "fp16", 16, [257, 128, 256], [127, 128, 129]), (7, 1, 64, "bf16", 64, [90, 37, 38], [0, 900, 63]),
+    (2, 1, 128, "bf16", 128, [33, 65, 1], [5000, 1, 4000])])
+def test_attend_tiles(Hq, Hkv, D, dtype, P, rows, cached):
+    c = attend_case(D + len(rows), [r + k for r, k in zip(rows, cached)], rows, Hq, Hkv, D, dtype, P)
+    out, lse = run_attend(c)
+    check_attend(c, out, lse)
+    again, low = run_attend(c)
+    assert torch.equal(out, again) and torch.equal(lse, low)
+
+
+def test_attend_tiles_many_sequences():
+    rng = np.random.default_rng(21)
+    rows = rng.integers(0, 50, 400)
+    rows[:200] = 0
+    c = attend_case(21, rows + rng.integers(0, 300, 400), rows, 2, 1, 64, "bf16", 16)
+    check_attend(c, *run_attend(c))
+
+
+def test_attend_tiles_none_live():
+    c = attend_case(22, [0, 5], [0, 0], 4, 1, 128, "bf16", 16)
+    out, lse = run_attend(c, max_rows=100)
+    assert torch.all(out == 7) and torch.all(lse == 7)
+
+
+def test_attend_tiles_more_rows_than_keys():
+    c = attend_case(23, [3, 0, 200], [60, 50, 300], 4, 2, 128, "bf16", 16)
+    check_attend(c, *run_attend(c))
+
+
+@pytest.mark.parametrize("spread", [0.01, 20.0])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_tiles_flat_and_peaked(spread, D):
+    c = attend_case(24, [1500, 400], [60, 300], 4, 2, D, "bf16", 16, spread=spread)
+    check_attend(c, *run_attend(c))
+
+
+@pytest.mark.parametrize("slope", [0.02, 0.5, 4.0, -1.0])
+def test_attend_tiles_rising_scores(slope):
+    # the maximum rises tile by tile by less and by more than the weights' bound
+    c = attend_case(25, [900], [50], 4, 1, 128, "bf16", 16)
+    n = c["pools"][0].shape[0]
+    ramp = np.arange(n * 16, dtype=np.float32) * slope
+    vals = np.zeros((n, 1, 16, 128), np.float32)
+    for p, page in enumerate(c["table"][0]):
+        vals[page, 0, :, :] = (ramp[p * 16:(p + 1) * 16] / 8)[:, None]
+    c["pools"][0] = step.make_pool(vals)
+    c["q"] = torch.ones_like(c["q"]) * 0.5
+    check_attend(c, *run_attend(c))
+
+
+def test_attend_tiles_query_range_and_scale():
+    c = attend_case(26, [200, 300], [90, 120], 4, 2, 128, "bf16", 16)
+    for mul, scale in ((1e30, 1e-31), (1e-30, 1e29), (1.0, -0.3), (1.0, 0.0)):
+        d = dict(c, q=(c["q"].float() * mul).to(torch.bfloat16))
+        check_attend(d, *run_attend(d, scale=scale, v_scale=-0.5), scale=scale, v_scale=-0.5)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_attend_tiles_masked_nan_does_not_leak(D):
+    lens, rows = [150, 129, 64], [60, 129, 40]
+    c = attend_case(27, lens, rows, 4, 2, D, "bf16", 16)
+    clean = check_attend(c, *run_attend(c))
+    used = {(int(c["table"][b, t // 16]), t % 16) for b, x in enumerate(lens) for t in range(x)}
+    for p in range(c["pools"][0].shape[0]):
+        for r in range(16):
+            if (p, r) not in used:
+                poison(c["pools"][0], D, p, r)
+                poison(c["pools"][1], D, p, r)
+    out, lse = run_attend(c)
+    assert np.isfinite(host(out)[clean["live"]]).all()
+    check_attend(c, out, lse)
+
+
+@pytest.mark.parametrize("which,block", [(0, None), (1, None), (1, 2)])
+@pytest.mark.parametrize("at", [0, 100, 180, 199])
+def test_attend_tiles_visible_nan_reaches_its_rows_only(which, block, at):
+    D, G, n = 128, 2, 100
+    c = attend_case(28, [200, 200, 40], [n, n, 30], 2 * G, 2, D, "fp16", 16)
+    clean, _ = run_attend(c)
+    poison(c["pools"][which], D, int(c["table"][1, at // 16]), at % 16, block)
+    out, _ = run_attend(c)
+    got, clean = host(out), host(clean)
+    assert np.array_equal(got[:n], clean[:n]) and np.array_equal(got[2 * n:], clean[2 * n:])
+    for i in range(n):
+        row = got[n + i]
+        if at > 200 - n + i:
+            assert np.array_equal(row, clean[n + i])
+        elif block is None:
+            assert np.isnan(row).all()
+        else:
+            assert np.isnan(row[:, 16 * block:16 * block + 16]).all()
+            assert np.isfinite(row[:, np.r_[0:16 * block, 16 * block + 16:D]]).all()
+
+
+def test_attend_tiles_bad_tables_and_lengths():
+    c = attend_case(29, [300, 400, 200], [90, 120, 60], 4, 2, 64, "bf16", 16)
+    c["table"][0, 1], c["table"][1, 0], c["table"][1, 13] = -1, 1 << 30, -(1 << 31)
+    c["table"][2, :12] = c["pools"][0].shape[0]
+    check_attend(c, *run_attend(c))
+    run_attend(dict(c, start=np.array([0, 500, -3, 200], np.int32)), max_rows=100)
+    torch.cuda.synchronize()
+
+
+def test_attend_tiles_in_pinned_host_memory():
+    c = attend_case(30, [300, 500], [50, 80], 8, 2, 128, "bf16", 16)
+    out, lse = run_attend(c, pools=[torch.from_numpy(p).pin_memory() for p in c["pools"]])
+    check_attend(c, out, lse)
+
+
 def test_attend_strided_queries_and_shared_pages():
     c = attend_case(12, [77, 90], [1, 1], 8, 2, 128, "bf16", 16)
     c["table"][1, :3] = c["table"][0, :3]  # a shared prefix

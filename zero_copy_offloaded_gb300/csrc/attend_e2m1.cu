@@ -690,13 +690,30 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workspace: descriptors | partial (max, sum) | partial o, two slots per CTA.
 size_t ws_desc() { return align256(kMaxCtas * sizeof(AttendDesc)); }
-size_t ws_ml(int R) { return align256((size_t)2 * kMaxCtas * R * 2 * 4); }
-size_t ws_o(int R, int D) { return align256((size_t)2 * kMaxCtas * R * D * 4); }
 
-// Query rows per item: the smallest of 8, 16, 24 and 32 that holds a sequence's rows.
+// Query rows per item: the smallest of 8, 16, 24 and 32 that holds a sequence's rows;
+// for more than kTcFrom rows the items of the tcgen05 kernel.
+constexpr int kTcFrom = 32;
 int rows_per_item(int G, int max_rows) {
   const long long rows = (long long)G * max_rows;
-  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : 32;
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 24 ? 24 : rows <= kTcFrom ? 32 : kTcRows;
+}
+int ctas_of(int R) { return R == kTcRows ? kSms : kMaxCtas; }
+size_t ws_ml(int R) { return align256((size_t)2 * ctas_of(R) * R * 2 * 4); }
+size_t ws_o(int R, int D) { return align256((size_t)2 * ctas_of(R) * R * D * 4); }
+
+template <typename T, int D>
+cudaError_t launch_join(const AttendParams& p, int R, int ctas, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, R / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p, R);
 }
 
 template <typename T, int D, int NT>
@@ -717,20 +734,15 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
   const int grid = kSms * (fit < C::kPerSm ? fit : C::kPerSm);
   attend_kernel<T, D, NT><<<grid, kThreads, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, NT);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p, C::R);
+  return launch_join<T, D>(p, C::R, grid, s);
 }
 
 template <typename T, int D>
 cudaError_t launch_rows(const AttendParams& p, int R, cudaStream_t s) {
+  if (R == kTcRows) {
+    const cudaError_t e = launch_attend_tc<T, D>(p, kSms, s);
+    return e == cudaSuccess ? launch_join<T, D>(p, R, kSms, s) : e;
+  }
   return R == 8    ? launch<T, D, 1>(p, s)
          : R == 16 ? launch<T, D, 2>(p, s)
          : R == 24 ? launch<T, D, 3>(p, s)

@@ -47,6 +47,11 @@ __device__ __forceinline__ void batch_entry(const AttendParams& p, int b, int& k
   }
 }
 
+// attend_e2m1_tc.cu: items of kTcRows query rows, one CTA on each of `grid` SMs.
+constexpr int kTcRows = 256;
+template <typename T, int D>
+cudaError_t launch_attend_tc(const AttendParams& p, int grid, cudaStream_t s);
+
 // Rows are normalised and rounded once; a row that saw no key is zero, its lse -infinity.
 // A NaN sum or output stays NaN.
 template <typename T, int V>
