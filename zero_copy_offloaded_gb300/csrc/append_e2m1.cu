@@ -18,6 +18,7 @@
 #include <stdio.h>
 
 #include "e2m1.cuh"
+#include "tc_common.cuh"
 
 namespace dkv {
 void set_last_error(dkv_status s, const char* msg);
@@ -50,7 +51,7 @@ struct AppendParams {
 };
 
 constexpr int kThreads = 256;
-constexpr int kIter = 4;  // rows of each lane group in flight
+constexpr int kIter = 4;  // rows of each lane group in an item
 
 // s + e of a and b with the rounding error kept (any order of magnitudes).
 __device__ __forceinline__ void two_sum(float& s, float& e, float b) {
@@ -79,211 +80,276 @@ __device__ __forceinline__ float inv_rms(float hi, float lo, float eps) {
 
 // The same in fp64, for rows whose squares leave fp32's range.
 template <int LPR>
-__device__ __noinline__ float inv_rms_wide(const float (&x)[8], float eps) {
-  double sum = 0;
+__device__ __noinline__ float inv_rms_wide(float a, float b, float c, float d, float e, float f, float g,
+                                           float h, float eps) {
+  double sum = (double)a * a + (double)b * b + (double)c * c + (double)d * d + (double)e * e +
+               (double)f * f + (double)g * g + (double)h * h;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sum = fma((double)x[e], (double)x[e], sum);
-#pragma unroll
-  for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor_sync(~0u, sum, d);
+  for (int m = 1; m < LPR; m <<= 1) sum += __shfl_xor_sync(~0u, sum, m);
   return (float)(1.0 / sqrt(sum / (8 * LPR) + (double)eps));
 }
 
 template <typename T>
-__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = DT<T>::to_f2(u[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+__device__ __forceinline__ void unpack4(const uint2& w, float* x) {
+  const float2 a = DT<T>::to_f2(w.x), b = DT<T>::to_f2(w.y);
+  x[0] = a.x; x[1] = a.y; x[2] = b.x; x[3] = b.y;
 }
 
 template <typename T>
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  uint32_t u[4];
+__device__ __forceinline__ uint2 pack4(const float* x) {
+  return make_uint2(tc::pack2<T>(x[0], x[1]), tc::pack2<T>(x[2], x[3]));
+}
+
+// x (8 elements of a row held by LPR lanes) times the row's 1 / rms and the norm weights.
+template <int LPR, bool EXACT>
+__device__ __forceinline__ void norm_row(float (&x)[8], const float (&g)[8], float eps) {
+  float hi = 0.f, lo = 0.f;
+  if constexpr (EXACT) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const T a = DT<T>::from_f(x[2 * i]), b = DT<T>::from_f(x[2 * i + 1]);
-    u[i] = (uint32_t)(*reinterpret_cast<const uint16_t*>(&a)) |
-           ((uint32_t)(*reinterpret_cast<const uint16_t*>(&b)) << 16);
+    for (int e = 0; e < 8; ++e) two_sum(hi, lo, __fmul_rn(x[e], x[e]));
+#pragma unroll
+    for (int d = 1; d < LPR; d <<= 1) {
+      const float oh = __shfl_xor_sync(~0u, hi, d), ol = __shfl_xor_sync(~0u, lo, d);
+      two_sum(hi, lo, oh);
+      lo = __fadd_rn(lo, ol);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) hi = fmaf(x[e], x[e], hi);
+#pragma unroll
+    for (int d = 1; d < LPR; d <<= 1) hi += __shfl_xor_sync(~0u, hi, d);
   }
-  return make_uint4(u[0], u[1], u[2], u[3]);
+  float r;
+  if constexpr (EXACT) {
+    r = inv_rms<8 * LPR>(hi, lo, eps);
+  } else {
+    const float m = fmaf(hi, 1.0f / (8 * LPR), eps);
+    r = m > 1e-30f && m < 1e30f ? rsqrtf(m) : 0.f;
+  }
+  if (__any_sync(~0u, r == 0.f)) {
+    const float wide = inv_rms_wide<LPR>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], eps);
+    if (r == 0.f) r = wide;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), g[e]);
+}
+
+// y / s correctly rounded for s whose correctly rounded reciprocal is r: the
+// quotient's residual is exact in one fused multiply-add, and a second one corrects it.
+__device__ __forceinline__ float divide(float y, float s, float r) {
+  const float q = __fmul_rn(y, r);
+  return __fmaf_rn(__fmaf_rn(-q, s, y), r, q);
+}
+
+// Quantises the 8 elements x of a lane (a block is two neighbouring lanes), stores codes and
+// scale at row `row` of a page, and leaves in x what the cache now holds.
+template <int D>
+__device__ __forceinline__ void store_codes(float (&x)[8], float inv, float mul, uint8_t* page,
+                                            int shift, int row, int l, bool write) {
+  uint32_t top = 0;  // as bits, NaN above infinity above every number
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    x[e] = __fmul_rn(x[e], inv);
+    top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
+  }
+  top = max(top, __shfl_xor_sync(~0u, top, 1));
+  const uint32_t sb = top >= 0x7f800000u  // a NaN scale: the block reads back as NaN
+                          ? 0x7fu
+                          : __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.0f), __NV_SATFINITE, __NV_E4M3);
+  const __half_raw sh = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sb, __NV_E4M3);
+  const float sf = __half2float(*reinterpret_cast<const __half*>(&sh));
+  const bool some = sf > 0.f;
+  const float r = __frcp_rn(some ? sf : 1.0f);
+  uint32_t code = 0;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 t = make_float2(some ? divide(x[2 * e], sf, r) : 0.f, some ? divide(x[2 * e + 1], sf, r) : 0.f);
+    code |= (uint32_t)__nv_cvt_float2_to_fp4x2(t, __NV_E2M1, cudaRoundNearest) << (8 * e);
+  }
+  if (write) {
+    *reinterpret_cast<uint32_t*>(page + (size_t)row * e2m1::code_bytes(D) + l * 4) = code;
+    if (!(l & 1))
+      page[((size_t)e2m1::code_bytes(D) << shift) + row * e2m1::scale_bytes(D) + l / 2] = (uint8_t)sb;
+  }
+  uint32_t h[4];
+  e2m1::codes_to_h2(code, h);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+    x[2 * e] = __fmul_rn(__fmul_rn(f.x, sf), mul);
+    x[2 * e + 1] = __fmul_rn(__fmul_rn(f.y, sf), mul);
+  }
 }
 
 // A warp takes one item: up to kIter * (32 / (D/8)) heads of one kind of one
-// token, D/8 lanes to a head row, 8 elements (16 bytes) to a lane.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) append_kernel(const AppendParams p) {
+// token, D/8 lanes to a head row, 8 elements to a lane.  Query rows need no blocks, so a
+// lane holds both partners of its pairs (two runs of 4 elements); key and value rows
+// keep 8 neighbouring elements on a lane, a block on two, and key partners are
+// exchanged.
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams p) {
   constexpr int LPR = D / 8, RPW = 32 / LPR, HEADS = kIter * RPW;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const int per_tok = p.q_items + 2 * p.kv_items;
   const long long items = (long long)p.N * per_tok;
   const long long step = (long long)gridDim.x * (kThreads / 32);
+  const float nan = __int_as_float(0x7fc00000);
   for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items;
        it += step) {
     const int tok = (int)(it / per_tok);
     int j = (int)(it - (long long)tok * per_tok);
-    int kind = 0;  // 0 query, 1 key, 2 value
-    if (j >= p.q_items) {
-      j -= p.q_items;
-      kind = 1;
-      if (j >= p.kv_items) {
-        j -= p.kv_items;
-        kind = 2;
+    const int slot = p.slot ? __ldg(p.slot + tok) : -1;
+    if (p.slot && (slot < 0 || slot >= p.slots)) continue;  // padding: nothing of it is written
+    const int pos = p.pos ? __ldg(p.pos + tok) : 0;
+    const bool far = p.pos && (pos < 0 || pos >= p.max_pos);
+    const bool turn = p.pos && !far, mine = turn && l * 8 < p.rot;
+    const int half = p.rot / 2;
+    const float* trig = p.cos_sin + (size_t)(turn ? pos : 0) * p.rot;
+
+    if (j < p.q_items) {
+      // ---- queries
+      const int h0 = j * HEADS;
+      const int off0 = !INTER && mine ? 4 * l : 8 * l, off1 = !INTER && mine ? half + 4 * l : 8 * l + 4;
+      const T* src = static_cast<const T*>(p.q) + (size_t)tok * p.qs;
+      const int rows = min(HEADS, p.Hq - h0);  // heads of this item
+      auto load = [&](int i, uint2& a, uint2& b) {
+        const int h = i * RPW + sub;
+        if (h < rows) {
+          const T* at = src + (size_t)(h0 + h) * D;
+          a = *reinterpret_cast<const uint2*>(at + off0);
+          b = *reinterpret_cast<const uint2*>(at + off1);
+        }
+      };
+      uint2 w0[2] = {}, w1[2] = {}, w2[2] = {};  // two rows ahead
+      load(0, w0[0], w0[1]);
+      load(1, w1[0], w1[1]);
+      float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (mine) {
+        c = __ldg(reinterpret_cast<const float4*>(trig + 4 * l));
+        s = __ldg(reinterpret_cast<const float4*>(trig + half + 4 * l));
       }
-    }
-    const int heads = kind == 0 ? p.Hq : p.Hkv, h0 = j * HEADS;
-    const int slot = p.slot ? p.slot[tok] : -1;
-    const int pos = p.pos ? p.pos[tok] : 0;
-    const bool skip = p.slot && (slot < 0 || slot >= p.slots);  // padding: nothing of it is written
-    if (skip) continue;
-    const T* src = kind == 0   ? static_cast<const T*>(p.q) + (size_t)tok * p.qs
-                   : kind == 1 ? static_cast<const T*>(p.k) + (size_t)tok * p.ks
-                               : static_cast<const T*>(p.v) + (size_t)tok * p.vs;
-    uint4 w[kIter];
+      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+      float g[8];
+      const T* gam = static_cast<const T*>(p.q_gamma);
+      if (gam) {
+        unpack4<T>(__ldg(reinterpret_cast<const uint2*>(gam + off0)), g);
+        unpack4<T>(__ldg(reinterpret_cast<const uint2*>(gam + off1)), g + 4);
+      }
+#pragma unroll 1
+      for (int i = 0; i * RPW < rows; ++i) {
+        load(i + 2, w2[0], w2[1]);
+        float x[8];
+        unpack4<T>(w0[0], x);
+        unpack4<T>(w0[1], x + 4);
+        w0[0] = w1[0]; w0[1] = w1[1];
+        w1[0] = w2[0]; w1[1] = w2[1];
+        if (gam) norm_row<LPR, false>(x, g, p.eps);
+        if (mine) {
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-      const int h = h0 + i * RPW + sub;
-      w[i] = h < heads ? *reinterpret_cast<const uint4*>(src + (size_t)h * D + l * 8)
-                       : make_uint4(0, 0, 0, 0);
+          for (int e = 0; e < 4; ++e) {
+            float &a = INTER ? x[2 * e] : x[e], &b = INTER ? x[2 * e + 1] : x[4 + e];
+            const float ra = __fsub_rn(__fmul_rn(a, cc[e]), __fmul_rn(b, ss[e]));
+            b = __fadd_rn(__fmul_rn(b, cc[e]), __fmul_rn(a, ss[e]));
+            a = ra;
+          }
+        }
+        if (far) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = nan;
+        }
+        if (i * RPW + sub < rows) {
+          T* out = static_cast<T*>(p.q_out) + ((size_t)tok * p.Hq + h0 + i * RPW + sub) * D;
+          *reinterpret_cast<uint2*>(out + off0) = pack4<T>(x);
+          *reinterpret_cast<uint2*>(out + off1) = pack4<T>(x + 4);
+        }
+      }
+      continue;
     }
-    // this lane's cosines and sines; `side`: 0 not rotated, -1 first of its pairs, 1 second
-    float c[8], s[8];
+    j -= p.q_items;
+    const bool key = j < p.kv_items;
+    const int h0 = (key ? j : j - p.kv_items) * HEADS;
+    const T* src = key ? static_cast<const T*>(p.k) + (size_t)tok * p.ks
+                       : static_cast<const T*>(p.v) + (size_t)tok * p.vs;
+    T* out = static_cast<T*>(key ? p.k_out : p.v_out);
+    const int rows = min(HEADS, p.Hkv - h0);
+    auto load = [&](int i, uint4& a) {
+      const int h = i * RPW + sub;
+      if (h < rows) a = *reinterpret_cast<const uint4*>(src + (size_t)(h0 + h) * D + l * 8);
+    };
+    uint4 w0 = {}, w1 = {}, w2 = {};
+    load(0, w0);
+    load(1, w1);
+    uint8_t* page = nullptr;
+    const int row = slot & ((1 << p.page_shift) - 1);
+    const size_t page_bytes = e2m1::page_bytes(D, 1 << p.page_shift);
+    if (p.slot) page = (key ? p.k_pool : p.v_pool) + (size_t)(slot >> p.page_shift) * p.Hkv * page_bytes;
+    // a key's cosines and sines; `side`: -1 first of its pairs, 1 second, 0 not rotated
+    float c[8], s[8], g[8];
     int side = 0;
-    const bool turn = kind < 2 && p.cos_sin != nullptr;
-    const bool far = turn && (pos < 0 || pos >= p.max_pos);
-    if (turn && l * 8 < p.rot && !far) {
-      const float* row = p.cos_sin + (size_t)pos * p.rot;
-      const int half = p.rot / 2;
-      if (p.inter) {
-        side = 2;
-        const float4 a = *reinterpret_cast<const float4*>(row + l * 4);
-        const float4 b = *reinterpret_cast<const float4*>(row + half + l * 4);
-        c[0] = a.x; c[1] = a.y; c[2] = a.z; c[3] = a.w;
-        s[0] = b.x; s[1] = b.y; s[2] = b.z; s[3] = b.w;
-      } else {
-        side = l * 8 < half ? -1 : 1;
-        const float* at = row + (side < 0 ? l * 8 : l * 8 - half);
+    const T* gam = static_cast<const T*>(p.k_gamma);
+    if (key) {
+      if (mine) {
+        side = INTER ? 2 : l * 8 < half ? -1 : 1;
+        const float* at = INTER ? trig + 4 * l : trig + (side < 0 ? l * 8 : l * 8 - half);
 #pragma unroll
-        for (int q4 = 0; q4 < 2; ++q4) {
-          const float4 a = *reinterpret_cast<const float4*>(at + 4 * q4);
-          const float4 b = *reinterpret_cast<const float4*>(at + half + 4 * q4);
+        for (int q4 = 0; q4 < (INTER ? 1 : 2); ++q4) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(at + 4 * q4));
+          const float4 b = __ldg(reinterpret_cast<const float4*>(at + half + 4 * q4));
           c[4 * q4] = a.x; c[4 * q4 + 1] = a.y; c[4 * q4 + 2] = a.z; c[4 * q4 + 3] = a.w;
           s[4 * q4] = b.x; s[4 * q4 + 1] = b.y; s[4 * q4 + 2] = b.z; s[4 * q4 + 3] = b.w;
         }
       }
-    }
-    const int partner = side < 0 ? lane + p.rot / 16 : side == 1 ? lane - p.rot / 16 : lane;
-    const T* gam = static_cast<const T*>(kind == 0 ? p.q_gamma : kind == 1 ? p.k_gamma : nullptr);
-    float g[8];
-    if (gam) unpack8<T>(*reinterpret_cast<const uint4*>(gam + l * 8), g);
-#pragma unroll
-    for (int i = 0; i < kIter; ++i) {
-      const int h = h0 + i * RPW + sub;
-      float x[8];
-      unpack8<T>(w[i], x);
       if (gam) {
-        float hi = 0.f, lo = 0.f;
-        if (kind == 1) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) two_sum(hi, lo, __fmul_rn(x[e], x[e]));
-#pragma unroll
-          for (int d = 1; d < LPR; d <<= 1) {
-            const float oh = __shfl_xor_sync(~0u, hi, d), ol = __shfl_xor_sync(~0u, lo, d);
-            two_sum(hi, lo, oh);
-            lo = __fadd_rn(lo, ol);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) hi = fmaf(x[e], x[e], hi);
-#pragma unroll
-          for (int d = 1; d < LPR; d <<= 1) hi += __shfl_xor_sync(~0u, hi, d);
-        }
-        float r = inv_rms<D>(hi, lo, p.eps);
-        if (__any_sync(~0u, r == 0.f)) {
-          const float wide = inv_rms_wide<LPR>(x, p.eps);
-          if (r == 0.f) r = wide;
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), g[e]);
+        const uint4 gw = __ldg(reinterpret_cast<const uint4*>(gam + l * 8));
+        unpack4<T>(make_uint2(gw.x, gw.y), g);
+        unpack4<T>(make_uint2(gw.z, gw.w), g + 4);
       }
-      if (turn) {
-        if (p.inter) {
-          if (side) {
+    }
+    const int partner = side == -1 ? lane + p.rot / 16 : side == 1 ? lane - p.rot / 16 : lane;
+#pragma unroll 1
+    for (int i = 0; i * RPW < rows; ++i) {
+      const int h = h0 + i * RPW + sub;
+      load(i + 2, w2);
+      float x[8];
+      unpack4<T>(make_uint2(w0.x, w0.y), x);
+      unpack4<T>(make_uint2(w0.z, w0.w), x + 4);
+      w0 = w1;
+      w1 = w2;
+      if (key) {
+        if (gam) norm_row<LPR, true>(x, g, p.eps);
+        if (turn) {
+          if constexpr (INTER) {
+            if (side) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float a = x[2 * e], b = x[2 * e + 1];
-              x[2 * e] = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
-              x[2 * e + 1] = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
+              for (int e = 0; e < 4; ++e) {
+                const float a = x[2 * e], b = x[2 * e + 1];
+                x[2 * e] = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
+                x[2 * e + 1] = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float o = __shfl_sync(~0u, x[e], partner);
+              if (side) {
+                const float sn = side < 0 ? -s[e] : s[e];
+                x[e] = __fadd_rn(__fmul_rn(x[e], c[e]), __fmul_rn(o, sn));
+              }
             }
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float o = __shfl_sync(~0u, x[e], partner);
-            if (side < 0) x[e] = __fsub_rn(__fmul_rn(x[e], c[e]), __fmul_rn(o, s[e]));
-            if (side > 0) x[e] = __fadd_rn(__fmul_rn(x[e], c[e]), __fmul_rn(o, s[e]));
-          }
         }
-        if (far) {  // no such row in the table
+        if (far) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __int_as_float(0x7fc00000);
+          for (int e = 0; e < 8; ++e) x[e] = nan;
         }
       }
-      if (kind == 0) {
-        if (h < heads)
-          *reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + ((size_t)tok * p.Hq + h) * D + l * 8) =
-              pack8<T>(x);
-        continue;
+      if (p.slot)
+        store_codes<D>(x, key ? p.k_inv : p.v_inv, key ? p.k_scale : p.v_scale,
+                       page + (size_t)min(h, p.Hkv - 1) * page_bytes, p.page_shift, row, l, h < p.Hkv);
+      if (out && h < p.Hkv) {
+        const uint2 a = pack4<T>(x), b = pack4<T>(x + 4);
+        *reinterpret_cast<uint4*>(out + ((size_t)tok * p.Hkv + h) * D + l * 8) = make_uint4(a.x, a.y, b.x, b.y);
       }
-      T* out = static_cast<T*>(kind == 1 ? p.k_out : p.v_out);
-      if (p.slot) {
-        const float inv = kind == 1 ? p.k_inv : p.v_inv;
-        uint32_t top = 0;  // as bits, NaN above infinity above every number
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[e] = __fmul_rn(x[e], inv);
-          top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-        }
-        top = max(top, __shfl_xor_sync(~0u, top, 1));
-        const float amax = __uint_as_float(top);
-        const uint32_t sb = top >= 0x7f800000u
-                                ? 0x7fu  // a NaN scale: the block reads back as NaN
-                                : __nv_cvt_float_to_fp8(__fdiv_rn(amax, 6.0f), __NV_SATFINITE, __NV_E4M3);
-        const __half_raw sh = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sb, __NV_E4M3);
-        const float sf = __half2float(*reinterpret_cast<const __half*>(&sh));
-        uint32_t code = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 t = sf > 0.f ? make_float2(__fdiv_rn(x[2 * e], sf), __fdiv_rn(x[2 * e + 1], sf))
-                                    : make_float2(0.f, 0.f);
-          code |= (uint32_t)__nv_cvt_float2_to_fp4x2(t, __NV_E2M1, cudaRoundNearest) << (8 * e);
-        }
-        if (h < heads) {
-          uint8_t* page = (kind == 1 ? p.k_pool : p.v_pool) +
-                          ((size_t)(slot >> p.page_shift) * p.Hkv + h) *
-                              e2m1::page_bytes(D, 1 << p.page_shift);
-          const int row = slot & ((1 << p.page_shift) - 1);
-          *reinterpret_cast<uint32_t*>(page + (size_t)row * e2m1::code_bytes(D) + l * 4) = code;
-          if (!(l & 1))
-            page[((size_t)e2m1::code_bytes(D) << p.page_shift) + row * e2m1::scale_bytes(D) + l / 2] =
-                (uint8_t)sb;
-        }
-        if (out) {  // what the cache now holds
-          const float mul = kind == 1 ? p.k_scale : p.v_scale;
-          uint32_t hh[4];
-          e2m1::codes_to_h2(code, hh);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hh[e]));
-            x[2 * e] = __fmul_rn(__fmul_rn(f.x, sf), mul);
-            x[2 * e + 1] = __fmul_rn(__fmul_rn(f.y, sf), mul);
-          }
-        }
-      }
-      if (out && h < heads)
-        *reinterpret_cast<uint4*>(out + ((size_t)tok * p.Hkv + h) * D + l * 8) = pack8<T>(x);
     }
   }
 }
@@ -302,7 +368,9 @@ void launch(AppendParams& p, cudaStream_t s) {
   p.kv_items = p.k ? (p.Hkv + HEADS - 1) / HEADS : 0;
   const long long items = (long long)p.N * (p.q_items + 2 * p.kv_items);
   const long long blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
-  append_kernel<T, D><<<(unsigned)(blocks < 152 * 8 ? blocks : 152 * 8), kThreads, 0, s>>>(p);
+  const unsigned grid = (unsigned)(blocks < 152 * 4 ? blocks : 152 * 4);  // four CTAs on an SM
+  if (p.inter) append_kernel<T, D, true><<<grid, kThreads, 0, s>>>(p);
+  else append_kernel<T, D, false><<<grid, kThreads, 0, s>>>(p);
 }
 
 }  // namespace
