@@ -46,12 +46,12 @@ struct AppendParams {
   long long slots;       // rows of the pool
   int N, Hq, Hkv, rot, max_pos, inter;
   int page_shift;
-  int q_items, kv_items;  // items (of kHeads heads) per token
+  int q_items, kv_items;  // head groups of queries, of keys and of values
   float eps, k_scale, v_scale, k_inv, v_inv;
 };
 
 constexpr int kThreads = 256;
-constexpr int kIter = 4;  // rows of each lane group in an item
+constexpr int kIter = 4;  // rows of each lane group for one token
 
 // s + e of a and b with the rounding error kept (any order of magnitudes).
 __device__ __forceinline__ void two_sum(float& s, float& e, float b) {
@@ -141,216 +141,197 @@ __device__ __forceinline__ float divide(float y, float s, float r) {
   return __fmaf_rn(__fmaf_rn(-q, s, y), r, q);
 }
 
-// Quantises the 8 elements x of a lane (a block is two neighbouring lanes), stores codes and
-// scale at row `row` of a page, and leaves in x what the cache now holds.
-template <int D>
-__device__ __forceinline__ void store_codes(float (&x)[8], float inv, float mul, uint8_t* page,
-                                            int shift, int row, int l, bool write) {
+// Quantises the 8 elements x of a lane (a block is two neighbouring lanes): the codes and, on
+// the even lane, the scale byte.  Leaves the block's scale in `sf`.
+__device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sb, float& sf) {
   uint32_t top = 0;  // as bits, NaN above infinity above every number
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    x[e] = __fmul_rn(x[e], inv);
-    top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
-  }
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(x[e]) & 0x7fffffffu);
   top = max(top, __shfl_xor_sync(~0u, top, 1));
-  const uint32_t sb = top >= 0x7f800000u  // a NaN scale: the block reads back as NaN
-                          ? 0x7fu
-                          : __nv_cvt_float_to_fp8(__fdiv_rn(__uint_as_float(top), 6.0f), __NV_SATFINITE, __NV_E4M3);
-  const __half_raw sh = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)sb, __NV_E4M3);
-  const float sf = __half2float(*reinterpret_cast<const __half*>(&sh));
+  sb = top >= 0x7f800000u  // a NaN scale: the block reads back as NaN
+           ? 0x7fu
+           : __nv_cvt_float_to_fp8(divide(__uint_as_float(top), 6.0f, 1.0f / 6.0f), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t sh = e2m1::scales_to_h2(sb);
+  sf = __low2float(*reinterpret_cast<const __half2*>(&sh));
   const bool some = sf > 0.f;
   const float r = __frcp_rn(some ? sf : 1.0f);
   uint32_t code = 0;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 t = make_float2(some ? divide(x[2 * e], sf, r) : 0.f, some ? divide(x[2 * e + 1], sf, r) : 0.f);
-    code |= (uint32_t)__nv_cvt_float2_to_fp4x2(t, __NV_E2M1, cudaRoundNearest) << (8 * e);
-  }
-  if (write) {
-    *reinterpret_cast<uint32_t*>(page + (size_t)row * e2m1::code_bytes(D) + l * 4) = code;
-    if (!(l & 1))
-      page[((size_t)e2m1::code_bytes(D) << shift) + row * e2m1::scale_bytes(D) + l / 2] = (uint8_t)sb;
-  }
-  uint32_t h[4];
-  e2m1::codes_to_h2(code, h);
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
-    x[2 * e] = __fmul_rn(__fmul_rn(f.x, sf), mul);
-    x[2 * e + 1] = __fmul_rn(__fmul_rn(f.y, sf), mul);
-  }
+  for (int e = 0; e < 4; ++e)
+    code |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(divide(x[2 * e], sf, r), divide(x[2 * e + 1], sf, r)),
+                                               __NV_E2M1, cudaRoundNearest)
+            << (8 * e);
+  return some ? code : 0;
 }
 
-// A warp takes one item: up to kIter * (32 / (D/8)) heads of one kind of one
-// token, D/8 lanes to a head row, 8 elements to a lane.  Query rows need no blocks, so a
-// lane holds both partners of its pairs (two runs of 4 elements); key and value rows
-// keep 8 neighbouring elements on a lane, a block on two, and key partners are
-// exchanged.
-template <typename T, int D, bool INTER>
-__global__ void __launch_bounds__(kThreads, 4) append_kernel(const AppendParams p) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR, HEADS = kIter * RPW;
-  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-  const int per_tok = p.q_items + 2 * p.kv_items;
-  const long long items = (long long)p.N * per_tok;
-  const long long step = (long long)gridDim.x * (kThreads / 32);
-  const float nan = __int_as_float(0x7fc00000);
-  for (long long it = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); it < items;
-       it += step) {
-    const int tok = (int)(it / per_tok);
-    int j = (int)(it - (long long)tok * per_tok);
-    const int slot = p.slot ? __ldg(p.slot + tok) : -1;
-    if (p.slot && (slot < 0 || slot >= p.slots)) continue;  // padding: nothing of it is written
-    const int pos = p.pos ? __ldg(p.pos + tok) : 0;
-    const bool far = p.pos && (pos < 0 || pos >= p.max_pos);
-    const bool turn = p.pos && !far, mine = turn && l * 8 < p.rot;
-    const int half = p.rot / 2;
-    const float* trig = p.cos_sin + (size_t)(turn ? pos : 0) * p.rot;
+constexpr int kQuery = 0, kKey = 1, kValue = 2;
 
-    if (j < p.q_items) {
-      // ---- queries
-      const int h0 = j * HEADS;
-      const int off0 = !INTER && mine ? 4 * l : 8 * l, off1 = !INTER && mine ? half + 4 * l : 8 * l + 4;
-      const T* src = static_cast<const T*>(p.q) + (size_t)tok * p.qs;
-      const int rows = min(HEADS, p.Hq - h0);  // heads of this item
-      auto load = [&](int i, uint2& a, uint2& b) {
-        const int h = i * RPW + sub;
-        if (h < rows) {
-          const T* at = src + (size_t)(h0 + h) * D;
-          a = *reinterpret_cast<const uint2*>(at + off0);
-          b = *reinterpret_cast<const uint2*>(at + off1);
-        }
-      };
-      uint2 w0[2] = {}, w1[2] = {}, w2[2] = {};  // two rows ahead
-      load(0, w0[0], w0[1]);
-      load(1, w1[0], w1[1]);
-      float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (mine) {
-        c = __ldg(reinterpret_cast<const float4*>(trig + 4 * l));
-        s = __ldg(reinterpret_cast<const float4*>(trig + half + 4 * l));
-      }
-      const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
-      float g[8];
-      const T* gam = static_cast<const T*>(p.q_gamma);
-      if (gam) {
-        unpack4<T>(__ldg(reinterpret_cast<const uint2*>(gam + off0)), g);
-        unpack4<T>(__ldg(reinterpret_cast<const uint2*>(gam + off1)), g + 4);
-      }
+// The rows of `heads` heads from h0 on, for tokens first, first + step, ...  A row takes D/8 lanes,
+// 8 elements each.  Query rows need no blocks, so a lane holds both partners of its pairs
+// (two runs of 4 elements); key and value rows keep 8 neighbouring elements on a lane, and
+// keys exchange their partners.
+template <typename T, int D, bool INTER, int KIND>
+__device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int heads, int first, int step) {
+  constexpr int LPR = D / 8, RPW = 32 / LPR;
+  constexpr bool PAIRED = KIND == kQuery && !INTER;
+  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
+  const float nan = __int_as_float(0x7fc00000);
+  const int half = p.rot / 2;
+  const bool in_rot = KIND != kValue && p.pos && l * 8 < p.rot;
+  const int off0 = PAIRED && in_rot ? 4 * l : 8 * l, off1 = PAIRED && in_rot ? half + 4 * l : 8 * l + 4;
+  const T* base = static_cast<const T*>(KIND == kQuery ? p.q : KIND == kKey ? p.k : p.v) + (size_t)(h0 + sub) * D;
+  const long long stride = KIND == kQuery ? p.qs : KIND == kKey ? p.ks : p.vs;
+  const int H = KIND == kQuery ? p.Hq : p.Hkv;
+  T* out = static_cast<T*>(KIND == kQuery ? p.q_out : KIND == kKey ? p.k_out : p.v_out);
+  const T* gam = static_cast<const T*>(KIND == kQuery ? p.q_gamma : KIND == kKey ? p.k_gamma : nullptr);
+  const bool norm = KIND != kValue && gam != nullptr;
+  float g[8];
+  if (norm) {
+    unpack4<T>(__ldg(reinterpret_cast<const uint2*>(gam + off0)), g);
+    unpack4<T>(__ldg(reinterpret_cast<const uint2*>(gam + off1)), g + 4);
+  }
+  // half pairs of keys: -1 the lane holds the first of its pairs, 1 the second
+  const int side = KIND == kKey && !INTER && in_rot ? (l * 8 < half ? -1 : 1) : 0;
+  const int partner = lane - side * (p.rot / 16);
+  const size_t page_bytes = e2m1::page_bytes(D, 1 << p.page_shift);
+  const float inv = KIND == kKey ? p.k_inv : p.v_inv, mul = KIND == kKey ? p.k_scale : p.v_scale;
+  uint8_t* pool = (KIND == kKey ? p.k_pool : p.v_pool) + (KIND == kQuery ? 0 : (size_t)(h0 + sub) * page_bytes);
+
 #pragma unroll 1
-      for (int i = 0; i * RPW < rows; ++i) {
-        load(i + 2, w2[0], w2[1]);
-        float x[8];
-        unpack4<T>(w0[0], x);
-        unpack4<T>(w0[1], x + 4);
-        w0[0] = w1[0]; w0[1] = w1[1];
-        w1[0] = w2[0]; w1[1] = w2[1];
-        if (gam) norm_row<LPR, false>(x, g, p.eps);
-        if (mine) {
+  for (int tok = first; tok < p.N; tok += step) {
+    const T* src = base + (size_t)tok * stride;
+    auto load = [&](int h, uint2& a, uint2& b) {  // head h0 + h + sub
+      if (h + sub < heads) {
+        if constexpr (PAIRED) {
+          a = *reinterpret_cast<const uint2*>(src + h * D + off0);
+          b = *reinterpret_cast<const uint2*>(src + h * D + off1);
+        } else {
+          const uint4 w = *reinterpret_cast<const uint4*>(src + h * D + l * 8);
+          a = make_uint2(w.x, w.y);
+          b = make_uint2(w.z, w.w);
+        }
+      }
+    };
+    uint2 w0[2] = {}, w1[2] = {}, w2[2] = {};  // two rows ahead
+    load(0, w0[0], w0[1]);
+    load(RPW, w1[0], w1[1]);
+    const int slot = p.slot ? __ldg(p.slot + tok) : 0;
+    if (p.slot && (slot < 0 || slot >= p.slots)) continue;  // padding: nothing of it is written
+    bool far = false, turn = false;
+    float c[8], s[8];
+    if (KIND != kValue && p.pos) {
+      const int pos = __ldg(p.pos + tok);
+      far = pos < 0 || pos >= p.max_pos;
+      turn = !far && in_rot;
+      if (turn) {
+        // 4 pairs of a lane's own, or the 8 pairs that its elements are one side of
+        const float* at = p.cos_sin + (size_t)pos * p.rot + (KIND == kKey && !INTER ? 8 * l - (side > 0 ? half : 0) : 4 * l);
+#pragma unroll
+        for (int i = 0; i < (KIND == kKey && !INTER ? 2 : 1); ++i) {
+          const float4 a = __ldg(reinterpret_cast<const float4*>(at + 4 * i));
+          const float4 b = __ldg(reinterpret_cast<const float4*>(at + half + 4 * i));
+          c[4 * i] = a.x; c[4 * i + 1] = a.y; c[4 * i + 2] = a.z; c[4 * i + 3] = a.w;
+          s[4 * i] = b.x; s[4 * i + 1] = b.y; s[4 * i + 2] = b.z; s[4 * i + 3] = b.w;
+        }
+        if (side < 0) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] = -s[e];
+        }
+      }
+    }
+    uint8_t* codes = nullptr;
+    uint8_t* scale = nullptr;
+    if (KIND != kQuery && p.slot) {
+      const int row = slot & ((1 << p.page_shift) - 1);
+      uint8_t* page = pool + (size_t)(slot >> p.page_shift) * p.Hkv * page_bytes;
+      codes = page + row * e2m1::code_bytes(D) + l * 4;
+      scale = page + ((size_t)e2m1::code_bytes(D) << p.page_shift) + row * e2m1::scale_bytes(D) + l / 2;
+    }
+    T* to = out ? out + ((size_t)tok * H + h0 + sub) * D : nullptr;
+#pragma unroll 1
+    for (int h = 0; h < heads; h += RPW) {
+      load(h + 2 * RPW, w2[0], w2[1]);
+      float x[8];
+      unpack4<T>(w0[0], x);
+      unpack4<T>(w0[1], x + 4);
+      w0[0] = w1[0]; w0[1] = w1[1];
+      w1[0] = w2[0]; w1[1] = w2[1];
+      if (norm) norm_row<LPR, KIND == kKey>(x, g, p.eps);
+      if constexpr (KIND == kKey && !INTER) {
+        if (p.pos) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float o = __shfl_sync(~0u, x[e], partner);
+            // the first of a pair: x c - o s, the second: x c + o s (the sign is in s)
+            if (turn) x[e] = __fadd_rn(__fmul_rn(x[e], c[e]), __fmul_rn(o, s[e]));
+          }
+        }
+      } else if constexpr (KIND != kValue) {
+        if (turn) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float &a = INTER ? x[2 * e] : x[e], &b = INTER ? x[2 * e + 1] : x[4 + e];
-            const float ra = __fsub_rn(__fmul_rn(a, cc[e]), __fmul_rn(b, ss[e]));
-            b = __fadd_rn(__fmul_rn(b, cc[e]), __fmul_rn(a, ss[e]));
+            const float ra = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
+            b = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
             a = ra;
           }
         }
-        if (far) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = nan;
-        }
-        if (i * RPW + sub < rows) {
-          T* out = static_cast<T*>(p.q_out) + ((size_t)tok * p.Hq + h0 + i * RPW + sub) * D;
-          *reinterpret_cast<uint2*>(out + off0) = pack4<T>(x);
-          *reinterpret_cast<uint2*>(out + off1) = pack4<T>(x + 4);
-        }
       }
-      continue;
-    }
-    j -= p.q_items;
-    const bool key = j < p.kv_items;
-    const int h0 = (key ? j : j - p.kv_items) * HEADS;
-    const T* src = key ? static_cast<const T*>(p.k) + (size_t)tok * p.ks
-                       : static_cast<const T*>(p.v) + (size_t)tok * p.vs;
-    T* out = static_cast<T*>(key ? p.k_out : p.v_out);
-    const int rows = min(HEADS, p.Hkv - h0);
-    auto load = [&](int i, uint4& a) {
-      const int h = i * RPW + sub;
-      if (h < rows) a = *reinterpret_cast<const uint4*>(src + (size_t)(h0 + h) * D + l * 8);
-    };
-    uint4 w0 = {}, w1 = {}, w2 = {};
-    load(0, w0);
-    load(1, w1);
-    uint8_t* page = nullptr;
-    const int row = slot & ((1 << p.page_shift) - 1);
-    const size_t page_bytes = e2m1::page_bytes(D, 1 << p.page_shift);
-    if (p.slot) page = (key ? p.k_pool : p.v_pool) + (size_t)(slot >> p.page_shift) * p.Hkv * page_bytes;
-    // a key's cosines and sines; `side`: -1 first of its pairs, 1 second, 0 not rotated
-    float c[8], s[8], g[8];
-    int side = 0;
-    const T* gam = static_cast<const T*>(p.k_gamma);
-    if (key) {
-      if (mine) {
-        side = INTER ? 2 : l * 8 < half ? -1 : 1;
-        const float* at = INTER ? trig + 4 * l : trig + (side < 0 ? l * 8 : l * 8 - half);
+      if (KIND != kValue && far) {
 #pragma unroll
-        for (int q4 = 0; q4 < (INTER ? 1 : 2); ++q4) {
-          const float4 a = __ldg(reinterpret_cast<const float4*>(at + 4 * q4));
-          const float4 b = __ldg(reinterpret_cast<const float4*>(at + half + 4 * q4));
-          c[4 * q4] = a.x; c[4 * q4 + 1] = a.y; c[4 * q4 + 2] = a.z; c[4 * q4 + 3] = a.w;
-          s[4 * q4] = b.x; s[4 * q4 + 1] = b.y; s[4 * q4 + 2] = b.z; s[4 * q4 + 3] = b.w;
+        for (int e = 0; e < 8; ++e) x[e] = nan;
+      }
+      const bool write = h + sub < heads;
+      if (KIND != kQuery && p.slot) {
+        if (inv != 1.0f) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], inv);
         }
-      }
-      if (gam) {
-        const uint4 gw = __ldg(reinterpret_cast<const uint4*>(gam + l * 8));
-        unpack4<T>(make_uint2(gw.x, gw.y), g);
-        unpack4<T>(make_uint2(gw.z, gw.w), g + 4);
-      }
-    }
-    const int partner = side == -1 ? lane + p.rot / 16 : side == 1 ? lane - p.rot / 16 : lane;
-#pragma unroll 1
-    for (int i = 0; i * RPW < rows; ++i) {
-      const int h = h0 + i * RPW + sub;
-      load(i + 2, w2);
-      float x[8];
-      unpack4<T>(make_uint2(w0.x, w0.y), x);
-      unpack4<T>(make_uint2(w0.z, w0.w), x + 4);
-      w0 = w1;
-      w1 = w2;
-      if (key) {
-        if (gam) norm_row<LPR, true>(x, g, p.eps);
-        if (turn) {
-          if constexpr (INTER) {
-            if (side) {
+        uint32_t sb;
+        float sf;
+        const uint32_t code = quantise(x, sb, sf);
+        if (write) {
+          *reinterpret_cast<uint32_t*>(codes + (size_t)h * page_bytes) = code;
+          if (!(l & 1)) scale[(size_t)h * page_bytes] = (uint8_t)sb;
+        }
+        if (to) {  // what the cache now holds
+          uint32_t y[4];
+          e2m1::codes_to_h2(code, y);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float a = x[2 * e], b = x[2 * e + 1];
-                x[2 * e] = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
-                x[2 * e + 1] = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float o = __shfl_sync(~0u, x[e], partner);
-              if (side) {
-                const float sn = side < 0 ? -s[e] : s[e];
-                x[e] = __fadd_rn(__fmul_rn(x[e], c[e]), __fmul_rn(o, sn));
-              }
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y[e]));
+            x[2 * e] = __fmul_rn(__fmul_rn(f.x, sf), mul);
+            x[2 * e + 1] = __fmul_rn(__fmul_rn(f.y, sf), mul);
           }
         }
-        if (far) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = nan;
+      }
+      if (to && write) {
+        const uint2 a = pack4<T>(x), b = pack4<T>(x + 4);
+        if constexpr (PAIRED) {
+          *reinterpret_cast<uint2*>(to + h * D + off0) = a;
+          *reinterpret_cast<uint2*>(to + h * D + off1) = b;
+        } else {
+          *reinterpret_cast<uint4*>(to + h * D + l * 8) = make_uint4(a.x, a.y, b.x, b.y);
         }
       }
-      if (p.slot)
-        store_codes<D>(x, key ? p.k_inv : p.v_inv, key ? p.k_scale : p.v_scale,
-                       page + (size_t)min(h, p.Hkv - 1) * page_bytes, p.page_shift, row, l, h < p.Hkv);
-      if (out && h < p.Hkv) {
-        const uint2 a = pack4<T>(x), b = pack4<T>(x + 4);
-        *reinterpret_cast<uint4*>(out + ((size_t)tok * p.Hkv + h) * D + l * 8) = make_uint4(a.x, a.y, b.x, b.y);
-      }
     }
+  }
+}
+
+// blockIdx.y: a group of up to kGroup head rows of one kind, keys first (they take longest), then
+// values, then queries; a warp takes one token of it at a time.
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams p) {
+  constexpr int GROUP = kIter * 32 / (D / 8);
+  const int first = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), step = gridDim.x * (kThreads / 32);
+  int j = blockIdx.y;
+  if (j < p.kv_items) {
+    append_rows<T, D, INTER, kKey>(p, j * GROUP, min(GROUP, p.Hkv - j * GROUP), first, step);
+  } else if ((j -= p.kv_items) < p.kv_items) {
+    append_rows<T, D, INTER, kValue>(p, j * GROUP, min(GROUP, p.Hkv - j * GROUP), first, step);
+  } else {
+    j -= p.kv_items;
+    append_rows<T, D, INTER, kQuery>(p, j * GROUP, min(GROUP, p.Hq - j * GROUP), first, step);
   }
 }
 
@@ -363,12 +344,13 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 template <typename T, int D>
 void launch(AppendParams& p, cudaStream_t s) {
-  constexpr int HEADS = kIter * 32 / (D / 8);
-  p.q_items = p.q ? (p.Hq + HEADS - 1) / HEADS : 0;
-  p.kv_items = p.k ? (p.Hkv + HEADS - 1) / HEADS : 0;
-  const long long items = (long long)p.N * (p.q_items + 2 * p.kv_items);
-  const long long blocks = (items + kThreads / 32 - 1) / (kThreads / 32);
-  const unsigned grid = (unsigned)(blocks < 152 * 4 ? blocks : 152 * 4);  // four CTAs on an SM
+  constexpr int GROUP = kIter * 32 / (D / 8);
+  p.q_items = p.q ? (p.Hq + GROUP - 1) / GROUP : 0;
+  p.kv_items = p.k ? (p.Hkv + GROUP - 1) / GROUP : 0;
+  // a token per warp up to eight waves of CTAs, so that the kinds' unequal times even out
+  const long long y = p.q_items + 2LL * p.kv_items, want = (p.N + kThreads / 32 - 1) / (kThreads / 32);
+  const long long most = (8 * 3 * 152 + y - 1) / y;
+  const dim3 grid((unsigned)(want < most ? want : most), (unsigned)y);
   if (p.inter) append_kernel<T, D, true><<<grid, kThreads, 0, s>>>(p);
   else append_kernel<T, D, false><<<grid, kThreads, 0, s>>>(p);
 }
