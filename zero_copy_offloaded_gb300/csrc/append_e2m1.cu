@@ -212,9 +212,9 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int h
         }
       }
     };
-    uint2 w0[2] = {}, w1[2] = {}, w2[2] = {};  // two rows ahead
-    load(0, w0[0], w0[1]);
-    load(RPW, w1[0], w1[1]);
+    uint2 w[kIter][2] = {};
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) load(i * RPW, w[i][0], w[i][1]);
     const int slot = p.slot ? __ldg(p.slot + tok) : 0;
     if (p.slot && (slot < 0 || slot >= p.slots)) continue;  // padding: nothing of it is written
     bool far = false, turn = false;
@@ -248,14 +248,13 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int h
       scale = page + ((size_t)e2m1::code_bytes(D) << p.page_shift) + row * e2m1::scale_bytes(D) + l / 2;
     }
     T* to = out ? out + ((size_t)tok * H + h0 + sub) * D : nullptr;
-#pragma unroll 1
-    for (int h = 0; h < heads; h += RPW) {
-      load(h + 2 * RPW, w2[0], w2[1]);
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int h = i * RPW;
+      if (h >= heads) break;
       float x[8];
-      unpack4<T>(w0[0], x);
-      unpack4<T>(w0[1], x + 4);
-      w0[0] = w1[0]; w0[1] = w1[1];
-      w1[0] = w2[0]; w1[1] = w2[1];
+      unpack4<T>(w[i][0], x);
+      unpack4<T>(w[i][1], x + 4);
       if (norm) norm_row<LPR, KIND == kKey>(x, g, p.eps);
       if constexpr (KIND == kKey && !INTER) {
         if (p.pos) {
