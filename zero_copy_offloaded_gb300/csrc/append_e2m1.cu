@@ -51,7 +51,8 @@ struct AppendParams {
 };
 
 constexpr int kThreads = 256;
-constexpr int kIter = 4;  // rows of each lane group for one token
+// Rows of each lane group for one token, loaded at once: a query row is the lighter work.
+constexpr int kIterQ = 8, kIterKV = 4;
 
 // s + e of a and b with the rounding error kept (any order of magnitudes).
 __device__ __forceinline__ void two_sum(float& s, float& e, float b) {
@@ -174,6 +175,7 @@ template <typename T, int D, bool INTER, int KIND>
 __device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int heads, int first, int step) {
   constexpr int LPR = D / 8, RPW = 32 / LPR;
   constexpr bool PAIRED = KIND == kQuery && !INTER;
+  constexpr int ITER = KIND == kQuery ? kIterQ : kIterKV;
   const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
   const float nan = __int_as_float(0x7fc00000);
   const int half = p.rot / 2;
@@ -212,9 +214,9 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int h
         }
       }
     };
-    uint2 w[kIter][2] = {};
+    uint2 w[ITER][2] = {};
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) load(i * RPW, w[i][0], w[i][1]);
+    for (int i = 0; i < ITER; ++i) load(i * RPW, w[i][0], w[i][1]);
     const int slot = p.slot ? __ldg(p.slot + tok) : 0;
     if (p.slot && (slot < 0 || slot >= p.slots)) continue;  // padding: nothing of it is written
     bool far = false, turn = false;
@@ -249,7 +251,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int h
     }
     T* to = out ? out + ((size_t)tok * H + h0 + sub) * D : nullptr;
 #pragma unroll
-    for (int i = 0; i < kIter; ++i) {
+    for (int i = 0; i < ITER; ++i) {
       const int h = i * RPW;
       if (h >= heads) break;
       float x[8];
@@ -317,11 +319,11 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int h
   }
 }
 
-// blockIdx.y: a group of up to kGroup head rows of one kind, keys first (they take longest), then
+// blockIdx.y: a group of head rows of one kind, keys first (they take longest), then
 // values, then queries; a warp takes one token of it at a time.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams p) {
-  constexpr int GROUP = kIter * 32 / (D / 8);
+  constexpr int GROUP = kIterKV * 32 / (D / 8), GROUPQ = kIterQ * 32 / (D / 8);
   const int first = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), step = gridDim.x * (kThreads / 32);
   int j = blockIdx.y;
   if (j < p.kv_items) {
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const AppendParams 
     append_rows<T, D, INTER, kValue>(p, j * GROUP, min(GROUP, p.Hkv - j * GROUP), first, step);
   } else {
     j -= p.kv_items;
-    append_rows<T, D, INTER, kQuery>(p, j * GROUP, min(GROUP, p.Hq - j * GROUP), first, step);
+    append_rows<T, D, INTER, kQuery>(p, j * GROUPQ, min(GROUPQ, p.Hq - j * GROUPQ), first, step);
   }
 }
 
@@ -343,8 +345,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 template <typename T, int D>
 void launch(AppendParams& p, cudaStream_t s) {
-  constexpr int GROUP = kIter * 32 / (D / 8);
-  p.q_items = p.q ? (p.Hq + GROUP - 1) / GROUP : 0;
+  constexpr int GROUP = kIterKV * 32 / (D / 8), GROUPQ = kIterQ * 32 / (D / 8);
+  p.q_items = p.q ? (p.Hq + GROUPQ - 1) / GROUPQ : 0;
   p.kv_items = p.k ? (p.Hkv + GROUP - 1) / GROUP : 0;
   // a token per warp up to eight waves of CTAs, so that the kinds' unequal times even out
   const long long y = p.q_items + 2LL * p.kv_items, want = (p.N + kThreads / 32 - 1) / (kThreads / 32);
