@@ -9,18 +9,19 @@
 // contiguous ranges; an item cut between CTAs leaves fp32 partials that
 // attend_join_kernel merges.
 //
-// Warps (512 threads, one CTA per SM): two softmax groups of four warps, one per Q tile,
+// Warps (448 threads, one CTA per SM): two softmax groups of four warps, one per Q tile,
 // a thread to a row; four warps that turn codes into fp16 tiles; one that issues every
 // MMA; one that fetches the codes (bulk copies, a run of 16 keys each).  The MMA order
 // per key tile is P.V and the next Q.K^T of tile 0, then of tile 1, so one tile's
 // softmax runs under the other tile's MMAs, and a finished Q.K^T also says that the P.V
 // before it is finished: O may be rescaled then without a barrier of its own.
 //
-// The running reference m of a row is the maximum of the first key tile that it
-// sees; a later tile whose weights sum to at most 2^15 has none above 2^15, which fp16
-// and the fp32 sums hold, so no maximum is taken.  A tile that sums to more (or to
-// NaN) makes its row take the tile's maximum as m and rescale O.  The largest weight is
-// at least 1 throughout.
+// A softmax thread takes its row's scores 32 at a time and writes the weights over columns
+// that it has read.  The running reference m of a row is the maximum of the first 32 scores
+// with a visible key; a later 32 whose weights sum to at most 2^15 have none above 2^15,
+// which fp16 and the fp32 sums hold, so no maximum is taken.  Where they sum to more (or to
+// infinity or NaN, as they do at the start) the row takes their maximum as m and rescales what
+// it has: the tile's earlier weights, l and O.  The largest weight is at least 1 throughout.
 //
 // What bounds it: 4 D flops per (row, key) on the tensor cores; the exponentials
 // (one per row and key) and the conversion of codes run beside them.
@@ -38,24 +39,13 @@ namespace {
 
 constexpr int kRows = 128;             // rows of a Q tile, lanes of TMEM
 constexpr int kKeys = 128;             // keys of a tile
-constexpr int kThreads = 16 * 32;
+constexpr int kThreads = 14 * 32;
 constexpr int kReg = 128 * 128;        // a 128-row x 128-byte swizzled region
 constexpr int kRaw = 3;                // raw half tiles (K or V codes and scales) in flight
 constexpr float kNone = -3e38f;        // m of a row that has seen no key
 constexpr float kSumBound = 32768.f;
 
 constexpr uint32_t kTmS = 0, kTmO = 256;  // S of tile t at 128 t, O at 256 + 128 t
-
-// Registers per thread: 128 at launch, then 176 for the softmax groups (a row's weights
-// stay in registers), 96 for the conversion and 64 for the rest: 4 x 128 = 2 x 176 + 96 + 64.
-template <int N>
-__device__ __forceinline__ void more_regs() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_regs() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 template <int D>
 struct Cfg {
@@ -81,7 +71,7 @@ struct Bars {
   uint64_t drain;
   uint32_t tmem;
   volatile int abort;
-  long long total, ctas;
+  long long total, ctas, from, to;  // the line's length and CTAs; this CTA's range of it
   int start[3];      // sequence, KV head, query tile of the CTA's first key tile
   int start_tile;
   uint32_t raw_valid[4];  // bit i: keys 16 i .. of the tile are on a page, by tile & 3
@@ -137,7 +127,7 @@ __device__ __forceinline__ void enter_seq(const AttendParams& p, Piece& c) {
 }
 
 // The CTA's next piece, `left` key tiles remaining from it on.
-__device__ __forceinline__ void next_piece(const AttendParams& p, Piece& c, long long left) {
+__device__ __forceinline__ void next_piece(const AttendParams& p, Piece& c, int left) {
   if (++c.qt >= c.qtiles) {
     c.qt = 0;
     if (++c.h >= p.Hkv) {
@@ -150,7 +140,7 @@ __device__ __forceinline__ void next_piece(const AttendParams& p, Piece& c, long
   }
   c.tile = 0;
   enter_item(p, c);
-  c.end = (int)min((long long)c.tiles, left);
+  c.end = min(c.tiles, left);
 }
 
 template <typename T, int D>
@@ -219,12 +209,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     for (int base = 0; base < p.B; base += 32)
       total += p.Hkv * __shfl_sync(~0u, scan(lane_tiles(base)), 31);
     const long long ctas = min(total, (long long)gridDim.x);
+    const bool busy = (long long)blockIdx.x < ctas;
+    const long long from = busy ? total * blockIdx.x / ctas : 0, to = busy ? total * (blockIdx.x + 1) / ctas : 0;
     if (lane == 0) {
       bars->total = total;
       bars->ctas = ctas;
+      bars->from = from;
+      bars->to = to;
     }
-    if ((long long)blockIdx.x < ctas) {
-      long long at = total * blockIdx.x / ctas, w = 0;
+    if (busy) {
+      long long at = from, w = 0;
       int b = 0;
       for (int base = 0;; base += 32) {
         const long long own = lane_tiles(base), sum = scan(own);
@@ -267,18 +261,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   tc::fence_after_sync();
   griddep_launch_dependents();
   const uint32_t tmem = bars->tmem;
-  const long long total = bars->total, ctas = bars->ctas;
-  long long left = 0;  // key tiles of this CTA from the current piece on
+  int left = (int)(bars->to - bars->from);  // key tiles of this CTA from the current piece on
   Piece c = {};
-  if ((long long)blockIdx.x < ctas) {
-    left = total * (blockIdx.x + 1) / ctas - total * blockIdx.x / ctas;
+  if (left > 0) {
     c.b = bars->start[0];
     c.h = bars->start[1];
     c.qt = bars->start[2];
     enter_seq(p, c);
     enter_item(p, c);
     c.tile = bars->start_tile;
-    c.end = (int)min((long long)c.tiles, c.tile + left);
+    c.end = min(c.tiles, c.tile + left);
   }
   auto advance = [&]() {  // to the next piece; false behind the last
     left -= c.end - c.tile;
@@ -289,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
 
   if (left > 0) {
     if (warp < 8) {
-      more_regs<176>();
       // ================================================================ softmax
       const int t = warp >> 2, quarter = warp & 3, row = quarter * 32 + lane;
       const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
@@ -301,50 +292,55 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       // Q of piece c's row into shared memory, as fp16; returns the scale of its scores
       auto load_q = [&]() {
         const int pr = c.qt * 2 * kRows + t * kRows + row;
-        uint4 w[D / 8];
-        float unscale = 1.0f;
-        if (pr <= c.last) {
-          const int tok = pr / G;
-          const uint4* src = reinterpret_cast<const uint4*>(
-              static_cast<const T*>(p.q) + (size_t)(c.row0 + tok) * p.q_stride +
-              (size_t)(c.h * G + pr - tok * G) * D);
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) w[i] = __ldg(src + i);
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) w[i] = make_uint4(0, 0, 0, 0);
-        }
+        const bool some = pr <= c.last;
+        const int tok = some ? pr / G : 0;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            static_cast<const T*>(p.q) + (size_t)(c.row0 + tok) * p.q_stride +
+            (size_t)(c.h * G + (some ? pr - tok * G : 0)) * D);
+        // the row twice (the second time from L1), eight 16-byte pieces in flight
+        float unscale = 1.0f, up = 1.0f;
         if constexpr (DT<T>::code == DKV_BF16) {
           float top = 0.f;
+#pragma unroll 1
+          for (int i0 = 0; i0 < D / 8; i0 += 8) {
+            uint4 w[8];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            for (int i = 0; i < 8; ++i) w[i] = some ? __ldg(src + i0 + i) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float2 f = DT<T>::to_f2(u[k]);
-              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = DT<T>::to_f2(u[k]);
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
             }
           }
           int e = (int)(__float_as_uint(top) >> 23) - 127;  // the largest goes to [2^13, 2^14)
           e = top > 0.f && top <= FLT_MAX ? max(e, -113) : 13;
-          const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+          up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
           unscale = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
+        }
+        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // the scale's sign goes to q
+#pragma unroll 1
+        for (int i0 = 0; i0 < D / 8; i0 += 8) {
+          uint4 w[8];
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
+          for (int i = 0; i < 8; ++i) w[i] = some ? __ldg(src + i0 + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
             uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float2 f = DT<T>::to_f2(u[k]);
-              u[k] = tc::pack2<__half>(f.x * up, f.y * up);
+              if constexpr (DT<T>::code == DKV_BF16) {
+                const float2 f = DT<T>::to_f2(u[k]);
+                u[k] = tc::pack2<__half>(f.x * up, f.y * up);
+              }
+              u[k] ^= sign;
             }
-            w[i] = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(qs + swz(row, i0 + i)) = make_uint4(u[0], u[1], u[2], u[3]);
           }
         }
-        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // the scale's sign goes to q
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          *reinterpret_cast<uint4*>(qs + swz(row, i)) =
-              make_uint4(w[i].x ^ sign, w[i].y ^ sign, w[i].z ^ sign, w[i].w ^ sign);
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->q_ready[t]);
@@ -361,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         const int vis = mine ? max(0, c.kv - c.n + pr / G + 1) : 0;
         const bool starts = c.tile == 0, ends = c.end == c.tiles;
         const int h = c.h, row0 = c.row0, first = c.qt * 2 * kRows, last = c.last, b_tiles = c.tiles;
-        const long long at = total * (blockIdx.x + 1) / ctas - left;
+        const long long at = bars->to - left;
         float m = kNone, l = 0.f;
         if (on) {
 #pragma unroll 1
@@ -376,31 +372,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             const uint32_t valid = bars->raw_valid[(all_tiles + tile - c.tile) & 3];
             const bool edge = k0 + kKeys > c.minvis || valid != 0xFFu;
             const int nvis = vis - k0;  // keys [0, nvis) of the tile are seen, where on a page
-            auto seen = [&](int k) { return k < nvis && ((valid >> (k >> 4)) & 1); };
-            // the tile's maximum, for a first reference and the rare raise
-            auto tile_max = [&](auto masked) {
-              float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-              for (int pc = 0; pc < kKeys / 32; ++pc) {
-                uint32_t r[32];
-                tc::tmem_ld32(ts + pc * 32, r);
-                tc::tmem_wait_ld();
+            for (int pc = 0; pc < kKeys / 32; ++pc) {
+              uint32_t r[32], w[16];
+              tc::tmem_ld32(ts + pc * 32, r);
+              tc::tmem_wait_ld();
+              if (edge) {
+                const int n = nvis - pc * 32;
+                uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
+                if (!((valid >> (2 * pc)) & 1)) see &= 0xFFFF0000u;
+                if (!((valid >> (2 * pc)) & 2)) see &= 0x0000FFFFu;
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                  if (!masked || seen(pc * 32 + k)) x[k & 3] = fmaxf(x[k & 3], __uint_as_float(r[k]));
+                  if (!((see >> k) & 1)) r[k] = 0xFF800000u;  // -infinity
               }
-              return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl;
-            };
-            uint32_t w[kKeys / 2];
-            float sum;
-            auto weights = [&](auto masked) {
-              const unsigned long long sl2 = tc::f2_pack(sl, sl), nm2 = tc::f2_pack(-m, -m);
-              unsigned long long acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-              for (int pc = 0; pc < kKeys / 32; ++pc) {
-                uint32_t r[32];
-                tc::tmem_ld32(ts + pc * 32, r);
-                tc::tmem_wait_ld();
+              float sum;
+              auto weights = [&]() {
+                const unsigned long long sl2 = tc::f2_pack(sl, sl), nm2 = tc::f2_pack(-m, -m);
+                unsigned long long acc[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                   float p0, p1;
@@ -409,44 +398,54 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                                 p0, p1);
                   p0 = tc::ex2_approx(p0);
                   p1 = tc::ex2_approx(p1);
-                  if constexpr (masked) {
-                    const int k = pc * 32 + 2 * e;
-                    p0 = seen(k) ? p0 : 0.f;
-                    p1 = seen(k + 1) ? p1 : 0.f;
-                  }
-                  w[pc * 16 + e] = tc::pack2<__half>(p0, p1);
+                  w[e] = tc::pack2<__half>(p0, p1);
                   acc[e & 3] = tc::f2_add(acc[e & 3], tc::f2_pack(p0, p1));
                 }
-              }
-              float s8[8];
+                float s8[8];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) tc::f2_unpack(acc[q], s8[2 * q], s8[2 * q + 1]);
-              sum = ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
-            };
-            if (tile == c.tile) m = fmaxf(m, edge ? tile_max(Yes()) : tile_max(No()));
-            if (edge) weights(Yes()); else weights(No());
-            const bool raise = tile != c.tile && !(sum <= kSumBound);
-            if (__any_sync(~0u, raise)) {
-              const float x = edge ? tile_max(Yes()) : tile_max(No());
-              const float nm = raise ? fmaxf(m, x) : m;
-              const float f = nm == m ? 1.0f : exp2f(m - nm);
-              m = nm;
-              l *= f;
+                for (int q = 0; q < 4; ++q) tc::f2_unpack(acc[q], s8[2 * q], s8[2 * q + 1]);
+                sum = ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
+              };
 #pragma unroll 1
-              for (int pc = 0; pc < D / 32; ++pc) {
-                uint32_t r[32];
-                tc::tmem_ld32(to + pc * 32, r);
-                tc::tmem_wait_ld();
+              for (int again = 0; again < 2; ++again) {
+                weights();
+                const bool raise = !(sum <= kSumBound);
+                if (again || !__any_sync(~0u, raise)) break;
+                float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * f);
-                tc::tmem_st32(to + pc * 32, r);
+                for (int k = 0; k < 32; ++k) x[k & 3] = fmaxf(x[k & 3], __uint_as_float(r[k]));
+                const float nm = raise ? fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl) : m;
+                const float f = nm == m ? 1.0f : exp2f(m - nm);
+                m = nm;
+                l *= f;
+                tc::tmem_wait_st();
+#pragma unroll 1
+                for (int q = 0; q < pc; ++q) {  // this tile's weights so far
+                  uint32_t v[16];
+                  tc::tmem_ld16(ts + q * 16, v);
+                  tc::tmem_wait_ld();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) {
+                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&v[e]));
+                    v[e] = tc::pack2<__half>(y.x * f, y.y * f);
+                  }
+                  tc::tmem_st16(ts + q * 16, v);
+                }
+                if (tile != c.tile) {  // O of the tiles before: their P.V finished before this S
+#pragma unroll 1
+                  for (int q = 0; q < D / 16; ++q) {
+                    uint32_t v[16];
+                    tc::tmem_ld16(to + q * 16, v);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                    tc::tmem_st16(to + q * 16, v);
+                  }
+                }
               }
-              tc::tmem_wait_st();
-              if (edge) weights(Yes()); else weights(No());
+              l += sum;
+              tc::tmem_st16(ts + pc * 16, w);
             }
-            l += sum;
-            tc::tmem_st32(ts, *reinterpret_cast<uint32_t(*)[32]>(w));
-            tc::tmem_st32(ts + 32, *reinterpret_cast<uint32_t(*)[32]>(w + 32));
             tc::tmem_wait_st();
             tc::fence_before_sync();
             __syncwarp();
@@ -521,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           if (starts && !ends && threadIdx.x == 0) {
             AttendDesc d;
             const long long end = at + b_tiles - 1;  // the item's last key tile, and the CTA that holds it
-            d.pieces = (int)(((end + 1) * ctas - 1) / total) - (int)blockIdx.x + 1;
+            d.pieces = (int)(((end + 1) * bars->ctas - 1) / bars->total) - (int)blockIdx.x + 1;
             d.row0 = row0; d.first = first; d.last = last; d.head0 = h * G;
             p.desc[blockIdx.x] = d;
           }
@@ -529,7 +528,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         sl = next_sl;
       }
     } else if (warp < 12) {
-      fewer_regs<96>();
       // ================================================== codes to fp16 tiles
       const int tid = threadIdx.x - 256;
       uint32_t half = 0, tiles = 0, items = 0;  // half tiles, tiles and items so far
@@ -593,9 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         ++items;
         go = advance();
       }
-    } else {
-     fewer_regs<64>();
-     if (warp == 12) {
+    } else if (warp == 12) {
       // ==================================================================== MMA
       if (lane == 0) {
         const uint32_t idesc_s = tc::idesc_f16(false, 128, kKeys, false, false);
@@ -678,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         tc::mma_commit(&bars->drain);
         mbar_wait_drain(&bars->drain, 0);
       }
-     } else if (warp == 13) {
+    } else if (warp == 13) {
       // ================================================================= loader
       uint32_t half = 0, tiles = 0;
       const int sub = (lane >> 1) & 7, scales = lane & 1;
@@ -725,7 +721,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           mbar_wait_drain(&bars->raw_full[i], 0);
           mbar_wait_drain(&bars->raw_full[i], 1);
         }
-     }
     }
   }
   __syncwarp();
