@@ -9,7 +9,7 @@
 // contiguous ranges; an item cut between CTAs leaves fp32 partials that
 // attend_join_kernel merges.
 //
-// Warps (448 threads, one CTA per SM): two softmax groups of four warps, one per Q tile,
+// Warps (512 threads, one CTA per SM): two softmax groups of four warps, one per Q tile,
 // a thread to a row; four warps that turn codes into fp16 tiles; one that issues every
 // MMA; one that fetches the codes (bulk copies, a run of 16 keys each).  The MMA order
 // per key tile is P.V and the next Q.K^T of tile 0, then of tile 1, so one tile's
@@ -46,6 +46,17 @@ constexpr float kNone = -3e38f;        // m of a row that has seen no key
 constexpr float kSumBound = 32768.f;
 
 constexpr uint32_t kTmS = 0, kTmO = 256;  // S of tile t at 128 t, O at 256 + 128 t
+
+// Registers per thread: 128 at launch, then 168 for the softmax groups, 96 for the conversion
+// and 80 for the last four warps: 4 x 128 = 2 x 168 + 96 + 80.
+template <int N>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <int D>
 struct Cfg {
@@ -93,6 +104,26 @@ __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* bars)
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, Bars* bars) {
   return __all_sync(~0u, wait(bar, parity, bars));
+}
+
+// The weights 2^(s sl - m) of 32 scores as fp16 pairs, and their fp32 sum.
+__device__ __forceinline__ float weights(const uint32_t (&r)[32], uint32_t (&w)[16], float sl, float m) {
+  const unsigned long long sl2 = tc::f2_pack(sl, sl), nm2 = tc::f2_pack(-m, -m);
+  unsigned long long acc[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    float p0, p1;
+    tc::f2_unpack(tc::f2_fma(tc::f2_pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])), sl2, nm2),
+                  p0, p1);
+    p0 = tc::ex2_approx(p0);
+    p1 = tc::ex2_approx(p1);
+    w[e] = tc::pack2<__half>(p0, p1);
+    acc[e & 3] = tc::f2_add(acc[e & 3], tc::f2_pack(p0, p1));
+  }
+  float s8[8];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) tc::f2_unpack(acc[q], s8[2 * q], s8[2 * q + 1]);
+  return ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
 }
 
 __device__ __forceinline__ int swz(int row, int cc) {
@@ -289,56 +320,53 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       uint32_t tiles_done = 0, items_done = 0;  // of this Q tile
       uint32_t items = 0, all_tiles = 0;        // of the CTA
       bool dead = false;
-      // Q of piece c's row into shared memory, as fp16; returns the scale of its scores
+      // Q of piece c's rows of this warp into shared memory, as fp16: D/8 lanes read a row, so
+      // that a load covers whole lines; returns the scale of the scores of this thread's row
       auto load_q = [&]() {
-        const int pr = c.qt * 2 * kRows + t * kRows + row;
-        const bool some = pr <= c.last;
-        const int tok = some ? pr / G : 0;
-        const uint4* src = reinterpret_cast<const uint4*>(
-            static_cast<const T*>(p.q) + (size_t)(c.row0 + tok) * p.q_stride +
-            (size_t)(c.h * G + (some ? pr - tok * G : 0)) * D);
-        // the row twice (the second time from L1), eight 16-byte pieces in flight
-        float unscale = 1.0f, up = 1.0f;
-        if constexpr (DT<T>::code == DKV_BF16) {
-          float top = 0.f;
+        constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes per row, rows per load
+        constexpr int STEP = 8;                     // loads in flight
+        const int l = lane % LPR, sub = lane / LPR, base = c.qt * 2 * kRows + t * kRows + quarter * 32;
+        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // the scale's sign goes to q
+        float unscale = 1.0f;
 #pragma unroll 1
-          for (int i0 = 0; i0 < D / 8; i0 += 8) {
-            uint4 w[8];
+        for (int i0 = 0; i0 < 32 / RPI; i0 += STEP) {
+          uint4 w[STEP];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = some ? __ldg(src + i0 + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 f = DT<T>::to_f2(u[k]);
-                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-              }
+          for (int i = 0; i < STEP; ++i) {
+            const int pr = base + (i0 + i) * RPI + sub;
+            w[i] = make_uint4(0, 0, 0, 0);
+            if (pr <= c.last) {
+              const int tok = pr / G;
+              w[i] = __ldg(reinterpret_cast<const uint4*>(
+                               static_cast<const T*>(p.q) + (size_t)(c.row0 + tok) * p.q_stride +
+                               (size_t)(c.h * G + pr - tok * G) * D) + l);
             }
           }
-          int e = (int)(__float_as_uint(top) >> 23) - 127;  // the largest goes to [2^13, 2^14)
-          e = top > 0.f && top <= FLT_MAX ? max(e, -113) : 13;
-          up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
-          unscale = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
-        }
-        const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // the scale's sign goes to q
-#pragma unroll 1
-        for (int i0 = 0; i0 < D / 8; i0 += 8) {
-          uint4 w[8];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) w[i] = some ? __ldg(src + i0 + i) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
+          for (int i = 0; i < STEP; ++i) {
             uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            if constexpr (DT<T>::code == DKV_BF16) {
+              float f[8], top = 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if constexpr (DT<T>::code == DKV_BF16) {
-                const float2 f = DT<T>::to_f2(u[k]);
-                u[k] = tc::pack2<__half>(f.x * up, f.y * up);
+              for (int k = 0; k < 4; ++k) {
+                const float2 y = DT<T>::to_f2(u[k]);
+                f[2 * k] = y.x;
+                f[2 * k + 1] = y.y;
+                top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
               }
-              u[k] ^= sign;
+#pragma unroll
+              for (int d = 1; d < LPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+              int e = (int)(__float_as_uint(top) >> 23) - 127;  // the largest goes to [2^13, 2^14)
+              e = top > 0.f && top <= FLT_MAX ? max(e, -113) : 13;
+              const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
+              // to the thread whose row this is
+              const int back = __shfl_sync(~0u, e, (lane % RPI) * LPR);
+              if (lane / RPI == i0 + i) unscale = __uint_as_float((uint32_t)(127 - 13 + back) << 23);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) u[k] = tc::pack2<__half>(f[2 * k] * up, f[2 * k + 1] * up);
             }
-            *reinterpret_cast<uint4*>(qs + swz(row, i0 + i)) = make_uint4(u[0], u[1], u[2], u[3]);
+            *reinterpret_cast<uint4*>(qs + swz(quarter * 32 + (i0 + i) * RPI + sub, l)) =
+                make_uint4(u[0] ^ sign, u[1] ^ sign, u[2] ^ sign, u[3] ^ sign);
           }
         }
         tc::fence_proxy_async_smem();
@@ -358,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         const bool starts = c.tile == 0, ends = c.end == c.tiles;
         const int h = c.h, row0 = c.row0, first = c.qt * 2 * kRows, last = c.last, b_tiles = c.tiles;
         const long long at = bars->to - left;
-        float m = kNone, l = 0.f;
+        float m = mine ? kNone : 0.f, l = 0.f;
         if (on) {
 #pragma unroll 1
           for (int tile = c.tile; tile < c.end; ++tile, ++tiles_done) {
@@ -372,11 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             const uint32_t valid = bars->raw_valid[(all_tiles + tile - c.tile) & 3];
             const bool edge = k0 + kKeys > c.minvis || valid != 0xFFu;
             const int nvis = vis - k0;  // keys [0, nvis) of the tile are seen, where on a page
-#pragma unroll 1
-            for (int pc = 0; pc < kKeys / 32; ++pc) {
-              uint32_t r[32], w[16];
-              tc::tmem_ld32(ts + pc * 32, r);
-              tc::tmem_wait_ld();
+            auto chunk = [&](int pc, uint32_t (&r)[32]) {
               if (edge) {
                 const int n = nvis - pc * 32;
                 uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
@@ -386,31 +410,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                 for (int k = 0; k < 32; ++k)
                   if (!((see >> k) & 1)) r[k] = 0xFF800000u;  // -infinity
               }
+              uint32_t w[16];
               float sum;
-              auto weights = [&]() {
-                const unsigned long long sl2 = tc::f2_pack(sl, sl), nm2 = tc::f2_pack(-m, -m);
-                unsigned long long acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  float p0, p1;
-                  tc::f2_unpack(tc::f2_fma(tc::f2_pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])),
-                                           sl2, nm2),
-                                p0, p1);
-                  p0 = tc::ex2_approx(p0);
-                  p1 = tc::ex2_approx(p1);
-                  w[e] = tc::pack2<__half>(p0, p1);
-                  acc[e & 3] = tc::f2_add(acc[e & 3], tc::f2_pack(p0, p1));
-                }
-                float s8[8];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tc::f2_unpack(acc[q], s8[2 * q], s8[2 * q + 1]);
-                sum = ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
-              };
 #pragma unroll 1
-              for (int again = 0; again < 2; ++again) {
-                weights();
-                const bool raise = !(sum <= kSumBound);
-                if (again || !__any_sync(~0u, raise)) break;
+              for (int again = 0;; ++again) {
+                sum = weights(r, w, sl, m);
+                const bool raise = m == kNone || !(sum <= kSumBound);
+                if (again) {  // above its own maximum: an infinity or a NaN is among the scores
+                  if (!(sum <= kSumBound)) sum = __int_as_float(0x7fc00000);
+                  break;
+                }
+                if (!__any_sync(~0u, raise)) break;
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k & 3] = fmaxf(x[k & 3], __uint_as_float(r[k]));
@@ -445,6 +455,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
               }
               l += sum;
               tc::tmem_st16(ts + pc * 16, w);
+            };
+#pragma unroll 1
+            for (int pc = 0; pc < kKeys / 32; ++pc) {
+              uint32_t ra[32];
+              tc::tmem_ld32(ts + pc * 32, ra);
+              tc::tmem_wait_ld();
+              chunk(pc, ra);
             }
             tc::tmem_wait_st();
             tc::fence_before_sync();
@@ -466,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           tc::fence_after_sync();
           const bool whole = starts && ends;
           const float bad = __int_as_float(0x7fc00000);
+          if (m == kNone && l == l) l = 0.f;  // no key of the piece is seen
           const float inv = dead ? bad : whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.0f;
           const int tok = pr / G;
           const size_t orow = (size_t)(row0 + tok) * p.Hq + h * G + (pr - tok * G);
@@ -566,18 +584,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
               }
               const uint32_t s2 = e2m1::scales_to_h2(sb);
               const uint32_t sc[2] = {__byte_perm(s2, 0, 0x1010), __byte_perm(s2, 0, 0x3232)};
-              const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+              // The pieces of a row's upper half write their words in another order, so that the
+              // eight lanes of one phase of a store hit eight different bank groups.
+              const bool flip = PPR == 4 && part >= 2;
+              const uint32_t w[4] = {flip ? w4.z : w4.x, flip ? w4.w : w4.y, flip ? w4.x : w4.z, flip ? w4.y : w4.w};
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 uint32_t x[4];
                 e2m1::codes_to_h2(w[k], x);
-                const __half2 s = *reinterpret_cast<const __half2*>(&sc[k / 2]);
+                const uint32_t sk = flip ? sc[1 - k / 2] : sc[k / 2];
+                const __half2 s = *reinterpret_cast<const __half2*>(&sk);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x[e]), s);
                   x[e] = *reinterpret_cast<const uint32_t*>(&y);
                 }
-                *reinterpret_cast<uint4*>(dst + swz(r, part * 4 + k)) = make_uint4(x[0], x[1], x[2], x[3]);
+                *reinterpret_cast<uint4*>(dst + swz(r, part * 4 + (flip ? k ^ 2 : k))) =
+                    make_uint4(x[0], x[1], x[2], x[3]);
               }
             }
             tc::fence_proxy_async_smem();
@@ -591,27 +614,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         ++items;
         go = advance();
       }
-    } else if (warp == 12) {
+    } else {
+     if (warp == 12) {
       // ==================================================================== MMA
       if (lane == 0) {
         const uint32_t idesc_s = tc::idesc_f16(false, 128, kKeys, false, false);
         const uint32_t idesc_o = tc::idesc_f16(false, 128, D, false, true);
         const uint32_t base = smem_u32(smem);
         uint32_t np[2] = {0, 0}, nq[2] = {0, 0}, no[2] = {0, 0};  // phases waited for, per Q tile
+        // Descriptors differ in their address field alone (16-byte units, low word): one add each.
+        const uint64_t d0 = tc::sdesc_sw128(base, 16, 1024), dv0 = tc::sdesc_sw128(base + C::kOffV, kReg, 1024);
         auto qk = [&](int t, uint32_t st) {
-          const uint32_t qa = base + C::kOffQ + t * C::kTileB, ka = base + C::kOffK + st * C::kTileB;
+          const uint64_t dq = d0 + ((C::kOffQ + t * C::kTileB) >> 4), dk = d0 + ((C::kOffK + st * C::kTileB) >> 4);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_ss(tmem + kTmS + 128 * t, tc::sdesc_sw128(qa + (kk / 4) * kReg + (kk % 4) * 32, 16, 1024),
-                       tc::sdesc_sw128(ka + (kk / 4) * kReg + (kk % 4) * 32, 16, 1024), idesc_s, kk != 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t at = ((kk / 4) * kReg + (kk % 4) * 32) >> 4;
+            tc::mma_ss(tmem + kTmS + 128 * t, dq + at, dk + at, idesc_s, kk != 0);
+          }
           tc::mma_commit(&bars->s_full[t]);
         };
         auto pv = [&](int t, uint32_t st, bool fresh) {
-          const uint32_t va = base + C::kOffV + st * C::kTileB;
+          const uint64_t dv = dv0 + ((st * C::kTileB) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc::mma_ts(tmem + kTmO + 128 * t, tmem + kTmS + 128 * t + kk * 8,
-                       tc::sdesc_sw128(va + kk * 2048, kReg, 1024), idesc_o, !(fresh && kk == 0));
+            tc::mma_ts(tmem + kTmO + 128 * t, tmem + kTmS + 128 * t + kk * 8, dv + (kk * 2048 >> 4), idesc_o,
+                       !(fresh && kk == 0));
         };
         // the piece of the current tile (cur) and of the next one (c runs one tile ahead)
         uint32_t j = 0;  // tile
@@ -674,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         tc::mma_commit(&bars->drain);
         mbar_wait_drain(&bars->drain, 0);
       }
-    } else if (warp == 13) {
+     } else if (warp == 13) {
       // ================================================================= loader
       uint32_t half = 0, tiles = 0;
       const int sub = (lane >> 1) & 7, scales = lane & 1;
@@ -721,6 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           mbar_wait_drain(&bars->raw_full[i], 0);
           mbar_wait_drain(&bars->raw_full[i], 1);
         }
+     }
     }
   }
   __syncwarp();
