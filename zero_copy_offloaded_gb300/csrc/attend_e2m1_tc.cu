@@ -617,7 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     } else {
      if (warp == 12) {
       // ==================================================================== MMA
-      if (lane == 0) {
+      {
+        const uint32_t one = tc::elect_one();
         const uint32_t idesc_s = tc::idesc_f16(false, 128, kKeys, false, false);
         const uint32_t idesc_o = tc::idesc_f16(false, 128, D, false, true);
         const uint32_t base = smem_u32(smem);
@@ -629,28 +630,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t at = ((kk / 4) * kReg + (kk % 4) * 32) >> 4;
-            tc::mma_ss(tmem + kTmS + 128 * t, dq + at, dk + at, idesc_s, kk != 0);
+            tc::mma_ss_one(tmem + kTmS + 128 * t, dq + at, dk + at, idesc_s, kk != 0, one);
           }
-          tc::mma_commit(&bars->s_full[t]);
+          if (one) tc::mma_commit(&bars->s_full[t]);
         };
         auto pv = [&](int t, uint32_t st, bool fresh) {
           const uint64_t dv = dv0 + ((st * C::kTileB) >> 4);
 #pragma unroll
           for (int kk = 0; kk < kKeys / 16; ++kk)
-            tc::mma_ts(tmem + kTmO + 128 * t, tmem + kTmS + 128 * t + kk * 8, dv + (kk * 2048 >> 4), idesc_o,
-                       !(fresh && kk == 0));
+            tc::mma_ts_one(tmem + kTmO + 128 * t, tmem + kTmS + 128 * t + kk * 8, dv + (kk * 2048 >> 4), idesc_o,
+                           !(fresh && kk == 0), one);
         };
         // the piece of the current tile (cur) and of the next one (c runs one tile ahead)
         uint32_t j = 0;  // tile
         bool two = c.last >= c.qt * 2 * kRows + kRows, fresh = true, ok = true;
         int at = c.tile, end = c.end;
-        ok = wait(&bars->k_full[0], 0, bars);
+        ok = warp_wait(&bars->k_full[0], 0, bars);
         for (int t = 0; ok && t < 1 + two; ++t) {
-          ok = wait(&bars->q_ready[t], nq[t]++ & 1, bars);
+          ok = warp_wait(&bars->q_ready[t], nq[t]++ & 1, bars);
           tc::fence_after_sync();
           if (ok) qk(t, 0);
         }
-        if (ok) tc::mma_commit(&bars->k_empty[0]);
+        if (ok) if (one) tc::mma_commit(&bars->k_empty[0]);
         while (ok) {
           const bool final_tile = at + 1 == end;  // of the piece
           bool more = true, next_two = two;
@@ -659,25 +660,25 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             if (more) next_two = c.last >= c.qt * 2 * kRows + kRows;
           }
           const uint32_t st = j & 1, sn = (j + 1) & 1;
-          ok = wait(&bars->v_full[st], (j >> 1) & 1, bars);
-          if (ok && more) ok = wait(&bars->k_full[sn], ((j + 1) >> 1) & 1, bars);
+          ok = warp_wait(&bars->v_full[st], (j >> 1) & 1, bars);
+          if (ok && more) ok = warp_wait(&bars->k_full[sn], ((j + 1) >> 1) & 1, bars);
           for (int t = 0; ok && t < 2; ++t) {
             if (t == 0 || two) {
-              ok = wait(&bars->p_ready[t], np[t]++ & 1, bars);
+              ok = warp_wait(&bars->p_ready[t], np[t]++ & 1, bars);
               // O of both tiles has been read out: neither group is more than an item behind
               for (int u = 0; u < 2 && ok && fresh; ++u)
-                if (no[u] > 0 && (u != 1 || t == 1 || !two)) ok = wait(&bars->o_free[u], (no[u] - 1) & 1, bars);
+                if (no[u] > 0 && (u != 1 || t == 1 || !two)) ok = warp_wait(&bars->o_free[u], (no[u] - 1) & 1, bars);
               if (!ok) break;
               tc::fence_after_sync();
               pv(t, st, fresh);
               if (final_tile) {
-                tc::mma_commit(&bars->o_full[t]);
+                if (one) tc::mma_commit(&bars->o_full[t]);
                 ++no[t];
               }
             }
             if (more && (t == 0 || next_two)) {
               if (final_tile) {
-                ok = wait(&bars->q_ready[t], nq[t]++ & 1, bars);
+                ok = warp_wait(&bars->q_ready[t], nq[t]++ & 1, bars);
                 if (!ok) break;
                 tc::fence_after_sync();
               }
@@ -685,8 +686,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             }
           }
           if (!ok || !more) break;
-          tc::mma_commit(&bars->v_empty[st]);
-          tc::mma_commit(&bars->k_empty[sn]);
+          if (one) tc::mma_commit(&bars->v_empty[st]);
+          if (one) tc::mma_commit(&bars->k_empty[sn]);
           ++j;
           fresh = final_tile;
           if (final_tile) {
@@ -698,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           }
         }
         // nothing may be in flight when TMEM and shared memory go
-        tc::mma_commit(&bars->drain);
+        if (one) tc::mma_commit(&bars->drain);
         mbar_wait_drain(&bars->drain, 0);
       }
      } else if (warp == 13) {
