@@ -39,7 +39,8 @@ namespace {
 
 constexpr int kRows = 128;             // rows of a Q tile, lanes of TMEM
 constexpr int kKeys = 128;             // keys of a tile
-constexpr int kThreads = 14 * 32;
+constexpr int kConvert = 6;            // warps that turn codes into fp16
+constexpr int kThreads = (10 + kConvert) * 32;
 constexpr int kReg = 128 * 128;        // a 128-row x 128-byte swizzled region
 constexpr int kRaw = 3;                // raw half tiles (K or V codes and scales) in flight
 constexpr float kNone = -3e38f;        // m of a row that has seen no key
@@ -187,12 +188,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   if (threadIdx.x == 0) {
     for (int i = 0; i < kRaw; ++i) {
       mbar_init(&bars->raw_full[i], 1);
-      mbar_init(&bars->raw_empty[i], 4);
+      mbar_init(&bars->raw_empty[i], kConvert);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->k_full[i], 4);
+      mbar_init(&bars->k_full[i], kConvert);
       mbar_init(&bars->k_empty[i], 1);
-      mbar_init(&bars->v_full[i], 4);
+      mbar_init(&bars->v_full[i], kConvert);
       mbar_init(&bars->v_empty[i], 1);
       mbar_init(&bars->q_ready[i], 4);
       mbar_init(&bars->s_full[i], 1);
@@ -206,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     p.desc[blockIdx.x].pieces = 0;
   }
   if (threadIdx.x < 32) bars->nan_key[threadIdx.x / 8][threadIdx.x % 8] = 0;
-  if (warp == 12) tc::tmem_alloc(&bars->tmem, 512);
+  if (warp == 8 + kConvert) tc::tmem_alloc(&bars->tmem, 512);
   if (warp == 0) {
     // The length of the line, then the place on it where this CTA begins.
     // Sequence b adds Hkv times the key tiles of its query tiles.
@@ -545,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         }
         sl = next_sl;
       }
-    } else if (warp < 12) {
+    } else if (warp < 8 + kConvert) {
       // ================================================== codes to fp16 tiles
       const int tid = threadIdx.x - 256;
       uint32_t half = 0, tiles = 0, items = 0;  // half tiles, tiles and items so far
@@ -562,8 +563,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             uint8_t* dst = smem + (kv ? C::kOffV : C::kOffK) + st * C::kTileB;
             constexpr int PPR = D / 32;  // 16-byte pieces of a row's codes: 32 elements each
 #pragma unroll
-            for (int i = 0; i < PPR; ++i) {
-              const int ch = i * 128 + tid, r = ch / PPR, part = ch % PPR;
+            for (int i = 0; i < (kKeys * PPR + kConvert * 32 - 1) / (kConvert * 32); ++i) {
+              const int ch = i * kConvert * 32 + tid, r = ch / PPR, part = ch % PPR;
+              if (kKeys * PPR % (kConvert * 32) && ch >= kKeys * PPR) break;
               const uint4 w4 = *reinterpret_cast<const uint4*>(raw + ch * 16);
               uint32_t sb = *reinterpret_cast<const uint16_t*>(raw + C::kCodes + r * e2m1::scale_bytes(D) + part * 2);
               const bool ok = (valid >> (r >> 4)) & 1;
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         go = advance();
       }
     } else {
-     if (warp == 12) {
+     if (warp == 8 + kConvert) {
       // ==================================================================== MMA
       {
         const uint32_t one = tc::elect_one();
@@ -702,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         if (one) tc::mma_commit(&bars->drain);
         mbar_wait_drain(&bars->drain, 0);
       }
-     } else if (warp == 13) {
+     } else if (warp == 9 + kConvert) {
       // ================================================================= loader
       uint32_t half = 0, tiles = 0;
       const int sub = (lane >> 1) & 7, scales = lane & 1;
@@ -755,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   __syncwarp();
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 12) tc::tmem_dealloc(tmem, 512);
+  if (warp == 8 + kConvert) tc::tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
