@@ -739,10 +739,7 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
 
 template <typename T, int D>
 cudaError_t launch_rows(const AttendParams& p, int R, cudaStream_t s) {
-  if (R == kTcRows) {
-    const cudaError_t e = launch_attend_tc<T, D>(p, kSms, s);
-    return e == cudaSuccess ? launch_join<T, D>(p, R, kSms, s) : e;
-  }
+  if (R == kTcRows) return launch_attend_tc<T, D>(p, kSms, s);
   return R == 8    ? launch<T, D, 1>(p, s)
          : R == 16 ? launch<T, D, 2>(p, s)
          : R == 24 ? launch<T, D, 3>(p, s)

@@ -47,7 +47,7 @@ __device__ __forceinline__ void batch_entry(const AttendParams& p, int b, int& k
   }
 }
 
-// attend_e2m1_tc.cu: items of kTcRows query rows, one CTA on each of `grid` SMs.
+// attend_e2m1_tc.cu: items of kTcRows query rows, one CTA on each of `grid` SMs, and their join.
 constexpr int kTcRows = 256;
 template <typename T, int D>
 cudaError_t launch_attend_tc(const AttendParams& p, int grid, cudaStream_t s);
@@ -59,15 +59,19 @@ __device__ __forceinline__ void store_row(const AttendParams& p, int row, int he
                                           const float (&acc)[V], float top, float sum, bool lead) {
   const float inv = sum == 0.f ? 0.f : p.v_scale / sum;
   T* o = static_cast<T*>(p.out) + ((size_t)row * p.Hq + head) * D + d0;
-  uint32_t w[V / 2];
+  uint32_t w[V / 2];  // V: 2, 4, 8 or 16
 #pragma unroll
   for (int i = 0; i < V / 2; ++i) {
     const T a = DT<T>::from_f(acc[2 * i] * inv), b = DT<T>::from_f(acc[2 * i + 1] * inv);
     w[i] = (uint32_t)(*reinterpret_cast<const uint16_t*>(&a)) |
            ((uint32_t)(*reinterpret_cast<const uint16_t*>(&b)) << 16);
   }
-  if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
-  else *reinterpret_cast<uint32_t*>(o) = w[0];
+  if constexpr (V == 2) *reinterpret_cast<uint32_t*>(o) = w[0];
+  else if constexpr (V == 4) *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+  else
+#pragma unroll
+    for (int i = 0; i < V / 8; ++i)
+      reinterpret_cast<uint4*>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
   if (lead && p.lse)
     p.lse[(size_t)row * p.Hq + head] =
         sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;

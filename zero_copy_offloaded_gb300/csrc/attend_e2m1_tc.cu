@@ -7,7 +7,7 @@
 //   O += P V   (tcgen05, P from TMEM, O in TMEM through the whole item).
 // All key tiles of all items form one line that is dealt to the CTAs in equal
 // contiguous ranges; an item cut between CTAs leaves fp32 partials that
-// attend_join_kernel merges.
+// attend_tc_join_kernel merges.
 //
 // Warps (512 threads, one CTA per SM): two softmax groups of four warps, one per Q tile,
 // a thread to a row; four warps that turn codes into fp16 tiles; one that issues every
@@ -489,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           const int tok = pr / G;
           const size_t orow = (size_t)(row0 + tok) * p.Hq + h * G + (pr - tok * G);
           T* out = static_cast<T*>(p.out) + orow * D;
-          float* po = p.part_o + ((size_t)slot * 2 * kRows + t * kRows + row) * D;
+          // partials: [slot][D / 4][256 rows][4], so that a warp's rows lie side by side
+          float4* po = reinterpret_cast<float4*>(p.part_o) + (size_t)slot * (D / 4) * kTcRows + t * kRows + row;
 #pragma unroll 1
           for (int pc = 0; pc < D / 32; ++pc) {
             uint32_t r[32];
@@ -520,8 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             } else if (mine) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<float4*>(po + pc * 32 + 4 * k) =
-                    make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+                po[(size_t)(pc * 8 + k) * kTcRows] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
             __syncwarp();
           }
@@ -760,6 +760,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   if (warp == 8 + kConvert) tc::tmem_dealloc(tmem, 512);
 }
 
+// Joins the partials of each cut item: block (c, y) takes 32 rows of the item that CTA c began and
+// left unfinished, a row to a lane, D/8 outputs to each of eight warps.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendParams p) {
+  griddep_wait();
+  const AttendDesc d = p.desc[blockIdx.x];
+  const int r = blockIdx.y * 32 + (threadIdx.x & 31), pr = d.first + r;
+  if (d.pieces < 2 || pr > d.last) return;
+  constexpr int Q = D / 32;  // groups of four outputs per thread
+  const int q0 = (threadIdx.x >> 5) * Q;
+  // piece i lies in slot 2 (c + i), but the first in slot 2 c + 1
+  auto slot = [&](int i) { return (size_t)(2 * (blockIdx.x + i) + (i == 0)); };
+  const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
+  for (int i = 0; i < d.pieces; ++i) top = fmaxf(top, ml[slot(i) * kTcRows + r].x);
+  float acc[4 * Q];
+#pragma unroll
+  for (int e = 0; e < 4 * Q; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < d.pieces; ++i) {
+    const float2 x = ml[slot(i) * kTcRows + r];
+    const float f = x.x == top ? 1.0f : exp2f(x.x - top);
+    sum = fmaf(x.y, f, sum);
+    const float4* o = reinterpret_cast<const float4*>(p.part_o) + (slot(i) * (D / 4) + q0) * kTcRows + r;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const float4 v = o[(size_t)q * kTcRows];
+      acc[4 * q] = fmaf(v.x, f, acc[4 * q]);
+      acc[4 * q + 1] = fmaf(v.y, f, acc[4 * q + 1]);
+      acc[4 * q + 2] = fmaf(v.z, f, acc[4 * q + 2]);
+      acc[4 * q + 3] = fmaf(v.w, f, acc[4 * q + 3]);
+    }
+  }
+  store_row<T, 4 * Q>(p, d.row0 + pr / p.G, d.head0 + pr % p.G, D, q0 * 4, acc, top, sum, q0 == 0);
+}
+
 }  // namespace
 
 template <typename T, int D>
@@ -768,7 +805,18 @@ cudaError_t launch_attend_tc(const AttendParams& p, int grid, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
   if (e != cudaSuccess) return e;
   k<<<grid, kThreads, Cfg<D>::kSmem, s>>>(p);
-  return cudaGetLastError();
+  const cudaError_t l = cudaGetLastError();
+  if (l != cudaSuccess) return l;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, kTcRows / 32);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_tc_join_kernel<T, D>, p);
 }
 template cudaError_t launch_attend_tc<__nv_bfloat16, 64>(const AttendParams&, int, cudaStream_t);
 template cudaError_t launch_attend_tc<__nv_bfloat16, 128>(const AttendParams&, int, cudaStream_t);
