@@ -127,6 +127,12 @@ __device__ __forceinline__ float weights(const uint32_t (&r)[32], uint32_t (&w)[
   return ((s8[0] + s8[1]) + (s8[2] + s8[3])) + ((s8[4] + s8[5]) + (s8[6] + s8[7]));
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
 __device__ __forceinline__ int swz(int row, int cc) {
   return (cc / 8) * kReg + row * 128 + (((cc % 8) ^ (row % 8)) * 16);
 }
@@ -217,10 +223,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       if (base + lane < p.B) batch_entry(p, base + lane, kv, row, n);
       const int qtiles = (n * G + 2 * kRows - 1) / (2 * kRows);
       long long w = 0;
-      if (__all_sync(~0u, qtiles <= 64)) {
+      const int seqs = min(32, p.B - base), most = __reduce_max_sync(~0u, qtiles);
+      if (most <= 2 * seqs) {
         for (int qt = 0; qt < qtiles; ++qt) w += tiles_of(kv, n, G, qt);
-      } else {  // long ones: the warp together
-        for (int i = 0; i < 32; ++i) {
+      } else {  // few long ones: the warp together
+        for (int i = 0; i < seqs; ++i) {
           const int kvi = __shfl_sync(~0u, kv, i), ni = __shfl_sync(~0u, n, i), qi = __shfl_sync(~0u, qtiles, i);
           long long wi = 0;
           for (int qt = lane; qt < qi; qt += 32) wi += tiles_of(kvi, ni, G, qt);
@@ -237,9 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       }
       return v;
     };
-    long long total = 0;
-    for (int base = 0; base < p.B; base += 32)
-      total += p.Hkv * __shfl_sync(~0u, scan(lane_tiles(base)), 31);
+    long long total = 0, own = 0, sum = 0;
+    for (int base = 0; base < p.B; base += 32) {
+      own = lane_tiles(base);
+      sum = scan(own);
+      total += p.Hkv * __shfl_sync(~0u, sum, 31);
+    }
     const long long ctas = min(total, (long long)gridDim.x);
     const bool busy = (long long)blockIdx.x < ctas;
     const long long from = busy ? total * blockIdx.x / ctas : 0, to = busy ? total * (blockIdx.x + 1) / ctas : 0;
@@ -253,7 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       long long at = from, w = 0;
       int b = 0;
       for (int base = 0;; base += 32) {
-        const long long own = lane_tiles(base), sum = scan(own);
+        if (p.B > 32) {  // else they are at hand
+          own = lane_tiles(base);
+          sum = scan(own);
+        }
         const long long whole = p.Hkv * __shfl_sync(~0u, sum, 31);
         if (at < whole) {
           const int i = __ffs(__ballot_sync(~0u, at < p.Hkv * sum)) - 1;
@@ -329,42 +342,44 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         const int l = lane % LPR, sub = lane / LPR, base = c.qt * 2 * kRows + t * kRows + quarter * 32;
         const uint32_t sign = p.scale_log2 < 0.f ? 0x80008000u : 0u;  // the scale's sign goes to q
         float unscale = 1.0f;
+        int pr = base + sub, tok = pr / G, g = pr - tok * G;  // of the next load
+        const T* q = static_cast<const T*>(p.q) + (size_t)c.row0 * p.q_stride + (size_t)c.h * G * D + l * 8;
 #pragma unroll 1
         for (int i0 = 0; i0 < 32 / RPI; i0 += STEP) {
           uint4 w[STEP];
 #pragma unroll
           for (int i = 0; i < STEP; ++i) {
-            const int pr = base + (i0 + i) * RPI + sub;
             w[i] = make_uint4(0, 0, 0, 0);
-            if (pr <= c.last) {
-              const int tok = pr / G;
-              w[i] = __ldg(reinterpret_cast<const uint4*>(
-                               static_cast<const T*>(p.q) + (size_t)(c.row0 + tok) * p.q_stride +
-                               (size_t)(c.h * G + pr - tok * G) * D) + l);
+            if (pr <= c.last) w[i] = __ldg(reinterpret_cast<const uint4*>(q + tok * p.q_stride + g * D));
+            pr += RPI;
+            g += RPI;
+            while (g >= G) {
+              g -= G;
+              ++tok;
             }
           }
 #pragma unroll
           for (int i = 0; i < STEP; ++i) {
             uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
             if constexpr (DT<T>::code == DKV_BF16) {
-              float f[8], top = 0.f;
+              // the largest magnitude, as bits of two bf16 side by side
+              uint32_t top2 = 0;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 y = DT<T>::to_f2(u[k]);
-                f[2 * k] = y.x;
-                f[2 * k + 1] = y.y;
-                top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
-              }
+              for (int k = 0; k < 4; ++k) top2 = max_u16x2(top2, u[k] & 0x7FFF7FFFu);
 #pragma unroll
-              for (int d = 1; d < LPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-              int e = (int)(__float_as_uint(top) >> 23) - 127;  // the largest goes to [2^13, 2^14)
-              e = top > 0.f && top <= FLT_MAX ? max(e, -113) : 13;
+              for (int d = 1; d < LPR; d <<= 1) top2 = max_u16x2(top2, __shfl_xor_sync(~0u, top2, d));
+              const uint32_t top = max(top2 & 0xFFFFu, top2 >> 16);
+              int e = (int)(top >> 7) - 127;  // the largest goes to [2^13, 2^14)
+              e = top > 0 && top < 0x7F80u ? max(e, -113) : 13;
               const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23);
               // to the thread whose row this is
               const int back = __shfl_sync(~0u, e, (lane % RPI) * LPR);
               if (lane / RPI == i0 + i) unscale = __uint_as_float((uint32_t)(127 - 13 + back) << 23);
 #pragma unroll
-              for (int k = 0; k < 4; ++k) u[k] = tc::pack2<__half>(f[2 * k] * up, f[2 * k + 1] * up);
+              for (int k = 0; k < 4; ++k) {
+                const float2 f = DT<T>::to_f2(u[k]);
+                u[k] = tc::pack2<__half>(f.x * up, f.y * up);
+              }
             }
             *reinterpret_cast<uint4*>(qs + swz(quarter * 32 + (i0 + i) * RPI + sub, l)) =
                 make_uint4(u[0] ^ sign, u[1] ^ sign, u[2] ^ sign, u[3] ^ sign);
