@@ -49,7 +49,6 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 16;                // keys of one MMA, one ring slot
 constexpr int kStep = 2 * kSub;         // keys of one warp step
 constexpr int kTile = kStep * kWarps;   // keys of one tile
-constexpr int kSlots = 4;               // ring slots per warp
 constexpr float kLazy = 8.0f;   // the running maximum moves only when passed by 2^8
 constexpr float kNone = -3e38f;  // the running maximum of a row that has seen no key
 
@@ -60,12 +59,12 @@ struct Cfg {
   static constexpr int kS = kSub * e2m1::scale_bytes(D);
   static constexpr int kSlot = 2 * (kC + kS);        // K codes | V codes | K scales | V scales
   static constexpr int kOffScale = 2 * kC;
-  static constexpr int kRing = kSlots * kSlot;       // per warp
+  static constexpr int kSteps = 2;                   // steps in a warp's ring
+  static constexpr int kRing = 2 * kSteps * kSlot;   // per warp
   static constexpr int kMerge = kWarps * 8 * D * 4;  // one 8-row round of every warp's O
   static constexpr int kOffMerge = kWarps * kRing;
   static constexpr int kOffMl = kOffMerge + kMerge;          // [2][kWarps][R] floats
-  static constexpr int kOffBar = kOffMl + 2 * kWarps * R * 4;  // a full barrier per warp and step
-  static constexpr int kOffBatch = kOffBar + kWarps * 2 * 8;
+  static constexpr int kOffBatch = kOffMl + 2 * kWarps * R * 4;
   // resident CTAs per SM, by registers: o takes 4 NT D/16, q 2 NT D/16
   static constexpr int kPerSm = NT == 1 ? 4 : NT == 2 ? 3 : 2;
   static constexpr int kBoth = NT == 1 ? 2 : 1;  // subs in flight at once
@@ -91,13 +90,8 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Copies `bytes` (a multiple of 16, both addresses on 16-byte boundaries) to shared memory.
-__device__ __forceinline__ void bulk_load(void* dst, const void* src, int bytes, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
+__device__ __forceinline__ void cp_async16_u32(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // Whether a sub's keys are all seen by every row of the item.
@@ -118,16 +112,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, c = lane & 3;
   // MMA row r of a sub is key (r >> 1) for even r, ((r >> 1) ^ 1) + 4 for odd r < 8, and 8 more in
-  // the upper half: two rows that one phase of a 16-byte load reads have different parity, and
-  // so have the keys of neighbouring lanes of V's loads, which keeps both off the same banks
-  // (V: two ways) with keys in their natural order.
+  // the upper half: two rows that one phase of K's 16-byte loads reads have different
+  // parity, and so have the keys of neighbouring lanes of V's loads, so that neither meets a
+  // bank conflict with K in its natural order.
   const int key_g = g & 1 ? ((g >> 1) ^ 1) + 4 : g >> 1;
   uint8_t* ring = smem + warp * C::kRing;
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* s_m = reinterpret_cast<float*>(smem + C::kOffMl);
   float* s_l = s_m + kWarps * R;
-  __shared__ volatile int s_abort;
-  if (threadIdx.x == 0) s_abort = 0;
   long long* s_pre = reinterpret_cast<long long*>(smem + C::kOffBatch);  // [B + 1]
   int* s_kv = reinterpret_cast<int*>(s_pre + p.B + 1);                   // [B]
   int* s_row = s_kv + p.B;                                               // [B]
@@ -199,61 +191,69 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   }
 
   // ---- producer side: this warp's next step to fetch -------------------------
-  // Lanes 0-7 each own one run of bytes of a step: sub (lane >> 2), and K codes, V codes,
-  // K scales or V scales (lane & 3).  A run is one bulk copy; a sub without keys (past the
-  // length, or a page outside the pool) has none.
+  // 16-byte asynchronous copies, a lane's share at fixed places: chunks `lane` and `lane + 32`
+  // of a sub's K and V codes, and lanes below 2 kS / 16 one chunk of its scales.  (Bulk copies
+  // of whole runs take one instruction sequence per lane that issues one: a warp that
+  // issues 8 of them for every step spends a third of its instructions there.)
   Pos prod = cons;
-  long long left = g1 - g0;  // steps not yet issued
-  int page = -1;             // pool page of this lane's run (-1: nothing to fetch)
-  uint32_t have = 0;         // bit 2 * (step & 1) + sub: the sub holds keys
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kOffBar) + 2 * warp;
-  const bool runner = lane < 8;
-  const int sub_in = (lane >> 2) & 1;
-  const uint8_t* run_pool = (lane & 1) ? p.v_pool : p.k_pool;
-  const int run_bytes = (lane & 2) ? C::kS : C::kC;
-  const int run_row = (lane & 2) ? e2m1::scale_bytes(D) : e2m1::code_bytes(D);
-  const size_t run_off = (lane & 2) ? (size_t)e2m1::code_bytes(D) << p.page_shift : 0;
-  uint8_t* run_dst = ring + sub_in * C::kSlot + ((lane & 2) ? C::kOffScale : 0) + (lane & 1) * run_bytes;
-  auto find_page = [&]() {
-    page = -1;
-    if (left <= 0 || !runner) return;
-    const int t = prod.tile * kTile + warp * kStep + sub_in * kSub;
-    if (t < s_kv[prod.b]) page = __ldg(p.table + (size_t)prod.b * p.max_pages + (t >> p.page_shift));
+  int left = (int)(g1 - g0);  // steps not yet issued
+  int page[2];                // pool pages of prod's two subs (-1: nothing to fetch)
+  uint32_t have = 0;          // bit 2 * (step in the ring) + sub: the sub holds keys
+  constexpr int SCH = C::kS / 16;                    // chunks of one scale block
+  constexpr int CPR = e2m1::code_bytes(D) / 16;      // chunks of a key's codes
+  const size_t page_stride = (size_t)p.Hkv * p.page_bytes;
+  const uint32_t ring_u = smem_u32(ring);
+  // V's chunks of keys 2, 3 mod 4 are swapped in pairs (D = 128), which keeps V's loads conflict-free
+  const uint32_t dst_k = ring_u + lane * 16;
+  const uint32_t dst_v = ring_u + C::kC + (D == 128 ? (lane ^ ((lane / CPR) & 2)) : lane) * 16;
+  const uint32_t dst_s = ring_u + C::kOffScale + lane * 16;
+  const uint8_t* scale_pool = lane < SCH ? p.k_pool : p.v_pool;
+  const size_t scale_off = ((size_t)e2m1::code_bytes(D) << p.page_shift) + (lane & (SCH - 1)) * 16;
+  auto find_pages = [&]() {
+    page[0] = page[1] = -1;
+    if (left <= 0) return;
+    const int t = prod.tile * kTile + warp * kStep, kv = s_kv[prod.b];
+    const int* row = p.table + (size_t)prod.b * p.max_pages;
+    if (t < kv) page[0] = __ldg(row + (t >> p.page_shift));
+    if (t + kSub < kv) page[1] = __ldg(row + ((t + kSub) >> p.page_shift));
   };
-  int in = 0;  // the step to issue, modulo 2
+  int in = 0;  // the step to issue, in the ring
   auto issue = [&]() {
-    const bool ok = page >= 0 && page < p.num_pages;
-    const uint32_t runs = __ballot_sync(~0u, ok);
-    have = (have & ~(3u << (2 * in))) | ((runs & 1) << (2 * in)) | (((runs >> 4) & 1) << (2 * in + 1));
-    if (lane == 0)
-      tc::mbar_expect_tx(bars + in, (uint32_t)__popc(runs & 0x11) * (uint32_t)C::kSlot);
-    __syncwarp();
-    if (ok) {
-      const int in_page = (prod.tile * kTile + warp * kStep + sub_in * kSub) & ((1 << p.page_shift) - 1);
-      bulk_load(run_dst + in * (2 * C::kSlot),
-                run_pool + ((size_t)page * p.Hkv + prod.h) * p.page_bytes + run_off + (size_t)in_page * run_row,
-                run_bytes, bars + in);
+    const size_t head = (size_t)prod.h * p.page_bytes;
+    const int t = prod.tile * kTile + warp * kStep, mask = (1 << p.page_shift) - 1;
+    have &= ~(3u << (2 * in));
+#pragma unroll
+    for (int sub = 0; sub < 2; ++sub) {
+      if ((uint32_t)page[sub] < (uint32_t)p.num_pages) {
+        const int row = (t + sub * kSub) & mask;
+        const size_t at = (size_t)page[sub] * page_stride + head;
+        const size_t codes = at + (size_t)row * e2m1::code_bytes(D) + lane * 16;
+        const uint32_t slot = (2 * in + sub) * C::kSlot;
+#pragma unroll
+        for (int i = 0; i < C::kC / 512; ++i) {
+          cp_async16_u32(dst_k + slot + i * 512, p.k_pool + codes + i * 512);
+          cp_async16_u32(dst_v + slot + i * 512, p.v_pool + codes + i * 512);
+        }
+        if (lane < 2 * SCH)
+          cp_async16_u32(dst_s + slot, scale_pool + at + scale_off + row * e2m1::scale_bytes(D));
+        have |= 1u << (2 * in + sub);
+      }
     }
-    in ^= 1;
+    cp_async_commit();
+    in = in + 1 == C::kSteps ? 0 : in + 1;
     if (left > 0) {
       --left;
       next_tile(prod);
-      find_page();
+      find_pages();
     }
   };
-  if (lane == 0) {
-    mbar_init(bars, 1);
-    mbar_init(bars + 1, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncwarp();
-  find_page();
-  issue();
-  issue();
+  find_pages();
+#pragma unroll 1
+  for (int i = 0; i < C::kSteps; ++i) issue();
   griddep_launch_dependents();
 
   // ---- consumer side -----------------------------------------------------------
-  int first_out = 0, parity = 0;  // slot of the step's first sub; phase of its barrier
+  int ring_at = 0;  // the step to take, in the ring
   long long at = g0;
   while (at < g1) {
     const int b = cons.b, h = cons.h, qt = cons.qt;
@@ -407,12 +407,12 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int t = (k & 1 ? c ^ 1 : c) + 4 * k;
-        const uint8_t* row = st + C::kC + t * e2m1::code_bytes(D) + g * (D / 16);
+        const uint8_t* row = st + C::kC + t * e2m1::code_bytes(D);
         if constexpr (D == 128) {
-          const uint2 w = *reinterpret_cast<const uint2*>(row);
+          const uint2 w = *reinterpret_cast<const uint2*>(row + ((g >> 1) ^ (t & 2)) * 16 + (g & 1) * 8);
           vw[k][0] = w.x; vw[k][1] = w.y;
         } else {
-          vw[k][0] = *reinterpret_cast<const uint32_t*>(row);
+          vw[k][0] = *reinterpret_cast<const uint32_t*>(row + g * 4);
         }
         sb[k] = sv[t * e2m1::scale_bytes(D)];
       }
@@ -485,17 +485,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
 
 #pragma unroll 1
     for (int tile = tile0; tile < tile1; ++tile) {
-      if (!mbar_wait_bounded(bars + (first_out >> 1), parity, &s_abort)) {
-        s_abort = 1;  // the copies did not land: give up, fetch no more, the rows become NaN
-        left = 0;
-        page = -1;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = __int_as_float(0x7fc00000);
-      }
+      cp_async_wait_group<C::kSteps - 1>();
       __syncwarp();
       const int t0 = tile * kTile + warp * kStep;
-      const uint8_t* st = ring + first_out * C::kSlot;
-      const uint32_t on = (have >> first_out) & 3;
+      const uint8_t* st = ring + ring_at * (2 * C::kSlot);
+      const uint32_t on = (have >> (2 * ring_at)) & 3;
       if (on == 3 && t0 + kStep <= minvis) {  // every row sees every key
         float s[2][NT][4];
         if constexpr (C::kBoth == 2) {
@@ -524,8 +518,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
           values(Edge(), st + k * C::kSlot, ts, s);
         }
       }
-      first_out ^= 2;
-      parity ^= first_out == 0;
+      ring_at = ring_at + 1 == C::kSteps ? 0 : ring_at + 1;
       __syncwarp();
       issue();
     }
@@ -613,13 +606,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     at += tile1 - tile0;
     cons.tile = tile1 - 1;
     next_tile(cons);
-  }
-  // the steps issued beyond the range carry no bytes: nothing is in flight, unless a wait gave up
-  if (s_abort) {
-    mbar_wait_drain(bars, 0);
-    mbar_wait_drain(bars, 1);
-    mbar_wait_drain(bars + 1, 0);
-    mbar_wait_drain(bars + 1, 1);
   }
 }
 
