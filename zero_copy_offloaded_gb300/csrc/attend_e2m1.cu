@@ -59,14 +59,14 @@ struct Cfg {
   static constexpr int kS = kSub * e2m1::scale_bytes(D);
   static constexpr int kSlot = 2 * (kC + kS);        // K codes | V codes | K scales | V scales
   static constexpr int kOffScale = 2 * kC;
-  static constexpr int kSteps = 2;                   // steps in a warp's ring
+  static constexpr int kSteps = D == 128 ? 3 : 4;                   // steps in a warp's ring
   static constexpr int kRing = 2 * kSteps * kSlot;   // per warp
   static constexpr int kMerge = kWarps * 8 * D * 4;  // one 8-row round of every warp's O
   static constexpr int kOffMerge = kWarps * kRing;
   static constexpr int kOffMl = kOffMerge + kMerge;          // [2][kWarps][R] floats
   static constexpr int kOffBatch = kOffMl + 2 * kWarps * R * 4;
   // resident CTAs per SM, by registers: o takes 4 NT D/16, q 2 NT D/16
-  static constexpr int kPerSm = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+  static constexpr int kPerSm = NT <= 2 ? 3 : 2;
   static constexpr int kBoth = NT == 1 ? 2 : 1;  // subs in flight at once
 };
 
@@ -670,7 +670,7 @@ dkv_status refuse(dkv_status s, const char* msg) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 constexpr int kSms = 152;
-constexpr int kMaxCtas = 4 * kSms;
+constexpr int kMaxCtas = 3 * kSms;
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
