@@ -59,7 +59,7 @@ struct Cfg {
   static constexpr int kS = kSub * e2m1::scale_bytes(D);
   static constexpr int kSlot = 2 * (kC + kS);        // K codes | V codes | K scales | V scales
   static constexpr int kOffScale = 2 * kC;
-  static constexpr int kSteps = D == 128 ? 3 : 4;                   // steps in a warp's ring
+  static constexpr int kSteps = D == 128 ? 3 : 4;    // steps in a warp's ring
   static constexpr int kRing = 2 * kSteps * kSlot;   // per warp
   static constexpr int kMerge = kWarps * 8 * D * 4;  // one 8-row round of every warp's O
   static constexpr int kOffMerge = kWarps * kRing;
