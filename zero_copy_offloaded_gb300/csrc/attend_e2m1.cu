@@ -11,8 +11,8 @@
 // All tiles of all items form one line that is dealt to the CTAs in equal
 // contiguous ranges, whatever the lengths are, from the lengths on the device
 // (no host copy, so a captured graph serves any lengths).  A CTA that holds a whole
-// item writes its rows; an item cut between CTAs leaves fp32 partials, which a
-// second kernel joins in CTA order.
+// item writes its rows; an item cut between CTAs leaves fp32 partials, which the CTA that
+// finishes last joins in CTA order (no CTA waits for another).
 //
 // Inside a CTA each of 4 warps takes 32 keys of every tile through its own
 // cp.async ring, with no barrier between warps until the item ends.  Per 16 keys:
@@ -31,6 +31,8 @@
 #include <math.h>
 #include <stdio.h>
 
+#include <atomic>
+#include <chrono>
 #include <type_traits>
 
 #include "attend_e2m1.cuh"
@@ -49,6 +51,9 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kSub = 16;                // keys of one MMA, one ring slot
 constexpr int kStep = 2 * kSub;         // keys of one warp step
 constexpr int kTile = kStep * kWarps;   // keys of one tile
+// What an item costs beside its key tiles (its queries, the join of the warps), in tiles: the
+// CTAs' ranges are dealt with it.
+constexpr int kItemCost = 3;
 constexpr float kLazy = 8.0f;   // the running maximum moves only when passed by 2^8
 constexpr float kNone = -3e38f;  // the running maximum of a row that has seen no key
 
@@ -61,7 +66,7 @@ struct Cfg {
   static constexpr int kOffScale = 2 * kC;
   static constexpr int kSteps = D == 128 ? 3 : 4;    // steps in a warp's ring
   static constexpr int kRing = 2 * kSteps * kSlot;   // per warp
-  static constexpr int kMerge = kWarps * 8 * D * 4;  // one 8-row round of every warp's O
+  static constexpr int kMerge = kWarps * 8 * (D + 8) * 4;  // one 8-row round of every warp's O
   static constexpr int kOffMerge = kWarps * kRing;
   static constexpr int kOffMl = kOffMerge + kMerge;          // [2][kWarps][R] floats
   static constexpr int kOffBatch = kOffMl + 2 * kWarps * R * 4;
@@ -94,6 +99,23 @@ __device__ __forceinline__ void cp_async16_u32(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
+template <int V>
+__device__ __forceinline__ void store_vec(float* to, const float (&x)[V]) {
+  if constexpr (V == 4) *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+  else *reinterpret_cast<float2*>(to) = make_float2(x[0], x[1]);
+}
+// From L2: another SM wrote it during this kernel.
+template <int V>
+__device__ __forceinline__ void load_vec(const float* from, float (&x)[V]) {
+  if constexpr (V == 4) {
+    const float4 y = __ldcg(reinterpret_cast<const float4*>(from));
+    x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+  } else {
+    const float2 y = __ldcg(reinterpret_cast<const float2*>(from));
+    x[0] = y.x; x[1] = y.y;
+  }
+}
+
 // Whether a sub's keys are all seen by every row of the item.
 using Inner = std::false_type;
 using Edge = std::true_type;
@@ -120,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* s_m = reinterpret_cast<float*>(smem + C::kOffMl);
   float* s_l = s_m + kWarps * R;
+  __shared__ int s_join[2];
   long long* s_pre = reinterpret_cast<long long*>(smem + C::kOffBatch);  // [B + 1]
   int* s_kv = reinterpret_cast<int*>(s_pre + p.B + 1);                   // [B]
   int* s_row = s_kv + p.B;                                               // [B]
@@ -133,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     s_kv[b] = kv;
     s_row[b] = row;
     s_n[b] = n;
-    s_pre[b + 1] = (long long)p.Hkv * ((n * G + R - 1) / R) * max(1, (kv + kTile - 1) / kTile);
+    s_pre[b + 1] = (long long)p.Hkv * ((n * G + R - 1) / R) * (max(1, (kv + kTile - 1) / kTile) + kItemCost);
   }
   if (threadIdx.x == 0) s_pre[0] = 0;
   __syncthreads();
@@ -152,20 +175,23 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   }
   __syncthreads();
   const long long total = s_pre[p.B];
-  // with fewer tiles than CTAs the first `total` CTAs take one each, so that an
+  // with less work than CTAs the first `total` CTAs take one unit each, so that an
   // item's pieces always lie in consecutive CTAs
   const long long ctas = min(total, (long long)gridDim.x);
-  if (threadIdx.x == 0) p.desc[blockIdx.x].pieces = 0;
   if ((long long)blockIdx.x >= ctas) return;
   const long long g0 = total * blockIdx.x / ctas, g1 = total * (blockIdx.x + 1) / ctas;
+  auto owner = [&](long long at) { return (int)(((at + 1) * ctas - 1) / total); };  // of a unit of the line
 
   auto enter = [&](Pos& at, int b) {
     at.b = b;
     at.qtiles = (s_n[b] * G + R - 1) / R;
     at.tiles = max(1, (s_kv[b] + kTile - 1) / kTile);
   };
-  auto next_tile = [&](Pos& at) {
+  // The tile after `at`; `left`, the units of the CTA's range from `at` on, goes with it.
+  auto next_tile = [&](Pos& at, int& left) {
+    --left;
     if (++at.tile < at.tiles) return;
+    left -= kItemCost;
     at.tile = 0;
     if (++at.qt < at.qtiles) return;
     at.qt = 0;
@@ -176,6 +202,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     if (b < p.B) enter(at, b);
   };
   Pos cons;
+  int left = (int)(g1 - g0);
   {
     int lo = 0, hi = p.B;  // s_pre[lo] <= g0 < s_pre[hi]
     while (hi - lo > 1) {
@@ -184,11 +211,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     }
     enter(cons, lo);
     const long long rem = g0 - s_pre[lo];
-    const long long item = rem / cons.tiles;
-    cons.tile = (int)(rem - item * cons.tiles);
+    const int units = cons.tiles + kItemCost;
+    const long long item = rem / units;
+    const int in_item = (int)(rem - item * units);  // an item's first units stand for its fixed cost
+    cons.tile = max(0, in_item - kItemCost);
+    left -= max(0, kItemCost - in_item);
     cons.h = (int)(item / cons.qtiles);
     cons.qt = (int)(item - (long long)cons.h * cons.qtiles);
   }
+  if (left <= 0) return;
 
   // ---- producer side: this warp's next step to fetch -------------------------
   // 16-byte asynchronous copies, a lane's share at fixed places: chunks `lane` and `lane + 32`
@@ -196,9 +227,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   // of whole runs take one instruction sequence per lane that issues one: a warp that
   // issues 8 of them for every step spends a third of its instructions there.)
   Pos prod = cons;
-  int left = (int)(g1 - g0);  // steps not yet issued
-  int page[2];                // pool pages of prod's two subs (-1: nothing to fetch)
-  uint32_t have = 0;          // bit 2 * (step in the ring) + sub: the sub holds keys
+  int to_issue = left;  // units from prod on
+  uint32_t have = 0;    // bit 2 * (step in the ring) + sub: the sub holds keys
   constexpr int SCH = C::kS / 16;                    // chunks of one scale block
   constexpr int CPR = e2m1::code_bytes(D) / 16;      // chunks of a key's codes
   const size_t page_stride = (size_t)p.Hkv * p.page_bytes;
@@ -209,18 +239,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   const uint32_t dst_s = ring_u + C::kOffScale + lane * 16;
   const uint8_t* scale_pool = lane < SCH ? p.k_pool : p.v_pool;
   const size_t scale_off = ((size_t)e2m1::code_bytes(D) << p.page_shift) + (lane & (SCH - 1)) * 16;
-  auto find_pages = [&]() {
+  // pool pages of prod's two subs (-1: nothing to fetch)
+  auto find_pages = [&](int (&page)[2]) {
     page[0] = page[1] = -1;
-    if (left <= 0) return;
+    if (to_issue <= 0) return;
     const int t = prod.tile * kTile + warp * kStep, kv = s_kv[prod.b];
     const int* row = p.table + (size_t)prod.b * p.max_pages;
     if (t < kv) page[0] = __ldg(row + (t >> p.page_shift));
     if (t + kSub < kv) page[1] = __ldg(row + ((t + kSub) >> p.page_shift));
   };
   int in = 0;  // the step to issue, in the ring
-  auto issue = [&]() {
-    const size_t head = (size_t)prod.h * p.page_bytes;
-    const int t = prod.tile * kTile + warp * kStep, mask = (1 << p.page_shift) - 1;
+  auto copy = [&](int h, int tile, const int (&page)[2]) {
+    const size_t head = (size_t)h * p.page_bytes;
+    const int t = tile * kTile + warp * kStep, mask = (1 << p.page_shift) - 1;
     have &= ~(3u << (2 * in));
 #pragma unroll
     for (int sub = 0; sub < 2; ++sub) {
@@ -241,25 +272,34 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     }
     cp_async_commit();
     in = in + 1 == C::kSteps ? 0 : in + 1;
-    if (left > 0) {
-      --left;
-      next_tile(prod);
-      find_pages();
-    }
   };
-  find_pages();
-#pragma unroll 1
-  for (int i = 0; i < C::kSteps; ++i) issue();
-  griddep_launch_dependents();
+  int page[2];
+  {  // the first steps: every page is looked up before the first one is waited for
+    int first[C::kSteps][2], hs[C::kSteps], tiles[C::kSteps];
+#pragma unroll
+    for (int i = 0; i < C::kSteps; ++i) {
+      find_pages(first[i]);
+      hs[i] = prod.h;
+      tiles[i] = prod.tile;
+      if (to_issue > 0) next_tile(prod, to_issue);
+    }
+    find_pages(page);
+#pragma unroll
+    for (int i = 0; i < C::kSteps; ++i) copy(hs[i], tiles[i], first[i]);
+  }
+  auto issue = [&]() {
+    copy(prod.h, prod.tile, page);
+    if (to_issue > 0) next_tile(prod, to_issue);
+    find_pages(page);
+  };
 
   // ---- consumer side -----------------------------------------------------------
   int ring_at = 0;  // the step to take, in the ring
-  long long at = g0;
-  while (at < g1) {
+  while (left > 0) {
     const int b = cons.b, h = cons.h, qt = cons.qt;
     const int kv = s_kv[b], n = s_n[b], row0 = s_row[b];
     const int tile0 = cons.tile;
-    const int tile1 = (int)min((long long)cons.tiles, tile0 + (g1 - at));
+    const int tile1 = min(cons.tiles, tile0 + left);
     const int last = min((qt + 1) * R, n * G) - 1;  // last packed row of the item
     const int minvis = max(0, kv - n + (qt * R) / G + 1), maxvis = max(0, kv - n + last / G + 1);
 
@@ -523,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       issue();
     }
 
-    // ---- the item's end: join the warps --------------------------------------
+    // ---- the piece's end: join the warps --------------------------------------
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -537,129 +577,123 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
           s_l[warp * R + nt * 8 + 2 * c + u] = x;
         }
       }
-    const bool starts = tile0 == 0, ends = tile1 == cons.tiles;
-    const int slot = 2 * blockIdx.x + (starts ? 1 : 0);
+    constexpr int V = D / 32, RS = D + 8;  // outputs of a lane; padded row of the merge buffer
+    const bool starts = tile0 == 0, ends = tile1 == cons.tiles, whole = starts && ends;
+    const int slot = 2 * blockIdx.x + (starts ? 1 : 0), rows = last - qt * R + 1, d0 = lane * V;
 #pragma unroll 1
     for (int nt = 0; nt < NT; ++nt) {
+      if (nt * 8 >= rows) break;
       __syncthreads();
-      // this warp's rows against the CTA's maximum
-      float f[2];
+      // this warp's rows against the CTA's maximum; dims 16 g + 2 i, + 1 lie at 16 i + 2 g
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int r = nt * 8 + 2 * c + u;
-        float top = -INFINITY;
+        if (r < rows) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * R + r]);
+          const float mine = s_m[warp * R + r], f = mine == top ? 1.0f : exp2f(mine - top);
+#pragma unroll
+          for (int n2 = 0; n2 < NT; ++n2)
+            if (n2 == nt) {
+#pragma unroll
+              for (int i = 0; i < J; ++i)
+                *reinterpret_cast<float2*>(merge + (warp * 8 + 2 * c + u) * RS + 16 * i + 2 * g) =
+                    make_float2(o[n2][i][u] * f, o[n2][i][u + 2] * f);
+            }
+        }
+      }
+      __syncthreads();
+      for (int r = nt * 8 + warp; r < min(rows, nt * 8 + 8); r += kWarps) {
+        const int pr = qt * R + r;
+        float acc[V], top = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * R + r]);
-        const float mine = s_m[warp * R + r];
-        f[u] = mine == top ? 1.0f : exp2f(mine - top);
-      }
 #pragma unroll
-      for (int n2 = 0; n2 < NT; ++n2)
-        if (n2 == nt) {
+        for (int w = 0; w < kWarps; ++w) {
+          const float mw = s_m[w * R + r];
+          sum += s_l[w * R + r] * (mw == top ? 1.0f : exp2f(mw - top));
+          // dims d0 .. d0 + V - 1 of row r (D/8 dims to a g, in pairs)
 #pragma unroll
-          for (int i = 0; i < J; ++i)
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-              *reinterpret_cast<float2*>(merge + (warp * 8 + 2 * c + u) * D + g * (D / 8) + 2 * i) =
-                  make_float2(o[n2][i][u] * f[u], o[n2][i][u + 2] * f[u]);
+          for (int e = 0; e < V; e += 2) {
+            const int gd = (d0 + e) / (D / 8), i = (d0 + e) % (D / 8) / 2;
+            const float2 x = *reinterpret_cast<const float2*>(merge + (w * 8 + r - nt * 8) * RS + 16 * i + 2 * gd);
+            acc[e] += x.x;
+            acc[e + 1] += x.y;
+          }
         }
+        if (whole) {
+          store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, top, sum, lane == 0);
+        } else {
+          store_vec<V>(p.part_o + ((size_t)slot * R + r) * D + d0, acc);
+          if (lane == 0)
+            *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * R + r) * 2) = make_float2(top, sum);
+        }
+      }
+    }
+    if (!whole) {
+      // ---- the CTA that finishes an item's last open piece joins them all, in CTA order.  The
+      // count of finished pieces needs no clearing before the call: it stands beside the
+      // call's own tag and starts from nothing wherever another tag is found.
       __syncthreads();
-      {
-        constexpr int V = D / 32;
-        const int d0 = lane * V;
-        for (int r = warp; r < 8; r += kWarps) {
-          const int pr = qt * R + nt * 8 + r;
-          float acc[V], top = -INFINITY, sum = 0.f;
+      if (threadIdx.x == 0) {
+        const long long first_unit =
+            s_pre[b] + ((long long)h * cons.qtiles + qt) * (cons.tiles + kItemCost) + kItemCost;
+        const int c0 = owner(first_unit), pieces = owner(first_unit + cons.tiles - 1) - c0 + 1;
+        __threadfence();
+        unsigned long long* word = p.done + c0;
+        const unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(word);
+        if ((seen ^ p.tag) >> 16) atomicCAS(word, seen, p.tag);
+        const bool final_piece = (int)(atomicAdd(word, 1ull) & 0xFFFF) == pieces - 1;
+        if (final_piece) *word = 0;
+        __threadfence();
+        s_join[0] = final_piece ? c0 : -1;
+        s_join[1] = pieces;
+      }
+      __syncthreads();
+      const int c0 = s_join[0], pieces = s_join[1];
+      if (c0 >= 0)
+        for (int r = warp; r < rows; r += kWarps) {
+          // piece i lies in slot 2 (c0 + i), but the first in slot 2 c0 + 1
+          auto at = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)) * R + r; };
+          const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+          float top = -INFINITY, sum = 0.f, acc[V];
+          for (int i = lane; i < pieces; i += 32) top = fmaxf(top, __ldcg(ml + at(i)).x);
+#pragma unroll
+          for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
 #pragma unroll
           for (int e = 0; e < V; ++e) acc[e] = 0.f;
+          for (int base = 0; base < pieces; base += 32) {
+            const int k = min(32, pieces - base);
+            float f = 0.f, part = 0.f;
+            if (lane < k) {
+              const float2 x = __ldcg(ml + at(base + lane));
+              f = x.x == top ? 1.0f : exp2f(x.x - top);
+              part = x.y * f;
+            }
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * R + nt * 8 + r]);
+            for (int w = 16; w; w >>= 1) part += __shfl_xor_sync(~0u, part, w);
+            sum += part;
+#pragma unroll 8
+            for (int i = 0; i < k; ++i) {
+              const float fi = __shfl_sync(~0u, f, i);
+              float v[V];
+              load_vec<V>(p.part_o + at(base + i) * D + d0, v);
 #pragma unroll
-          for (int w = 0; w < kWarps; ++w) {
-            const float mw = s_m[w * R + nt * 8 + r];
-            sum += s_l[w * R + nt * 8 + r] * (mw == top ? 1.0f : exp2f(mw - top));
-#pragma unroll
-            for (int e = 0; e < V; ++e) acc[e] += merge[(w * 8 + r) * D + d0 + e];
-          }
-          if (starts && ends) {
-            if (pr <= last) store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, top, sum, lane == 0);
-          } else {
-            float* po = p.part_o + ((size_t)slot * R + nt * 8 + r) * D + d0;
-#pragma unroll
-            for (int e = 0; e < V; ++e) po[e] = acc[e];
-            if (lane == 0) {
-              p.part_ml[((size_t)slot * R + nt * 8 + r) * 2] = top;
-              p.part_ml[((size_t)slot * R + nt * 8 + r) * 2 + 1] = sum;
+              for (int e = 0; e < V; ++e) acc[e] = fmaf(v[e], fi, acc[e]);
             }
           }
+          const int pr = qt * R + r;
+          store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, top, sum, lane == 0);
         }
-      }
     }
-    if (starts && !ends && threadIdx.x == 0) {
-      AttendDesc d;
-      const long long end = at + cons.tiles - 1;  // the item's last tile, and the CTA that holds it
-      d.pieces = (int)(((end + 1) * ctas - 1) / total) - (int)blockIdx.x + 1;
-      d.row0 = row0; d.first = qt * R; d.last = last; d.head0 = h * G;
-      p.desc[blockIdx.x] = d;
-    }
-    __syncthreads();  // s_m, s_l and merge are free for the next item
-    at += tile1 - tile0;
+    __syncthreads();  // s_m, s_l, merge and s_join are free for the next piece
+    left -= tile1 - tile0 - 1;
     cons.tile = tile1 - 1;
-    next_tile(cons);
+    next_tile(cons, left);
   }
-}
-
-// Joins the partials of each cut item: block c takes the item whose first piece
-// CTA c left unfinished, whose further pieces CTAs c+1, c+2, ... hold.  A warp takes
-// a row: its lanes read the pieces' maxima and sums 32 at a time, then the
-// outputs are read with nothing to wait for between pieces.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) attend_join_kernel(const AttendParams p, int R) {
-  griddep_wait();
-  const AttendDesc d = p.desc[blockIdx.x];
-  if (d.pieces < 2) return;
-  constexpr int V = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const int pr = d.first + r;
-  if (r >= R || pr > d.last) return;
-  // piece i lies in slot 2 (c + i), but the first in slot 2 c + 1
-  auto at = [&](int i) { return (size_t)(2 * (blockIdx.x + i) + (i == 0)) * R + r; };
-  float top = -INFINITY;
-  for (int i = lane; i < d.pieces; i += 32) top = fmaxf(top, p.part_ml[2 * at(i)]);
-#pragma unroll
-  for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
-  float sum = 0.f, acc[V];
-#pragma unroll
-  for (int e = 0; e < V; ++e) acc[e] = 0.f;
-  for (int base = 0; base < d.pieces; base += 32) {
-    const int n = min(32, d.pieces - base);
-    float f = 0.f, l = 0.f;
-    if (lane < n) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at(base + lane));
-      f = ml.x == top ? 1.0f : exp2f(ml.x - top);
-      l = ml.y * f;
-    }
-#pragma unroll
-    for (int w = 16; w; w >>= 1) l += __shfl_xor_sync(~0u, l, w);
-    sum += l;
-#pragma unroll 8
-    for (int i = 0; i < n; ++i) {
-      const float fi = __shfl_sync(~0u, f, i);
-      const float* o = p.part_o + at(base + i) * D + lane * V;
-      float v[V];
-      if constexpr (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(o);
-        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(o);
-        v[0] = x.x; v[1] = x.y;
-      }
-#pragma unroll
-      for (int e = 0; e < V; ++e) acc[e] = fmaf(v[e], fi, acc[e]);
-    }
-  }
-  store_row<T, V>(p, d.row0 + pr / p.G, d.head0 + pr % p.G, D, lane * V, acc, top, sum, lane == 0);
 }
 
 dkv_status refuse(dkv_status s, const char* msg) {
@@ -675,7 +709,18 @@ constexpr int kMaxCtas = 3 * kSms;
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workspace: descriptors | partial (max, sum) | partial o, two slots per CTA.
-size_t ws_desc() { return align256(kMaxCtas * sizeof(AttendDesc)); }
+size_t ws_desc() { return align256(kMaxCtas * (sizeof(AttendDesc) > 8 ? sizeof(AttendDesc) : 8)); }
+
+// The tag of a call: 48 bits that no earlier call of this process had, scattered so that memory
+// left by anything else does not hold one.
+unsigned long long next_tag() {
+  static std::atomic<unsigned long long> calls{(unsigned long long)std::chrono::steady_clock::now().time_since_epoch().count()};
+  unsigned long long z = calls.fetch_add(0x9E3779B97F4A7C15ull) + 0x9E3779B97F4A7C15ull;
+  z = (z ^ (z >> 30)) * 0xBF58476D1CE4E5B9ull;
+  z = (z ^ (z >> 27)) * 0x94D049BB133111EBull;
+  z = (z ^ (z >> 31)) | 1ull << 63;
+  return z & ~0xFFFFull;
+}
 
 // Query rows per item: the smallest of 8, 16, 24 and 32 that holds a sequence's rows;
 // for more than kTcFrom rows the items of the tcgen05 kernel.
@@ -687,20 +732,6 @@ int rows_per_item(int G, int max_rows) {
 int ctas_of(int R) { return R == kTcRows ? kSms : kMaxCtas; }
 size_t ws_ml(int R) { return align256((size_t)2 * ctas_of(R) * R * 2 * 4); }
 size_t ws_o(int R, int D) { return align256((size_t)2 * ctas_of(R) * R * D * 4); }
-
-template <typename T, int D>
-cudaError_t launch_join(const AttendParams& p, int R, int ctas, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, R / 8);
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D>, p, R);
-}
 
 template <typename T, int D, int NT>
 cudaError_t launch(const AttendParams& p, cudaStream_t s) {
@@ -719,8 +750,7 @@ cudaError_t launch(const AttendParams& p, cudaStream_t s) {
   const int fit = 228 * 1024 / (smem + 1024);
   const int grid = kSms * (fit < C::kPerSm ? fit : C::kPerSm);
   attend_kernel<T, D, NT><<<grid, kThreads, smem, s>>>(p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_join<T, D>(p, C::R, grid, s);
+  return cudaGetLastError();
 }
 
 template <typename T, int D>
@@ -782,6 +812,8 @@ extern "C" dkv_status dkv_paged_attend(const dkv_attend_t* a, void* stream) {
   AttendParams p;
   char* w = static_cast<char*>(a->workspace);
   p.desc = reinterpret_cast<AttendDesc*>(w);
+  p.done = reinterpret_cast<unsigned long long*>(w);
+  p.tag = next_tag();
   p.part_ml = reinterpret_cast<float*>(w + ws_desc());
   p.part_o = reinterpret_cast<float*>(w + ws_desc() + ws_ml(R));
   p.q = a->q; p.k_pool = static_cast<const uint8_t*>(a->k_pool); p.v_pool = static_cast<const uint8_t*>(a->v_pool);

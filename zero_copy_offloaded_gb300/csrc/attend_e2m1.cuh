@@ -25,7 +25,9 @@ struct AttendParams {
   const int* row_start;  // [B + 1], or null: row b is sequence b's only one
   void* out;
   float* lse;
-  AttendDesc* desc;
+  AttendDesc* desc;             // many rows: by CTA
+  unsigned long long* done;     // few rows: finished pieces of the item that a CTA began
+  unsigned long long tag;       // the call's own, in the upper 48 bits
   float* part_ml;
   float* part_o;
   long long q_stride;
