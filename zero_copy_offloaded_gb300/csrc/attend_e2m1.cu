@@ -71,7 +71,7 @@ struct Cfg {
   static constexpr int kOffMl = kOffMerge + kMerge;          // [2][kWarps][R] floats
   static constexpr int kOffBatch = kOffMl + 2 * kWarps * R * 4;
   // resident CTAs per SM, by registers: o takes 4 NT D/16, q 2 NT D/16
-  static constexpr int kPerSm = NT <= 2 ? 3 : 2;
+  static constexpr int kPerSm = NT == 1 || (NT == 2 && D == 64) ? 3 : 2;
   static constexpr int kBoth = NT == 1 ? 2 : 1;  // subs in flight at once
 };
 
