@@ -69,9 +69,11 @@ struct Cfg {
   static constexpr int kMerge = kWarps * 8 * (D + 8) * 4;  // one 8-row round of every warp's O
   static constexpr int kOffMerge = kWarps * kRing;
   static constexpr int kOffMl = kOffMerge + kMerge;          // [2][kWarps][R] floats
-  static constexpr int kOffBatch = kOffMl + 2 * kWarps * R * 4;
-  // resident CTAs per SM, by registers: o takes 4 NT D/16, q 2 NT D/16
-  static constexpr int kPerSm = NT == 1 || (NT == 2 && D == 64) ? 3 : 2;
+  static constexpr int kQueries = NT > 1 ? NT * (D / 16) * 32 * 8 : 0;  // B fragments of the rows
+  static constexpr int kOffQ = kOffMl + 2 * kWarps * R * 4;             // and their scales, visible keys
+  static constexpr int kOffBatch = kOffQ + kQueries + (NT > 1 ? 2 * R * 4 : 0);
+  // resident CTAs per SM, by registers: o takes 4 NT D/16 of a thread's
+  static constexpr int kPerSm = NT == 1 || (NT <= 3 && D == 64) ? 3 : 2;
   static constexpr int kBoth = NT == 1 ? 2 : 1;  // subs in flight at once
 };
 
@@ -142,6 +144,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* s_m = reinterpret_cast<float*>(smem + C::kOffMl);
   float* s_l = s_m + kWarps * R;
+  uint2* s_q = reinterpret_cast<uint2*>(smem + C::kOffQ);
+  float* s_scale = reinterpret_cast<float*>(smem + C::kOffQ + C::kQueries);
+  int* s_vis = reinterpret_cast<int*>(s_scale + R);
   __shared__ int s_join[2];
   long long* s_pre = reinterpret_cast<long long*>(smem + C::kOffBatch);  // [B + 1]
   int* s_kv = reinterpret_cast<int*>(s_pre + p.B + 1);                   // [B]
@@ -303,11 +308,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     const int last = min((qt + 1) * R, n * G) - 1;  // last packed row of the item
     const int minvis = max(0, kv - n + (qt * R) / G + 1), maxvis = max(0, kv - n + last / G + 1);
 
-    uint32_t qf[NT][2 * J];
-    float sl[NT][2];
-    int vis[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    // Queries as B fragments: eight rows in registers, more in shared memory, where each warp
+    // prepares some groups of eight for all.
+    constexpr bool QS = C::kQueries > 0;
+    uint32_t qf[QS ? 1 : NT][2 * J];
+    float sl1[2];  // eight rows: the scales and visible keys of this thread's two score columns
+    int vis1[2];
+    auto load_q = [&](int nt, uint32_t (&f)[2 * J]) {  // returns what undoes the rows' scaling
       const int pr = qt * R + nt * 8 + g;
       float unscale = 1.0f;
       if (pr <= last) {
@@ -318,18 +325,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
 #pragma unroll
         for (int i = 0; i < J / 2; ++i) {
           const uint4 w = __ldg(src + i);
-          qf[nt][4 * i] = w.x; qf[nt][4 * i + 1] = w.y; qf[nt][4 * i + 2] = w.z; qf[nt][4 * i + 3] = w.w;
+          f[4 * i] = w.x; f[4 * i + 1] = w.y; f[4 * i + 2] = w.z; f[4 * i + 3] = w.w;
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 2 * J; ++i) qf[nt][i] = 0;
+        for (int i = 0; i < 2 * J; ++i) f[i] = 0;
       }
       if constexpr (DT<T>::code == DKV_BF16) {
         float top = 0.f;
 #pragma unroll
         for (int i = 0; i < 2 * J; ++i) {
-          const float2 f = DT<T>::to_f2(qf[nt][i]);
-          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+          const float2 y = DT<T>::to_f2(f[i]);
+          top = fmaxf(top, fmaxf(fabsf(y.x), fabsf(y.y)));
         }
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
@@ -340,22 +347,46 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
         unscale = __uint_as_float((uint32_t)(127 - 13 + e) << 23);
 #pragma unroll
         for (int i = 0; i < 2 * J; ++i) {
-          const float2 f = DT<T>::to_f2(qf[nt][i]);
-          qf[nt][i] = tc::pack2<__half>(f.x * up, f.y * up);
+          const float2 y = DT<T>::to_f2(f[i]);
+          f[i] = tc::pack2<__half>(y.x * up, y.y * up);
         }
       }
       if (p.scale_log2 < 0.f) {  // the scale's sign goes to the queries
 #pragma unroll
-        for (int i = 0; i < 2 * J; ++i) qf[nt][i] ^= 0x80008000u;
+        for (int i = 0; i < 2 * J; ++i) f[i] ^= 0x80008000u;
       }
+      // positive and finite, so that a masked -infinity stays one
+      return fminf(fmaxf(fabsf(p.scale_log2) * unscale, 1e-37f), FLT_MAX);
+    };
+    if constexpr (QS) {
+      for (int nt = warp; nt < NT; nt += kWarps) {
+        uint32_t f[2 * J];
+        const float scale = load_q(nt, f);
+#pragma unroll
+        for (int j = 0; j < J; ++j) s_q[(nt * J + j) * 32 + lane] = make_uint2(f[2 * j], f[2 * j + 1]);
+        if (c == 0) {
+          const int pr = qt * R + nt * 8 + g;
+          s_scale[nt * 8 + g] = scale;
+          s_vis[nt * 8 + g] = pr <= last ? max(0, kv - n + pr / G + 1) : 0;
+        }
+      }
+      __syncthreads();
+    }
+    if constexpr (!QS) {
+      const float scale = load_q(0, qf[0]);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
-        // positive and finite, so that a masked -infinity stays one
-        sl[nt][u] = fminf(fmaxf(fabsf(p.scale_log2) * __shfl_sync(~0u, unscale, (2 * c + u) * 4), 1e-37f), FLT_MAX);
-        const int pc = qt * R + nt * 8 + 2 * c + u;
-        vis[nt][u] = pc <= last ? max(0, kv - n + pc / G + 1) : 0;
+        sl1[u] = __shfl_sync(~0u, scale, (2 * c + u) * 4);
+        const int pc = qt * R + 2 * c + u;
+        vis1[u] = pc <= last ? max(0, kv - n + pc / G + 1) : 0;
       }
     }
+    auto scales = [&](int nt) {
+      return QS ? *reinterpret_cast<const float2*>(s_scale + nt * 8 + 2 * c) : make_float2(sl1[0], sl1[1]);
+    };
+    auto visible = [&](int nt) {
+      return QS ? *reinterpret_cast<const int2*>(s_vis + nt * 8 + 2 * c) : make_int2(vis1[0], vis1[1]);
+    };
 
     // running maximum (base 2, scaled), the raw score that moves it, sum, output
     float m[NT][2], thr[NT][2], l[NT][2], o[NT][J][4];
@@ -408,7 +439,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
             a[rr + 2] = hmul2(x[rr][2 * jj + 1], ks[rr][D == 128 ? w / 2 : 0]);
           }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], a, qf[nt][2 * j], qf[nt][2 * j + 1]);
+          for (int nt = 0; nt < NT; ++nt) {
+            if constexpr (QS) {
+              const uint2 q = s_q[(nt * J + j) * 32 + lane];
+              mma16816(s[nt], a, q.x, q.y);
+            } else {
+              mma16816(s[nt], a, qf[nt][2 * j], qf[nt][2 * j + 1]);
+            }
+          }
         }
       }
       const int tok = t0 + key_g;
@@ -416,9 +454,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         if constexpr (edge) {
+          const int2 vis = visible(nt);
 #pragma unroll
           for (int u = 0; u < 4; ++u)
-            if (tok + 8 * (u >> 1) >= vis[nt][u & 1]) s[nt][u] = -INFINITY;
+            if (tok + 8 * (u >> 1) >= (u & 1 ? vis.y : vis.x)) s[nt][u] = -INFINITY;
         }
         up |= fmaxf(s[nt][0], s[nt][2]) > thr[nt][0];
         up |= fmaxf(s[nt][1], s[nt][3]) > thr[nt][1];
@@ -431,10 +470,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float p0 = tc::ex2_approx(fmaf(s[nt][0], sl[nt][0], -m[nt][0]));
-        const float p1 = tc::ex2_approx(fmaf(s[nt][1], sl[nt][1], -m[nt][1]));
-        const float p2 = tc::ex2_approx(fmaf(s[nt][2], sl[nt][0], -m[nt][0]));
-        const float p3 = tc::ex2_approx(fmaf(s[nt][3], sl[nt][1], -m[nt][1]));
+        const float2 sl = scales(nt);
+        const float p0 = tc::ex2_approx(fmaf(s[nt][0], sl.x, -m[nt][0]));
+        const float p1 = tc::ex2_approx(fmaf(s[nt][1], sl.y, -m[nt][1]));
+        const float p2 = tc::ex2_approx(fmaf(s[nt][2], sl.x, -m[nt][0]));
+        const float p3 = tc::ex2_approx(fmaf(s[nt][3], sl.y, -m[nt][1]));
         l[nt][0] += p0 + p2;
         l[nt][1] += p1 + p3;
         pb[nt][0] = transpose8x8(tc::pack2<__half>(p0, p1));
@@ -488,12 +528,14 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
         for (int t = 0; t < kSub; ++t)
           if ((sv[t * e2m1::scale_bytes(D)] & 0x7f) == 0x7f) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+              const int2 vis = visible(nt);
 #pragma unroll
               for (int i = 0; i < J; ++i)
 #pragma unroll
                 for (int u = 0; u < 4; ++u)
-                  if (t0 + t < vis[nt][u & 1]) o[nt][i][u] = __int_as_float(0x7fc00000);
+                  if (t0 + t < (u & 1 ? vis.y : vis.x)) o[nt][i][u] = __int_as_float(0x7fc00000);
+            }
           }
       }
     };
@@ -503,16 +545,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float f[2];
+        const float2 sl = scales(nt);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          const float su = u ? sl.y : sl.x;
           float x = fmaxf(s[nt][u], s[nt][u + 2]);
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-          x = fmaxf(x * sl[nt][u], m[nt][u]);
+          x = fmaxf(x * su, m[nt][u]);
           f[u] = x == m[nt][u] ? 1.0f : exp2f(m[nt][u] - x);
           m[nt][u] = x;
-          if (x != kNone) thr[nt][u] = __fdividef(x + kLazy, sl[nt][u]);
+          if (x != kNone) thr[nt][u] = __fdividef(x + kLazy, su);
           l[nt][u] *= f[u];
         }
 #pragma unroll
@@ -542,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
           values(Inner(), st, t0, s[0]);
           values(Inner(), st + C::kSlot, t0 + kSub, s[1]);
         } else {
-#pragma unroll
+#pragma unroll 1
           for (int k = 0; k < 2; ++k) {
             if (__any_sync(~0u, scores(Inner(), st + k * C::kSlot, t0 + k * kSub, s[0]))) raise(s[0]);
             values(Inner(), st + k * C::kSlot, t0 + k * kSub, s[0]);
