@@ -307,8 +307,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   griddep_launch_dependents();
   const uint32_t tmem = bars->tmem;
   int left = (int)(bars->to - bars->from);  // key tiles of this CTA from the current piece on
-  Piece c = {};
-  if (left > 0) {
+  // Each warp's place on the line, in shared memory (its fields are read once an item or a tile:
+  // the registers are the softmax's), moved by one lane.
+  __shared__ Piece s_piece[kThreads / 32];
+  Piece& c = s_piece[warp];
+  if (left > 0 && lane == 0) {
     c.b = bars->start[0];
     c.h = bars->start[1];
     c.qt = bars->start[2];
@@ -317,10 +320,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
     c.tile = bars->start_tile;
     c.end = min(c.tiles, c.tile + left);
   }
+  __syncwarp();
   auto advance = [&]() {  // to the next piece; false behind the last
     left -= c.end - c.tile;
     if (left <= 0) return false;
-    next_piece(p, c, left);
+    __syncwarp();
+    if (lane == 0) next_piece(p, c, left);
+    __syncwarp();
     return true;
   };
 
@@ -404,8 +410,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         const long long at = bars->to - left;
         float m = mine ? kNone : 0.f, l = 0.f;
         if (on) {
+          const int tile0 = c.tile, tile1 = c.end, minvis = c.minvis;
 #pragma unroll 1
-          for (int tile = c.tile; tile < c.end; ++tile, ++tiles_done) {
+          for (int tile = tile0; tile < tile1; ++tile, ++tiles_done) {
             if (!dead && !warp_wait(&bars->s_full[t], tiles_done & 1, bars)) dead = true;
             if (dead) {
               l = __int_as_float(0x7fc00000);
@@ -413,8 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             }
             tc::fence_after_sync();
             const int k0 = tile * kKeys;
-            const uint32_t valid = bars->raw_valid[(all_tiles + tile - c.tile) & 3];
-            const bool edge = k0 + kKeys > c.minvis || valid != 0xFFu;
+            const uint32_t valid = bars->raw_valid[(all_tiles + tile - tile0) & 3];
+            const bool edge = k0 + kKeys > minvis || valid != 0xFFu;
             const int nvis = vis - k0;  // keys [0, nvis) of the tile are seen, where on a page
             auto chunk = [&](int pc, uint32_t (&r)[32]) {
               if (edge) {
@@ -457,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                   }
                   tc::tmem_st16(ts + q * 16, v);
                 }
-                if (tile != c.tile) {  // O of the tiles before: their P.V finished before this S
+                if (tile != tile0) {  // O of the tiles before: their P.V finished before this S
 #pragma unroll 1
                   for (int q = 0; q < D / 16; ++q) {
                     uint32_t v[16];
