@@ -632,6 +632,51 @@ def test_attend_repeats_bit_for_bit_and_on_other_streams():
     assert all(torch.equal(out, x) for x in got)
 
 
+def test_attend_workspace_shared_in_turn():
+    # one workspace for calls of every kernel, in turn, and for two graphs replayed in turn
+    cases = [attend_case(31, [3000, 40], [1, 1], 8, 2, 128, "bf16", 16), attend_case(32, [2000, 300], [100, 70], 8, 2, 128, "bf16", 16),
+             attend_case(33, [2500, 31], [3, 2], 8, 2, 128, "bf16", 16)]
+    want = [run_attend(c) for c in cases]
+    size = max(dkv.dkv_paged_attend_workspace(2, 8, 2, 128, m) for m in (1, 3, 100))
+    ws = torch.full((size,), 0xAB, dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 0, 2, 1, 2, 0):
+        out, lse = run_attend(cases[i], workspace=ws)
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1]), i
+    graphs = []
+    for c in cases:
+        q, out = c["q"].cuda(), torch.full(c["q"].shape, 7.0, dtype=c["q"].dtype, device="cuda")
+        a = (q, *[dev(p) for p in c["pools"]], i32(c["table"]), i32(c["lens"]), out)
+        kw = dict(row_start=i32(c["start"]), max_rows=int(np.diff(c["start"]).max()), workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            dkv.dkv_paged_attend(*a, **kw)
+        graphs.append((g, out, a, kw))
+    for i in (0, 1, 2, 2, 0, 1, 0):
+        graphs[i][1].fill_(7.0)
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(graphs[i][1], want[i][0]), i
+
+
+def test_attend_two_streams_at_once():
+    cases = [attend_case(34, [9000, 40, 7000], [1, 1, 1], 8, 2, 128, "bf16", 16),
+             attend_case(35, [6000, 300], [100, 70], 8, 2, 128, "bf16", 16)]
+    want = [run_attend(c)[0] for c in cases]
+    sets = []
+    for c in cases:
+        out = torch.full(c["q"].shape, 7.0, dtype=c["q"].dtype, device="cuda")
+        kw = dict(row_start=i32(c["start"]), max_rows=int(np.diff(c["start"]).max()), stream=torch.cuda.Stream())
+        sets.append((c["q"].cuda(), *[dev(p) for p in c["pools"]], i32(c["table"]), i32(c["lens"]), out, kw))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for a in sets:
+            dkv.dkv_paged_attend(*a[:-1], **a[-1])
+    torch.cuda.synchronize()
+    for a, w in zip(sets, want):
+        assert torch.equal(a[5], w)
+
+
 def test_attend_many_sequences():
     rng = np.random.default_rng(15)
     lens = rng.integers(0, 40, 1024)

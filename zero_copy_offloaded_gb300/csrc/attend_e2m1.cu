@@ -27,6 +27,19 @@
 // 2^-27 of its row's largest may lose bits).  P is rounded to fp16 (2^-11
 // relative, as the tensor operand must be 16 bits); scores, maxima, sums and
 // outputs stay in fp32.
+//
+// Why mma.sync here: tcgen05 takes at least 128 rows (or columns) a tile and its operands from
+// shared memory, so the converted keys would be written and read there once more.  Sixteen
+// rows of 32/8 heads over 16 x 8192 keys take 122 us in attend_e2m1_tc.cu's kernel, 70 here;
+// 32 rows 125 and 118 (heads of 64: 102 and 71); 33 rows and more go there.
+//
+// What bounds it: reading 9/16 byte an element, 1152 bytes for 16 keys of a head of 128.  The
+// 8 x 32769 keys of 8 heads (302 MB) take 73 us, 4.1 TB/s of 6.8 measured (4 x 131073 keys:
+// 126 us, 4.8 TB/s).  With nothing converted or multiplied the same copies take 62 us, and the
+// conversion and MMAs on resident data 57 us: the two do not overlap fully with 12 warps on
+// an SM.  A sub costs about 260 instructions, 64 of them the conversions of two codes each.
+// 168 registers a thread and three CTAs beat 128 and four (75 and 80 us): with fewer the
+// compiler computes addresses again and again.
 #include <float.h>
 #include <math.h>
 #include <stdio.h>
@@ -52,7 +65,8 @@ constexpr int kSub = 16;                // keys of one MMA, one ring slot
 constexpr int kStep = 2 * kSub;         // keys of one warp step
 constexpr int kTile = kStep * kWarps;   // keys of one tile
 // What an item costs beside its key tiles (its queries, the join of the warps), in tiles: the
-// CTAs' ranges are dealt with it.
+// CTAs' ranges are dealt with it.  48 sequences of up to 8193 keys of 32 heads of 64 take 187 us
+// with 0, 185 with 1, 150 with 3, 154 with 6.
 constexpr int kItemCost = 3;
 constexpr float kLazy = 8.0f;   // the running maximum moves only when passed by 2^8
 constexpr float kNone = -3e38f;  // the running maximum of a row that has seen no key
@@ -79,7 +93,7 @@ struct Cfg {
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1) {
-  asm(
+  asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -88,7 +102,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 

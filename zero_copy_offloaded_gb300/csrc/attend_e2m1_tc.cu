@@ -10,7 +10,8 @@
 // attend_tc_join_kernel merges.
 //
 // Warps (512 threads, one CTA per SM): two softmax groups of four warps, one per Q tile,
-// a thread to a row; four warps that turn codes into fp16 tiles; one that issues every
+// a thread to a row; six warps that turn codes into fp16 tiles (four: 1.67 ms against 1.64 with
+// six); one that issues every
 // MMA; one that fetches the codes (bulk copies, a run of 16 keys each).  The MMA order
 // per key tile is P.V and the next Q.K^T of tile 0, then of tile 1, so one tile's
 // softmax runs under the other tile's MMAs, and a finished Q.K^T also says that the P.V
@@ -23,8 +24,15 @@
 // infinity or NaN, as they do at the start) the row takes their maximum as m and rescales what
 // it has: the tile's earlier weights, l and O.  The largest weight is at least 1 throughout.
 //
-// What bounds it: 4 D flops per (row, key) on the tensor cores; the exponentials
-// (one per row and key) and the conversion of codes run beside them.
+// What bounds it: 4 D flops per (row, key) on the tensor cores.  4096 rows of 32/8 heads of 128
+// over 28672 keys and themselves (2.06 TFLOP) take 1.55 ms, 1327 TFLOP/s of 1912 measured.  A key
+// tile's MMAs are 2048 cycles; what is left is the softmax's latency (about 2000 cycles for a
+// tile's 128 x 128 per group, whose exponentials alone take 1024 of the special-function units),
+// which two Q tiles hide only in part, and shared memory's bandwidth, which the MMAs' operands
+// (192 KB a key tile) and the converted tiles (64 KB) share.  Tensor memory is full (S and O of two
+// tiles), which rules out a third tile and a Q in tensor memory.  Part of the exponentials as
+// polynomials on the FMA pipe, and scores fetched 32 ahead, both cost more registers than
+// they gained (2.2 and 2.3 ms).
 #include <float.h>
 #include <math.h>
 
@@ -824,8 +832,15 @@ __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendParams 
 template <typename T, int D>
 cudaError_t launch_attend_tc(const AttendParams& p, int grid, cudaStream_t s) {
   auto k = attend_tc_kernel<T, D>;
-  const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !attr_set[dev]) {
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr_set[dev] = true;
+  }
   k<<<grid, kThreads, Cfg<D>::kSmem, s>>>(p);
   const cudaError_t l = cudaGetLastError();
   if (l != cudaSuccess) return l;
