@@ -17,8 +17,8 @@
 //
 // What bounds it: each byte once through memory, 26 KB a row of 32/8 heads of 128.  4096 such rows
 // take 29 us (3.7 TB/s of 6.8 measured), 16384 rows of 32/32 fp16 heads of 64, rotated in half
-// and without norms, 86 us (5.2 TB/s): at 75% of the issue slots the norms, quantisation and
-// exact sums are what the first waits for (queries alone 15 us, keys and values alone 14).
+// and without norms, 86 us (5.1 TB/s).  The first has 65% of its issue slots busy: the norms, the
+// exact sums and the quantisation (queries alone take 15 us, keys and values alone 14).
 #include <float.h>
 #include <stdio.h>
 

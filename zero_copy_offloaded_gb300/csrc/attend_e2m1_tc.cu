@@ -10,12 +10,11 @@
 // attend_tc_join_kernel merges.
 //
 // Warps (512 threads, one CTA per SM): two softmax groups of four warps, one per Q tile,
-// a thread to a row; six warps that turn codes into fp16 tiles (four: 1.67 ms against 1.64 with
-// six); one that issues every
-// MMA; one that fetches the codes (bulk copies, a run of 16 keys each).  The MMA order
-// per key tile is P.V and the next Q.K^T of tile 0, then of tile 1, so one tile's
-// softmax runs under the other tile's MMAs, and a finished Q.K^T also says that the P.V
-// before it is finished: O may be rescaled then without a barrier of its own.
+// a thread to a row; six warps that turn codes into fp16 tiles (1.64 ms against 1.67 with four);
+// one that issues every MMA; one that fetches the codes (bulk copies, a run of 16 keys
+// each).  The MMA order per key tile is P.V and the next Q.K^T of tile 0, then of tile 1,
+// so one tile's softmax runs under the other tile's MMAs, and a finished Q.K^T also says
+// that the P.V before it is finished: O may be rescaled then without a barrier of its own.
 //
 // A softmax thread takes its row's scores 32 at a time and writes the weights over columns
 // that it has read.  The running reference m of a row is the maximum of the first 32 scores
@@ -30,9 +29,9 @@
 // tile's 128 x 128 per group, whose exponentials alone take 1024 of the special-function units),
 // which two Q tiles hide only in part, and shared memory's bandwidth, which the MMAs' operands
 // (192 KB a key tile) and the converted tiles (64 KB) share.  Tensor memory is full (S and O of two
-// tiles), which rules out a third tile and a Q in tensor memory.  Part of the exponentials as
-// polynomials on the FMA pipe, and scores fetched 32 ahead, both cost more registers than
-// they gained (2.2 and 2.3 ms).
+// tiles), which rules out a third tile and a Q in tensor memory.  Five of sixteen exponentials as
+// degree-4 polynomials on the FMA pipe took 2.20 ms where all of them on the special-function units
+// took 1.86.
 #include <float.h>
 #include <math.h>
 
@@ -55,17 +54,6 @@ constexpr float kNone = -3e38f;        // m of a row that has seen no key
 constexpr float kSumBound = 32768.f;
 
 constexpr uint32_t kTmS = 0, kTmO = 256;  // S of tile t at 128 t, O at 256 + 128 t
-
-// Registers per thread: 128 at launch, then 168 for the softmax groups, 96 for the conversion
-// and 80 for the last four warps: 4 x 128 = 2 x 168 + 96 + 80.
-template <int N>
-__device__ __forceinline__ void more_regs() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_regs() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 template <int D>
 struct Cfg {
