@@ -44,6 +44,7 @@
 #include <math.h>
 #include <stdio.h>
 
+#include <algorithm>
 #include <atomic>
 #include <chrono>
 #include <type_traits>
@@ -68,6 +69,9 @@ constexpr int kTile = kStep * kWarps;   // keys of one tile
 // CTAs' ranges are dealt with it.  48 sequences of up to 8193 keys of 32 heads of 64 take 187 us
 // with 0, 185 with 1, 150 with 3, 154 with 6.
 constexpr int kItemCost = 3;
+// Pieces joined at once, and to a group beyond that (456 pieces: 29 groups of 16).
+constexpr int kJoinOnce = 32, kGroup = 16;
+constexpr int kSms = 152, kMaxCtas = 3 * kSms;
 constexpr float kLazy = 8.0f;   // the running maximum moves only when passed by 2^8
 constexpr float kNone = -3e38f;  // the running maximum of a row that has seen no key
 
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   uint2* s_q = reinterpret_cast<uint2*>(smem + C::kOffQ);
   float* s_scale = reinterpret_cast<float*>(smem + C::kOffQ + C::kQueries);
   int* s_vis = reinterpret_cast<int*>(s_scale + R);
-  __shared__ int s_join[2];
+  __shared__ int s_join[3];
   long long* s_pre = reinterpret_cast<long long*>(smem + C::kOffBatch);  // [B + 1]
   int* s_kv = reinterpret_cast<int*>(s_pre + p.B + 1);                   // [B]
   int* s_row = s_kv + p.B;                                               // [B]
@@ -692,42 +696,52 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       }
     }
     if (!whole) {
-      // ---- the CTA that finishes an item's last open piece joins them all, in CTA order.  The
-      // count of finished pieces needs no clearing before the call: it stands beside the
-      // call's own tag and starts from nothing wherever another tag is found.
-      __syncthreads();
+      // ---- the CTA that finishes an item's last open piece joins them all, in CTA order.  An
+      // item in many pieces is joined in two levels, first each kGroup consecutive pieces by the
+      // CTA that finishes last among them, so that no CTA reads more than a few dozen.
       if (threadIdx.x == 0) {
         const long long first_unit =
             s_pre[b] + ((long long)h * cons.qtiles + qt) * (cons.tiles + kItemCost) + kItemCost;
-        const int c0 = owner(first_unit), pieces = owner(first_unit + cons.tiles - 1) - c0 + 1;
-        __threadfence();
-        unsigned long long* word = p.done + c0;
-        const unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(word);
-        if ((seen ^ p.tag) >> 16) atomicCAS(word, seen, p.tag);
-        const bool final_piece = (int)(atomicAdd(word, 1ull) & 0xFFFF) == pieces - 1;
-        if (final_piece) *word = 0;
-        __threadfence();
-        s_join[0] = final_piece ? c0 : -1;
-        s_join[1] = pieces;
+        s_join[0] = owner(first_unit);
+        s_join[1] = owner(first_unit + cons.tiles - 1) - s_join[0] + 1;
       }
       __syncthreads();
       const int c0 = s_join[0], pieces = s_join[1];
-      if (c0 >= 0)
+      // piece i lies in slot 2 (c0 + i), but the first in slot 2 c0 + 1
+      auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0); };
+      // this CTA's part is stored: one more of `parts` at a counter; whether it was the last
+      auto finish = [&](unsigned long long* word, int parts) {
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          __threadfence();
+          const unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(word);
+          // the count needs no clearing before the call: it stands beside the call's own tag and
+          // starts from nothing wherever another tag is found
+          if ((seen ^ p.tag) >> 16) atomicCAS(word, seen, p.tag);
+          const bool final_part = (int)(atomicAdd(word, 1ull) & 0xFFFF) == parts - 1;
+          if (final_part) *word = 0;
+          __threadfence();
+          s_join[2] = final_part;
+        }
+        __syncthreads();
+        return s_join[2] != 0;
+      };
+      // joins pieces at, at + stride, ...: `count` of them, into the outputs or into piece `at`
+      auto join = [&](int at, int stride, int count, bool out) {
         for (int r = warp; r < rows; r += kWarps) {
-          // piece i lies in slot 2 (c0 + i), but the first in slot 2 c0 + 1
-          auto at = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0)) * R + r; };
+          auto place = [&](int i) { return (size_t)slot_of(at + i * stride) * R + r; };
           const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
           float top = -INFINITY, sum = 0.f, acc[V];
-          for (int i = lane; i < pieces; i += 32) top = fmaxf(top, __ldcg(ml + at(i)).x);
+          for (int i = lane; i < count; i += 32) top = fmaxf(top, __ldcg(ml + place(i)).x);
 #pragma unroll
           for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
 #pragma unroll
           for (int e = 0; e < V; ++e) acc[e] = 0.f;
-          for (int base = 0; base < pieces; base += 32) {
-            const int k = min(32, pieces - base);
+          for (int base = 0; base < count; base += 32) {
+            const int k = min(32, count - base);
             float f = 0.f, part = 0.f;
             if (lane < k) {
-              const float2 x = __ldcg(ml + at(base + lane));
+              const float2 x = __ldcg(ml + place(base + lane));
               f = x.x == top ? 1.0f : exp2f(x.x - top);
               part = x.y * f;
             }
@@ -738,14 +752,32 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
             for (int i = 0; i < k; ++i) {
               const float fi = __shfl_sync(~0u, f, i);
               float v[V];
-              load_vec<V>(p.part_o + at(base + i) * D + d0, v);
+              load_vec<V>(p.part_o + place(base + i) * D + d0, v);
 #pragma unroll
               for (int e = 0; e < V; ++e) acc[e] = fmaf(v[e], fi, acc[e]);
             }
           }
-          const int pr = qt * R + r;
-          store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, top, sum, lane == 0);
+          if (out) {
+            const int pr = qt * R + r;
+            store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, top, sum, lane == 0);
+          } else {  // the row's loads above are all done: a warp has a row to itself
+            __syncwarp();
+            store_vec<V>(p.part_o + place(0) * D + d0, acc);
+            if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + place(0) * 2) = make_float2(top, sum);
+          }
         }
+      };
+      unsigned long long* whole_item = p.done + 2 * kMaxCtas + c0;
+      if (pieces <= kJoinOnce) {
+        if (finish(whole_item, pieces)) join(0, 1, pieces, true);
+      } else {
+        const int first = ((int)blockIdx.x - c0) / kGroup * kGroup, size = min(kGroup, pieces - first);
+        if (finish(p.done + slot_of(first), size)) {
+          join(first, 1, size, false);
+          const int groups = (pieces + kGroup - 1) / kGroup;
+          if (finish(whole_item, groups)) join(0, kGroup, groups, true);
+        }
+      }
     }
     __syncthreads();  // s_m, s_l, merge and s_join are free for the next piece
     left -= tile1 - tile0 - 1;
@@ -761,13 +793,11 @@ dkv_status refuse(dkv_status s, const char* msg) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-constexpr int kSms = 152;
-constexpr int kMaxCtas = 3 * kSms;
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace: descriptors | partial (max, sum) | partial o, two slots per CTA.
-size_t ws_desc() { return align256(kMaxCtas * (sizeof(AttendDesc) > 8 ? sizeof(AttendDesc) : 8)); }
+// Workspace: descriptors or counts | partial (max, sum) | partial o, two slots per CTA.
+size_t ws_desc() { return align256(std::max(kMaxCtas * sizeof(AttendDesc), 3 * kMaxCtas * sizeof(unsigned long long))); }
 
 // The tag of a call: 48 bits that no earlier call of this process had, scattered so that memory
 // left by anything else does not hold one.

@@ -26,7 +26,8 @@ struct AttendParams {
   void* out;
   float* lse;
   AttendDesc* desc;             // many rows: by CTA
-  unsigned long long* done;     // few rows: finished pieces of the item that a CTA began
+  unsigned long long* done;     // few rows: finished pieces, by slot of a group's first one and by the
+                                // CTA that began the item
   unsigned long long tag;       // the call's own, in the upper 48 bits
   float* part_ml;
   float* part_o;
