@@ -7,13 +7,14 @@
 
 namespace dkv {
 
-// The item that a CTA began and left unfinished.
+// The item that a CTA left unfinished: one that it began, or one that fills it.
 struct AttendDesc {
-  int pieces;           // how many CTAs hold it, this one first; 0: there is none
+  int pieces;           // how many CTAs hold it; 0: there is none
+  int begin;            // the first of them
   int row0;             // first query row of the sequence
   int first, last;      // packed rows (token-major over the group's heads) of the item
   int head0;            // first query head of the group
-  int pad[3];
+  int pad[2];
 };
 
 struct AttendParams {

@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         const int vis = mine ? max(0, c.kv - c.n + pr / G + 1) : 0;
         const bool starts = c.tile == 0, ends = c.end == c.tiles;
         const int h = c.h, row0 = c.row0, first = c.qt * 2 * kRows, last = c.last, b_tiles = c.tiles;
-        const long long at = bars->to - left;
+        const long long at = bars->to - left - c.tile;  // where the item begins on the line
         float m = mine ? kNone : 0.f, l = 0.f;
         if (on) {
           const int tile0 = c.tile, tile1 = c.end, minvis = c.minvis;
@@ -554,10 +554,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           tc::fence_before_sync();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars->o_free[t]);
-          if (starts && !ends && threadIdx.x == 0) {
+          if (!ends && threadIdx.x == 0) {
             AttendDesc d;
-            const long long end = at + b_tiles - 1;  // the item's last key tile, and the CTA that holds it
-            d.pieces = (int)(((end + 1) * bars->ctas - 1) / bars->total) - (int)blockIdx.x + 1;
+            auto holder = [&](long long tile) { return (int)(((tile + 1) * bars->ctas - 1) / bars->total); };
+            d.begin = holder(at);
+            d.pieces = holder(at + b_tiles - 1) - d.begin + 1;
             d.row0 = row0; d.first = first; d.last = last; d.head0 = h * G;
             p.desc[blockIdx.x] = d;
           }
@@ -778,41 +779,86 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
   if (warp == 8 + kConvert) tc::tmem_dealloc(tmem, 512);
 }
 
-// Joins the partials of each cut item: block (c, y) takes 32 rows of the item that CTA c began and
-// left unfinished, a row to a lane, D/8 outputs to each of eight warps.
+// Joins the partials of each cut item.  An item in few pieces: block (c, y) takes 32 rows, a row
+// to a lane, of the item that CTA c began, and each of its eight warps D / 8 outputs.  An item
+// in more pieces than 32-output parts of a row: the blocks of the CTAs that it fills take a part
+// each, their warps every eighth piece, and the eight meet in shared memory.  (One block a CTA's
+// rows for all pieces took 52 us of 82 for 16 rows of one KV head over 131072 keys.)
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendParams p) {
+  __shared__ float4 s_acc[8][8][32];  // [warp][four outputs][row]
+  __shared__ float2 s_ml[8][32];
   griddep_wait();
   const AttendDesc d = p.desc[blockIdx.x];
-  const int r = blockIdx.y * 32 + (threadIdx.x & 31), pr = d.first + r;
-  if (d.pieces < 2 || pr > d.last) return;
-  constexpr int Q = D / 32;  // groups of four outputs per thread
-  const int q0 = (threadIdx.x >> 5) * Q;
+  constexpr int kParts = D / 32;
+  const int rank = (int)blockIdx.x - d.begin;  // among the CTAs that hold the item
+  const bool many = d.pieces > kParts;
+  if (d.pieces < 2 || rank >= (many ? kParts : 1) || d.first + (int)blockIdx.y * 32 > d.last) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, r = blockIdx.y * 32 + lane, pr = d.first + r;
   // piece i lies in slot 2 (c + i), but the first in slot 2 c + 1
-  auto slot = [&](int i) { return (size_t)(2 * (blockIdx.x + i) + (i == 0)); };
+  auto slot = [&](int i) { return (size_t)(2 * (d.begin + i) + (i == 0)); };
   const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+  const float4* po = reinterpret_cast<const float4*>(p.part_o);
   float top = -INFINITY, sum = 0.f;
-#pragma unroll 8
-  for (int i = 0; i < d.pieces; ++i) top = fmaxf(top, ml[slot(i) * kTcRows + r].x);
-  float acc[4 * Q];
+  auto add = [](float4& a, const float4& v, float f) {
+    a.x = fmaf(v.x, f, a.x);
+    a.y = fmaf(v.y, f, a.y);
+    a.z = fmaf(v.z, f, a.z);
+    a.w = fmaf(v.w, f, a.w);
+  };
+  auto store = [&]<int W>(const float4 (&a)[W], int q) {
+    if (pr > d.last) return;
+    float o[4 * W];
 #pragma unroll
-  for (int e = 0; e < 4 * Q; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = 0; i < d.pieces; ++i) {
-    const float2 x = ml[slot(i) * kTcRows + r];
+    for (int k = 0; k < W; ++k) o[4 * k] = a[k].x, o[4 * k + 1] = a[k].y, o[4 * k + 2] = a[k].z, o[4 * k + 3] = a[k].w;
+    store_row<T, 4 * W>(p, d.row0 + pr / p.G, d.head0 + pr % p.G, D, 4 * q, o, top, sum, q == 0);
+  };
+  if (!many) {
+    constexpr int W = D / 32;  // its outputs in fours
+    float4 a[W] = {};
+#pragma unroll
+    for (int i = 0; i < kParts; ++i)
+      if (i < d.pieces) top = fmaxf(top, ml[slot(i) * kTcRows + r].x);
+#pragma unroll
+    for (int i = 0; i < kParts; ++i) {
+      if (i >= d.pieces) break;
+      const float2 x = ml[slot(i) * kTcRows + r];
+      const float f = x.x == top ? 1.0f : exp2f(x.x - top);
+      sum = fmaf(x.y, f, sum);
+#pragma unroll
+      for (int k = 0; k < W; ++k) add(a[k], po[(slot(i) * (D / 4) + warp * W + k) * kTcRows + r], f);
+    }
+    store(a, warp * W);
+    return;
+  }
+  const int q0 = rank * 8;
+  float t = -INFINITY, l = 0.f;
+  for (int i = warp; i < d.pieces; i += 8) t = fmaxf(t, ml[slot(i) * kTcRows + r].x);
+  {
+    float4 a[8] = {};
+    for (int i = warp; i < d.pieces; i += 8) {
+      const float2 x = ml[slot(i) * kTcRows + r];
+      const float f = x.x == t ? 1.0f : exp2f(x.x - t);
+      l = fmaf(x.y, f, l);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) add(a[q], po[(slot(i) * (D / 4) + q0 + q) * kTcRows + r], f);
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s_acc[warp][q][lane] = a[q];
+    s_ml[warp][lane] = make_float2(t, l);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, s_ml[w][lane].x);
+  float4 a[1] = {};
+#pragma unroll
+  for (int w = 0; w < 8; ++w) {
+    const float2 x = s_ml[w][lane];
     const float f = x.x == top ? 1.0f : exp2f(x.x - top);
     sum = fmaf(x.y, f, sum);
-    const float4* o = reinterpret_cast<const float4*>(p.part_o) + (slot(i) * (D / 4) + q0) * kTcRows + r;
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      const float4 v = o[(size_t)q * kTcRows];
-      acc[4 * q] = fmaf(v.x, f, acc[4 * q]);
-      acc[4 * q + 1] = fmaf(v.y, f, acc[4 * q + 1]);
-      acc[4 * q + 2] = fmaf(v.z, f, acc[4 * q + 2]);
-      acc[4 * q + 3] = fmaf(v.w, f, acc[4 * q + 3]);
-    }
+    add(a[0], s_acc[w][warp][lane], f);
   }
-  store_row<T, 4 * Q>(p, d.row0 + pr / p.G, d.head0 + pr % p.G, D, q0 * 4, acc, top, sum, q0 == 0);
+  store(a, q0 + warp);
 }
 
 }  // namespace
