@@ -726,44 +726,53 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
         __syncthreads();
         return s_join[2] != 0;
       };
-      // joins pieces at, at + stride, ...: `count` of them, into the outputs or into piece `at`
+      // joins pieces at, at + stride, ...: `count` of them (at most 32), into the outputs or into
+      // piece `at`; a warp takes every fourth row, all of them at once, so that their loads
+      // are in flight together
       auto join = [&](int at, int stride, int count, bool out) {
-        for (int r = warp; r < rows; r += kWarps) {
-          auto place = [&](int i) { return (size_t)slot_of(at + i * stride) * R + r; };
-          const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
-          float top = -INFINITY, sum = 0.f, acc[V];
-          for (int i = lane; i < count; i += 32) top = fmaxf(top, __ldcg(ml + place(i)).x);
+        constexpr int RW = R / kWarps;
+        auto place = [&](int i, int k) { return (size_t)slot_of(at + i * stride) * R + warp + k * kWarps; };
+        const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
+        float2 x[RW];
+        float f[RW], top[RW], acc[RW][V];
 #pragma unroll
-          for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, w));
+        for (int k = 0; k < RW; ++k)
+          x[k] = lane < count && warp + k * kWarps < rows ? __ldcg(ml + place(lane, k)) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-          for (int e = 0; e < V; ++e) acc[e] = 0.f;
-          for (int base = 0; base < count; base += 32) {
-            const int k = min(32, count - base);
-            float f = 0.f, part = 0.f;
-            if (lane < k) {
-              const float2 x = __ldcg(ml + place(base + lane));
-              f = x.x == top ? 1.0f : exp2f(x.x - top);
-              part = x.y * f;
-            }
+        for (int k = 0; k < RW; ++k) {
+          top[k] = x[k].x;
 #pragma unroll
-            for (int w = 16; w; w >>= 1) part += __shfl_xor_sync(~0u, part, w);
-            sum += part;
-#pragma unroll 8
-            for (int i = 0; i < k; ++i) {
-              const float fi = __shfl_sync(~0u, f, i);
+          for (int w = 16; w; w >>= 1) top[k] = fmaxf(top[k], __shfl_xor_sync(~0u, top[k], w));
+          f[k] = x[k].x == top[k] ? 1.0f : exp2f(x[k].x - top[k]);
+          x[k].y *= f[k];
+#pragma unroll
+          for (int w = 16; w; w >>= 1) x[k].y += __shfl_xor_sync(~0u, x[k].y, w);
+#pragma unroll
+          for (int e = 0; e < V; ++e) acc[k][e] = 0.f;
+        }
+#pragma unroll(16 / RW)
+        for (int i = 0; i < count; ++i) {
+#pragma unroll
+          for (int k = 0; k < RW; ++k) {
+            const float fi = __shfl_sync(~0u, f[k], i);
+            if (warp + k * kWarps < rows) {
               float v[V];
-              load_vec<V>(p.part_o + place(base + i) * D + d0, v);
+              load_vec<V>(p.part_o + place(i, k) * D + d0, v);
 #pragma unroll
-              for (int e = 0; e < V; ++e) acc[e] = fmaf(v[e], fi, acc[e]);
+              for (int e = 0; e < V; ++e) acc[k][e] = fmaf(v[e], fi, acc[k][e]);
             }
           }
+        }
+#pragma unroll
+        for (int k = 0; k < RW; ++k) {
+          const int r = warp + k * kWarps, pr = qt * R + r;
+          if (r >= rows) break;
           if (out) {
-            const int pr = qt * R + r;
-            store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, top, sum, lane == 0);
+            store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc[k], top[k], x[k].y, lane == 0);
           } else {  // the row's loads above are all done: a warp has a row to itself
             __syncwarp();
-            store_vec<V>(p.part_o + place(0) * D + d0, acc);
-            if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + place(0) * 2) = make_float2(top, sum);
+            store_vec<V>(p.part_o + place(0, k) * D + d0, acc[k]);
+            if (lane == 0) *reinterpret_cast<float2*>(p.part_ml + place(0, k) * 2) = make_float2(top[k], x[k].y);
           }
         }
       };
