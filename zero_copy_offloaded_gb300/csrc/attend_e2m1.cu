@@ -84,11 +84,11 @@ struct Cfg {
   static constexpr int kOffScale = 2 * kC;
   static constexpr int kSteps = D == 128 ? 3 : 4;    // steps in a warp's ring
   static constexpr int kRing = 2 * kSteps * kSlot;   // per warp
-  static constexpr int kMerge = kWarps * 8 * (D + 8) * 4;  // one 8-row round of every warp's O
+  static constexpr int kMerge = kWarps * 8 * D * 4;  // one 8-row round of every warp's O
   static constexpr int kOffMerge = kWarps * kRing;
-  static constexpr int kOffMl = kOffMerge + kMerge;          // [2][kWarps][R] floats
+  static constexpr int kOffMl = kOffMerge + kMerge;          // m, l and factor [kWarps][R], m and l [R]
   static constexpr int kQueries = NT > 1 ? NT * (D / 16) * 32 * 8 : 0;  // B fragments of the rows
-  static constexpr int kOffQ = kOffMl + 2 * kWarps * R * 4;             // and their scales, visible keys
+  static constexpr int kOffQ = kOffMl + (3 * kWarps + 2) * R * 4;       // and their scales, visible keys
   static constexpr int kOffBatch = kOffQ + kQueries + (NT > 1 ? 2 * R * 4 : 0);
   // resident CTAs per SM, by registers: o takes 4 NT D/16 of a thread's
   static constexpr int kPerSm = NT == 1 || (NT <= 3 && D == 64) ? 3 : 2;
@@ -123,6 +123,16 @@ template <int V>
 __device__ __forceinline__ void store_vec(float* to, const float (&x)[V]) {
   if constexpr (V == 4) *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
   else *reinterpret_cast<float2*>(to) = make_float2(x[0], x[1]);
+}
+template <int V>
+__device__ __forceinline__ void load_shared(const float* from, float (&x)[V]) {
+  if constexpr (V == 4) {
+    const float4 y = *reinterpret_cast<const float4*>(from);
+    x[0] = y.x; x[1] = y.y; x[2] = y.z; x[3] = y.w;
+  } else {
+    const float2 y = *reinterpret_cast<const float2*>(from);
+    x[0] = y.x; x[1] = y.y;
+  }
 }
 // From L2: another SM wrote it during this kernel.
 template <int V>
@@ -161,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   uint8_t* ring = smem + warp * C::kRing;
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
   float* s_m = reinterpret_cast<float*>(smem + C::kOffMl);
-  float* s_l = s_m + kWarps * R;
+  float *s_l = s_m + kWarps * R, *s_f = s_l + kWarps * R, *s_top = s_f + kWarps * R, *s_sum = s_top + R;
   uint2* s_q = reinterpret_cast<uint2*>(smem + C::kOffQ);
   float* s_scale = reinterpret_cast<float*>(smem + C::kOffQ + C::kQueries);
   int* s_vis = reinterpret_cast<int*>(s_scale + R);
@@ -326,6 +336,24 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     const int last = min((qt + 1) * R, n * G) - 1;  // last packed row of the item
     const int minvis = max(0, kv - n + (qt * R) / G + 1), maxvis = max(0, kv - n + last / G + 1);
 
+    // A piece of a cut item: which CTAs hold it, and the counter of its finished pieces, which
+    // stands beside the call's own tag and starts from nothing wherever another tag is found,
+    // so that it needs no clearing before the call.  The tag is set here, while nothing waits.
+    const bool cut = tile0 > 0 || tile1 < cons.tiles;
+    // piece i lies in slot 2 (c0 + i), but the first in slot 2 c0 + 1
+    auto slot_of = [&](int c0, int i) { return 2 * (c0 + i) + (i == 0); };
+    unsigned long long *counter = nullptr, seen = 0;  // of thread 0
+    if (cut && threadIdx.x == 0) {
+      const long long first_unit =
+          s_pre[b] + ((long long)h * cons.qtiles + qt) * (cons.tiles + kItemCost) + kItemCost;
+      const int c0 = owner(first_unit), pieces = owner(first_unit + cons.tiles - 1) - c0 + 1;
+      s_join[0] = c0;
+      s_join[1] = pieces;
+      counter = pieces <= kJoinOnce ? p.done + 2 * kMaxCtas + c0
+                                    : p.done + slot_of(c0, ((int)blockIdx.x - c0) / kGroup * kGroup);
+      seen = *reinterpret_cast<volatile unsigned long long*>(counter);
+    }
+
     // Queries as B fragments: eight rows in registers, more in shared memory, where each warp
     // prepares some groups of eight for all.
     constexpr bool QS = C::kQueries > 0;
@@ -405,6 +433,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     auto visible = [&](int nt) {
       return QS ? *reinterpret_cast<const int2*>(s_vis + nt * 8 + 2 * c) : make_int2(vis1[0], vis1[1]);
     };
+
+    auto tag = [&](unsigned long long* word, unsigned long long was) {
+      if ((was ^ p.tag) >> 16) atomicCAS(word, was, p.tag);
+    };
+    if (cut && threadIdx.x == 0) tag(counter, seen);
 
     // running maximum (base 2, scaled), the raw score that moves it, sum, output
     float m[NT][2], thr[NT][2], l[NT][2], o[NT][J][4];
@@ -626,6 +659,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     }
 
     // ---- the piece's end: join the warps --------------------------------------
+    // This runs once a piece and mostly waits for its own instructions: loops stay rolled where
+    // they can, and the rows of a round are moved to where the one copy of its code takes them.
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -639,85 +674,89 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
           s_l[warp * R + nt * 8 + 2 * c + u] = x;
         }
       }
-    constexpr int V = D / 32, RS = D + 8;  // outputs of a lane; padded row of the merge buffer
+    __syncthreads();
+    if (threadIdx.x < kWarps * R) {  // what a warp's part of a row counts against the CTA's maximum
+      const int r = threadIdx.x % R;
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * R + r]);
+#pragma unroll 1
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = s_m[w * R + r], f = mw == top ? 1.0f : exp2f(mw - top);
+        sum += s_l[w * R + r] * f;
+        if (threadIdx.x == w * R + r) s_f[w * R + r] = f;
+      }
+      if (threadIdx.x < R) {
+        s_top[r] = top;
+        s_sum[r] = sum;
+      }
+    }
+    constexpr int V = D / 32;  // outputs of a lane
     const bool starts = tile0 == 0, ends = tile1 == cons.tiles, whole = starts && ends;
     const int slot = 2 * blockIdx.x + (starts ? 1 : 0), rows = last - qt * R + 1, d0 = lane * V;
 #pragma unroll 1
-    for (int nt = 0; nt < NT; ++nt) {
-      if (nt * 8 >= rows) break;
+    for (int r0 = 0; r0 < rows; r0 += 8) {
+      // Eight rows of every warp, a row's pair i of the D/8 dims of thread group g at place
+      // J g + (i ^ x), x from the row and g: neither these stores nor the loads below meet a
+      // bank conflict (with plain padded rows a round took 1600 cycles, two thirds of them for conflicts).
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int i = 0; i < J; ++i)
+          reinterpret_cast<float2*>(merge)[(warp * 8 + 2 * c + u) * (D / 2) + J * g +
+                                           (i ^ (D == 128 ? (g >> 1 & 1) | c << 1 : c))] =
+              make_float2(o[0][i][u], o[0][i][u + 2]);
       __syncthreads();
-      // this warp's rows against the CTA's maximum; dims 16 g + 2 i, + 1 lie at 16 i + 2 g
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int r = nt * 8 + 2 * c + u;
-        if (r < rows) {
-          float top = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * R + r]);
-          const float mine = s_m[warp * R + r], f = mine == top ? 1.0f : exp2f(mine - top);
-#pragma unroll
-          for (int n2 = 0; n2 < NT; ++n2)
-            if (n2 == nt) {
-#pragma unroll
-              for (int i = 0; i < J; ++i)
-                *reinterpret_cast<float2*>(merge + (warp * 8 + 2 * c + u) * RS + 16 * i + 2 * g) =
-                    make_float2(o[n2][i][u] * f, o[n2][i][u + 2] * f);
-            }
-        }
-      }
-      __syncthreads();
-      for (int r = nt * 8 + warp; r < min(rows, nt * 8 + 8); r += kWarps) {
+#pragma unroll 1
+      for (int r = r0 + warp; r < min(rows, r0 + 8); r += kWarps) {
         const int pr = qt * R + r;
-        float acc[V], top = -INFINITY, sum = 0.f;
+        float acc[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w * R + r]);
-#pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          const float mw = s_m[w * R + r];
-          sum += s_l[w * R + r] * (mw == top ? 1.0f : exp2f(mw - top));
-          // dims d0 .. d0 + V - 1 of row r (D/8 dims to a g, in pairs)
+          const float f = s_f[w * R + r];
+          const int rl = r - r0;
+          float x[V];
+          load_shared<V>(merge + (w * 8 + rl) * D + g * (2 * J) + (c ^ rl >> 1) * V, x);
 #pragma unroll
-          for (int e = 0; e < V; e += 2) {
-            const int gd = (d0 + e) / (D / 8), i = (d0 + e) % (D / 8) / 2;
-            const float2 x = *reinterpret_cast<const float2*>(merge + (w * 8 + r - nt * 8) * RS + 16 * i + 2 * gd);
-            acc[e] += x.x;
-            acc[e + 1] += x.y;
-          }
+          for (int e = 0; e < V; ++e) acc[e] = fmaf(x[e], f, acc[e]);
+        }
+        if (D == 128 && (lane & 8)) {  // its two pairs lie the other way round
+          const float a0 = acc[0], a1 = acc[1];
+          acc[0] = acc[V - 2];
+          acc[1] = acc[V - 1];
+          acc[V - 2] = a0;
+          acc[V - 1] = a1;
         }
         if (whole) {
-          store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, top, sum, lane == 0);
+          store_row<T, V>(p, row0 + pr / G, h * G + pr % G, D, d0, acc, s_top[r], s_sum[r], lane == 0);
         } else {
           store_vec<V>(p.part_o + ((size_t)slot * R + r) * D + d0, acc);
           if (lane == 0)
-            *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * R + r) * 2) = make_float2(top, sum);
+            *reinterpret_cast<float2*>(p.part_ml + ((size_t)slot * R + r) * 2) = make_float2(s_top[r], s_sum[r]);
         }
+      }
+      if constexpr (NT > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt + 1 < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < J; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) o[nt][i][u] = o[nt + 1][i][u];
       }
     }
     if (!whole) {
       // ---- the CTA that finishes an item's last open piece joins them all, in CTA order.  An
       // item in many pieces is joined in two levels, first each kGroup consecutive pieces by the
       // CTA that finishes last among them, so that no CTA reads more than a few dozen.
-      if (threadIdx.x == 0) {
-        const long long first_unit =
-            s_pre[b] + ((long long)h * cons.qtiles + qt) * (cons.tiles + kItemCost) + kItemCost;
-        s_join[0] = owner(first_unit);
-        s_join[1] = owner(first_unit + cons.tiles - 1) - s_join[0] + 1;
-      }
-      __syncthreads();
       const int c0 = s_join[0], pieces = s_join[1];
-      // piece i lies in slot 2 (c0 + i), but the first in slot 2 c0 + 1
-      auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0); };
-      // this CTA's part is stored: one more of `parts` at a counter; whether it was the last
+      // this CTA's part is stored: one more of `parts` at a tagged counter; whether it was the last
       auto finish = [&](unsigned long long* word, int parts) {
         __syncthreads();
         if (threadIdx.x == 0) {
           __threadfence();
-          const unsigned long long seen = *reinterpret_cast<volatile unsigned long long*>(word);
-          // the count needs no clearing before the call: it stands beside the call's own tag and
-          // starts from nothing wherever another tag is found
-          if ((seen ^ p.tag) >> 16) atomicCAS(word, seen, p.tag);
           const bool final_part = (int)(atomicAdd(word, 1ull) & 0xFFFF) == parts - 1;
           if (final_part) *word = 0;
           __threadfence();
@@ -731,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       // are in flight together
       auto join = [&](int at, int stride, int count, bool out) {
         constexpr int RW = R / kWarps;
-        auto place = [&](int i, int k) { return (size_t)slot_of(at + i * stride) * R + warp + k * kWarps; };
+        auto place = [&](int i, int k) { return (size_t)slot_of(c0, at + i * stride) * R + warp + k * kWarps; };
         const float2* ml = reinterpret_cast<const float2*>(p.part_ml);
         float2 x[RW];
         float f[RW], top[RW], acc[RW][V];
@@ -778,10 +817,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       };
       unsigned long long* whole_item = p.done + 2 * kMaxCtas + c0;
       if (pieces <= kJoinOnce) {
-        if (finish(whole_item, pieces)) join(0, 1, pieces, true);
+        if (finish(counter, pieces)) join(0, 1, pieces, true);
       } else {
         const int first = ((int)blockIdx.x - c0) / kGroup * kGroup, size = min(kGroup, pieces - first);
-        if (finish(p.done + slot_of(first), size)) {
+        if (finish(counter, size)) {
+          if (threadIdx.x == 0) tag(whole_item, *reinterpret_cast<volatile unsigned long long*>(whole_item));
           join(first, 1, size, false);
           const int groups = (pieces + kGroup - 1) / kGroup;
           if (finish(whole_item, groups)) join(0, kGroup, groups, true);
