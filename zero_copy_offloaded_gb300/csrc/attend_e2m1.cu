@@ -92,7 +92,9 @@ struct Cfg {
   static constexpr int kOffBatch = kOffQ + kQueries + (NT > 1 ? 2 * R * 4 : 0);
   // resident CTAs per SM, by registers: o takes 4 NT D/16 of a thread's
   static constexpr int kPerSm = NT == 1 || (NT <= 3 && D == 64) ? 3 : 2;
-  static constexpr int kBoth = NT == 1 ? 2 : 1;  // subs in flight at once
+  // subs in flight at once: 20 rows over 16 x 32768 keys of 8 heads of 128 take 214 us with two, 225
+  // with one; of 64 141 and 142; four groups of rows have no registers for it
+  static constexpr int kBoth = NT == 1 || (NT <= 3 && D == 128) ? 2 : 1;
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
