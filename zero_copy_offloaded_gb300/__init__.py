@@ -435,24 +435,25 @@ def _arg(t, what, dtype, index, shape=None):
 
 def _rows(t, what, dtype, index, rows, D):
     """Address, heads and token stride of [rows, heads, D] whose heads are contiguous in each row."""
-    if t.dim() != 3 or t.shape[0] != rows or t.shape[2] != D:
-        raise ValueError(f"{what} has shape {tuple(t.shape)}: [{rows}, heads, {D}] is wanted")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != rows or shape[2] != D:
+        raise ValueError(f"{what} has shape {tuple(shape)}: [{rows}, heads, {D}] is wanted")
     if t.dtype != dtype or t.get_device() != index:
         _bad(t, what, dtype, index, None)
-    h, st = t.shape[1], t.stride()
+    h, st = shape[1], t.stride()
     if st[2] != 1 or (h > 1 and st[1] != D):
         raise ValueError(f"the heads of a row of {what} must be contiguous")
     return t.data_ptr(), h, (st[0] if rows > 1 else h * D)
 
 
-def _pool(t, what, index, D):
+def _pool(t, what, u8, index, D):
     """Address and (num_pages, n_kv_heads, page_tokens) of an E2M1 pool: CUDA, or pinned host memory."""
-    import torch
-    if t.dtype != torch.uint8 or t.dim() != 3 or not t.is_contiguous():
+    shape = t.shape
+    if t.dtype != u8 or len(shape) != 3 or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous uint8 [num_pages, n_kv_heads, page bytes]")
     if t.get_device() != index and not (t.get_device() < 0 and t.is_pinned()):
         raise ValueError(f"{what} is neither with the other tensors nor in pinned host memory")
-    pages, heads, nbytes = t.shape
+    pages, heads, nbytes = shape
     per = D * 9 // 16
     if nbytes % per:
         raise ValueError(f"{what}: a page of {nbytes} bytes does not hold rows of {per}")
@@ -544,8 +545,8 @@ def dkv_qkv_append(q, k, v, positions=None, slots=None, k_pool=None, v_pool=None
     if k_pool is not None:
         if v_pool is None or k is None:
             raise ValueError("both pools and the keys come together")
-        pkp, shape = _pool(k_pool, "k_pool", dev, D)
-        pvp, other = _pool(v_pool, "v_pool", dev, D)
+        pkp, shape = _pool(k_pool, "k_pool", torch.uint8, dev, D)
+        pvp, other = _pool(v_pool, "v_pool", torch.uint8, dev, D)
         if shape != other or shape[1] != hkv:
             raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens) for {hkv} heads")
         pages, page_tokens = shape[0], shape[2]
@@ -574,34 +575,40 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
                      scale=None, v_scale=1.0, lse=None, workspace=None, stream=None):
     """Attention of q [rows, n_q_heads, D] over an E2M1 pool (see include/dkv.h); scale None is
     1/sqrt(D).  Without a workspace (uint8, dkv_paged_attend_workspace bytes) one is taken from
-    torch's allocator on the launching stream."""
+    torch's caching allocator, on the launching stream."""
     import torch
-    if q.dim() != 3 or page_table.dim() != 2:
+    shape, i32 = q.shape, torch.int32
+    if len(shape) != 3 or page_table.dim() != 2:
         raise ValueError("q is [rows, n_q_heads, head_dim], page_table [batch, max_pages]")
-    dev, dt, i32 = q.get_device(), q.dtype, torch.int32
+    dev, dt = q.get_device(), q.dtype
     code = _dtype_of(q)
     s = _launch(dev, stream)
-    n, _, D = q.shape
+    n, _, D = shape
     pq, hq, sq = _rows(q, "q", dt, dev, n, D)
-    pkp, shape = _pool(k_pool, "k_pool", dev, D)
-    pvp, other = _pool(v_pool, "v_pool", dev, D)
+    pkp, shape = _pool(k_pool, "k_pool", torch.uint8, dev, D)
+    pvp, other = _pool(v_pool, "v_pool", torch.uint8, dev, D)
     if shape != other:
         raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens)")
     pages, hkv, page_tokens = shape
     B, max_pages = page_table.shape
+    pt, pkl = _arg(page_table, "page_table", i32, dev), _arg(kv_len, "kv_len", i32, dev, (B,))
+    prs, po = _arg(row_start, "row_start", i32, dev, (B + 1,)), _arg(out, "out", dt, dev, (n, hq, D))
+    pl = _arg(lse, "lse", torch.float32, dev, (n, hq))
+    taken = 0
     if workspace is None:
-        need = max(1, dkv_paged_attend_workspace(B, hq, hkv, D, max_rows))
-        if stream is None:
-            workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-        else:  # owned by the launching stream, so that it is not handed out again before it ran
-            with torch.cuda.stream(torch.cuda.ExternalStream(s, device=q.device)):
-                workspace = torch.empty((need,), dtype=torch.uint8, device=q.device)
-    st = lib().dkv_paged_attend(
-        _ATTEND.pack(pq, sq, pkp, pvp, _arg(page_table, "page_table", i32, dev), _arg(kv_len, "kv_len", i32, dev, (B,)),
-                     _arg(row_start, "row_start", i32, dev, (B + 1,)), _arg(out, "out", dt, dev, (n, hq, D)),
-                     _arg(lse, "lse", torch.float32, dev, (n, hq)), _arg(workspace, "workspace", torch.uint8, dev),
-                     workspace.numel(), B, n, max_rows, hq, hkv, D, code, page_tokens, pages, max_pages,
-                     D ** -0.5 if scale is None else scale, v_scale), s)
+        # The allocator's own call: a tensor around the bytes costs 3 us of the smallest calls' 13.
+        # The bytes are the launching stream's, so that they are not handed out again before it ran.
+        size = max(1, dkv_paged_attend_workspace(B, hq, hkv, D, max_rows))
+        pw = taken = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, s)
+    else:
+        pw, size = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
+    try:
+        st = lib().dkv_paged_attend(
+            _ATTEND.pack(pq, sq, pkp, pvp, pt, pkl, prs, po, pl, pw, size, B, n, max_rows, hq, hkv, D, code,
+                         page_tokens, pages, max_pages, D ** -0.5 if scale is None else scale, v_scale), s)
+    finally:
+        if taken:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(taken)
     if st:
         _check(st, "dkv_paged_attend")
 
