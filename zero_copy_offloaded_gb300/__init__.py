@@ -427,8 +427,8 @@ def _arg(t, what, dtype, index, shape=None):
     """Address of a contiguous tensor of this dtype, device index and shape; 0 for None."""
     if t is None:
         return 0
-    if (t.dtype != dtype or t.get_device() != index or (shape is not None and t.shape != shape)
-            or not t.is_contiguous()):
+    if (t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()
+            or (shape is not None and t.shape != shape)):
         _bad(t, what, dtype, index, shape)
     return t.data_ptr()
 
@@ -463,7 +463,7 @@ def _pool(t, what, u8, index, D):
 def _launch(index, stream):
     """The stream to launch on; the tensors must be on the current device, as the library launches there."""
     import torch
-    if index < 0 or index != torch.cuda.current_device():
+    if index < 0 or index != torch._C._cuda_getDevice():  # a CUDA tensor is there: torch is set up
         raise ValueError("the tensors are not on the current CUDA device")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
