@@ -371,6 +371,14 @@ def test_attend_long_and_split(D):
     check_attend(c, *run_attend(c))
 
 
+@pytest.mark.parametrize("Hq,D,rows,keys", [
+    (2, 64, 1, 320_011), (4, 128, 1, 60_001), (2, 128, 16, 40_003), (2, 64, 10, 60_001), (2, 128, 20, 20_003),
+    (1, 64, 200, 1_500), (1, 128, 129, 700)])
+def test_attend_one_item_over_all_ctas(Hq, D, rows, keys):
+    # one KV head: its pieces, up to one a CTA, are joined in groups, or by the blocks of several CTAs
+    check_attend(c := attend_case(keys, [keys], [rows], Hq, 1, D, "fp16", 64), *run_attend(c))
+
+
 @pytest.mark.parametrize("spread", [0.01, 20.0])
 def test_attend_flat_and_peaked(spread):
     # near-uniform weights, and scores whose running maximum keeps moving by hundreds

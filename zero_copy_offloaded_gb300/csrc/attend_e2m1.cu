@@ -69,9 +69,11 @@ constexpr int kTile = kStep * kWarps;   // keys of one tile
 // CTAs' ranges are dealt with it.  48 sequences of up to 8193 keys of 32 heads of 64 take 187 us
 // with 0, 185 with 1, 150 with 3, 154 with 6.
 constexpr int kItemCost = 3;
-// Pieces joined at once, and to a group beyond that (456 pieces: 29 groups of 16).
+// Pieces joined at once; beyond that in groups first, of sixteen (one KV head over 131072 keys of 64:
+// 16.6 us with 16, 17.6 with 20) or of as many as leave kJoinOnce groups.
 constexpr int kJoinOnce = 32, kGroup = 16;
-constexpr int kSms = 152, kMaxCtas = 3 * kSms;
+__device__ __forceinline__ int group_size(int pieces) { return max(kGroup, (pieces + kJoinOnce - 1) / kJoinOnce); }
+constexpr int kSms = 152, kMaxCtas = 4 * kSms;
 constexpr float kLazy = 8.0f;   // the running maximum moves only when passed by 2^8
 constexpr float kNone = -3e38f;  // the running maximum of a row that has seen no key
 
@@ -90,8 +92,10 @@ struct Cfg {
   static constexpr int kQueries = NT > 1 ? NT * (D / 16) * 32 * 8 : 0;  // B fragments of the rows
   static constexpr int kOffQ = kOffMl + (3 * kWarps + 2) * R * 4;       // and their scales, visible keys
   static constexpr int kOffBatch = kOffQ + kQueries + (NT > 1 ? 2 * R * 4 : 0);
-  // resident CTAs per SM, by registers: o takes 4 NT D/16 of a thread's
-  static constexpr int kPerSm = NT == 1 || (NT <= 3 && D == 64) ? 3 : 2;
+  // resident CTAs per SM, by registers: o takes 4 NT D/16 of a thread's.  Eight rows of heads of
+  // 64: 48 sequences of up to 8193 keys of 32 heads take 139 us with four, 149 with three; but
+  // 16 x 512 keys of 8 heads 11.6 and 10.4, so that the fourth stays out of short ranges.
+  static constexpr int kPerSm = NT == 1 && D == 64 ? 4 : NT == 1 || (NT <= 3 && D == 64) ? 3 : 2;
   // subs in flight at once: 20 rows over 16 x 32768 keys of 8 heads of 128 take 214 us with two, 225
   // with one; of 64 141 and 142; four groups of rows have no registers for it
   static constexpr int kBoth = NT == 1 || (NT <= 3 && D == 128) ? 2 : 1;
@@ -211,8 +215,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
   __syncthreads();
   const long long total = s_pre[p.B];
   // with less work than CTAs the first `total` CTAs take one unit each, so that an
-  // item's pieces always lie in consecutive CTAs
-  const long long ctas = min(total, (long long)gridDim.x);
+  // item's pieces always lie in consecutive CTAs; a fourth CTA an SM only for long ranges
+  long long ctas = min(total, (long long)gridDim.x);
+  if (C::kPerSm > 3 && total < 4 * (long long)gridDim.x) ctas = min(ctas, (long long)3 * kSms);
   if ((long long)blockIdx.x >= ctas) return;
   const long long g0 = total * blockIdx.x / ctas, g1 = total * (blockIdx.x + 1) / ctas;
   auto owner = [&](long long at) { return (int)(((at + 1) * ctas - 1) / total); };  // of a unit of the line
@@ -352,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       s_join[0] = c0;
       s_join[1] = pieces;
       counter = pieces <= kJoinOnce ? p.done + 2 * kMaxCtas + c0
-                                    : p.done + slot_of(c0, ((int)blockIdx.x - c0) / kGroup * kGroup);
+                                    : p.done + slot_of(c0, ((int)blockIdx.x - c0) / group_size(pieces) * group_size(pieces));
       seen = *reinterpret_cast<volatile unsigned long long*>(counter);
     }
 
@@ -821,12 +826,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       if (pieces <= kJoinOnce) {
         if (finish(counter, pieces)) join(0, 1, pieces, true);
       } else {
-        const int first = ((int)blockIdx.x - c0) / kGroup * kGroup, size = min(kGroup, pieces - first);
+        const int group = group_size(pieces);
+        const int first = ((int)blockIdx.x - c0) / group * group, size = min(group, pieces - first);
         if (finish(counter, size)) {
           if (threadIdx.x == 0) tag(whole_item, *reinterpret_cast<volatile unsigned long long*>(whole_item));
           join(first, 1, size, false);
-          const int groups = (pieces + kGroup - 1) / kGroup;
-          if (finish(whole_item, groups)) join(0, kGroup, groups, true);
+          const int groups = (pieces + group - 1) / group;
+          if (finish(whole_item, groups)) join(0, group, groups, true);
         }
       }
     }
