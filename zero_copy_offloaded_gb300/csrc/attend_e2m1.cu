@@ -12,7 +12,8 @@
 // contiguous ranges, whatever the lengths are, from the lengths on the device
 // (no host copy, so a captured graph serves any lengths).  A CTA that holds a whole
 // item writes its rows; an item cut between CTAs leaves fp32 partials, which the CTA that
-// finishes last joins in CTA order (no CTA waits for another).
+// finishes last joins in CTA order (no CTA waits for another), many pieces in groups first: one
+// KV head over 131072 keys takes 19 us, and took 98 with its 456 pieces joined by one CTA, row by row.
 //
 // Inside a CTA each of 4 warps takes 32 keys of every tile through its own
 // cp.async ring, with no barrier between warps until the item ends.  Per 16 keys:
@@ -30,8 +31,9 @@
 //
 // Why mma.sync here: tcgen05 takes at least 128 rows (or columns) a tile and its operands from
 // shared memory, so the converted keys would be written and read there once more.  Sixteen
-// rows of 32/8 heads over 16 x 8192 keys take 122 us in attend_e2m1_tc.cu's kernel, 70 here;
-// 32 rows 125 and 118 (heads of 64: 102 and 71); 33 rows and more go there.
+// rows of 32/8 heads over 16 x 8192 keys take 111 us in attend_e2m1_tc.cu's kernel, 58 here;
+// 32 rows 111 and 84 (heads of 64: 98 and 57); 33 rows and more, for whose outputs there
+// are no registers here, go there.
 //
 // What bounds it: reading 9/16 byte an element, 1152 bytes for 16 keys of a head of 128.  The
 // 8 x 32769 keys of 8 heads (302 MB) take 73 us, 4.1 TB/s of 6.8 measured (4 x 131073 keys:
@@ -39,7 +41,10 @@
 // conversion and MMAs on resident data 57 us: the two do not overlap fully with 12 warps on
 // an SM.  A sub costs about 260 instructions, 64 of them the conversions of two codes each.
 // 168 registers a thread and three CTAs beat 128 and four (75 and 80 us): with fewer the
-// compiler computes addresses again and again.
+// compiler computes addresses again and again.  More rows: an MMA m16n8k16 takes 8 cycles of
+// a scheduler, 96 of them a warp's 32 keys at 24 rows, a quarter of the time that two
+// warps a scheduler need (20 rows over 16 x 8192 keys: 69 us); and a piece has a fixed cost, queries,
+// join of the warps and of the CTAs, of about 10000 cycles, near three of its tiles of 128 keys.
 #include <float.h>
 #include <math.h>
 #include <stdio.h>
