@@ -74,7 +74,8 @@ def check_plan(case, P, max_rows, inplace=False):
 
 @pytest.mark.parametrize("B,P,max_new,max_rows", [
     (1, 16, 1, 1), (1, 1, 5, 9), (3, 16, 1, 8), (31, 16, 40, 1300), (32, 64, 1, 32), (33, 16, 17, 600),
-    (257, 32, 3, 800), (1024, 16, 1, 1024), (1024, 4096, 30, 31000), (64, 16, 100, 6400), (5, 2, 3000, 15001)])
+    (257, 32, 3, 800), (1024, 16, 1, 1024), (1024, 4096, 30, 31000), (64, 16, 100, 6400), (5, 2, 3000, 15001),
+    (700, 16, 60, 40001), (1, 16, 20000, 20011)])
 @pytest.mark.parametrize("inplace", [False, True])
 def test_plan(B, P, max_new, max_rows, inplace):
     max_pages = -(-(2000 + max_new) // P)

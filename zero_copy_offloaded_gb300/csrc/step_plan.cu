@@ -16,7 +16,7 @@
 // that lengths and the free count may be updated in place); pages are moved by
 // the warps of all CTAs, and behind a second barrier all threads fill the rows.
 // In a graph of such launches, a step with one token for each of 64 sequences takes 4.7 us (one
-// CTA: 4.9), of 1024 sequences 6.4 us (8.7), with 64 each for 64 sequences 6.6 us (9.7).
+// CTA: 4.9), of 1024 sequences 6.4 us (8.7), with 64 each for 64 sequences 5.9 us (9.7).
 #include <stdio.h>
 
 #include "dkv_internal.cuh"
@@ -59,25 +59,33 @@ __device__ __forceinline__ Sums shfl_up(const Sums& v, int d) {
           __shfl_up_sync(~0u, v.rows, d)};
 }
 
-// Positions and slots of rows [first, last) with `stride` threads: the sequence
-// of a row is found by bisection of the row starts.
+// Positions and slots of the rows first, first + stride, ...: the sequence of a row is found by
+// bisection of the row starts, U rows of a thread at once.
+template <int U>
 __device__ __forceinline__ void fill_rows(const PlanParams& p, const int* start, const int* kv,
                                           int first, int stride) {
   const int total = start[p.B];
-  for (int r = first; r < p.max_rows; r += stride) {
-    int pos = 0, slot = -1;
-    if (r < total) {
-      int lo = 0, hi = p.B;  // start[lo] <= r < start[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= r) lo = mid; else hi = mid;
-      }
-      pos = kv[lo] - (start[lo + 1] - r);
-      const int page = __ldcg(p.table + (size_t)lo * p.max_pages + (pos >> p.shift));
-      slot = (page << p.shift) + (pos & ((1 << p.shift) - 1));
+  for (long long r0 = first; r0 < p.max_rows; r0 += (long long)U * stride) {
+    int r[U], seq[U] = {}, pos[U], page[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) r[i] = (int)min(r0 + (long long)i * stride, (long long)p.max_rows);
+    for (int step = 1 << (31 - __clz(p.B)); step; step >>= 1) {  // the last whose start is at most r
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (seq[i] + step < p.B && start[seq[i] + step] <= r[i]) seq[i] += step;
     }
-    p.row_pos[r] = pos;
-    p.row_slot[r] = slot;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const bool on = r[i] < total;
+      pos[i] = on ? kv[seq[i]] - (start[seq[i] + 1] - r[i]) : 0;
+      page[i] = on ? __ldcg(p.table + (size_t)seq[i] * p.max_pages + (pos[i] >> p.shift)) : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (r[i] >= p.max_rows) break;
+      p.row_pos[r[i]] = pos[i];
+      p.row_slot[r[i]] = r[i] < total ? (page[i] << p.shift) + (pos[i] & ((1 << p.shift) - 1)) : -1;
+    }
   }
 }
 
@@ -182,15 +190,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanParams 
   }
   // pages taken, from the top of the stack
   if (s_need[p.B] > 0) {
-    for (int s = cta * warps + warp; s < p.B; s += ctas * warps) {
-      const int at = s_need[s], n = s_need[s + 1] - at, h = s_held[s];
-#pragma unroll 4
-      for (int i = lane; i < n; i += 32)
-        p.table[(size_t)s * p.max_pages + h + i] = __ldcg(p.free_pages + stack - 1 - at - i);
+    for (int k = cta * kPlanThreads + b; k < s_need[p.B]; k += ctas * kPlanThreads) {
+      const int page = __ldcg(p.free_pages + stack - 1 - k);
+      int s = 0;  // the last sequence whose first page is at most the k-th
+      for (int step = 1 << (31 - __clz(p.B)); step; step >>= 1)
+        if (s + step < p.B && s_need[s + step] <= k) s += step;
+      p.table[(size_t)s * p.max_pages + s_held[s] + k - s_need[s]] = page;
     }
     cluster_sync();
   }
-  fill_rows(p, s_start, s_kv, cta * kPlanThreads + b, ctas * kPlanThreads);
+  // Many rows, four of a thread at once, so that their reads do not wait for one another: 65536
+  // rows of 512 sequences take 11.6 us so, 13.4 row by row; 1024 rows of as many 7.3 and 6.4.
+  const int first = cta * kPlanThreads + b, stride = ctas * kPlanThreads;
+  if (p.max_rows > 2 * stride) fill_rows<4>(p, s_start, s_kv, first, stride);
+  else fill_rows<1>(p, s_start, s_kv, first, stride);
 }
 
 constexpr int kCluster = 8;
