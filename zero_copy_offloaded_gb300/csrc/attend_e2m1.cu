@@ -559,14 +559,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
         }
         sb[k] = sv[t * e2m1::scale_bytes(D)];
       }
-      bool nan = false;  // among this thread's scales
       if constexpr (edge) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // nobody sees this key, or its NaN is dealt out below
-          const bool n = (sb[k] & 0x7f) == 0x7f;
-          nan |= n;
-          if (n || t0 + (k & 1 ? c ^ 1 : c) + 4 * k >= maxvis) sb[k] = 0;
-        }
+        for (int k = 0; k < 4; ++k)  // nobody sees this key, or its NaN is dealt out below
+          if (t0 + (k & 1 ? c ^ 1 : c) + 4 * k >= maxvis || (sb[k] & 0x7f) == 0x7f) sb[k] = 0;
       }
       const uint32_t vs[2] = {e2m1::scales_to_h2(sb[0] | (sb[1] << 8)),
                               e2m1::scales_to_h2(sb[2] | (sb[3] << 8))};
@@ -591,6 +587,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       if constexpr (edge) {
         // A NaN block of V reaches the rows that see its key, and no others (a
         // zero weight times NaN would reach them all).
+        bool nan = false;  // in this thread's four keys: read again, so that the loop above keeps no flag
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          nan |= (reinterpret_cast<const volatile uint8_t*>(sv)[(c + 4 * k) * e2m1::scale_bytes(D)] & 0x7f) == 0x7f;
 #pragma unroll 1
         for (int t = __any_sync(~0u, nan) ? 0 : kSub; t < kSub; ++t)
           if ((sv[t * e2m1::scale_bytes(D)] & 0x7f) == 0x7f) {
