@@ -1,0 +1,99 @@
+"""The device-side step where sums, ranges and waits have little room: peaked softmaxes, items in many
+pieces, scales, waits that run out."""
+import numpy as np
+import pytest
+
+import zero_copy_offloaded_gb300 as dkv
+from oracle import paged_step as step
+
+from .test_step_gpu import HALF, dev, host, i32, tdt
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+# ---- one key far above the others ------------------------------------------------------------
+
+def sink_case(keys, Hkv, D, at, P=64):
+    """Pools of one sequence: key `at` is a row of ones (as the format holds them) with value 0, every other
+    key is 0, its value one of the format's positive numbers times 32, another one for each head and dim."""
+    pages = keys // P
+    t = np.arange(keys)
+    k = np.zeros((keys, D), np.float32)
+    k[at] = 1.0
+    h, d = np.arange(Hkv)[:, None, None], np.arange(D)
+    v = 32.0 * step.E2M1[1 + (3 * t[:, None] + t[:, None] // 64 + h + d // 16) % 7]  # [Hkv, keys, D]
+    v[:, at] = 0.0
+    pool = lambda x: step.make_pool(np.ascontiguousarray(  # noqa: E731
+        np.broadcast_to(x, (Hkv, keys, D)).reshape(Hkv, pages, P, D).transpose(1, 0, 2, 3)).astype(np.float32))
+    pools = pool(k), pool(v)
+    one = step.read_pool(pools[0][at // P][None], D)[0, 0, at % P, 0]
+    held = step.read_pool(pools[1], D).transpose(1, 0, 2, 3).reshape(Hkv, keys, D)
+    return pools, one, held
+
+
+@pytest.mark.parametrize("bits", [16.6, 20.6, 24.4, 26.3])
+@pytest.mark.parametrize("at", [0, 77, 2049])
+@pytest.mark.parametrize("rows,Hkv,D,dtype,keys,B", [
+    (1, 32, 64, "fp16", 4096, 16), (1, 8, 128, "bf16", 8192, 64), (3, 32, 128, "fp16", 4096, 16), (8, 32, 64, "bf16", 4096, 16)])
+def test_small_weights_beside_a_large_one(rows, Hkv, D, dtype, keys, B, at, bits):
+    """Each of thousands of keys weighs 2^-bits of one whose value is 0, so the output is theirs alone.
+
+    A row's weights are rounded to fp16 with the largest at 2^10 or above: 2^-11 of a weight that fp16 holds
+    as a normal number, 2^(-25 - 10) of the largest below that, which is 2^(bits - 35) of the weight.  All
+    values are positive, so the output is off by no more than that, relative.  2^-12 covers the
+    rest: the scores (one fp32 sum of D products and the scale, |score| <= 26.3: 2^-18), the exponential
+    2^-21, and the fp32 sums of 2 x 4096 equal terms and fewer, 2^-13 for numerator and denominator each."""
+    G = 4 if rows == 3 else 1
+    pools, one, v = sink_case(keys, Hkv, D, at)
+    scale = bits * np.log(2) / (D * one)
+    table = np.broadcast_to(np.arange(keys // 64, dtype=np.int32), (B, keys // 64))
+    q = torch.ones((B * rows, Hkv * G, D), dtype=tdt(dtype), device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    dkv.dkv_paged_attend(q, dev(pools[0]), dev(pools[1]), i32(table), i32([keys] * B), out,
+                         row_start=i32(np.arange(B + 1) * rows), max_rows=rows, scale=scale, lse=lse)
+    seen = keys - rows + 1 + np.arange(rows)
+    w = 2.0 ** -bits
+    total = 1 + (seen - 1) * w  # of the largest weight
+    want = w * np.cumsum(v, 1)[:, seen - 1] / total[:, None]  # [Hkv, rows, D]
+    want = np.tile(np.repeat(want.transpose(1, 0, 2), G, 1), (B, 1, 1))
+    r = max(2.0 ** -11, 2.0 ** (bits - 35)) + 2.0 ** -12
+    err = np.abs(host(out) - want)
+    tol = (HALF[dtype] + r) * want + 2.0 ** -25 * (dtype == "fp16")
+    assert np.all(err <= tol), (err / want).max()
+    low = np.tile(bits * np.log(2) + np.log(total), B)[:, None]
+    assert np.all(np.abs(host(lse) - low) <= 2.0 ** -12)
+
+
+@pytest.mark.parametrize("rows,dtype,sign", [(1, "fp16", 1), (5, "bf16", 1), (1, "bf16", -1)])
+@pytest.mark.parametrize("step_up", [0.3, 3.0, 20.0])
+def test_scores_of_two_million(rows, dtype, sign, step_up):
+    """Scores of 2^21, which fp32 resolves to 1/4 and no better, that rise from key to key.  A row stays a
+    weighted mean of the values, and its lse its largest score: both bounds hold whatever the rounding of
+    the scores, which is (D + 8) 2^-23 of 2^21, 35 at most, plus log(keys)."""
+    D, keys, P = 128, 600, 16
+    pages = -(-keys // P)
+    t = np.arange(pages * P, dtype=np.float32)
+    k = np.empty((1, pages * P, D), np.float32)
+    k[..., :112] = 6.0
+    k[..., 112:] = (t * step_up / 16)[:, None]
+    v = np.random.default_rng(1).uniform(1, 3, (1, pages * P, D)).astype(np.float32)
+    pools = [step.make_pool(x.reshape(1, pages, P, D).transpose(1, 0, 2, 3).copy()) for x in (k, v)]
+    kd, vd = [step.read_pool(x, D)[:, 0].reshape(-1, D) for x in pools]
+    q = torch.full((rows, 2, D), 1024.0, device="cuda")
+    q[..., 112:] = 1.0
+    scale = sign * 2.0 ** 21 / (1024.0 * 112 * kd[0, 0])
+    q *= sign
+    q[..., 112:] /= abs(scale)
+    q = q.to(tdt(dtype))
+    out, lse = torch.empty_like(q), torch.empty((rows, 2), device="cuda")
+    dkv.dkv_paged_attend(q, dev(pools[0]), dev(pools[1]), i32(np.arange(pages)[None]), i32([keys]), out,
+                         row_start=i32([0, rows]), max_rows=rows, scale=scale, lse=lse)
+    got, low = host(out), host(lse)
+    half = HALF[dtype]
+    for i in range(rows):
+        n = keys - rows + 1 + i
+        assert np.all(got[i] >= vd[:n].min(0) * (1 - 2 * half - 2.0 ** -10)), (i, got[i].min())
+        assert np.all(got[i] <= vd[:n].max(0) * (1 + 2 * half + 2.0 ** -10)), (i, got[i].max())
+        s = scale * (kd[:n] @ host(q)[i].T)
+        assert np.all(np.abs(low[i] - s.max(0)) <= 36 + np.log(n))

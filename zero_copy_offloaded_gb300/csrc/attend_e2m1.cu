@@ -25,9 +25,9 @@
 // fp16 in registers; code x scale is exact in fp16 (6 significant bits), so the
 // MMA operands carry no rounding of the cache.  bf16 queries are brought to fp16's
 // range by a power of two per row (exact, undone on the scores; an element below
-// 2^-27 of its row's largest may lose bits).  P is rounded to fp16 (2^-11
-// relative, as the tensor operand must be 16 bits); scores, maxima, sums and
-// outputs stay in fp32.
+// 2^-27 of its row's largest may lose bits).  P is rounded to fp16, as the tensor
+// operand must be 16 bits: 2^-11 of a weight, and 2^-35 of the row's largest for
+// weights below 2^-24 of it (kBias); scores, references, sums and outputs stay in fp32.
 //
 // Why mma.sync here: tcgen05 takes at least 128 rows (or columns) a tile and its operands from
 // shared memory, so the converted keys would be written and read there once more.  Sixteen
@@ -79,8 +79,14 @@ constexpr int kItemCost = 3;
 constexpr int kJoinOnce = 32, kGroup = 16;
 __device__ __forceinline__ int group_size(int pieces) { return max(kGroup, (pieces + kJoinOnce - 1) / kJoinOnce); }
 constexpr int kSms = 152, kMaxCtas = 4 * kSms;
-constexpr float kLazy = 8.0f;   // the running maximum moves only when passed by 2^8
-constexpr float kNone = -3e38f;  // the running maximum of a row that has seen no key
+// A row's weights are 2^(s - m) with m below its running maximum, so that the largest are 2^kBias to
+// 2^(kBias + kLazy): fp16 has room above 1, and a weight keeps all its bits down to 2^-24 of the
+// row's largest and counts down to 2^-35 (with m at the maximum itself 2^-14 and 2^-25: thousands of
+// keys beside one that is 17 above them were lost).  A factor of 4 is left below fp16's largest number
+// for the rounding of m and of its threshold, at most 2^-2 each for scores up to 2^21.
+constexpr float kBias = 10.0f;
+constexpr float kLazy = 4.0f;   // m moves only when a score passes m + kBias by this
+constexpr float kNone = -3e38f;  // m of a row that has seen no key
 
 template <int D, int NT>
 struct Cfg {
@@ -451,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     };
     if (cut && threadIdx.x == 0) tag(counter, seen);
 
-    // running maximum (base 2, scaled), the raw score that moves it, sum, output
+    // reference of the weights (base 2, scaled), the raw score that moves it, sum, output
     float m[NT][2], thr[NT][2], l[NT][2], o[NT][J][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       for (int i = 0; i < J; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
 
-    // raw scores of one sub, masked; whether one passes its lazy maximum
+    // raw scores of one sub, masked; whether one moves its row's reference
     auto scores = [&](auto edge, const uint8_t* st, int t0, float (&s)[NT][4]) -> bool {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
@@ -607,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
       }
     };
 
-    // takes these scores into the running maxima and rescales what was summed under the old ones
+    // takes these scores into the references and rescales what was summed under the old ones
     auto raise = [&](const float (&s)[NT][4]) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -620,10 +626,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
           x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
-          x = fmaxf(x * su, m[nt][u]);
+          x = fmaxf(fmaf(x, su, -kBias), m[nt][u]);
           f[u] = x == m[nt][u] ? 1.0f : exp2f(m[nt][u] - x);
           m[nt][u] = x;
-          if (x != kNone) thr[nt][u] = __fdividef(x + kLazy, su);
+          if (x != kNone) thr[nt][u] = __fdividef(x + (kBias + kLazy), su);
           l[nt][u] *= f[u];
         }
 #pragma unroll
