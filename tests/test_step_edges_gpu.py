@@ -35,7 +35,8 @@ def sink_case(keys, Hkv, D, at, P=64):
 @pytest.mark.parametrize("bits", [16.6, 20.6, 24.4, 26.3])
 @pytest.mark.parametrize("at", [0, 77, 2049])
 @pytest.mark.parametrize("rows,Hkv,D,dtype,keys,B", [
-    (1, 32, 64, "fp16", 4096, 16), (1, 8, 128, "bf16", 8192, 64), (3, 32, 128, "fp16", 4096, 16), (8, 32, 64, "bf16", 4096, 16)])
+    (1, 32, 64, "fp16", 4096, 16), (1, 8, 128, "bf16", 8192, 64), (3, 32, 128, "fp16", 4096, 16), (8, 32, 64, "bf16", 4096, 16),
+    (40, 8, 128, "bf16", 8192, 20), (64, 8, 64, "fp16", 8192, 20)])
 def test_small_weights_beside_a_large_one(rows, Hkv, D, dtype, keys, B, at, bits):
     """Each of thousands of keys weighs 2^-bits of one whose value is 0, so the output is theirs alone.
 
@@ -65,7 +66,7 @@ def test_small_weights_beside_a_large_one(rows, Hkv, D, dtype, keys, B, at, bits
     assert np.all(np.abs(host(lse) - low) <= 2.0 ** -12)
 
 
-@pytest.mark.parametrize("rows,dtype,sign", [(1, "fp16", 1), (5, "bf16", 1), (1, "bf16", -1)])
+@pytest.mark.parametrize("rows,dtype,sign", [(1, "fp16", 1), (5, "bf16", 1), (1, "bf16", -1), (40, "fp16", 1), (70, "bf16", -1)])
 @pytest.mark.parametrize("step_up", [0.3, 3.0, 20.0])
 def test_scores_of_two_million(rows, dtype, sign, step_up):
     """Scores of 2^21, which fp32 resolves to 1/4 and no better, that rise from key to key.  A row stays a

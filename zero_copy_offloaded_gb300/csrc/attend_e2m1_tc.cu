@@ -17,11 +17,12 @@
 // that the P.V before it is finished: O may be rescaled then without a barrier of its own.
 //
 // A softmax thread takes its row's scores 32 at a time and writes the weights over columns
-// that it has read.  The running reference m of a row is the maximum of the first 32 scores
-// with a visible key; a later 32 whose weights sum to at most 2^15 have none above 2^15,
-// which fp16 and the fp32 sums hold, so no maximum is taken.  Where they sum to more (or to
-// infinity or NaN, as they do at the start) the row takes their maximum as m and rescales what
-// it has: the tile's earlier weights, l and O.  The largest weight is at least 1 throughout.
+// that it has read.  The running reference m of a row is 10 (a weight of 2^10) below the maximum of
+// the first 32 scores with a visible key; a later 32 whose weights sum to at most 60000 have none
+// above that, which fp16 and the fp32 sums hold, so no maximum is taken.  Where they sum to more (or to
+// infinity or NaN, as they do at the start) the row takes their maximum, less 10, as m and rescales what
+// it has: the tile's earlier weights, l and O.  The largest weight is at least 2^10 throughout, so
+// a weight keeps all of fp16's bits down to 2^-24 of the row's largest and counts down to 2^-35.
 //
 // What bounds it: 4 D flops per (row, key) on the tensor cores.  4096 rows of 32/8 heads of 128
 // over 28672 keys and themselves (2.06 TFLOP) take 1.55 ms, 1327 TFLOP/s of 1912 measured.  A key
@@ -51,7 +52,9 @@ constexpr int kThreads = (10 + kConvert) * 32;
 constexpr int kReg = 128 * 128;        // a 128-row x 128-byte swizzled region
 constexpr int kRaw = 3;                // raw half tiles (K or V codes and scales) in flight
 constexpr float kNone = -3e38f;        // m of a row that has seen no key
-constexpr float kSumBound = 32768.f;
+constexpr float kBias = 10.f;          // m below the maximum that it is taken from
+// 32 weights just taken as reference sum to 2^15 at most, 2^15.3 with the rounding of m for scores up to 2^21
+constexpr float kSumBound = 60000.f;
 
 constexpr uint32_t kTmS = 0, kTmO = 256;  // S of tile t at 128 t, O at 256 + 128 t
 
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                 for (int k = 0; k < 32; ++k) x[k & 3] = fmaxf(x[k & 3], __uint_as_float(r[k]));
-                const float nm = raise ? fmaxf(m, fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * sl) : m;
+                const float nm = raise ? fmaxf(m, fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), sl, -kBias)) : m;
                 const float f = nm == m ? 1.0f : exp2f(m - nm);
                 m = nm;
                 l *= f;
