@@ -569,6 +569,9 @@ dkv_status dkv_qkv_append(const dkv_append_t* args, void* stream);
  * workspace: device memory of dkv_paged_attend_workspace bytes (0 for arguments
  * that dkv_paged_attend refuses), on a 256-byte boundary; its contents do not matter
  * before and after a call.
+ * The kernel for more than 32 rows times heads per KV head waits on the device for its own
+ * copies and products, for a second at most; where a wait gives up, the affected rows of out and
+ * lse are NaN.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim not 64 or 128), CUDA. */
 typedef struct {
     const void* q;
@@ -587,6 +590,10 @@ typedef struct {
 dkv_status dkv_paged_attend(const dkv_attend_t* args, void* stream);
 size_t dkv_paged_attend_workspace(int batch, int n_q_heads, int n_kv_heads, int head_dim,
                                   int max_rows);
+
+/* Test hook (process-wide, off by default): with enable != 0 that kernel of the calls that follow never
+ * signals an item's outputs, so that its waits run out (some seconds). */
+dkv_status dkv_paged_attend_debug_withhold(int enable);
 
 /* Number of kernel launches the last dkv_decode / dkv_prefill enqueued. */
 int dkv_last_launch_count(void);

@@ -98,3 +98,33 @@ def test_scores_of_two_million(rows, dtype, sign, step_up):
         assert np.all(got[i] <= vd[:n].max(0) * (1 + 2 * half + 2.0 ** -10)), (i, got[i].max())
         s = scale * (kd[:n] @ host(q)[i].T)
         assert np.all(np.abs(low[i] - s.max(0)) <= 36 + np.log(n))
+
+
+# ---- a wait that runs out ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("keys,B", [(100, 3), (3000, 2)])
+def test_withheld_outputs_time_out_then_recover(keys, B):
+    """The many-row kernel's waits for its outputs run out: out and lse of every row are NaN, whether a CTA holds
+    a whole item or a piece of one, and the next call is right."""
+    rows, Hkv, D, P = 40, 2, 128, 16
+    rng = np.random.default_rng(3)
+    pages = -(-keys // P)
+    pools = [dev(step.make_pool(rng.standard_normal((pages, Hkv, P, D)).astype(np.float32))) for _ in "kv"]
+    q = torch.from_numpy(rng.standard_normal((B * rows, 4, D)).astype(np.float32)).bfloat16().cuda()
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    args = (q, *pools, i32(np.broadcast_to(np.arange(pages, dtype=np.int32), (B, pages))), i32([keys] * B))
+    kw = dict(row_start=i32(np.arange(B + 1) * rows), max_rows=rows)
+    dkv.dkv_paged_attend(*args, out, lse=lse, **kw)
+    torch.cuda.synchronize()
+    late, low = torch.zeros_like(out), torch.zeros_like(lse)
+    dkv.dkv_paged_attend_debug_withhold(True)
+    try:
+        dkv.dkv_paged_attend(*args, late, lse=low, **kw)
+        torch.cuda.synchronize()
+    finally:
+        dkv.dkv_paged_attend_debug_withhold(False)
+    assert late.float().isnan().all()
+    assert low.isnan().all()
+    dkv.dkv_paged_attend(*args, late, lse=low, **kw)
+    torch.cuda.synchronize()
+    assert out.float().isfinite().all() and torch.equal(late, out) and torch.equal(low, lse)

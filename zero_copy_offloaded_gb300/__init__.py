@@ -31,6 +31,7 @@ __all__ = [
     "dkv_cache_alloc_ex", "KV_FORMATS", "dkv_decode_noalloc", "dkv_decode_noalloc_status",
     "dkv_decode_noalloc_debug_withhold", "dkv_pci_numa_node", "dkv_numa_probe",
     "dkv_step_plan", "dkv_qkv_append", "dkv_paged_attend", "dkv_paged_attend_workspace",
+    "dkv_paged_attend_debug_withhold",
     "rope_table", "MAX_STEP_BATCH",
 ]
 
@@ -136,6 +137,7 @@ def lib(build_if_missing: bool = False):
         "dkv_step_plan": [P, P, P, P, P, I, I, I, I, I, P, P, P, P, P, P, P],
         "dkv_qkv_append": [P, P],
         "dkv_paged_attend": [P, P],
+        "dkv_paged_attend_debug_withhold": [I],
         "dkv_project": [P, P, P, I, I, I, I, P],
         "dkv_cache_debug_withhold": [P, I],
     }
@@ -611,6 +613,10 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
             torch._C._cuda_cudaCachingAllocator_raw_delete(taken)
     if st:
         _check(st, "dkv_paged_attend")
+
+
+def dkv_paged_attend_debug_withhold(enable=True):
+    _check(lib().dkv_paged_attend_debug_withhold(int(bool(enable))), "dkv_paged_attend_debug_withhold")
 
 
 class KVCache:

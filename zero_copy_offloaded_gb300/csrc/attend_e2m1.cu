@@ -871,6 +871,8 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 // Workspace: descriptors or counts | partial (max, sum) | partial o, two slots per CTA.
 size_t ws_desc() { return align256(std::max(kMaxCtas * sizeof(AttendDesc), 3 * kMaxCtas * sizeof(unsigned long long))); }
 
+std::atomic<int> g_debug_withhold{0};
+
 // The tag of a call: 48 bits that no earlier call of this process had, scattered so that memory
 // left by anything else does not hold one.
 unsigned long long next_tag() {
@@ -986,6 +988,7 @@ extern "C" dkv_status dkv_paged_attend(const dkv_attend_t* a, void* stream) {
   p.page_bytes = e2m1::page_bytes(D, a->page_tokens);
   p.scale_log2 = (float)(1.4426950408889634 * (double)a->scale);
   p.v_scale = a->v_scale;
+  p.debug_withhold = g_debug_withhold;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (a->dtype == DKV_BF16)
@@ -996,5 +999,10 @@ extern "C" dkv_status dkv_paged_attend(const dkv_attend_t* a, void* stream) {
     cudaGetLastError();
     return refuse(DKV_ERR_CUDA, cudaGetErrorString(e));
   }
+  return DKV_OK;
+}
+
+extern "C" dkv_status dkv_paged_attend_debug_withhold(int enable) {
+  g_debug_withhold = enable ? 1 : 0;
   return DKV_OK;
 }

@@ -37,6 +37,7 @@ struct AttendParams {
   int B, N, Hq, Hkv, G;
   int num_pages, max_pages, page_shift;
   float scale_log2, v_scale;
+  int debug_withhold;    // test hook: the many-row kernel never signals that an item's outputs are done
 };
 
 // Sequence b's cached keys, first row and rows, held inside what the buffers have.

@@ -506,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           const bool whole = starts && ends;
           const float bad = __int_as_float(0x7fc00000);
           if (m == kNone && l == l) l = 0.f;  // no key of the piece is seen
+          if (dead) l = bad;  // the wait for O may be the one that gave up: no lse beside outputs that are NaN
           const float inv = dead ? bad : whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.0f;
           const int tok = pr / G;
           const size_t orow = (size_t)(row0 + tok) * p.Hq + h * G + (pr - tok * G);
@@ -696,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
               tc::fence_after_sync();
               pv(t, st, fresh);
               if (final_tile) {
-                if (one) tc::mma_commit(&bars->o_full[t]);
+                if (one && !p.debug_withhold) tc::mma_commit(&bars->o_full[t]);
                 ++no[t];
               }
             }
