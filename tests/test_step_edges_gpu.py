@@ -128,3 +128,31 @@ def test_withheld_outputs_time_out_then_recover(keys, B):
     dkv.dkv_paged_attend(*args, late, lse=low, **kw)
     torch.cuda.synchronize()
     assert out.float().isfinite().all() and torch.equal(late, out) and torch.equal(low, lse)
+
+
+# ---- scales of the append --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("scale", [41.0, 47.0, 0.37, 1e-30, 2.0 ** 127])
+def test_append_divides_by_the_scales(D, scale):
+    """The pools hold k / scale and v / scale, rounded once: 41 times a number half way between two codes is
+    that number again when divided by 41, and lies below it when multiplied by the rounded 1 / 41."""
+    Hkv, P, N = 2, 16, 32
+    tie = np.array([6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0] * 2, np.float32)
+    x = np.tile(tie, D // 16) * np.float32(41) * (1 + np.arange(N * Hkv, dtype=np.float32).reshape(N, Hkv, 1) % 8 / 8)
+    k = torch.from_numpy(x.astype(np.float16)).cuda()
+    v = torch.from_numpy(x[::-1].astype(np.float16)).cuda()
+    pools = [torch.zeros((N // P, Hkv, P * D * 9 // 16), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    dkv.dkv_qkv_append(None, k, v, None, i32(np.arange(N)), *pools, k_scale=scale, v_scale=scale)
+    s = np.float32(scale)
+    moved = 0
+    for pool, t in zip(pools, (k, v)):
+        y = t.float().cpu().numpy()
+        code, sc = step.quantise(y / s)
+        other = step.quantise(y * (np.float32(1) / s))
+        moved += int((code != other[0]).sum() + (sc != other[1]).sum())
+        raw, got = step.pool_views(pool.cpu().numpy(), D)
+        rows = lambda a: a.transpose(0, 2, 1, 3).reshape(N, Hkv, -1)  # noqa: E731
+        assert np.array_equal(rows(got), sc)
+        assert np.array_equal(rows(raw), code[..., 0::2] | (code[..., 1::2] << 4))
+    assert moved > 0 or scale != 41.0  # the two differ here

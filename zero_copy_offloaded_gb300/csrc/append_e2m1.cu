@@ -52,7 +52,7 @@ struct AppendParams {
   int N, Hq, Hkv, rot, max_pos, inter;
   int page_shift;
   int q_items, kv_items;  // head groups of queries, of keys and of values
-  float eps, k_scale, v_scale, k_inv, v_inv;
+  float eps, k_scale, v_scale;
 };
 
 constexpr int kThreads = 256;
@@ -201,7 +201,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int h
   const int side = KIND == kKey && !INTER && in_rot ? (l * 8 < half ? -1 : 1) : 0;
   const int partner = lane - side * (p.rot / 16);
   const size_t page_bytes = e2m1::page_bytes(D, 1 << p.page_shift);
-  const float inv = KIND == kKey ? p.k_inv : p.v_inv, mul = KIND == kKey ? p.k_scale : p.v_scale;
+  const float mul = KIND == kKey ? p.k_scale : p.v_scale;
   uint8_t* pool = (KIND == kKey ? p.k_pool : p.v_pool) + (KIND == kQuery ? 0 : (size_t)(h0 + sub) * page_bytes);
 
 #pragma unroll 1
@@ -289,9 +289,9 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int h
       }
       const bool write = h + sub < heads;
       if (KIND != kQuery && p.slot) {
-        if (inv != 1.0f) {
+        if (mul != 1.0f) {  // (a reciprocal would round twice, and move codes next to a border)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(x[e], inv);
+          for (int e = 0; e < 8; ++e) x[e] = __fdiv_rn(x[e], mul);
         }
         uint32_t sb;
         float sf;
@@ -423,8 +423,6 @@ extern "C" dkv_status dkv_qkv_append(const dkv_append_t* a, void* stream) {
   p.page_shift = 0;
   while (a->k_pool && (1 << p.page_shift) < a->page_tokens) ++p.page_shift;
   p.eps = a->eps; p.k_scale = a->k_scale; p.v_scale = a->v_scale;
-  p.k_inv = a->k_pool ? 1.0f / a->k_scale : 1.0f;
-  p.v_inv = a->k_pool ? 1.0f / a->v_scale : 1.0f;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (a->dtype == DKV_BF16) {
     if (D == 64) launch<__nv_bfloat16, 64>(p, s); else launch<__nv_bfloat16, 128>(p, s);
