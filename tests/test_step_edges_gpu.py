@@ -1,5 +1,7 @@
 """The device-side step where sums, ranges and waits have little room: peaked softmaxes, items in many
 pieces, scales, waits that run out."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -156,3 +158,56 @@ def test_append_divides_by_the_scales(D, scale):
         assert np.array_equal(rows(got), sc)
         assert np.array_equal(rows(raw), code[..., 0::2] | (code[..., 1::2] << 4))
     assert moved > 0 or scale != 41.0  # the two differ here
+
+
+# ---- a capture that torch does not know ------------------------------------------------------------
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("given", [False, True])
+def test_foreign_capture_needs_a_workspace(rows, given):
+    """A workspace of torch's allocator is free again behind the call: fine in a graph whose memory pool torch
+    keeps, not in one that it does not know.  Such a capture is refused without a workspace, and replays
+    with one."""
+    try:
+        rt = ctypes.CDLL("libcudart.so.13")
+    except OSError:
+        pytest.skip("no shared CUDA runtime")
+    ok = lambda e: pytest.fail(f"CUDA error {e}") if e else None  # noqa: E731
+    rng = np.random.default_rng(3)
+    pools = [dev(step.make_pool(rng.standard_normal((32, 2, 16, 64)).astype(np.float32))) for _ in "kv"]
+    q = torch.from_numpy(rng.standard_normal((rows, 4, 64)).astype(np.float32)).half().cuda()
+    want, out = torch.zeros_like(q), torch.zeros_like(q)
+    args = (q, *pools, i32(np.arange(32)[None]), i32([500]))
+    kw = dict(row_start=i32([0, rows]), max_rows=rows)
+    dkv.dkv_paged_attend(*args, want, **kw)
+    ws = torch.empty(dkv.dkv_paged_attend_workspace(1, 4, 2, 64, rows), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    if given:  # the call's own stream, another one than the current
+        kw["stream"] = s
+    torch.cuda.synchronize()
+    raw, graph, ex = ctypes.c_void_p(s.cuda_stream), ctypes.c_void_p(), ctypes.c_void_p()
+    with torch.cuda.stream(torch.cuda.current_stream() if given else s):
+        ok(rt.cudaStreamBeginCapture(raw, 2))  # relaxed
+        try:
+            with pytest.raises(ValueError, match="needs a workspace"):
+                dkv.dkv_paged_attend(*args, out, **kw)
+            dkv.dkv_paged_attend(*args, out, workspace=ws, **kw)
+        finally:
+            ended = rt.cudaStreamEndCapture(raw, ctypes.byref(graph))
+    ok(ended)
+    ok(rt.cudaGraphInstantiate(ctypes.byref(ex), graph, ctypes.c_ulonglong(0)))
+    ok(rt.cudaGraphLaunch(ex, raw))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+    ok(rt.cudaGraphExecDestroy(ex))
+    ok(rt.cudaGraphDestroy(graph))
+    # one of torch's needs none, on the capturing stream or on one that joined the capture
+    out.zero_()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        dkv.dkv_paged_attend(*args, out, **kw)
+        torch.cuda.current_stream().wait_stream(s)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)

@@ -573,11 +573,30 @@ def dkv_paged_attend_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_rows=
     return lib().dkv_paged_attend_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_rows)
 
 
+def _capturing(stream, index):
+    """Whether this raw stream is being captured."""
+    import torch
+    if stream == torch._C._cuda_getCurrentRawStream(index):
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, index)):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _in_a_pool(address):
+    """Whether the allocator holds this address in a pool of its own, as it does for the graphs that torch captures."""
+    import torch
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= address < s["address"] + s["total_size"]:
+            return tuple(s["segment_pool_id"]) != (0, 0)
+    return False
+
+
 def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None, max_rows=1,
                      scale=None, v_scale=1.0, lse=None, workspace=None, stream=None):
     """Attention of q [rows, n_q_heads, D] over an E2M1 pool (see include/dkv.h); scale None is
     1/sqrt(D).  Without a workspace (uint8, dkv_paged_attend_workspace bytes) one is taken from
-    torch's caching allocator, on the launching stream."""
+    torch's caching allocator, on the launching stream; under a stream capture that is not torch's
+    own (torch.cuda.graph) the call needs one, which the graph's owner keeps."""
     import torch
     shape, i32 = q.shape, torch.int32
     if len(shape) != 3 or page_table.dim() != 2:
@@ -602,6 +621,9 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
         # The bytes are the launching stream's, so that they are not handed out again before it ran.
         size = max(1, dkv_paged_attend_workspace(B, hq, hkv, D, max_rows))
         pw = taken = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, s)
+        if _capturing(s, dev) and not _in_a_pool(taken):  # the allocator would hand them out while the graph lives
+            torch._C._cuda_cudaCachingAllocator_raw_delete(taken)
+            raise ValueError("a stream capture that torch does not know needs a workspace of its own")
     else:
         pw, size = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
     try:
