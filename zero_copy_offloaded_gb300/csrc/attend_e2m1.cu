@@ -899,16 +899,15 @@ template <typename T, int D, int NT>
 cudaError_t launch(const AttendParams& p, cudaStream_t s) {
   using C = Cfg<D, NT>;
   const int smem = C::kOffBatch + (p.B + 1) * 8 + 3 * p.B * 4;
-  static bool attr_set[64] = {};
+  static PerDevice smem_set;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(attend_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             C::kOffBatch + (DKV_MAX_STEP_BATCH + 1) * 20);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr_set[dev] = true;
-  }
+  e = smem_set(dev, [] {
+    return cudaFuncSetAttribute(attend_kernel<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                C::kOffBatch + (DKV_MAX_STEP_BATCH + 1) * 20);
+  });
+  if (e != cudaSuccess) return e;
   const int fit = 228 * 1024 / (smem + 1024);
   const int grid = kSms * (fit < C::kPerSm ? fit : C::kPerSm);
   attend_kernel<T, D, NT><<<grid, kThreads, smem, s>>>(p);

@@ -4,6 +4,7 @@
 #include <math.h>
 
 #include "e2m1.cuh"
+#include "per_device.h"
 
 namespace dkv {
 

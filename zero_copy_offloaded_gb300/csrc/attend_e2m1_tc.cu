@@ -870,15 +870,12 @@ __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendParams 
 template <typename T, int D>
 cudaError_t launch_attend_tc(const AttendParams& p, int grid, cudaStream_t s) {
   auto k = attend_tc_kernel<T, D>;
-  static bool attr_set[64] = {};
+  static PerDevice smem_set;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 64 || !attr_set[dev]) {
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr_set[dev] = true;
-  }
+  e = smem_set(dev, [k] { return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::kSmem); });
+  if (e != cudaSuccess) return e;
   k<<<grid, kThreads, Cfg<D>::kSmem, s>>>(p);
   const cudaError_t l = cudaGetLastError();
   if (l != cudaSuccess) return l;
