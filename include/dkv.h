@@ -488,7 +488,8 @@ dkv_status dkv_decode_noalloc_debug_withhold(int enable);
  *                       page; the k-th page taken, in that order too, is the k-th
  *                       from the top.
  * Written: row_start [batch + 1]; row_pos, row_slot [max_rows] (position and slot
- * = page * page_tokens + offset of each row; 0 and -1 behind the last);
+ * = page * page_tokens + offset of each row, a slot of -1 where the table or the stack holds a page
+ * outside [0, num_pages); 0 and -1 behind the last);
  * kv_len [batch], the lengths with the new rows; free_left [1]; report [4] =
  * {status, rows, pages taken, longest kv_len}.
  * All or nothing: where the pages, the rows (max_rows) or a sequence's table

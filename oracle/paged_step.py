@@ -117,7 +117,8 @@ def plan(lengths, new, table, free, free_count, P, max_rows):
                 table[b, c] = stack.pop()
             for t in range(int(new[b])):
                 at = int(lengths[b]) + t
-                pos[r], slot[r] = at, table[b, at // P] * P + at % P
+                page = int(table[b, at // P])
+                pos[r], slot[r] = at, page * P + at % P if 0 <= page < len(free) else -1
                 r += 1
         start[b + 1] = r
     return dict(table=table, free=free, row_start=start, pos=pos, slot=slot,

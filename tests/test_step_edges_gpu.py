@@ -8,7 +8,7 @@ import pytest
 import zero_copy_offloaded_gb300 as dkv
 from oracle import paged_step as step
 
-from .test_step_gpu import HALF, dev, host, i32, tdt
+from .test_step_gpu import HALF, check_plan, dev, host, i32, tdt
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -211,3 +211,25 @@ def test_foreign_capture_needs_a_workspace(rows, given):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+# ---- pages that are none -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("P", [16, 256])
+def test_plan_pages_outside_the_pool_are_padding(P):
+    """A page index whose slots pass 2^32 must not come back as a slot of another page."""
+    pages = 64
+    bad = [-1, pages, (1 << 32) // P // 2 + 3, (1 << 31) - 1, -(1 << 31), -((1 << 31) // P) + 5, (1 << 28) + 1]
+    B = len(bad) + 1
+    table = np.full((B, 4), -1, np.int32)
+    table[:-1, 0] = bad
+    table[-1, 0] = 5
+    free = np.full(pages, -1, np.int32)
+    free[:4] = [9, 1 << 28, -7, pages - 1]  # two sequences take pages, one of them no page of the pool
+    length, new = np.full(B, P - 2, np.int32), np.full(B, 2, np.int32)
+    new[[0, 1, 2]] = 4
+    case = (length, new, table, free, 4)
+    want = check_plan(case, P, 40)
+    assert want["report"][0] == 0
+    live = want["slot"][:want["report"][1]]
+    assert sorted(live[live >= 0]) == sorted([5 * P + P - 2, 5 * P + P - 1, (pages - 1) * P, (pages - 1) * P + 1])

@@ -78,13 +78,15 @@ __device__ __forceinline__ void fill_rows(const PlanParams& p, const int* start,
     for (int i = 0; i < U; ++i) {
       const bool on = r[i] < total;
       pos[i] = on ? kv[seq[i]] - (start[seq[i] + 1] - r[i]) : 0;
-      page[i] = on ? __ldcg(p.table + (size_t)seq[i] * p.max_pages + (pos[i] >> p.shift)) : 0;
+      page[i] = on ? __ldcg(p.table + (size_t)seq[i] * p.max_pages + (pos[i] >> p.shift)) : -1;
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
       if (r[i] >= p.max_rows) break;
       p.row_pos[r[i]] = pos[i];
-      p.row_slot[r[i]] = r[i] < total ? (page[i] << p.shift) + (pos[i] & ((1 << p.shift) - 1)) : -1;
+      // no page of the pool (whose slots fit 30 bits; beyond that they would wrap into another page's): padding
+      p.row_slot[r[i]] =
+          (uint32_t)page[i] < (uint32_t)p.num_pages ? (page[i] << p.shift) + (pos[i] & ((1 << p.shift) - 1)) : -1;
     }
   }
 }
