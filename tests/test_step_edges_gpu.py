@@ -8,6 +8,7 @@ import pytest
 import zero_copy_offloaded_gb300 as dkv
 from oracle import paged_step as step
 
+from .step_tiles import CASES, Tiles
 from .test_step_gpu import HALF, check_plan, dev, host, i32, tdt
 
 torch = pytest.importorskip("torch")
@@ -233,3 +234,48 @@ def test_plan_pages_outside_the_pool_are_padding(P):
     assert want["report"][0] == 0
     live = want["slot"][:want["report"][1]]
     assert sorted(live[live >= 0]) == sorted([5 * P + P - 2, 5 * P + P - 1, (pages - 1) * P, (pages - 1) * P + 1])
+
+
+# ---- every tile of every item counts once ------------------------------------------------------------
+
+def run_tiles(case):
+    N = int(case.start[-1]) + 3  # three rows of no sequence
+    q = dev(np.broadcast_to(case.q[None, :, None], (N, case.Hq, case.D)), tdt(case.dtype))
+    out = torch.full(q.shape, 7.0, dtype=q.dtype, device="cuda")
+    lse = torch.full(q.shape[:2], 7.0, device="cuda")
+    dkv.dkv_paged_attend(q, *[dev(p) for p in case.pools], i32(case.table), i32(case.lens), out,
+                         row_start=i32(case.start), max_rows=max(1, max(case.rows)), scale=case.scale, lse=lse)
+    return host(out), host(lse)
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_every_tile_counts_once(name):
+    case = Tiles(*CASES[name])
+    out, lse = run_tiles(case)
+    for b, n in enumerate(case.rows):
+        at = slice(case.start[b], case.start[b] + n)
+        if n:
+            assert case.bad(b, out[at], lse[at], case.reference(b)) == (0, 0), b
+    assert np.all(out[case.start[-1]:] == 7) and np.all(lse[case.start[-1]:] == 7)
+
+
+def test_many_rows_with_offsets_past_32_bits():
+    # 4.6 GB pools, the pages at their end and one at their start
+    case = Tiles([1000, 300], [90, 40], 16, 8, 128, "bf16")
+    n, Hkv, nbytes = case.pools[0].shape
+    pages = 46 * 10 ** 8 // (Hkv * nbytes)
+    big = [torch.empty((pages, Hkv, nbytes), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    assert big[0].numel() > 1 << 32
+    for b, p in zip(big, case.pools):
+        b[0] = dev(p[:1])[0]
+        b[pages - n:] = dev(p)
+    table = np.where(case.table == 0, 0, case.table + pages - n)
+    assert (table == 0).any() and table.max() > (1 << 32) // (Hkv * nbytes)
+    N = int(case.start[-1])
+    q = dev(np.broadcast_to(case.q[None, :, None], (N, 16, 128)), torch.bfloat16)
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+    dkv.dkv_paged_attend(q, *big, i32(table), i32(case.lens), out, row_start=i32(case.start), max_rows=90,
+                         scale=case.scale, lse=lse)
+    for b in range(2):
+        at = slice(case.start[b], case.start[b + 1])
+        assert case.bad(b, host(out)[at], host(lse)[at], case.reference(b)) == (0, 0), b
