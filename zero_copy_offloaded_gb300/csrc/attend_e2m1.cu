@@ -26,8 +26,8 @@
 // MMA operands carry no rounding of the cache.  bf16 queries are brought to fp16's
 // range by a power of two per row (exact, undone on the scores; an element below
 // 2^-27 of its row's largest may lose bits).  P is rounded to fp16, as the tensor
-// operand must be 16 bits: 2^-11 of a weight, and 2^-35 of the row's largest for
-// weights below 2^-24 of it (kBias); scores, references, sums and outputs stay in fp32.
+// operand must be 16 bits: 2^-11 of a weight, and 2^-32 of the row's largest for
+// weights below 2^-21 of it (kBias); scores, references, sums and outputs stay in fp32.
 //
 // Why mma.sync here: tcgen05 takes at least 128 rows (or columns) a tile and its operands from
 // shared memory, so the converted keys would be written and read there once more.  Sixteen
@@ -80,12 +80,13 @@ constexpr int kJoinOnce = 32, kGroup = 16;
 __device__ __forceinline__ int group_size(int pieces) { return max(kGroup, (pieces + kJoinOnce - 1) / kJoinOnce); }
 constexpr int kSms = 152, kMaxCtas = 4 * kSms;
 // A row's weights are 2^(s - m) with m below its running maximum, so that the largest are 2^kBias to
-// 2^(kBias + kLazy): fp16 has room above 1, and a weight keeps all its bits down to 2^-24 of the
-// row's largest and counts down to 2^-35 (with m at the maximum itself 2^-14 and 2^-25: thousands of
-// keys beside one that is 17 above them were lost).  A factor of 4 is left below fp16's largest number
-// for the rounding of m and of its threshold, at most 2^-2 each for scores up to 2^21.
-constexpr float kBias = 10.0f;
-constexpr float kLazy = 4.0f;   // m moves only when a score passes m + kBias by this
+// 2^(kBias + kLazy): fp16 has room above 1, and a weight keeps all its bits down to 2^-21 of the
+// row's largest and counts down to 2^-32 (with m at the maximum itself 2^-14 and 2^-25: thousands of
+// keys beside one that is 17 above them were lost).  A factor of 2 is left below fp16's largest number
+// for the rounding of m and of its threshold, at most 2^-2 each for scores up to 2^21.  More bias leaves less
+// to kLazy: drafts of 5 with scores of a standard deviation of 4 take 52.4 us with 7 and 8, 54.6 with 10 and 5.
+constexpr float kBias = 7.0f;
+constexpr float kLazy = 8.0f;    // m moves only when a score passes m + kBias by this
 constexpr float kNone = -3e38f;  // m of a row that has seen no key
 
 template <int D, int NT>

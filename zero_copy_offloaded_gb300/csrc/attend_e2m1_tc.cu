@@ -17,12 +17,15 @@
 // that the P.V before it is finished: O may be rescaled then without a barrier of its own.
 //
 // A softmax thread takes its row's scores 32 at a time and writes the weights over columns
-// that it has read.  The running reference m of a row is 10 (a weight of 2^10) below the maximum of
+// that it has read.  The running reference m of a row is 7 (a weight of 2^7) below the maximum of
 // the first 32 scores with a visible key; a later 32 whose weights sum to at most 60000 have none
 // above that, which fp16 and the fp32 sums hold, so no maximum is taken.  Where they sum to more (or to
-// infinity or NaN, as they do at the start) the row takes their maximum, less 10, as m and rescales what
-// it has: the tile's earlier weights, l and O.  The largest weight is at least 2^10 throughout, so
-// a weight keeps all of fp16's bits down to 2^-24 of the row's largest and counts down to 2^-35.
+// infinity or NaN, as they do at the start) the row takes their maximum, less 7, as m and rescales what
+// it has: the tile's earlier weights, l and O.  The largest weight is at least 2^7 throughout, so
+// a weight keeps all of fp16's bits down to 2^-21 of the row's largest and counts down to 2^-32.  A lower
+// m keeps more and moves more often: with scores of a standard deviation of 1, 2, 4 and 16 the chunk
+// below takes 1.54, 1.54, 1.77 and 1.97 ms with 7, 1.54, 1.73, 1.82 and 2.04 with 10, and 1.54, 1.54, 1.59 and
+// 1.88 with 0, where weights below 2^-25 were lost.
 //
 // What bounds it: 4 D flops per (row, key) on the tensor cores.  4096 rows of 32/8 heads of 128
 // over 28672 keys and themselves (2.06 TFLOP) take 1.55 ms, 1327 TFLOP/s of 1912 measured.  A key
@@ -52,8 +55,8 @@ constexpr int kThreads = (10 + kConvert) * 32;
 constexpr int kReg = 128 * 128;        // a 128-row x 128-byte swizzled region
 constexpr int kRaw = 3;                // raw half tiles (K or V codes and scales) in flight
 constexpr float kNone = -3e38f;        // m of a row that has seen no key
-constexpr float kBias = 10.f;          // m below the maximum that it is taken from
-// 32 weights just taken as reference sum to 2^15 at most, 2^15.3 with the rounding of m for scores up to 2^21
+constexpr float kBias = 7.f;           // m below the maximum that it is taken from
+// (32 weights whose maximum gave m sum to 2^12, 2^12.3 with the rounding of m for scores up to 2^21)
 constexpr float kSumBound = 60000.f;
 
 constexpr uint32_t kTmS = 0, kTmO = 256;  // S of tile t at 128 t, O at 256 + 128 t
