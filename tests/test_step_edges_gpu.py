@@ -279,3 +279,31 @@ def test_many_rows_with_offsets_past_32_bits():
     for b in range(2):
         at = slice(case.start[b], case.start[b + 1])
         assert case.bad(b, host(out)[at], host(lse)[at], case.reference(b)) == (0, 0), b
+
+
+def test_public_calls_of_torch_do(monkeypatch):
+    # a torch without the inner calls that the binding prefers
+    rng = np.random.default_rng(3)
+    pools = [dev(step.make_pool(rng.standard_normal((32, 2, 16, 64)).astype(np.float32))) for _ in "kv"]
+    q = torch.from_numpy(rng.standard_normal((2, 4, 64)).astype(np.float32)).half().cuda()
+    args = (q, *pools, i32(np.arange(32).reshape(2, 16)), i32([200, 100]))
+    want, out, side = [torch.zeros_like(q) for _ in range(3)]
+    dkv.dkv_paged_attend(*args, want)
+    had = {n: getattr(torch._C, n) for n in ("_cuda_getDevice", "_cuda_getCurrentRawStream", "_cuda_cudaCachingAllocator_raw_alloc",
+                                            "_cuda_cudaCachingAllocator_raw_delete") if hasattr(torch._C, n)}
+    dkv._torch_calls.cache_clear()
+    try:
+        with monkeypatch.context() as m:  # torch's public calls use some of them themselves
+            for n in had:
+                m.delattr(torch._C, n)
+            public = dkv._torch_calls()
+        assert not any(f in had.values() for f in public)
+        dkv.dkv_paged_attend(*args, out)
+        s = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        dkv.dkv_paged_attend(*args, side, stream=s)
+        torch.cuda.synchronize()
+        assert dkv._torch_calls() is public
+    finally:
+        dkv._torch_calls.cache_clear()
+    assert torch.equal(out, want) and torch.equal(side, want)

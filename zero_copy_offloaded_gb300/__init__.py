@@ -462,13 +462,27 @@ def _pool(t, what, u8, index, D):
     return t.data_ptr(), (pages, heads, nbytes // per)
 
 
+@functools.lru_cache(maxsize=None)
+def _torch_calls():
+    """torch's current device, raw current stream of a device, and its allocator's allocate (size, raw stream)
+    and free: the calls inside its public ones, which take 1 to 3 us more of the 10 that the smallest
+    operators take, or the public ones where a release does not have them."""
+    import torch
+    c, cuda = torch._C, torch.cuda
+    return (getattr(c, "_cuda_getDevice", cuda.current_device),
+            getattr(c, "_cuda_getCurrentRawStream", lambda index: cuda.current_stream(index).cuda_stream),
+            getattr(c, "_cuda_cudaCachingAllocator_raw_alloc",
+                    lambda size, stream: cuda.caching_allocator_alloc(size, stream=stream)),
+            getattr(c, "_cuda_cudaCachingAllocator_raw_delete", cuda.caching_allocator_delete))
+
+
 def _launch(index, stream):
     """The stream to launch on; the tensors must be on the current device, as the library launches there."""
-    import torch
-    if index < 0 or index != torch._C._cuda_getDevice():  # a CUDA tensor is there: torch is set up
+    device, current, _, _ = _torch_calls()
+    if index < 0 or index != device():  # a CUDA tensor is there: torch is set up
         raise ValueError("the tensors are not on the current CUDA device")
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
+        return current(index)
     return _stream(stream)
 
 
@@ -576,7 +590,7 @@ def dkv_paged_attend_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_rows=
 def _capturing(stream, index):
     """Whether this raw stream is being captured."""
     import torch
-    if stream == torch._C._cuda_getCurrentRawStream(index):
+    if stream == _torch_calls()[1](index):
         return torch.cuda.is_current_stream_capturing()
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, index)):
         return torch.cuda.is_current_stream_capturing()
@@ -620,9 +634,10 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
         # The allocator's own call: a tensor around the bytes costs 3 us of the smallest calls' 13.
         # The bytes are the launching stream's, so that they are not handed out again before it ran.
         size = max(1, dkv_paged_attend_workspace(B, hq, hkv, D, max_rows))
-        pw = taken = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, s)
+        _, _, allocate, release = _torch_calls()
+        pw = taken = allocate(size, s)
         if _capturing(s, dev) and not _in_a_pool(taken):  # the allocator would hand them out while the graph lives
-            torch._C._cuda_cudaCachingAllocator_raw_delete(taken)
+            release(taken)
             raise ValueError("a stream capture that torch does not know needs a workspace of its own")
     else:
         pw, size = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
@@ -632,7 +647,7 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
                          page_tokens, pages, max_pages, D ** -0.5 if scale is None else scale, v_scale), s)
     finally:
         if taken:
-            torch._C._cuda_cudaCachingAllocator_raw_delete(taken)
+            release(taken)
     if st:
         _check(st, "dkv_paged_attend")
 
