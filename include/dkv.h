@@ -469,7 +469,8 @@ dkv_status dkv_decode_noalloc_debug_withhold(int enable);
  * row_start[b+1]-1, and rows behind the last sequence are padding (slot -1):
  * nothing of them is written.  Pools are device-accessible pointers: HBM, or
  * the mapped alias of pinned host memory (dkv_cache_device_ptrs of a
- * DKV_KV_E2M1 cache), which is then read across the host link.
+ * DKV_KV_E2M1 cache), which is then read across the host link (see dkv_paged_attend for
+ * how often).
  * Nothing here allocates, synchronises or keeps state between calls; errors
  * return before anything is enqueued.  Calls that may overlap on the GPU need
  * outputs and workspaces of their own. */
@@ -530,7 +531,10 @@ dkv_status dkv_step_plan(const int32_t* lengths, const int32_t* new_tokens, int3
  * Arithmetic is fp32, each operation rounded once, the key norm's sum of squares in
  * two words.  A block of 16 takes the scale e4m3(max|y| / 6), saturating at 448, and
  * the codes e2m1(y / scale), both to nearest even, saturating; a block with a NaN
- * or an infinity gets a NaN scale and reads back as NaN.
+ * or an infinity gets a NaN scale and reads back as NaN.  Where max|y| is below 0.0059 the block's
+ * scale, and so the block, is 0, and below 0.094 the scale is subnormal, with one to three bits: a
+ * k_scale or v_scale below 1 brings the rows of a model with such small keys or values (V as
+ * a rule) into range.
  * Errors: INVALID_ARG, UNSUPPORTED (head_dim not 64 or 128), CUDA. */
 typedef struct {
     const void *q, *k, *v;
@@ -558,9 +562,16 @@ dkv_status dkv_qkv_append(const dkv_append_t* args, void* stream);
  * the natural log of the sum of exp(scale * q . k).  Rows of no sequence are left as
  * they were.
  * max_rows: no sequence has more rows than this; it chooses the kernel, any lengths
- * on the device are then served.  Lengths above max_pages * page_tokens are cut to
- * that; a page index outside [0, num_pages) counts as a page without keys.  K's
- * scale (dkv_append_t.k_scale) belongs into `scale`.
+ * on the device are then served.  It does so for the whole call: up to 32 packed rows
+ * (max_rows * heads per KV head) a kernel for few rows, above that one for many, in which
+ * a single token costs about three times as much (64 of them at 32768 keys beside a chunk of
+ * 2048 rows: 2.4 ms, as two calls 1.3).  The few-row kernel reads a sequence's keys once
+ * for all its packed rows, the many-row kernel once for each 256 of them: a pool in host
+ * memory crosses the link that often (4096 rows with 4 heads per KV head: 64 times), so
+ * chunks want their pages in HBM.
+ * Lengths above max_pages * page_tokens are cut to that; a page index outside
+ * [0, num_pages) counts as a page without keys.  K's scale (dkv_append_t.k_scale) belongs
+ * into `scale`.
  * A NaN in a key or value reaches the rows that see it and no others.
  * q, k.v products run on fp16 tensor operands (cache values and fp16 queries exactly;
  * bf16 queries scaled by a power of two per row; weights rounded to fp16, which costs

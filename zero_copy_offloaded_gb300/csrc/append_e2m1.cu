@@ -17,8 +17,10 @@
 //
 // What bounds it: each byte once through memory, 26 KB a row of 32/8 heads of 128.  4096 such rows
 // take 29 us (3.7 TB/s of 6.8 measured), 16384 rows of 32/32 fp16 heads of 64, rotated in half
-// and without norms, 86 us (5.1 TB/s).  The first has 65% of its issue slots busy: the norms, the
-// exact sums and the quantisation (queries alone take 15 us, keys and values alone 14).
+// and without norms, 86 us (5.1 TB/s).  In the first neither memory nor a pipe is full: its warps wait for
+// their own chains of scalar fp32 (norms, exact sums, quantisation; 65 % of the issue slots), and queries
+// alone (15 us) and keys and values alone (14) add up.  A pool in host memory takes 53 us for them: the codes
+// cross the link in stores of 4 bytes a lane, the scales of 1.
 #include <float.h>
 #include <stdio.h>
 
@@ -59,7 +61,8 @@ constexpr int kThreads = 256;
 // Rows of each lane group for one token, loaded at once: a query row is the lighter work.
 constexpr int kIterQ = 8, kIterKV = 4;
 
-// s + e of a and b with the rounding error kept (any order of magnitudes).
+// s + b with its rounding error added to e, for any order of magnitudes (Knuth, The Art of Computer
+// Programming, volume 2, section 4.2.2).
 __device__ __forceinline__ void two_sum(float& s, float& e, float b) {
   const float t = __fadd_rn(s, b);
   const float z = __fsub_rn(t, s);
@@ -140,8 +143,10 @@ __device__ __forceinline__ void norm_row(float (&x)[8], const float (&g)[8], flo
   for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), g[e]);
 }
 
-// y / s correctly rounded for s whose correctly rounded reciprocal is r: the
-// quotient's residual is exact in one fused multiply-add, and a second one corrects it.
+// y / s for s whose correctly rounded reciprocal is r: the quotient's residual is exact in one fused
+// multiply-add, and a second one corrects it (Markstein, Computation of elementary functions on the IBM RISC
+// System/6000 processor, 1990).  For the divisors here, E4M3 numbers (four bits) and 6, the result is
+// the correctly rounded quotient for every significand of y.
 __device__ __forceinline__ float divide(float y, float s, float r) {
   const float q = __fmul_rn(y, r);
   return __fmaf_rn(__fmaf_rn(-q, s, y), r, q);

@@ -13,7 +13,7 @@
 // (no host copy, so a captured graph serves any lengths).  A CTA that holds a whole
 // item writes its rows; an item cut between CTAs leaves fp32 partials, which the CTA that
 // finishes last joins in CTA order (no CTA waits for another), many pieces in groups first: one
-// KV head over 131072 keys takes 19 us, and took 98 with its 456 pieces joined by one CTA, row by row.
+// KV head over 131072 keys takes 19 us so, 98 where one CTA joins its 456 pieces row by row.
 //
 // Inside a CTA each of 4 warps takes 32 keys of every tile through its own
 // cp.async ring, with no barrier between warps until the item ends.  Per 16 keys:
@@ -81,8 +81,8 @@ __device__ __forceinline__ int group_size(int pieces) { return max(kGroup, (piec
 constexpr int kSms = 152, kMaxCtas = 4 * kSms;
 // A row's weights are 2^(s - m) with m below its running maximum, so that the largest are 2^kBias to
 // 2^(kBias + kLazy): fp16 has room above 1, and a weight keeps all its bits down to 2^-21 of the
-// row's largest and counts down to 2^-32 (with m at the maximum itself 2^-14 and 2^-25: thousands of
-// keys beside one that is 17 above them were lost).  A factor of 2 is left below fp16's largest number
+// row's largest and counts down to 2^-32 (with m at the maximum itself 2^-14 and 2^-25, where thousands of
+// keys beside one that is 17 above them are lost).  A factor of 2 is left below fp16's largest number
 // for the rounding of m and of its threshold, at most 2^-2 each for scores up to 2^21.  More bias leaves less
 // to kLazy: drafts of 5 with scores of a standard deviation of 4 take 52.4 us with 7 and 8, 54.6 with 10 and 5.
 constexpr float kBias = 7.0f;
@@ -721,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, NT>::kPerSm) attend_kernel(co
     for (int r0 = 0; r0 < rows; r0 += 8) {
       // Eight rows of every warp, a row's pair i of the D/8 dims of thread group g at place
       // J g + (i ^ x), x from the row and g: neither these stores nor the loads below meet a
-      // bank conflict (with plain padded rows a round took 1600 cycles, two thirds of them for conflicts).
+      // bank conflict (with plain padded rows a round takes 1600 cycles, two thirds of them for conflicts).
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll

@@ -25,7 +25,7 @@
 // a weight keeps all of fp16's bits down to 2^-21 of the row's largest and counts down to 2^-32.  A lower
 // m keeps more and moves more often: with scores of a standard deviation of 1, 2, 4 and 16 the chunk
 // below takes 1.54, 1.54, 1.77 and 1.97 ms with 7, 1.54, 1.73, 1.82 and 2.04 with 10, and 1.54, 1.54, 1.59 and
-// 1.88 with 0, where weights below 2^-25 were lost.
+// 1.88 with 0, where weights below 2^-25 are lost.
 //
 // What bounds it: 4 D flops per (row, key) on the tensor cores.  4096 rows of 32/8 heads of 128
 // over 28672 keys and themselves (2.06 TFLOP) take 1.55 ms, 1327 TFLOP/s of 1912 measured.  A key
@@ -33,9 +33,11 @@
 // tile's 128 x 128 per group, whose exponentials alone take 1024 of the special-function units),
 // which two Q tiles hide only in part, and shared memory's bandwidth, which the MMAs' operands
 // (192 KB a key tile) and the converted tiles (64 KB) share.  Tensor memory is full (S and O of two
-// tiles), which rules out a third tile and a Q in tensor memory.  Five of sixteen exponentials as
-// degree-4 polynomials on the FMA pipe took 2.20 ms where all of them on the special-function units
-// took 1.86.
+// tiles), which rules out a third tile and a Q in tensor memory.  Exponentials as degree-4 polynomials
+// on the FMA pipe do not help (five of sixteen: 2.20 ms against 1.86).
+//
+// Every item reads its keys, so a pool is read once for each 256 packed rows.  From HBM that is hidden;
+// a pool in host memory crosses the link as often (4096 rows of 32/8 heads over 28672 keys: 10.8 ms).
 #include <float.h>
 #include <math.h>
 
@@ -693,7 +695,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           for (int t = 0; ok && t < 2; ++t) {
             if (t == 0 || two) {
               ok = warp_wait(&bars->p_ready[t], np[t]++ & 1, bars);
-              // O of both tiles has been read out: neither group is more than an item behind
+              // O of both tiles has been read out: neither group is more than an item behind.  (In a piece of
+              // one key tile the second Q tile waits for the first's read-out of the same piece.)
               for (int u = 0; u < 2 && ok && fresh; ++u)
                 if (no[u] > 0 && (u != 1 || t == 1 || !two)) ok = warp_wait(&bars->o_free[u], (no[u] - 1) & 1, bars);
               if (!ok) break;
@@ -790,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
 // to a lane, of the item that CTA c began, and each of its eight warps D / 8 outputs.  An item
 // in more pieces than 32-output parts of a row: the blocks of the CTAs that it fills take a part
 // each, their warps every eighth piece, and the eight meet in shared memory.  (One block a CTA's
-// rows for all pieces took 52 us of 82 for 16 rows of one KV head over 131072 keys.)
+// rows for all pieces: 82 us instead of 44 for 16 rows of one KV head over 131072 keys.)
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attend_tc_join_kernel(const AttendParams p) {
   __shared__ float4 s_acc[8][8][32];  // [warp][four outputs][row]
