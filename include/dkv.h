@@ -603,7 +603,11 @@ dkv_status dkv_paged_attend(const dkv_attend_t* args, void* stream);
 size_t dkv_paged_attend_workspace(int batch, int n_q_heads, int n_kv_heads, int head_dim,
                                   int max_rows);
 
-/* Test hook (process-wide, off by default): with enable != 0 that kernel of the calls that follow never
+/* 1: the stream is being captured into a graph, which then owns what its launches use; 0: it is
+ * not; -1: the stream cannot say. */
+int dkv_stream_capturing(void* stream);
+
+/* Test hook (process-wide, off by default): with enable != 0 the many-row kernel of the calls that follow never
  * signals an item's outputs, so that its waits run out (some seconds). */
 dkv_status dkv_paged_attend_debug_withhold(int enable);
 

@@ -1,6 +1,9 @@
 """The device-side step where sums, ranges and waits have little room: peaked softmaxes, items in many
 pieces, scales, waits that run out."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -307,3 +310,34 @@ def test_public_calls_of_torch_do(monkeypatch):
     finally:
         dkv._torch_calls.cache_clear()
     assert torch.equal(out, want) and torch.equal(side, want)
+
+
+ASYNC = """
+import numpy as np, torch
+import zero_copy_offloaded_gb300 as dkv
+from oracle import paged_step as step
+assert torch.cuda.get_allocator_backend() == "cudaMallocAsync"
+rng = np.random.default_rng(3)
+pools = [torch.from_numpy(step.make_pool(rng.standard_normal((32, 2, 16, 64)).astype(np.float32))).cuda() for _ in "kv"]
+q = torch.from_numpy(rng.standard_normal((2, 4, 64)).astype(np.float32)).half().cuda()
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+args = (q, *pools, i(list(range(32))).view(2, 16), i([200, 100]))
+want, out = torch.zeros_like(q), torch.zeros_like(q)
+dkv.dkv_paged_attend(*args, want)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    dkv.dkv_paged_attend(*args, out)
+g.replay()
+torch.cuda.synchronize()
+assert torch.equal(out, want)
+print("as without a graph")
+"""
+
+
+def test_capture_with_another_allocator():
+    # torch's cudaMallocAsync backend makes the workspace a node of the graph
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    env = dict(os.environ, PYTORCH_CUDA_ALLOC_CONF="backend:cudaMallocAsync", PYTHONPATH=root)
+    r = subprocess.run([sys.executable, "-c", ASYNC], env=env, cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "as without a graph" in r.stdout, r.stderr[-2000:]

@@ -153,6 +153,8 @@ def lib(build_if_missing: bool = False):
     L.dkv_last_launch_count.restype = ctypes.c_int
     L.dkv_pci_numa_node.argtypes = [ctypes.c_char_p, ctypes.c_char_p]
     L.dkv_pci_numa_node.restype = ctypes.c_int
+    L.dkv_stream_capturing.argtypes = [P]
+    L.dkv_stream_capturing.restype = ctypes.c_int
     L.dkv_paged_attend_workspace.argtypes = [I] * 5
     L.dkv_paged_attend_workspace.restype = ctypes.c_size_t
     L.dkv_numa_probe.argtypes = [ctypes.c_int]
@@ -587,18 +589,12 @@ def dkv_paged_attend_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_rows=
     return lib().dkv_paged_attend_workspace(batch, n_q_heads, n_kv_heads, head_dim, max_rows)
 
 
-def _capturing(stream, index):
-    """Whether this raw stream is being captured."""
+def _kept_for_graph(address):
+    """Whether torch's allocator keeps this address for a graph: in a pool of its own, as it does for the graphs that
+    torch captures, or (other allocators) as a node of the graph."""
     import torch
-    if stream == _torch_calls()[1](index):
-        return torch.cuda.is_current_stream_capturing()
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, index)):
-        return torch.cuda.is_current_stream_capturing()
-
-
-def _in_a_pool(address):
-    """Whether the allocator holds this address in a pool of its own, as it does for the graphs that torch captures."""
-    import torch
+    if torch.cuda.get_allocator_backend() != "native":
+        return True
     for s in torch.cuda.memory_snapshot():
         if s["address"] <= address < s["address"] + s["total_size"]:
             return tuple(s["segment_pool_id"]) != (0, 0)
@@ -636,7 +632,8 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
         size = max(1, dkv_paged_attend_workspace(B, hq, hkv, D, max_rows))
         _, _, allocate, release = _torch_calls()
         pw = taken = allocate(size, s)
-        if _capturing(s, dev) and not _in_a_pool(taken):  # the allocator would hand them out while the graph lives
+        if lib().dkv_stream_capturing(s) == 1 and not _kept_for_graph(taken):
+            # the allocator would hand the bytes out again while the graph lives
             release(taken)
             raise ValueError("a stream capture that torch does not know needs a workspace of its own")
     else:

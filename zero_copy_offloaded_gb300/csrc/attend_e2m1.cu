@@ -1002,6 +1002,15 @@ extern "C" dkv_status dkv_paged_attend(const dkv_attend_t* a, void* stream) {
   return DKV_OK;
 }
 
+extern "C" int dkv_stream_capturing(void* stream) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(static_cast<cudaStream_t>(stream), &status) != cudaSuccess) {
+    cudaGetLastError();
+    return -1;
+  }
+  return status != cudaStreamCaptureStatusNone;
+}
+
 extern "C" dkv_status dkv_paged_attend_debug_withhold(int enable) {
   g_debug_withhold = enable ? 1 : 0;
   return DKV_OK;
