@@ -574,10 +574,11 @@ dkv_status dkv_qkv_append(const dkv_append_t* args, void* stream);
  * into `scale`.
  * A NaN in a key or value reaches the rows that see it and no others.
  * q, k.v products run on fp16 tensor operands (cache values and fp16 queries exactly;
- * bf16 queries scaled by a power of two per row; weights rounded to fp16, which costs
- * 2^-11 of a weight, or 2^-32 of the row's largest where a weight is below 2^-21 of it),
- * sums and softmax statistics in fp32.  |scale * q . k| up to 2^21 is served; where it is larger
- * a row may become NaN.  The result does not depend on timing.
+ * bf16 queries scaled by a power of two per row, where an element below 2^-27 of its row's
+ * largest may lose bits; weights rounded to fp16, which costs 2^-11 of a weight, or 2^-32 of
+ * the row's largest where a weight is below 2^-21 of it), sums and softmax statistics in
+ * fp32 (one head over 2^24 keys: 2^-10 and less).  |scale * q . k| up to 2^21 is served; where it
+ * is larger a row may become NaN.  The result does not depend on timing.
  * workspace: device memory of dkv_paged_attend_workspace bytes (0 for arguments
  * that dkv_paged_attend refuses), on a 256-byte boundary; its contents do not matter
  * before and after a call.
