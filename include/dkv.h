@@ -612,6 +612,81 @@ int dkv_stream_capturing(void* stream);
  * signals an item's outputs, so that its waits run out (some seconds). */
 dkv_status dkv_paged_attend_debug_withhold(int enable);
 
+/* ---- the life of a cache's pages ------------------------------------------- */
+
+/* Sequences share, move and give back pages on the GPU.  A pool's pages have no counters: the page
+ * table says who holds what (the ceil(kv_len / page_tokens) first entries of a sequence's row), and a page that no
+ * sequence holds is free.  Several rows may name one page; dkv_step_plan appends to a sequence's last,
+ * partly filled page only, which dkv_pages_fork never shares.  A sequence that may share pages ends by
+ * dkv_pages_fork (source -1): dkv_step_plan's release would put a shared page on the stack while others
+ * hold it.  A table that serves several pools (layers; keys, values and their scales) takes one fork or
+ * compaction and one dkv_pages_copy over all of them:
+ *
+ *   dkv_pages_fork     sequences go on as copies of others, or end
+ *   dkv_pages_compact  the pages held move to the front of the pool
+ *   dkv_pages_copy     the bytes that the two (or the caller) want moved
+ *
+ * workspace: device memory of dkv_pages_workspace bytes (0 for sizes that the calls refuse) on a 256-byte
+ * boundary, for fork and compact; its contents do not matter before and after a call.  Nothing
+ * allocates, synchronises or keeps state; all of it can be captured.  Calls that may overlap on the GPU need
+ * outputs and workspaces of their own. */
+size_t dkv_pages_workspace(int batch, int max_pages, int num_pages);
+
+/* New sequence b becomes old sequence sources[b]: its length, and its pages.  Below 0: b ends (or stays
+ * empty).  All int32 device memory.
+ *   page_table [batch][max_pages], kv_len [batch]  before the call
+ *   sources    [batch]  0 .. batch - 1, or below 0
+ *   free_pages [num_pages], free_count [1]  the stack of dkv_step_plan
+ * Full pages are shared.  Where the last page of a sequence is filled in part, one of the rows that go on as it keeps
+ * that page (the sequence itself if sources[b] = b, else the lowest such b); every other one takes a page from
+ * the stack, in order of b, the k-th from the top, and has copies[b] = {the source's page, its own}.  Pages that were
+ * held before and are not any more are pushed first, in ascending order.
+ * Written: table_out [batch][max_pages] (the entries of pages held; others are left as they were), len_out [batch],
+ * free_left [1], copies [batch][2] ({-1, -1}: nothing to copy), report [4] = {status, pages released, pages
+ * taken, longest len_out}.
+ * All or nothing: where the stack does not hold enough (or would hold more than num_pages), or a length is above
+ * max_pages * page_tokens, report[0] is DKV_ERR_CAPACITY, and with a source of batch or more
+ * DKV_ERR_INVALID_ARG; nothing is copied, and table_out, len_out and free_left are what came in.
+ * A page index outside [0, num_pages) is handed on and never released.  Lengths below 0 count as 0.
+ * table_out may be page_table, len_out kv_len and free_left free_count (in place); other buffers
+ * must not overlap.  Errors: INVALID_ARG, CUDA. */
+dkv_status dkv_pages_fork(const int32_t* page_table, const int32_t* kv_len, const int32_t* sources,
+                          int32_t* free_pages, const int32_t* free_count, int batch, int max_pages,
+                          int page_tokens, int num_pages, int32_t* table_out, int32_t* len_out,
+                          int32_t* free_left, int32_t* copies, int32_t* report, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* The pages that any sequence holds, `live` of them, move to pages 0 .. live - 1: the i-th of them from page
+ * `live` on, in ascending order, goes to the i-th page below `live` that nobody holds.  Pages held by
+ * something other than a row of the table count as free.
+ * Written: table_out [batch][max_pages] (entries of pages held), moves [max_moves][2] = {from, to} in that order, {-1, -1} behind the
+ * last (max_moves is num_pages / 2 at least, moves may be null where num_pages is 1), free_pages [num_pages]:
+ * num_pages - 1 down to live, so that the lowest page is taken first, the rest left as it was; free_left [1]; report [4] = {status,
+ * pages moved, live, longest kv_len}.  A page index outside [0, num_pages) is left as it is.
+ * With a length above max_pages * page_tokens report[0] is DKV_ERR_CAPACITY, nothing moves, table_out is
+ * page_table, and free_pages and free_left are not written.
+ * The bytes move by dkv_pages_copy(moves), of every pool behind the table; until then the new table
+ * must not be used.  table_out may be page_table; other buffers must not overlap.  Errors: INVALID_ARG, CUDA. */
+dkv_status dkv_pages_compact(const int32_t* page_table, const int32_t* kv_len, int batch, int max_pages,
+                             int page_tokens, int num_pages, int32_t* table_out, int32_t* free_pages,
+                             int32_t* free_left, int32_t* moves, int max_moves, int32_t* report,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Page `to` of each pool's dst takes the bytes of page `from` of its src, for every {from, to} of pairs
+ * [n_pairs][2] (device memory).  A pair with an index outside the pool is skipped.  src and dst may be one
+ * pool, or two of different sizes, in HBM or in pinned host memory (pages leave for the host, or come back).
+ * No page may be `to` of two pairs, nor `to` of one and `from` of another in the same pool.
+ * pools is host memory; up to 64 pools of one alignment go in one launch.
+ * Errors: INVALID_ARG (page_bytes not a multiple of 4 or above 2^30, a pool not on a 4-byte boundary), CUDA. */
+typedef struct {
+    const void* src;
+    void* dst;
+    size_t page_bytes;
+    int src_pages, dst_pages;
+} dkv_page_pool_t;
+dkv_status dkv_pages_copy(const int32_t* pairs, int n_pairs, const dkv_page_pool_t* pools, int n_pools,
+                          void* stream);
+
 /* Number of kernel launches the last dkv_decode / dkv_prefill enqueued. */
 int dkv_last_launch_count(void);
 

@@ -32,6 +32,7 @@ __all__ = [
     "dkv_decode_noalloc_debug_withhold", "dkv_pci_numa_node", "dkv_numa_probe",
     "dkv_step_plan", "dkv_qkv_append", "dkv_paged_attend", "dkv_paged_attend_workspace",
     "dkv_paged_attend_debug_withhold",
+    "dkv_pages_fork", "dkv_pages_compact", "dkv_pages_copy", "dkv_pages_workspace",
     "rope_table", "MAX_STEP_BATCH",
 ]
 
@@ -79,6 +80,7 @@ class _CacheDesc(ctypes.Structure):
 # The argument structures of include/dkv.h, packed in one call (native alignment)
 _APPEND = struct.Struct("@3P3q10P10i3f")
 _ATTEND = struct.Struct("@PqPPPPPPPPN10i2f")
+_PAGE_POOL = struct.Struct("@PPN2i")
 KV_FORMATS = {"native": 0, "e4m3": 1, "e2m1": 2}
 MAX_STEP_BATCH = 1024
 
@@ -138,6 +140,9 @@ def lib(build_if_missing: bool = False):
         "dkv_qkv_append": [P, P],
         "dkv_paged_attend": [P, P],
         "dkv_paged_attend_debug_withhold": [I],
+        "dkv_pages_fork": [P] * 5 + [I] * 4 + [P] * 6 + [Z, P],
+        "dkv_pages_compact": [P, P, I, I, I, I, P, P, P, P, I, P, P, Z, P],
+        "dkv_pages_copy": [P, I, P, I, P],
         "dkv_project": [P, P, P, I, I, I, I, P],
         "dkv_cache_debug_withhold": [P, I],
     }
@@ -157,6 +162,8 @@ def lib(build_if_missing: bool = False):
     L.dkv_stream_capturing.restype = ctypes.c_int
     L.dkv_paged_attend_workspace.argtypes = [I] * 5
     L.dkv_paged_attend_workspace.restype = ctypes.c_size_t
+    L.dkv_pages_workspace.argtypes = [I] * 3
+    L.dkv_pages_workspace.restype = ctypes.c_size_t
     L.dkv_numa_probe.argtypes = [ctypes.c_int]
     L.dkv_numa_probe.restype = ctypes.c_int
     _lib = L
@@ -601,6 +608,24 @@ def _kept_for_graph(address):
     return False
 
 
+def _workspace(workspace, wanted, dev, s):
+    """Address and size of the caller's workspace, or of one taken from torch's allocator, whose address comes last and
+    which the caller releases once the call is enqueued."""
+    if workspace is not None:
+        import torch
+        return _arg(workspace, "workspace", torch.uint8, dev), workspace.numel(), 0
+    # The allocator's own call: a tensor around the bytes costs 3 us of the smallest calls' 13.
+    # The bytes are the launching stream's, so that they are not handed out again before it ran.
+    size = max(1, wanted())
+    _, _, allocate, release = _torch_calls()
+    taken = allocate(size, s)
+    if lib().dkv_stream_capturing(s) == 1 and not _kept_for_graph(taken):
+        # the allocator would hand the bytes out again while the graph lives
+        release(taken)
+        raise ValueError("a stream capture that torch does not know needs a workspace of its own")
+    return taken, size, taken
+
+
 def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None, max_rows=1,
                      scale=None, v_scale=1.0, lse=None, workspace=None, stream=None):
     """Attention of q [rows, n_q_heads, D] over an E2M1 pool (see include/dkv.h); scale None is
@@ -625,32 +650,111 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
     pt, pkl = _arg(page_table, "page_table", i32, dev), _arg(kv_len, "kv_len", i32, dev, (B,))
     prs, po = _arg(row_start, "row_start", i32, dev, (B + 1,)), _arg(out, "out", dt, dev, (n, hq, D))
     pl = _arg(lse, "lse", torch.float32, dev, (n, hq))
-    taken = 0
-    if workspace is None:
-        # The allocator's own call: a tensor around the bytes costs 3 us of the smallest calls' 13.
-        # The bytes are the launching stream's, so that they are not handed out again before it ran.
-        size = max(1, dkv_paged_attend_workspace(B, hq, hkv, D, max_rows))
-        _, _, allocate, release = _torch_calls()
-        pw = taken = allocate(size, s)
-        if lib().dkv_stream_capturing(s) == 1 and not _kept_for_graph(taken):
-            # the allocator would hand the bytes out again while the graph lives
-            release(taken)
-            raise ValueError("a stream capture that torch does not know needs a workspace of its own")
-    else:
-        pw, size = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
+    pw, size, taken = _workspace(workspace, lambda: dkv_paged_attend_workspace(B, hq, hkv, D, max_rows), dev, s)
     try:
         st = lib().dkv_paged_attend(
             _ATTEND.pack(pq, sq, pkp, pvp, pt, pkl, prs, po, pl, pw, size, B, n, max_rows, hq, hkv, D, code,
                          page_tokens, pages, max_pages, D ** -0.5 if scale is None else scale, v_scale), s)
     finally:
         if taken:
-            release(taken)
+            _torch_calls()[3](taken)
     if st:
         _check(st, "dkv_paged_attend")
 
 
 def dkv_paged_attend_debug_withhold(enable=True):
     _check(lib().dkv_paged_attend_debug_withhold(int(bool(enable))), "dkv_paged_attend_debug_withhold")
+
+
+# ---- the life of a cache's pages -----------------------------------------------------
+
+@functools.lru_cache(maxsize=256)
+def dkv_pages_workspace(batch, max_pages, num_pages) -> int:
+    """Bytes of device memory that dkv_pages_fork and dkv_pages_compact need (0 for sizes that they refuse)."""
+    return lib().dkv_pages_workspace(batch, max_pages, num_pages)
+
+
+def dkv_pages_fork(page_table, kv_len, sources, free_pages, free_count, page_tokens, table_out, len_out, free_left,
+                   copies, report, workspace=None, stream=None):
+    """Sequence b becomes a copy of sequence sources[b], or ends (see include/dkv.h).  All tensors are int32 and
+    CUDA; page_table and table_out [batch, max_pages], free_pages [num_pages], copies [batch, 2], report [4].
+    Without a workspace (uint8, dkv_pages_workspace bytes) one is taken as dkv_paged_attend does."""
+    import torch
+    i32 = torch.int32
+    if page_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("page_table is [batch, max_pages], free_pages [num_pages]")
+    B, max_pages = page_table.shape
+    pages, dev, each, one = free_pages.shape[0], page_table.get_device(), (B,), (1,)
+    s = _launch(dev, stream)
+    args = (_arg(page_table, "page_table", i32, dev), _arg(kv_len, "kv_len", i32, dev, each),
+            _arg(sources, "sources", i32, dev, each), _arg(free_pages, "free_pages", i32, dev),
+            _arg(free_count, "free_count", i32, dev, one), B, max_pages, page_tokens, pages,
+            _arg(table_out, "table_out", i32, dev, (B, max_pages)), _arg(len_out, "len_out", i32, dev, each),
+            _arg(free_left, "free_left", i32, dev, one), _arg(copies, "copies", i32, dev, (B, 2)),
+            _arg(report, "report", i32, dev, (4,)))
+    pw, size, taken = _workspace(workspace, lambda: dkv_pages_workspace(B, max_pages, pages), dev, s)
+    try:
+        st = lib().dkv_pages_fork(*args, pw, size, s)
+    finally:
+        if taken:
+            _torch_calls()[3](taken)
+    if st:
+        _check(st, "dkv_pages_fork")
+
+
+def dkv_pages_compact(page_table, kv_len, page_tokens, table_out, free_pages, free_left, moves, report,
+                      workspace=None, stream=None):
+    """The pages held move to the front of the pool of free_pages.shape[0] pages (see include/dkv.h).  All tensors are
+    int32 and CUDA; moves [at least num_pages // 2, 2], report [4]."""
+    import torch
+    i32 = torch.int32
+    if page_table.dim() != 2 or free_pages.dim() != 1 or moves.dim() != 2 or moves.shape[1] != 2:
+        raise ValueError("page_table is [batch, max_pages], free_pages [num_pages], moves [max_moves, 2]")
+    B, max_pages = page_table.shape
+    pages, dev = free_pages.shape[0], page_table.get_device()
+    s = _launch(dev, stream)
+    args = (_arg(page_table, "page_table", i32, dev), _arg(kv_len, "kv_len", i32, dev, (B,)), B, max_pages,
+            page_tokens, pages, _arg(table_out, "table_out", i32, dev, (B, max_pages)),
+            _arg(free_pages, "free_pages", i32, dev), _arg(free_left, "free_left", i32, dev, (1,)),
+            _arg(moves, "moves", i32, dev), moves.shape[0], _arg(report, "report", i32, dev, (4,)))
+    pw, size, taken = _workspace(workspace, lambda: dkv_pages_workspace(B, max_pages, pages), dev, s)
+    try:
+        st = lib().dkv_pages_compact(*args, pw, size, s)
+    finally:
+        if taken:
+            _torch_calls()[3](taken)
+    if st:
+        _check(st, "dkv_pages_compact")
+
+
+def dkv_pages_copy(pairs, pools, into=None, stream=None):
+    """Page pairs[i, 1] of each tensor of `into` takes the bytes of page pairs[i, 0] of the tensor of `pools` beside it
+    (see include/dkv.h).  pairs: int32 CUDA [n, 2], {-1, -1} for nothing.  pools, into: lists of contiguous
+    tensors [pages, ...], CUDA or in pinned host memory; into None: the same pools."""
+    import torch
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs is [n, 2]")
+    dev = pairs.get_device()
+    into = pools if into is None else into
+    if len(into) != len(pools):
+        raise ValueError(f"{len(pools)} pools into {len(into)}")
+    packed = bytearray()
+    for i, (a, b) in enumerate(zip(pools, into)):
+        if a.dtype != b.dtype or a.dim() < 2 or a.shape[1:] != b.shape[1:]:
+            raise ValueError(f"pool {i}: {a.dtype} {tuple(a.shape)} does not go into {b.dtype} {tuple(b.shape)}")
+        for t in (a,) if a is b else (a, b):
+            if not t.is_contiguous():
+                raise ValueError(f"pool {i} must be contiguous")
+            if t.get_device() != dev and not (t.get_device() < 0 and t.is_pinned()):
+                raise ValueError(f"pool {i} is neither with the pairs nor in pinned host memory")
+        n = a.shape[0]
+        packed += _PAGE_POOL.pack(a.data_ptr(), b.data_ptr(), a.numel() // n * a.element_size() if n else 0, n, b.shape[0])
+    n = pairs.shape[0]
+    st = lib().dkv_pages_copy(_arg(pairs, "pairs", torch.int32, dev), n,
+                              ctypes.addressof(ctypes.c_char.from_buffer(packed)) if packed else None, len(pools),
+                              _launch(dev, stream))
+    if st:
+        _check(st, "dkv_pages_copy")
 
 
 class KVCache:

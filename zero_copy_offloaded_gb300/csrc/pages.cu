@@ -1,0 +1,608 @@
+// dkv_pages_fork, dkv_pages_compact, dkv_pages_copy: the life of a paged cache's pages on the GPU.
+//
+// No page carries a count of its holders: the page table says who holds what.  Old sequence s holds the
+// ceil(len_s / P) first pages of its row.  A fork lets new sequence b be old sequence src_b: it is every old row's
+// fate to go on (some b has src_b = s) or to vanish, and the pages that go back are those that a vanished
+// row names and no row that goes on does.  A compaction needs the pages that any row names; with L of them the
+// i-th page named from L on moves to the i-th page not named below L.  Both are a mark of the pool's pages (a byte
+// each, plain stores: all writers write 1), a scan over the marks in page order, and a pass over the table.
+//
+// What bounds them: the table's entries, read once to mark (a scattered byte store each) and once to be
+// rewritten, and latency.  The marks and the rewrite want the whole GPU, the scan one cluster; a small table
+// takes all three in one launch of that cluster (see kOneLaunch).
+#include <stdio.h>
+
+#include <algorithm>
+
+#include "dkv_internal.cuh"
+
+namespace dkv {
+void set_last_error(dkv_status s, const char* msg);
+}
+
+namespace {
+
+using namespace dkv;
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32, kCluster = 8, kSms = 152;
+constexpr int kSegment = 256;  // table entries of a warp at a time, eight to a lane
+// Table entries plus pages up to which one cluster does everything in one launch.
+constexpr long long kOneLaunch = 1 << 16;
+
+enum Phase : int { kAll = -1, kClear = 0, kMark = 1, kScan = 2, kWrite = 3 };
+
+struct Row {
+  int source;  // old row that this one becomes a copy of; -1: none
+  int shared;  // its entries that go on
+  int page;    // the entry behind them, or -1
+  int pad;
+};
+
+struct PageParams {
+  const int* table;
+  const int* len;
+  const int* sources;    // fork
+  int* free_pages;
+  const int* free_count; // fork
+  int* table_out;
+  int* len_out;          // fork
+  int* free_left;
+  int* pairs;            // copies [B][2] or moves [max_moves][2]
+  int* report;
+  uint8_t* live;         // [num_pages, rounded up to 16]
+  uint8_t* dead;         // fork: the same
+  Row* rows;             // fork: [B]
+  int* old;              // fork in place: [B][max_pages]
+  int* rank;             // compact: [num_pages], of pages that move
+  int* sums;             // [4][kCluster], then a flag: the tables are rewritten
+  int B, max_pages, shift, num_pages, max_moves;
+};
+constexpr int kSums = 4 * kCluster + 1;
+
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ long long pages_of(long long len, int shift) { return (len + (1 << shift) - 1) >> shift; }
+
+// Sum of v over the CTA's threads before this one; `total`: over all.
+__device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+  for (int d = 1; d < 32; d <<= 1) {
+    const int o = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += o;
+  }
+  __syncthreads();  // s_warp is free
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = s_warp[lane];
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_up_sync(~0u, w, d);
+      if (lane >= d) w += o;
+    }
+    s_warp[lane] = w;
+  }
+  __syncthreads();
+  total = s_warp[kWarps - 1];
+  return x - v + (warp ? s_warp[warp - 1] : 0);
+}
+
+// The same over the cluster: what the CTAs before this one have, and `total`; slots: its kCluster words.
+__device__ __forceinline__ int cluster_base(int own, int* slots, int& total) {
+  if (threadIdx.x == 0) slots[blockIdx.x] = own;
+  cluster_sync();
+  int base = 0;
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < kCluster; ++i) {
+    const int v = __ldcg(slots + i);
+    base += i < (int)blockIdx.x ? v : 0;
+    total += v;
+  }
+  return base;
+}
+
+__device__ __forceinline__ void clear(uint8_t* at, int bytes) {
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < (bytes + 15) / 16;
+       i += (long long)gridDim.x * kThreads)
+    reinterpret_cast<uint4*>(at)[i] = make_uint4(0, 0, 0, 0);
+}
+
+// f(row, first entry) for each segment of the rows, a warp at a time.
+template <typename F>
+__device__ __forceinline__ void segments(const PageParams& p, F&& f) {
+  const int parts = (p.max_pages + kSegment - 1) / kSegment;
+  for (long long w = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); w < (long long)p.B * parts;
+       w += (long long)gridDim.x * kWarps) {
+    const int b = (int)(w / parts);
+    f(b, (int)(w - (long long)b * parts) * kSegment);
+  }
+}
+
+// Eight entries of a lane, from `first` on, below `end`.
+__device__ __forceinline__ void load_segment(const int* row, int first, int end, int (&page)[8]) {
+  const int at = first + (threadIdx.x & 31);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) page[i] = at + 32 * i < end ? __ldcg(row + at + 32 * i) : -1;
+}
+
+__device__ __forceinline__ void mark(const PageParams& p, uint8_t* at, const int (&page)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if ((uint32_t)page[i] < (uint32_t)p.num_pages) at[page[i]] = 1;
+}
+
+// This thread's pages of the scan: [first, first + 16 n).
+__device__ __forceinline__ void scan_range(const PageParams& p, long long& first, int& n) {
+  const long long words = (p.num_pages + 15LL) / 16, threads = (long long)kCluster * kThreads;
+  n = (int)((words + threads - 1) / threads);
+  const long long at = ((long long)blockIdx.x * kThreads + threadIdx.x) * n;
+  first = at * 16;
+  n = (int)max(0LL, min((long long)n, words - at));
+}
+
+__device__ __forceinline__ int count_bytes(const uint4& w) {
+  return __popc(w.x | w.y << 1 | w.z << 2 | w.w << 3);  // bytes are 0 or 1
+}
+
+// ---- fork -----------------------------------------------------------------------------------
+
+// What every CTA finds out about the batch for itself.
+struct Batch {
+  int heir[kThreads];  // of old row s: -1 itself, else the lowest row that goes on as it; INT_MAX: none
+  int warp[kWarps];
+  int longest;
+};
+
+__device__ void fork_phase(const PageParams& p, int phase, Batch& s) {
+  const int b = threadIdx.x, lane = b & 31;
+  const bool all = phase == kAll;
+  if (phase == kClear || all) {
+    clear(p.live, p.num_pages);
+    clear(p.dead, p.num_pages);
+    if (!all) return;
+    cluster_sync();
+  }
+  const long long cap = (long long)p.max_pages << p.shift;
+  if (phase != kWrite) {
+    s.heir[b] = 0x7fffffff;
+    if (b == 0) s.longest = 0;
+    __syncthreads();
+    const int src = b < p.B ? p.sources[b] : -1;
+    long long len = b < p.B ? max(p.len[b], 0) : 0;
+    const bool wrong = __syncthreads_or(src >= p.B), far = __syncthreads_or(len > cap);
+    if (far && len > cap) len = cap;  // nothing is forked then; marks stay inside the row
+    if (src >= 0 && src < p.B) atomicMin(&s.heir[src], src == b ? -1 : b);
+    __syncthreads();
+    const bool vanishes = len > 0 && s.heir[b] == 0x7fffffff;
+    const bool any = __syncthreads_or(vanishes);
+    if (phase == kMark || all) {
+      segments(p, [&](int r, int first) {
+        const int end = (int)pages_of(min((long long)max(p.len[r], 0), cap), p.shift);
+        if (first >= end) return;
+        const int heir = s.heir[r];
+        const bool goes = heir != 0x7fffffff;
+        // in place, a row that another one becomes is read again after it may have been written
+        const bool keep = p.old && goes;
+        if (!any && !keep) return;
+        int page[8];
+        load_segment(p.table + (size_t)r * p.max_pages, first, end, page);
+        if (any) mark(p, goes ? p.live : p.dead, page);
+        if (keep) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if (first + lane + 32 * i < end) p.old[(size_t)r * p.max_pages + first + lane + 32 * i] = page[i];
+        }
+      });
+      if (!all) return;
+      cluster_sync();
+    }
+    // ---- scan: pages that go back, in page order
+    const bool on = src >= 0 && src < p.B;
+    const long long new_len = on ? min((long long)max(p.len[on ? src : 0], 0), cap) : 0;
+    const int held = (int)pages_of(new_len, p.shift);
+    const bool need = on && (new_len & ((1 << p.shift) - 1)) && s.heir[src] != (src == b ? -1 : b);
+    int needed, freed = 0, at = 0;
+    const int k = block_scan(need, s.warp, needed);
+    const int free_count = min(max(*p.free_count, 0), p.num_pages);
+    long long first = 0;
+    int n = 0, mine = 0;
+    if (any) {
+      scan_range(p, first, n);
+      for (int i = 0; i < n; ++i) {
+        const uint4 d = __ldcg(reinterpret_cast<const uint4*>(p.dead + first) + i);
+        const uint4 l = __ldcg(reinterpret_cast<const uint4*>(p.live + first) + i);
+        mine += count_bytes(make_uint4(d.x & ~l.x, d.y & ~l.y, d.z & ~l.z, d.w & ~l.w));
+      }
+      int own;
+      at = block_scan(mine, s.warp, own);
+      at += cluster_base(own, p.sums, freed);
+    }
+    const long long stack = (long long)free_count + freed;
+    const bool ok = !wrong && !far && needed <= stack && stack <= p.num_pages;
+    if (any && ok && mine) {
+      int* to = p.free_pages + free_count + at;
+      for (int i = 0; i < n; ++i) {
+        const uint4 d = __ldcg(reinterpret_cast<const uint4*>(p.dead + first) + i);
+        const uint4 l = __ldcg(reinterpret_cast<const uint4*>(p.live + first) + i);
+        const uint32_t w[4] = {d.x & ~l.x, d.y & ~l.y, d.z & ~l.z, d.w & ~l.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          for (uint32_t m = w[q]; m; m &= m - 1) *to++ = (int)(first + 16 * i + 4 * q) + (__ffs(m) - 1) / 8;
+      }
+    }
+    // What the inputs say has been read; lengths may be written in place behind this.
+    cluster_sync();
+    if (blockIdx.x == 0) {
+      const int longest = (int)(ok ? new_len : min(len, cap));
+      atomicMax(&s.longest, b < p.B ? (far ? max(p.len[b], 0) : longest) : 0);
+      if (b < p.B) {
+        Row r = {ok ? (on ? src : -1) : b, ok ? held - need : (int)pages_of(len, p.shift), -1, 0};
+        int from = -1;
+        if (ok && need) {
+          r.page = __ldcg(p.free_pages + stack - 1 - k);
+          from = p.table[(size_t)src * p.max_pages + held - 1];
+        }
+        p.rows[b] = r;
+        reinterpret_cast<int2*>(p.pairs)[b] = make_int2(from, r.page);
+      }
+      __syncthreads();
+      if (b < p.B) p.len_out[b] = ok ? (int)new_len : max(p.len[b], 0);
+      if (b == 0) {
+        *p.free_left = ok ? (int)(stack - needed) : free_count;
+        p.report[0] = ok ? DKV_OK : wrong ? DKV_ERR_INVALID_ARG : DKV_ERR_CAPACITY;
+        p.report[1] = ok ? freed : 0;
+        p.report[2] = ok ? needed : 0;
+        p.report[3] = s.longest;
+      }
+    }
+    if (!all) return;
+    cluster_sync();
+  }
+  // ---- write the rows
+  segments(p, [&](int r, int first) {
+    const int4 w = __ldcg(reinterpret_cast<const int4*>(p.rows + r));
+    const Row row = {w.x, w.y, w.z, 0};
+    if (row.source < 0 || first >= row.shared + 1 || (p.old && row.source == r)) return;
+    int page[8];
+    load_segment((p.old ? p.old : p.table) + (size_t)row.source * p.max_pages, first, row.shared, page);
+    int* to = p.table_out + (size_t)r * p.max_pages;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = first + lane + 32 * i;
+      if (c < row.shared) to[c] = page[i];
+      else if (c == row.shared && row.page >= 0) to[c] = row.page;
+    }
+  });
+}
+
+__global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, int phase) {
+  __shared__ Batch s;
+  fork_phase(p, phase, s);
+}
+
+// ---- compaction -----------------------------------------------------------------------------
+
+__global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PageParams p, int phase) {
+  __shared__ int s_warp[kWarps], s_longest;
+  const bool all = phase == kAll;
+  const int lane = threadIdx.x & 31, t = threadIdx.x;
+  const long long cap = (long long)p.max_pages << p.shift;
+  auto end_of = [&](int r) { return (int)pages_of(min((long long)max(p.len[r], 0), cap), p.shift); };
+  if (phase == kClear || all) {
+    clear(p.live, p.num_pages);
+    if (!all) return;
+    cluster_sync();
+  }
+  if (phase == kMark || all) {
+    segments(p, [&](int r, int first) {
+      const int end = end_of(r);
+      if (first >= end) return;
+      int page[8];
+      load_segment(p.table + (size_t)r * p.max_pages, first, end, page);
+      mark(p, p.live, page);
+    });
+    if (!all) return;
+    cluster_sync();
+  }
+  if (phase == kScan || all) {
+    if (t == 0) s_longest = 0;
+    const int len = t < p.B ? max(p.len[t], 0) : 0;
+    const bool ok = !__syncthreads_or(len > cap);
+    atomicMax(&s_longest, len);
+    long long first;
+    int n, mine = 0, high = 0, own, live, moves;
+    scan_range(p, first, n);
+    const uint4* words = reinterpret_cast<const uint4*>(p.live + first);
+    for (int i = 0; i < n; ++i) mine += count_bytes(__ldcg(words + i));
+    int before = block_scan(mine, s_warp, own);  // pages named before this thread's
+    before += cluster_base(own, p.sums, live);
+    // f(page, named, pages named before it)
+    auto each = [&](auto&& f) {
+      int at = before;
+      for (int i = 0; i < n; ++i) {
+        const uint4 v = __ldcg(words + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 1
+        for (int q = 0; q < 16; ++q) {
+          const uint32_t word = q < 8 ? (q < 4 ? w[0] : w[1]) : (q < 12 ? w[2] : w[3]);
+          const int on = (word >> (8 * (q & 3))) & 1;
+          const long long page = first + 16 * i + q;
+          if (page < p.num_pages) f((int)page, on, at);
+          at += on;
+        }
+      }
+    };
+    if (first >= live) high = mine;
+    else if (first + 16LL * n > live) each([&](int page, int on, int) { high += on && page >= live; });
+    block_scan(high, s_warp, own);
+    cluster_base(own, p.sums + kCluster, moves);
+    if (ok) {
+      const int low = live - moves;  // pages named below `live`: they stay
+      each([&](int page, int on, int at) {
+        if (page < live) {
+          if (!on) p.pairs[2 * (page - at) + 1] = page;
+        } else if (on) {
+          p.pairs[2 * (at - low)] = page;
+          p.rank[page] = at - low;
+        }
+      });
+    }
+    const int rest = ok ? moves : 0;
+    for (int i = rest + blockIdx.x * kThreads + t; i < p.max_moves; i += kCluster * kThreads)
+      reinterpret_cast<int2*>(p.pairs)[i] = make_int2(-1, -1);
+    if (ok)
+      for (int i = blockIdx.x * kThreads + t; i < p.num_pages - live; i += kCluster * kThreads)
+        p.free_pages[i] = p.num_pages - 1 - i;
+    if (blockIdx.x == 0 && t == 0) {
+      if (ok) *p.free_left = p.num_pages - live;
+      p.report[0] = ok ? DKV_OK : DKV_ERR_CAPACITY;
+      p.report[1] = rest;
+      p.report[2] = ok ? live : 0;
+      p.report[3] = s_longest;
+      p.sums[4 * kCluster] = ok ? live : 0x7fffffff;
+    }
+    if (!all) return;
+    cluster_sync();
+  }
+  // ---- the tables follow
+  const int live = __ldcg(p.sums + 4 * kCluster);  // entries from it on have moved
+  segments(p, [&](int r, int first) {
+    const int end = end_of(r);
+    if (first >= end) return;
+    int page[8], to[8];
+    load_segment(p.table + (size_t)r * p.max_pages, first, end, page);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bool moved = page[i] >= live && page[i] < p.num_pages;
+      to[i] = moved ? __ldcg(p.rank + page[i]) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (to[i] >= 0) page[i] = __ldcg(p.pairs + 2 * to[i] + 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (first + lane + 32 * i < end) p.table_out[(size_t)r * p.max_pages + first + lane + 32 * i] = page[i];
+  });
+}
+
+// ---- copy -----------------------------------------------------------------------------------
+
+constexpr int kPools = 64;       // of one launch
+constexpr int kCopyThreads = 256;
+constexpr int kInFlight = 8;     // loads of a lane
+
+struct CopyParams {
+  const int2* pairs;
+  const uint8_t* src[kPools];
+  uint8_t* dst[kPools];
+  unsigned long long bytes[kPools];
+  int src_pages[kPools], dst_pages[kPools];
+  int first[kPools + 1];  // segments before the pool's, of one pair
+  int n_pairs, n_pools;
+};
+
+// A warp takes a segment of 32 lanes x 8 loads of one page.
+template <typename W>
+__global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constant__ CopyParams p) {
+  constexpr int kBytes = 32 * kInFlight * sizeof(W);
+  const int lane = threadIdx.x & 31, segs = p.first[p.n_pools];
+  for (long long w = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5);
+       w < (long long)p.n_pairs * segs; w += (long long)gridDim.x * (kCopyThreads / 32)) {
+    const int i = (int)(w / segs), seg = (int)(w - (long long)i * segs);
+    int pool = 0;
+    while (seg >= p.first[pool + 1]) ++pool;
+    const int2 pair = __ldg(p.pairs + i);
+    if ((uint32_t)pair.x >= (uint32_t)p.src_pages[pool] || (uint32_t)pair.y >= (uint32_t)p.dst_pages[pool]) continue;
+    const unsigned long long bytes = p.bytes[pool];
+    const unsigned long long at = (unsigned long long)(seg - p.first[pool]) * kBytes + lane * sizeof(W);
+    const uint8_t* from = p.src[pool] + pair.x * bytes + at;
+    uint8_t* to = p.dst[pool] + pair.y * bytes + at;
+    const long long room = (long long)(bytes - at);  // may be negative: behind the page
+    W x[kInFlight];
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k)
+      if (k * 32LL * (int)sizeof(W) < room) x[k] = __ldcs(reinterpret_cast<const W*>(from) + k * 32);
+#pragma unroll
+    for (int k = 0; k < kInFlight; ++k)
+      if (k * 32LL * (int)sizeof(W) < room) __stcs(reinterpret_cast<W*>(to) + k * 32, x[k]);
+  }
+}
+
+// ---- entry points ---------------------------------------------------------------------------
+
+dkv_status refuse(dkv_status s, const char* msg) {
+  set_last_error(s, msg);
+  return s;
+}
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
+const char* bad_sizes(int batch, int max_pages, int page_tokens, int num_pages) {
+  if (batch <= 0 || batch > DKV_MAX_STEP_BATCH) return "batch outside [1, DKV_MAX_STEP_BATCH]";
+  if (page_tokens < 1 || page_tokens > 4096 || (page_tokens & (page_tokens - 1)))
+    return "page_tokens must be a power of two in [1, 4096]";
+  if (max_pages <= 0 || (long long)max_pages * page_tokens > (1LL << 30))
+    return "max_pages must be positive, max_pages * page_tokens at most 2^30";
+  if (num_pages <= 0 || (long long)num_pages * page_tokens > (1LL << 30))
+    return "num_pages must be positive, num_pages * page_tokens at most 2^30";
+  return nullptr;
+}
+
+// Workspace: sums | rows | marks | marks or ranks | the old table.
+size_t ws_rows() { return align256(kSums * sizeof(int)); }
+size_t ws_live() { return ws_rows() + align256(DKV_MAX_STEP_BATCH * sizeof(Row)); }
+size_t ws_more(int num_pages) { return ws_live() + align256(num_pages); }
+size_t ws_old(int num_pages) { return ws_more(num_pages) + align256((size_t)num_pages * 4); }
+
+template <typename K>
+cudaError_t launch_one(K* kernel, const PageParams& p, int phase, int grid, bool cluster, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kCluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p, phase);
+}
+
+template <typename K>
+dkv_status launch(K* kernel, const PageParams& p, cudaStream_t s) {
+  cudaError_t e;
+  if ((long long)p.B * p.max_pages + p.num_pages <= kOneLaunch) {
+    e = launch_one(kernel, p, kAll, kCluster, true, s);
+  } else {
+    const long long parts = (long long)p.B * ((p.max_pages + kSegment - 1) / kSegment);
+    const int grid = (int)std::min<long long>((parts + kWarps - 1) / kWarps, kSms);
+    const int wide = (int)std::min<long long>((p.num_pages / 16 + kThreads) / kThreads, kSms);
+    e = launch_one(kernel, p, kClear, wide, false, s);
+    if (e == cudaSuccess) e = launch_one(kernel, p, kMark, grid, false, s);
+    if (e == cudaSuccess) e = launch_one(kernel, p, kScan, kCluster, true, s);
+    if (e == cudaSuccess) e = launch_one(kernel, p, kWrite, grid, false, s);
+  }
+  if (e != cudaSuccess) cudaGetLastError();
+  return e == cudaSuccess ? DKV_OK : refuse(DKV_ERR_CUDA, cudaGetErrorString(e));
+}
+
+void set_workspace(PageParams& p, void* workspace) {
+  char* w = static_cast<char*>(workspace);
+  p.sums = reinterpret_cast<int*>(w);
+  p.rows = reinterpret_cast<Row*>(w + ws_rows());
+  p.live = reinterpret_cast<uint8_t*>(w + ws_live());
+  p.dead = reinterpret_cast<uint8_t*>(w + ws_more(p.num_pages));
+  p.rank = reinterpret_cast<int*>(w + ws_more(p.num_pages));
+  p.old = reinterpret_cast<int*>(w + ws_old(p.num_pages));
+}
+
+int shift_of(int page_tokens) {
+  int s = 0;
+  while ((1 << s) < page_tokens) ++s;
+  return s;
+}
+
+}  // namespace
+
+extern "C" size_t dkv_pages_workspace(int batch, int max_pages, int num_pages) {
+  if (bad_sizes(batch, max_pages, 1, num_pages)) return 0;
+  return ws_old(num_pages) + align256((size_t)batch * max_pages * 4);
+}
+
+extern "C" dkv_status dkv_pages_fork(const int32_t* page_table, const int32_t* kv_len, const int32_t* sources,
+                                     int32_t* free_pages, const int32_t* free_count, int batch, int max_pages,
+                                     int page_tokens, int num_pages, int32_t* table_out, int32_t* len_out,
+                                     int32_t* free_left, int32_t* copies, int32_t* report, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  if (!page_table || !kv_len || !sources || !free_pages || !free_count || !table_out || !len_out || !free_left ||
+      !copies || !report || !workspace)
+    return refuse(DKV_ERR_INVALID_ARG, "null pointer argument");
+  if (const char* why = bad_sizes(batch, max_pages, page_tokens, num_pages)) return refuse(DKV_ERR_INVALID_ARG, why);
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) || (reinterpret_cast<uintptr_t>(copies) & 7))
+    return refuse(DKV_ERR_INVALID_ARG, "the workspace must start on a 256-byte boundary, the pairs on 8");
+  if (workspace_bytes < dkv_pages_workspace(batch, max_pages, num_pages))
+    return refuse(DKV_ERR_INVALID_ARG, "workspace smaller than dkv_pages_workspace says");
+  PageParams p = {};
+  p.table = page_table; p.len = kv_len; p.sources = sources; p.free_pages = free_pages; p.free_count = free_count;
+  p.table_out = table_out; p.len_out = len_out; p.free_left = free_left; p.pairs = copies; p.report = report;
+  p.B = batch; p.max_pages = max_pages; p.num_pages = num_pages; p.shift = shift_of(page_tokens);
+  set_workspace(p, workspace);
+  if (table_out != page_table) p.old = nullptr;
+  return launch(fork_kernel, p, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dkv_status dkv_pages_compact(const int32_t* page_table, const int32_t* kv_len, int batch, int max_pages,
+                                        int page_tokens, int num_pages, int32_t* table_out, int32_t* free_pages,
+                                        int32_t* free_left, int32_t* moves, int max_moves, int32_t* report,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (!page_table || !kv_len || !table_out || !free_pages || !free_left || !report || !workspace ||
+      (!moves && num_pages > 1))
+    return refuse(DKV_ERR_INVALID_ARG, "null pointer argument");
+  if (const char* why = bad_sizes(batch, max_pages, page_tokens, num_pages)) return refuse(DKV_ERR_INVALID_ARG, why);
+  if (max_moves < num_pages / 2) return refuse(DKV_ERR_INVALID_ARG, "max_moves below num_pages / 2");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255) || (reinterpret_cast<uintptr_t>(moves) & 7))
+    return refuse(DKV_ERR_INVALID_ARG, "the workspace must start on a 256-byte boundary, the pairs on 8");
+  if (workspace_bytes < dkv_pages_workspace(batch, max_pages, num_pages))
+    return refuse(DKV_ERR_INVALID_ARG, "workspace smaller than dkv_pages_workspace says");
+  PageParams p = {};
+  p.table = page_table; p.len = kv_len; p.free_pages = free_pages; p.table_out = table_out; p.free_left = free_left;
+  p.pairs = moves; p.report = report;
+  p.B = batch; p.max_pages = max_pages; p.num_pages = num_pages; p.shift = shift_of(page_tokens);
+  p.max_moves = moves ? max_moves : 0;
+  set_workspace(p, workspace);
+  return launch(compact_kernel, p, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dkv_status dkv_pages_copy(const int32_t* pairs, int n_pairs, const dkv_page_pool_t* pools, int n_pools,
+                                     void* stream) {
+  if (!pairs || !pools) return refuse(DKV_ERR_INVALID_ARG, "null pointer argument");
+  if (n_pairs <= 0 || n_pairs > (1 << 30)) return refuse(DKV_ERR_INVALID_ARG, "pairs outside [1, 2^30]");
+  if (n_pools <= 0 || n_pools > 65536) return refuse(DKV_ERR_INVALID_ARG, "pools outside [1, 65536]");
+  if (reinterpret_cast<uintptr_t>(pairs) & 7) return refuse(DKV_ERR_INVALID_ARG, "the pairs must start on an 8-byte boundary");
+  for (int i = 0; i < n_pools; ++i) {
+    const dkv_page_pool_t& a = pools[i];
+    if (!a.src || !a.dst) return refuse(DKV_ERR_INVALID_ARG, "null pool");
+    if (a.src_pages <= 0 || a.dst_pages <= 0) return refuse(DKV_ERR_INVALID_ARG, "a pool without pages");
+    if (!a.page_bytes || a.page_bytes % 4 || a.page_bytes > (1ull << 30))
+      return refuse(DKV_ERR_INVALID_ARG, "page_bytes must be a multiple of 4, at most 2^30");
+    if ((reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst)) & 3)
+      return refuse(DKV_ERR_INVALID_ARG, "pools must start on 4-byte boundaries");
+  }
+  // Pages in words of 16 bytes first, then those that only have words of 4.
+  for (int wide = 1; wide >= 0; --wide) {
+    CopyParams p;
+    p.pairs = reinterpret_cast<const int2*>(pairs);
+    p.n_pairs = n_pairs;
+    p.n_pools = 0;
+    p.first[0] = 0;
+    for (int i = 0; i < n_pools; ++i) {
+      const dkv_page_pool_t& a = pools[i];
+      const bool w16 = !((reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst) | a.page_bytes) & 15);
+      if (w16 == (wide == 1)) {
+        const int k = p.n_pools++;
+        const size_t seg = 32 * kInFlight * (wide ? 16 : 4);
+        p.src[k] = static_cast<const uint8_t*>(a.src);
+        p.dst[k] = static_cast<uint8_t*>(a.dst);
+        p.bytes[k] = a.page_bytes;
+        p.src_pages[k] = a.src_pages;
+        p.dst_pages[k] = a.dst_pages;
+        p.first[k + 1] = p.first[k] + (int)((a.page_bytes + seg - 1) / seg);
+      }
+      if (p.n_pools == kPools || (i == n_pools - 1 && p.n_pools)) {
+        const long long warps = (long long)n_pairs * p.first[p.n_pools];
+        const int grid = (int)std::min<long long>((warps + kCopyThreads / 32 - 1) / (kCopyThreads / 32), 8LL * 8 * kSms);
+        if (wide) copy_kernel<uint4><<<grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+        else copy_kernel<uint32_t><<<grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return refuse(DKV_ERR_CUDA, cudaGetErrorString(e));
+        p.n_pools = 0;
+      }
+    }
+  }
+  return DKV_OK;
+}
