@@ -612,6 +612,46 @@ int dkv_stream_capturing(void* stream);
  * signals an item's outputs, so that its waits run out (some seconds). */
 dkv_status dkv_paged_attend_debug_withhold(int enable);
 
+/* ---- the same step over an 8-bit paged cache with block scales ------------------ */
+
+/* A pool of E4M3 codes [num_pages][n_kv_heads][page_tokens][head_dim] (one byte an element, the layout of a
+ * paged DKV_KV_E4M3 cache) with fp32 scales [num_pages][n_kv_heads][page_tokens / 16]: an element is its
+ * code times the scale of its block, 16 consecutive tokens of a page and head.  Pages hold 16 to 4096 tokens.
+ * Three significant bits more than E2M1's two, for twice the bytes; dkv_step_plan plans it, dkv_pages_* share and move
+ * its pages (codes and scales are pools of one table).  Pools may be HBM or the mapped alias of pinned host
+ * memory, scales too. */
+
+/* Norm, rotation and append of one step's projected rows: dkv_append_t's arguments and arithmetic, keys and values
+ * into blocks.  k, v, both pools, their scales and slots are needed; q may be null.
+ * For the rows y of a call in one block: need = the smallest power of two with max|y| <= 448 need (2^-64 at least),
+ * s = max(need, scale so far), where a block whose first token is among the rows (slot a multiple of 16) has no scale
+ * so far, and one whose scale is not a positive finite number neither.  The block's scale becomes s; if it grew, codes that are
+ * there become e4m3(code * old / s); the rows' codes are e4m3(y / s), to nearest even.  A NaN or an infinity becomes a
+ * NaN of its element alone, and does not count for the scale.
+ * Rows of one block must be consecutive rows of the call (as dkv_step_plan deals them), and no two may have one slot;
+ * sequences that append to the same block must not share it (dkv_pages_fork sees to that).  So a
+ * sequence that is cut back and appended to again keeps its block's scale, which is then larger than it has to be, until
+ * the block begins anew.
+ * k_out, v_out [rows][n_kv_heads][head_dim] or null: the values that the cache now holds, rounded to `dtype` (an
+ * infinity where E4M3 has rounded the type's largest numbers up beyond it).
+ * Errors: INVALID_ARG, UNSUPPORTED (head_dim not 64 or 128), CUDA. */
+typedef struct {
+    const void *q, *k, *v;
+    long long q_stride, k_stride, v_stride;
+    const void *q_gamma, *k_gamma;
+    const float* cos_sin;
+    const int32_t *positions, *slots;
+    void *k_pool, *v_pool;
+    float *k_scales, *v_scales;
+    void *q_out, *k_out, *v_out;
+    int rows, n_q_heads, n_kv_heads, head_dim;
+    dkv_dtype dtype;
+    int rotary_dim, max_positions, interleaved;
+    int page_tokens, num_pages;
+    float eps;
+} dkv_block_append_t;
+dkv_status dkv_block_append(const dkv_block_append_t* args, void* stream);
+
 /* ---- the life of a cache's pages ------------------------------------------- */
 
 /* Sequences share, move and give back pages on the GPU.  A pool's pages have no counters: the page

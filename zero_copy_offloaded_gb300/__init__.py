@@ -32,6 +32,7 @@ __all__ = [
     "dkv_decode_noalloc_debug_withhold", "dkv_pci_numa_node", "dkv_numa_probe",
     "dkv_step_plan", "dkv_qkv_append", "dkv_paged_attend", "dkv_paged_attend_workspace",
     "dkv_paged_attend_debug_withhold",
+    "dkv_block_append",
     "dkv_pages_fork", "dkv_pages_compact", "dkv_pages_copy", "dkv_pages_workspace",
     "rope_table", "MAX_STEP_BATCH",
 ]
@@ -80,6 +81,7 @@ class _CacheDesc(ctypes.Structure):
 # The argument structures of include/dkv.h, packed in one call (native alignment)
 _APPEND = struct.Struct("@3P3q10P10i3f")
 _ATTEND = struct.Struct("@PqPPPPPPPPN10i2f")
+_BLOCK_APPEND = struct.Struct("@3P3q12P10if")
 _PAGE_POOL = struct.Struct("@PPN2i")
 KV_FORMATS = {"native": 0, "e4m3": 1, "e2m1": 2}
 MAX_STEP_BATCH = 1024
@@ -140,6 +142,7 @@ def lib(build_if_missing: bool = False):
         "dkv_qkv_append": [P, P],
         "dkv_paged_attend": [P, P],
         "dkv_paged_attend_debug_withhold": [I],
+        "dkv_block_append": [P, P],
         "dkv_pages_fork": [P] * 5 + [I] * 4 + [P] * 6 + [Z, P],
         "dkv_pages_compact": [P, P, I, I, I, I, P, P, P, P, I, P, P, Z, P],
         "dkv_pages_copy": [P, I, P, I, P],
@@ -537,11 +540,9 @@ def _dtype_of(t):
     raise ValueError(f"{t.dtype} is neither bfloat16 nor float16")
 
 
-def dkv_qkv_append(q, k, v, positions=None, slots=None, k_pool=None, v_pool=None, q_out=None,
-                   k_out=None, v_out=None, q_gamma=None, k_gamma=None, eps=1e-6, cos_sin=None,
-                   interleaved=False, k_scale=1.0, v_scale=1.0, stream=None):
-    """Head norms and rotation of q and k, append of k and v to an E2M1 pool (see include/dkv.h).
-    q [rows, n_q_heads, D] and k, v [rows, n_kv_heads, D] may be slices of one projection's output."""
+def _append_args(q, k, v, positions, slots, q_out, k_out, v_out, q_gamma, k_gamma, cos_sin):
+    """What the appends check alike: (device index, head_dim, KV heads) and the fields of dkv_append_t up to slots, the
+    three outputs, and the numbers from rows to max_positions."""
     import torch
     some = q if q is not None else k
     if some is None:
@@ -566,6 +567,25 @@ def dkv_qkv_append(q, k, v, positions=None, slots=None, k_pool=None, v_pool=None
         pkg = _arg(k_gamma, "k_gamma", dt, dev, (D,))
     elif v is not None:
         raise ValueError("keys and values come together")
+    pcs = pp = max_positions = rotary_dim = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin is [max_positions, rotary_dim]")
+        pcs = _arg(cos_sin, "cos_sin", f32, dev)
+        max_positions, rotary_dim = cos_sin.shape
+        pp = _arg(positions, "positions", i32, dev, (n,))
+    return ((dev, D, hkv), (pq, pk, pv, sq, sk, sv, pqg, pkg, pcs, pp, _arg(slots, "slots", i32, dev, (n,))),
+            (pqo, pko, pvo), (n, hq, hkv, D, code, rotary_dim, max_positions))
+
+
+def dkv_qkv_append(q, k, v, positions=None, slots=None, k_pool=None, v_pool=None, q_out=None,
+                   k_out=None, v_out=None, q_gamma=None, k_gamma=None, eps=1e-6, cos_sin=None,
+                   interleaved=False, k_scale=1.0, v_scale=1.0, stream=None):
+    """Head norms and rotation of q and k, append of k and v to an E2M1 pool (see include/dkv.h).
+    q [rows, n_q_heads, D] and k, v [rows, n_kv_heads, D] may be slices of one projection's output."""
+    import torch
+    (dev, D, hkv), rows, outs, numbers = _append_args(q, k, v, positions, slots, q_out, k_out, v_out, q_gamma,
+                                                      k_gamma, cos_sin)
     pkp = pvp = pages = page_tokens = 0
     if k_pool is not None:
         if v_pool is None or k is None:
@@ -575,19 +595,54 @@ def dkv_qkv_append(q, k, v, positions=None, slots=None, k_pool=None, v_pool=None
         if shape != other or shape[1] != hkv:
             raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens) for {hkv} heads")
         pages, page_tokens = shape[0], shape[2]
-    pcs = pp = max_positions = rotary_dim = 0
-    if cos_sin is not None:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin is [max_positions, rotary_dim]")
-        pcs = _arg(cos_sin, "cos_sin", f32, dev)
-        max_positions, rotary_dim = cos_sin.shape
-        pp = _arg(positions, "positions", i32, dev, (n,))
     st = lib().dkv_qkv_append(
-        _APPEND.pack(pq, pk, pv, sq, sk, sv, pqg, pkg, pcs, pp, _arg(slots, "slots", i32, dev, (n,)), pkp, pvp,
-                     pqo, pko, pvo, n, hq, hkv, D, code, rotary_dim, max_positions, bool(interleaved),
-                     page_tokens, pages, eps, k_scale, v_scale), _launch(dev, stream))
+        _APPEND.pack(*rows, pkp, pvp, *outs, *numbers, bool(interleaved), page_tokens, pages, eps, k_scale, v_scale),
+        _launch(dev, stream))
     if st:
         _check(st, "dkv_qkv_append")
+
+
+def _near(t, what, index):
+    """Address of a contiguous tensor on this device, or in pinned host memory."""
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    if t.get_device() != index and not (t.get_device() < 0 and t.is_pinned()):
+        raise ValueError(f"{what} is neither with the other tensors nor in pinned host memory")
+    return t.data_ptr()
+
+
+def _block_pools(k_pool, v_pool, k_scales, v_scales, index, D):
+    """Addresses of the pools and scales of an 8-bit cache, and (num_pages, n_kv_heads, page_tokens)."""
+    import torch
+    shape = k_pool.shape
+    if len(shape) != 4 or shape[3] != D or v_pool.shape != shape:
+        raise ValueError(f"pools of {tuple(shape)} and {tuple(v_pool.shape)}: both are [num_pages, n_kv_heads, page_tokens, {D}]")
+    pages, heads, page_tokens, _ = shape
+    for t, what in ((k_pool, "k_pool"), (v_pool, "v_pool")):
+        if t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError(f"{what} is {t.dtype}, neither float8_e4m3fn nor its bytes (uint8)")
+    for t, what in ((k_scales, "k_scales"), (v_scales, "v_scales")):
+        if t.dtype != torch.float32 or page_tokens % 16 or t.shape != (pages, heads, page_tokens // 16):
+            raise ValueError(f"{what} is {t.dtype} {tuple(t.shape)}: float32 [{pages}, {heads}, {page_tokens} / 16] is wanted")
+    return (_near(k_pool, "k_pool", index), _near(v_pool, "v_pool", index), _near(k_scales, "k_scales", index),
+            _near(v_scales, "v_scales", index)), (pages, heads, page_tokens)
+
+
+def dkv_block_append(q, k, v, positions, slots, k_pool, v_pool, k_scales, v_scales, q_out=None, k_out=None, v_out=None,
+                     q_gamma=None, k_gamma=None, eps=1e-6, cos_sin=None, interleaved=False, stream=None):
+    """dkv_qkv_append into an 8-bit pool with block scales (see include/dkv.h): k_pool, v_pool float8_e4m3fn
+    [num_pages, n_kv_heads, page_tokens, D], k_scales, v_scales fp32 [num_pages, n_kv_heads, page_tokens // 16].  q may
+    be None."""
+    (dev, D, hkv), rows, outs, numbers = _append_args(q, k, v, positions, slots, q_out, k_out, v_out, q_gamma,
+                                                      k_gamma, cos_sin)
+    pools, shape = _block_pools(k_pool, v_pool, k_scales, v_scales, dev, D)
+    if k is None or shape[1] != hkv:
+        raise ValueError(f"pools of {shape} (pages, heads, page_tokens) for {hkv} heads")
+    st = lib().dkv_block_append(
+        _BLOCK_APPEND.pack(*rows, *pools, *outs, *numbers, bool(interleaved), shape[2], shape[0], eps),
+        _launch(dev, stream))
+    if st:
+        _check(st, "dkv_block_append")
 
 
 @functools.lru_cache(maxsize=256)

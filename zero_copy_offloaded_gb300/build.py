@@ -17,7 +17,7 @@ OUT = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT, "libdkv.so")
 SOURCES = ["dkv_api.cu", "decode.cu", "probes.cu", "decode_noalloc.cu", "gemm_tc.cu",
            "prefill_tc.cu", "numa_host.cu", "step_plan.cu", "append_e2m1.cu", "attend_e2m1.cu", "attend_e2m1_tc.cu",
-           "pages.cu"]
+           "pages.cu", "append_e4m3.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
