@@ -652,6 +652,30 @@ typedef struct {
 } dkv_block_append_t;
 dkv_status dkv_block_append(const dkv_block_append_t* args, void* stream);
 
+/* dkv_paged_attend over such a pool, with its arguments, kernels and limits (v_scale aside, which the blocks' scales
+ * take the place of):
+ *   o = softmax(scale * q . k) . v,  k and v the codes times their blocks' scales.
+ * Scales of blocks that a row sees are positive, finite and not subnormal; those of V that one row sees lie
+ * within 2^100 of one another.  |scale * q . k| up to 2^21 is served.  A weight is rounded to fp16 as what it adds to the
+ * outputs, V's scale included: 2^-11 of it, or 2^-32 of the largest where it is below 2^-21 of that.
+ * workspace: dkv_paged_attend_workspace bytes.  Errors: as dkv_paged_attend. */
+typedef struct {
+    const void* q;
+    long long q_stride;
+    const void *k_pool, *v_pool;
+    const float *k_scales, *v_scales;
+    const int32_t *page_table, *kv_len, *row_start;
+    void* out;
+    float* lse;
+    void* workspace;
+    size_t workspace_bytes;
+    int batch, rows, max_rows, n_q_heads, n_kv_heads, head_dim;
+    dkv_dtype dtype;
+    int page_tokens, num_pages, max_pages;
+    float scale;
+} dkv_block_attend_t;
+dkv_status dkv_block_attend(const dkv_block_attend_t* args, void* stream);
+
 /* ---- the life of a cache's pages ------------------------------------------- */
 
 /* Sequences share, move and give back pages on the GPU.  A pool's pages have no counters: the page

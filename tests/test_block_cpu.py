@@ -67,6 +67,23 @@ def test_append_refuses(L, change, status):
     assert L.dkv_block_append(None, None) == 1
 
 
+ATTEND = dict(q=A, qs=512, kp=A, vp=A, ksc=A, vsc=A, pt=A, kl=A, rs=A, out=A, lse=0, ws=A, size=1 << 30, batch=4, rows=9,
+              max_rows=3, hq=8, hkv=2, d=64, dtype=0, page=16, pages=8, max_pages=4, scale=0.125)
+
+
+@pytest.mark.parametrize("change,status", [
+    ({"q": 0}, 1), ({"kp": 0}, 1), ({"vp": 0}, 1), ({"ksc": 0}, 1), ({"vsc": 0}, 1), ({"pt": 0}, 1), ({"kl": 0}, 1),
+    ({"out": 0}, 1), ({"ws": 0}, 1), ({"batch": 0}, 1), ({"batch": 1025}, 1), ({"rows": 0}, 1), ({"max_rows": 0}, 1),
+    ({"rs": 0}, 1), ({"dtype": 2}, 1), ({"d": 96}, 2), ({"hq": 7}, 1), ({"hkv": 0}, 1), ({"qs": 508}, 1), ({"qs": 256}, 1),
+    ({"page": 8}, 1), ({"page": 24}, 1), ({"page": 8192}, 1), ({"pages": 0}, 1), ({"max_pages": 0}, 1),
+    ({"max_pages": 1 << 27}, 1), ({"q": A + 8}, 1), ({"kp": A + 8}, 1), ({"ksc": A + 2}, 1), ({"out": A + 4}, 1), ({"ws": A + 64}, 1),
+    ({"size": 1000}, 1), ({"scale": float("inf")}, 1), ({"scale": float("nan")}, 1)])
+def test_attend_refuses(L, change, status):
+    assert L.dkv_block_attend(dkv._BLOCK_ATTEND.pack(*{**ATTEND, **change}.values()), None) == status
+    assert dkv.dkv_last_error()
+    assert L.dkv_block_attend(None, None) == 1
+
+
 def test_binding_refuses():
     torch = pytest.importorskip("torch")
     bf = torch.bfloat16

@@ -32,7 +32,7 @@ __all__ = [
     "dkv_decode_noalloc_debug_withhold", "dkv_pci_numa_node", "dkv_numa_probe",
     "dkv_step_plan", "dkv_qkv_append", "dkv_paged_attend", "dkv_paged_attend_workspace",
     "dkv_paged_attend_debug_withhold",
-    "dkv_block_append",
+    "dkv_block_append", "dkv_block_attend",
     "dkv_pages_fork", "dkv_pages_compact", "dkv_pages_copy", "dkv_pages_workspace",
     "rope_table", "MAX_STEP_BATCH",
 ]
@@ -82,6 +82,7 @@ class _CacheDesc(ctypes.Structure):
 _APPEND = struct.Struct("@3P3q10P10i3f")
 _ATTEND = struct.Struct("@PqPPPPPPPPN10i2f")
 _BLOCK_APPEND = struct.Struct("@3P3q12P10if")
+_BLOCK_ATTEND = struct.Struct("@PqPPPPPPPPPPN10if")
 _PAGE_POOL = struct.Struct("@PPN2i")
 KV_FORMATS = {"native": 0, "e4m3": 1, "e2m1": 2}
 MAX_STEP_BATCH = 1024
@@ -143,6 +144,7 @@ def lib(build_if_missing: bool = False):
         "dkv_paged_attend": [P, P],
         "dkv_paged_attend_debug_withhold": [I],
         "dkv_block_append": [P, P],
+        "dkv_block_attend": [P, P],
         "dkv_pages_fork": [P] * 5 + [I] * 4 + [P] * 6 + [Z, P],
         "dkv_pages_compact": [P, P, I, I, I, I, P, P, P, P, I, P, P, Z, P],
         "dkv_pages_copy": [P, I, P, I, P],
@@ -681,12 +683,9 @@ def _workspace(workspace, wanted, dev, s):
     return taken, size, taken
 
 
-def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None, max_rows=1,
-                     scale=None, v_scale=1.0, lse=None, workspace=None, stream=None):
-    """Attention of q [rows, n_q_heads, D] over an E2M1 pool (see include/dkv.h); scale None is
-    1/sqrt(D).  Without a workspace (uint8, dkv_paged_attend_workspace bytes) one is taken from
-    torch's caching allocator, on the launching stream; under a stream capture that is not torch's
-    own (torch.cuda.graph) the call needs one, which the graph's owner keeps."""
+def _attend_args(q, page_table, kv_len, out, row_start, lse, stream):
+    """What the attentions check alike: (device index, stream, rows, query heads, head_dim, dtype code, batch,
+    max_pages) and the addresses of q with its stride, of page_table, kv_len and row_start, and of out and lse."""
     import torch
     shape, i32 = q.shape, torch.int32
     if len(shape) != 3 or page_table.dim() != 2:
@@ -696,25 +695,53 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
     s = _launch(dev, stream)
     n, _, D = shape
     pq, hq, sq = _rows(q, "q", dt, dev, n, D)
+    B, max_pages = page_table.shape
+    pt, pkl = _arg(page_table, "page_table", i32, dev), _arg(kv_len, "kv_len", i32, dev, (B,))
+    prs, po = _arg(row_start, "row_start", i32, dev, (B + 1,)), _arg(out, "out", dt, dev, (n, hq, D))
+    pl = _arg(lse, "lse", torch.float32, dev, (n, hq))
+    return (dev, s, n, hq, D, code, B, max_pages), (pq, sq), (pt, pkl, prs), (po, pl)
+
+
+def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None, max_rows=1,
+                     scale=None, v_scale=1.0, lse=None, workspace=None, stream=None):
+    """Attention of q [rows, n_q_heads, D] over an E2M1 pool (see include/dkv.h); scale None is
+    1/sqrt(D).  Without a workspace (uint8, dkv_paged_attend_workspace bytes) one is taken from
+    torch's caching allocator, on the launching stream; under a stream capture that is not torch's
+    own (torch.cuda.graph) the call needs one, which the graph's owner keeps."""
+    import torch
+    (dev, s, n, hq, D, code, B, max_pages), qs, tables, outs = _attend_args(q, page_table, kv_len, out, row_start, lse, stream)
     pkp, shape = _pool(k_pool, "k_pool", torch.uint8, dev, D)
     pvp, other = _pool(v_pool, "v_pool", torch.uint8, dev, D)
     if shape != other:
         raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens)")
     pages, hkv, page_tokens = shape
-    B, max_pages = page_table.shape
-    pt, pkl = _arg(page_table, "page_table", i32, dev), _arg(kv_len, "kv_len", i32, dev, (B,))
-    prs, po = _arg(row_start, "row_start", i32, dev, (B + 1,)), _arg(out, "out", dt, dev, (n, hq, D))
-    pl = _arg(lse, "lse", torch.float32, dev, (n, hq))
     pw, size, taken = _workspace(workspace, lambda: dkv_paged_attend_workspace(B, hq, hkv, D, max_rows), dev, s)
     try:
         st = lib().dkv_paged_attend(
-            _ATTEND.pack(pq, sq, pkp, pvp, pt, pkl, prs, po, pl, pw, size, B, n, max_rows, hq, hkv, D, code,
+            _ATTEND.pack(*qs, pkp, pvp, *tables, *outs, pw, size, B, n, max_rows, hq, hkv, D, code,
                          page_tokens, pages, max_pages, D ** -0.5 if scale is None else scale, v_scale), s)
     finally:
         if taken:
             _torch_calls()[3](taken)
     if st:
         _check(st, "dkv_paged_attend")
+
+
+def dkv_block_attend(q, k_pool, v_pool, k_scales, v_scales, page_table, kv_len, out, row_start=None, max_rows=1,
+                     scale=None, lse=None, workspace=None, stream=None):
+    """dkv_paged_attend over an 8-bit pool with block scales (see include/dkv.h), as dkv_block_append fills it."""
+    (dev, s, n, hq, D, code, B, max_pages), qs, tables, outs = _attend_args(q, page_table, kv_len, out, row_start, lse, stream)
+    pools, (pages, hkv, page_tokens) = _block_pools(k_pool, v_pool, k_scales, v_scales, dev, D)
+    pw, size, taken = _workspace(workspace, lambda: dkv_paged_attend_workspace(B, hq, hkv, D, max_rows), dev, s)
+    try:
+        st = lib().dkv_block_attend(
+            _BLOCK_ATTEND.pack(*qs, *pools, *tables, *outs, pw, size, B, n, max_rows, hq, hkv, D, code,
+                               page_tokens, pages, max_pages, D ** -0.5 if scale is None else scale), s)
+    finally:
+        if taken:
+            _torch_calls()[3](taken)
+    if st:
+        _check(st, "dkv_block_attend")
 
 
 def dkv_paged_attend_debug_withhold(enable=True):

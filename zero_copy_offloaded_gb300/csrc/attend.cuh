@@ -1,12 +1,17 @@
-// What the kernels of the 4-bit paged attention share.
+// What the kernels of the paged attention share.
 #pragma once
 
 #include <math.h>
 
 #include "e2m1.cuh"
+#include "e4m3.cuh"
 #include "per_device.h"
 
 namespace dkv {
+
+enum Format : int { kE2M1, kE4M3 };
+
+constexpr int kSms = 152, kMaxCtas = 4 * kSms;
 
 // The item that a CTA left unfinished: one that it began, or one that fills it.
 struct AttendDesc {
@@ -22,6 +27,8 @@ struct AttendParams {
   const void* q;
   const uint8_t* k_pool;
   const uint8_t* v_pool;
+  const float* k_scales;  // E4M3: [num_pages][Hkv][page_tokens / 16]
+  const float* v_scales;
   const int* table;      // [B][max_pages]
   const int* kv_len;     // [B]
   const int* row_start;  // [B + 1], or null: row b is sequence b's only one
@@ -53,10 +60,13 @@ __device__ __forceinline__ void batch_entry(const AttendParams& p, int b, int& k
   }
 }
 
-// attend_e2m1_tc.cu: items of kTcRows query rows, one CTA on each of `grid` SMs, and their join.
+// attend_few.cuh: items of R query rows (8, 16, 24 or 32).
+template <Format F, typename T, int D>
+cudaError_t launch_attend_few(const AttendParams& p, int R, cudaStream_t s);
+// attend_many.cuh: items of kTcRows query rows, one CTA on each of `grid` SMs, and their join.
 constexpr int kTcRows = 256;
-template <typename T, int D>
-cudaError_t launch_attend_tc(const AttendParams& p, int grid, cudaStream_t s);
+template <Format F, typename T, int D>
+cudaError_t launch_attend_many(const AttendParams& p, int grid, cudaStream_t s);
 
 // Rows are normalised and rounded once; a row that saw no key is zero, its lse -infinity.
 // A NaN sum or output stays NaN.

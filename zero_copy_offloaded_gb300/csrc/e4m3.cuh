@@ -36,6 +36,12 @@ __device__ __forceinline__ uint32_t hi_to_h2(uint32_t w) {
   return r;
 }
 
+// log2 of a positive normal number: its exponent, exactly, and its significand's to 2^-22.
+__device__ __forceinline__ float log2_of(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (float)((int)(u >> 23) - 127) + __log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+}
+
 // Codes of four numbers, to nearest even; a NaN gives NaN, what is above 448 gives 448.
 __device__ __forceinline__ uint32_t to_codes(float a, float b, float c, float d) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3) |
