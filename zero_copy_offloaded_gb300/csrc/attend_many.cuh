@@ -54,13 +54,10 @@ namespace {
 
 constexpr int kRows = 128;             // rows of a Q tile, lanes of TMEM
 constexpr int kKeys = 128;             // keys of a tile
-constexpr int kConvert = 6;            // warps that turn codes into fp16
+constexpr int kConvert = 6;            // warps that turn codes into fp16 (E4M3, which needs no loader: one more)
 constexpr int kThreads = (10 + kConvert) * 32;
 constexpr int kReg = 128 * 128;        // a 128-row x 128-byte swizzled region
-// Raw units (K or V codes, E2M1's scales with them) in flight.  A loader that is three units ahead writes what it says of
-// tile j (raw_valid, block) once V of tile j - 2 (E2M1, heads of 64) or K of j - 1 has been converted, so that the softmax
-// has done with tile j - 4, whose place that is.
-constexpr int kRaw = 3;
+constexpr int kRaw = 3;                // E2M1: raw half tiles (K or V codes and scales) in flight
 constexpr float kNone = -3e38f;        // m of a row that has seen no key
 constexpr float kBias = 7.f;           // m below the maximum that it is taken from
 // (32 weights whose maximum gave m sum to 2^12, 2^12.3 with the rounding of m for scores up to 2^21)
@@ -71,17 +68,15 @@ constexpr uint32_t kTmS = 0, kTmO = 256;  // S of tile t at 128 t, O at 256 + 12
 template <Format F, int D>
 struct Cfg {
   static constexpr int kCode = F == kE2M1 ? e2m1::code_bytes(D) : D;  // bytes of a key's codes
-  static constexpr int kUnits = F == kE4M3 && D == 128 ? 2 : 1;       // raw units of K or V of a tile
-  static constexpr int kUnitKeys = kKeys / kUnits;
   static constexpr int DR = D / 64;                 // regions per row
   static constexpr int kTileB = DR * kReg;          // Q, K or V tile as fp16
-  static constexpr int kCodes = kUnitKeys * kCode;
+  static constexpr int kCodes = kKeys * kCode;
   static constexpr int kHalf = kCodes + (F == kE2M1 ? kKeys * e2m1::scale_bytes(D) : 0);
   static constexpr int kOffQ = 0;                   // two Q tiles
   static constexpr int kOffK = 2 * kTileB;          // two K stages
   static constexpr int kOffV = 4 * kTileB;          // two V stages
   static constexpr int kOffRaw = 6 * kTileB;
-  static constexpr int kEnd = kOffRaw + kRaw * kHalf;
+  static constexpr int kEnd = kOffRaw + (F == kE2M1 ? kRaw * kHalf : 0);
   static constexpr int kSmem = kEnd + 1024;         // room to align the tiles to 1024
 };
 
@@ -105,7 +100,12 @@ struct Bars {
   static constexpr int kNan = F == kE2M1 ? 8 : 128;
   unsigned long long nan_key[4][kNan];
   uint32_t nan_item[4];   // E4M3: item + 1 of one that has any
-  float4 block[F == kE2M1 ? 1 : 4][8];  // E4M3, by tile & 3: K's scale, log2 of V's, its inverse
+  // E4M3.  By item & 3: the powers of two that K's and V's tiles of a piece are converted by.  By tile & 3, for each
+  // run of 16 keys: 1 where a scale is left over, 2 where there is no page; K's scale that is left over, log2 of V's and
+  // its inverse.
+  float2 ref[4];
+  uint2 flags[4];
+  float4 block[F == kE2M1 ? 1 : 4][8];
 };
 
 // Where a role is on the line: an item, and the key tiles [tile, end) of it here.
@@ -177,6 +177,19 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+// A load that is issued where it stands.
+__device__ __forceinline__ void load_now(uint4& w, const uint8_t* from) {
+  asm volatile("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "l"(from));
+}
+__device__ __forceinline__ void load_now(float& x, const float* from) {
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(from));
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
 __device__ __forceinline__ int swz(int row, int cc) {
   return (cc / 8) * kReg + row * 128 + (((cc % 8) ^ (row % 8)) * 16);
 }
@@ -241,9 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       mbar_init(&bars->raw_empty[i], kConvert);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars->k_full[i], kConvert);
+      mbar_init(&bars->k_full[i], F == kE2M1 ? kConvert : kConvert + 1);
       mbar_init(&bars->k_empty[i], 1);
-      mbar_init(&bars->v_full[i], kConvert);
+      mbar_init(&bars->v_full[i], F == kE2M1 ? kConvert : kConvert + 1);
       mbar_init(&bars->v_empty[i], 1);
       mbar_init(&bars->q_ready[i], 4);
       mbar_init(&bars->s_full[i], 1);
@@ -465,10 +478,32 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
             }
             tc::fence_after_sync();
             const int k0 = tile * kKeys;
-            const uint32_t valid = bars->raw_valid[(all_tiles + tile - tile0) & 3];
+            uint32_t valid = 0xFFu;
+            bool slow = false;  // E4M3: blocks have scales of their own left
+            const uint32_t place = (all_tiles + tile - tile0) & 3;
+            if constexpr (F == kE2M1) {
+              valid = bars->raw_valid[place];
+            } else {
+              const uint2 f = bars->flags[place];
+              if (f.x | f.y) {
+                slow = (f.x | f.y) & 0x01010101u;
+                // bit 1 of four bytes side by side
+                valid ^= (f.x >> 1 & 0x01010101u) * 0x10204080u >> 28 | ((f.y >> 1 & 0x01010101u) * 0x10204080u >> 28) << 4;
+              }
+              if (tile == tile0) sl = fminf(fmaxf(sl * bars->ref[items & 3].x, 1e-37f), FLT_MAX);
+            }
             const bool edge = k0 + kKeys > minvis || valid != 0xFFu;
             const int nvis = vis - k0;  // keys [0, nvis) of the tile are seen, where on a page
-            auto chunk = [&](int pc, uint32_t (&r)[32]) {
+            auto chunk = [&](auto scaled, int pc, uint32_t (&r)[32]) {
+              // the scales that are left to the chunk's two blocks, neutral where the row sees none of one
+              float2 bsl, blv, brv;
+              if constexpr (scaled) {
+                const float4 b0 = bars->block[place][2 * pc], b1 = bars->block[place][2 * pc + 1];
+                const bool see0 = nvis - pc * 32 > 0, see1 = nvis - pc * 32 > 16;
+                bsl = make_float2(see0 ? sl * b0.x : 1.f, see1 ? sl * b1.x : 1.f);
+                blv = make_float2(see0 ? b0.y : 0.f, see1 ? b1.y : 0.f);
+                brv = make_float2(see0 ? b0.z : 1.f, see1 ? b1.z : 1.f);
+              }
               if (edge) {
                 const int n = nvis - pc * 32;
                 uint32_t see = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1;
@@ -480,23 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
               }
               uint32_t w[16];
               float sum;
-              // E4M3: the scales of the two blocks, neutral where the row sees none of one
-              float2 bsl, blv, brv;
-              if constexpr (F == kE4M3) {
-                const float4 b0 = bars->block[(all_tiles + tile - tile0) & 3][2 * pc];
-                const float4 b1 = bars->block[(all_tiles + tile - tile0) & 3][2 * pc + 1];
-                bsl = make_float2(sl * b0.x, sl * b1.x);
-                blv = make_float2(b0.y, b1.y);
-                brv = make_float2(b0.z, b1.z);
-                if (edge) {
-                  if (nvis - pc * 32 <= 0) bsl.x = 1.f, blv.x = 0.f, brv.x = 1.f;
-                  if (nvis - pc * 32 <= 16) bsl.y = 1.f, blv.y = 0.f, brv.y = 1.f;
-                }
-              }
 #pragma unroll 1
               for (int again = 0;; ++again) {
                 float part = 0.f;
-                if constexpr (F == kE4M3) {
+                if constexpr (scaled) {
                   const float2 two = block_weights(r, w, bsl, make_float2(blv.x - m, blv.y - m));
                   sum = two.x + two.y;
                   part = fmaf(two.x, brv.x, two.y * brv.y);
@@ -506,21 +528,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                 const bool raise = m == kNone || !(sum <= kSumBound);
                 if (again) {  // above its own maximum: an infinity or a NaN is among the scores
                   if (!(sum <= kSumBound)) sum = __int_as_float(0x7fc00000);
-                  else if (F == kE4M3) sum = part;
+                  else if (scaled) sum = part;
                   break;
                 }
                 if (!__any_sync(~0u, raise)) {
-                  if (F == kE4M3) sum = part;
+                  if (scaled) sum = part;
                   break;
                 }
                 float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int k = 0; k < 32; ++k) {  // E4M3: a block to two of them
-                  const int at = F == kE4M3 ? (k >> 4) * 2 + (k & 1) : k & 3;
+                for (int k = 0; k < 32; ++k) {  // scaled: a block to two of them
+                  const int at = scaled ? (k >> 4) * 2 + (k & 1) : k & 3;
                   x[at] = fmaxf(x[at], __uint_as_float(r[k]));
                 }
                 float top;
-                if constexpr (F == kE4M3)
+                if constexpr (scaled)
                   top = fmaxf(fmaf(fmaxf(x[0], x[1]), bsl.x, blv.x - kBias), fmaf(fmaxf(x[2], x[3]), bsl.y, blv.y - kBias));
                 else top = fmaf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), sl, -kBias);
                 const float nm = raise ? fmaxf(m, top) : m;
@@ -555,12 +577,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
               l += sum;
               tc::tmem_st16(ts + pc * 16, w);
             };
+            auto all = [&](auto scaled) {
 #pragma unroll 1
-            for (int pc = 0; pc < kKeys / 32; ++pc) {
-              uint32_t ra[32];
-              tc::tmem_ld32(ts + pc * 32, ra);
-              tc::tmem_wait_ld();
-              chunk(pc, ra);
+              for (int pc = 0; pc < kKeys / 32; ++pc) {
+                uint32_t ra[32];
+                tc::tmem_ld32(ts + pc * 32, ra);
+                tc::tmem_wait_ld();
+                chunk(scaled, pc, ra);
+              }
+            };
+            if constexpr (F == kE4M3) {
+              if (slow) all(Yes());
+              else all(No());
+            } else {
+              all(No());
             }
             tc::tmem_wait_st();
             tc::fence_before_sync();
@@ -584,7 +614,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           const float bad = __int_as_float(0x7fc00000);
           if (m == kNone && l == l) l = 0.f;  // no key of the piece is seen
           if (dead) l = bad;  // the wait for O may be the one that gave up: no lse beside outputs that are NaN
-          const float inv = dead ? bad : whole ? (l == 0.f ? 0.f : p.v_scale / l) : 1.0f;
+          const float vs = F == kE4M3 ? bars->ref[item & 3].y : p.v_scale;
+          const float inv = dead ? bad : whole ? (l == 0.f ? 0.f : vs / l) : F == kE4M3 ? vs : 1.0f;
           const int tok = pr / G;
           const size_t orow = (size_t)(row0 + tok) * p.Hq + h * G + (pr - tok * G);
           T* out = static_cast<T*>(p.out) + orow * D;
@@ -647,7 +678,179 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         }
         sl = next_sl;
       }
-    } else if (warp < 8 + kConvert) {
+    } else if (F == kE4M3 && warp != 8 + kConvert) {
+      // ================================================== E4M3: codes to fp16 tiles
+      // Seven warps deal out a tile's groups of 512 bytes (4 keys of 128, 8 of 64).  Codes come from memory straight
+      // into registers (staged in shared memory they would take another eighth of its bandwidth), V's while K's are
+      // converted, the next tile's K's while V's are, and that tile's pages before.  Lane i looks after the place
+      // and the scales of the warp's i-th group.  The loads are volatile: the compiler would move them to where
+      // their values are needed.
+      constexpr int kWarps = kConvert + 1, kRowsOf = 512 / D, kGroups = kKeys / kRowsOf, kIter = (kGroups + kWarps - 1) / kWarps;
+      constexpr int PPR = D / 16;            // 16-byte pieces of a row
+      constexpr uint32_t kNowhere = ~0u;
+      const int cw = warp < 8 + kConvert ? warp - 8 : kConvert, mask = (1 << p.page_shift) - 1;
+      auto group = [&](int i) { return i * kWarps + cw; };
+      const bool mine = lane < kIter && group(lane) < kGroups;
+      const int run = mine ? group(lane) * kRowsOf / 16 : 0;           // of this lane's group, in the tile
+      const bool speaks = mine && group(lane) * kRowsOf % 16 == 0;      // for its run
+      uint4 wk[kIter], wv[kIter];
+      uint32_t at[kIter];        // the groups' runs of 16 keys in a pool
+      float ks = 1.f, vs = 1.f;  // of the run's block
+      float kref = 1.f, vref = 1.f, kback = 1.f, vback = 1.f;  // the piece's powers of two, and their inverses
+      auto lookup = [&](int tile, int first) {  // the page of keys tile * 128 + first ..
+        const int key = tile * kKeys + first;
+        return key < c.kv ? __ldg(p.table + (size_t)c.b * p.max_pages + (key >> p.page_shift)) : -1;
+      };
+      // a run of 16 keys in a pool, of less than 4 TB (and its block's scale)
+      auto place = [&](int tile, int first, int head, int page) {
+        return (uint32_t)page < (uint32_t)p.num_pages
+                   ? (((uint32_t)page * p.Hkv + head) << (p.page_shift - 4)) + (((tile * kKeys + first) & mask) >> 4) : kNowhere;
+      };
+      auto fetch = [&](const uint8_t* pool, uint4 (&w)[kIter]) {
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          w[i] = make_uint4(0, 0, 0, 0);
+          if (at[i] != kNowhere)
+            load_now(w[i], pool + (size_t)at[i] * (16 * D) + (group(i) * 512 & (16 * D - 1)) + lane * 16);
+        }
+      };
+      auto fetch_keys = [&](uint32_t mine_at) {
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          at[i] = __shfl_sync(~0u, mine_at, i);
+          if (group(i) >= kGroups) at[i] = kNowhere;
+        }
+        fetch(p.k_pool, wk);
+      };
+      auto fetch_scales = [&](uint32_t at, float& k, float& v) {
+        k = v = 1.f;
+        if (at != kNowhere) {
+          load_now(k, p.k_scales + at);
+          load_now(v, p.v_scales + at);
+        }
+      };
+      int tile = c.tile, minvis = c.minvis, maxvis = c.maxvis;
+      uint32_t item = 0;
+      const int part = lane % PPR;
+      // The pieces of a row's upper half write their words in the other order, so that the
+      // eight lanes of one phase of a store hit eight different bank groups.
+      const bool flip = PPR == 8 && part >= 4;
+      const int to = swz(cw * kRowsOf + lane / PPR, part * 2 + flip);  // of the first word of group 0
+      auto convert = [&](uint8_t* dst, uint4 (&w)[kIter], bool value, uint32_t factor) {
+        if ((tile + 1) * kKeys > minvis) {
+          // a key that nobody sees must weigh nothing; a NaN of V in a tile that some rows see in part is
+          // dealt out by the epilogue
+#pragma unroll
+          for (int i = 0; i < kIter; ++i) {
+            const int key = tile * kKeys + group(i) * kRowsOf + lane / PPR;
+            if (key >= maxvis) {
+              w[i] = make_uint4(0, 0, 0, 0);
+            } else if (value) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                uint32_t& wq = q == 0 ? w[i].x : q == 1 ? w[i].y : q == 2 ? w[i].z : w[i].w;
+                const uint32_t nan = __vcmpeq4(wq & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                wq &= ~nan;
+#pragma unroll 1
+                for (int e = 0; nan && e < 4; ++e)
+                  if ((nan >> (8 * e)) & 1) {
+                    atomicMax(&bars->nan_key[item & 3][part * 16 + q * 4 + e],
+                              ((unsigned long long)(item + 1) << 32) | ~(uint32_t)key);
+                    bars->nan_item[item & 3] = item + 1;
+                  }
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kIter; ++i) {
+          if (group(i) >= kGroups) break;
+          const uint32_t f = __shfl_sync(~0u, factor, i);
+          const uint32_t x[4] = {flip ? w[i].z : w[i].x, flip ? w[i].w : w[i].y, flip ? w[i].x : w[i].z, flip ? w[i].y : w[i].w};
+          // groups of four rows: every other of a warp's is four rows further in the swizzle
+          uint8_t* row = dst + (D == 128 && (i & 1) ? to ^ 64 : to) + i * (kWarps * kRowsOf * 128);
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<uint4*>(k ? dst + ((D == 128 && (i & 1) ? to ^ 64 : to) ^ 16) + i * (kWarps * kRowsOf * 128) : row) =
+                make_uint4(hmul2(e4m3::lo_to_h2(x[2 * k]), f), hmul2(e4m3::hi_to_h2(x[2 * k]), f),
+                           hmul2(e4m3::lo_to_h2(x[2 * k + 1]), f), hmul2(e4m3::hi_to_h2(x[2 * k + 1]), f));
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+      };
+      // The factor that codes are multiplied by, as an fp16 pair, and what is left of the scale: all of scale / ref
+      // where that is a power of two from 2^-15 to 2^7, which fp16 takes exactly (but for codes below 2^-24).
+      auto split = [](float ratio, float& rest) {
+        const uint32_t bits = __float_as_uint(ratio);
+        const int up = (int)(bits >> 23) - 127;
+        const bool taken = !(bits & 0x807fffffu) && up >= -15 && up <= 7;
+        rest = taken ? 1.f : ratio;
+        return !taken ? 0x3c003c00u : up < -14 ? 0x02000200u : (uint32_t)(up + 15) * 0x04000400u;
+      };
+      uint32_t lead = place(tile, 0, c.h, lookup(tile, 0));  // the piece's first block
+      uint32_t here = place(tile, run * 16, c.h, lookup(tile, run * 16));
+      bool opens = true;  // the piece
+      fetch_keys(here);
+      fetch_scales(here, ks, vs);
+#pragma unroll 1
+      for (uint32_t j = 0;; ++j) {
+        const uint32_t st = j & 1, parity = ((j >> 1) & 1) ^ 1;
+        fetch(p.v_pool, wv);
+        const bool opened = opens;
+        if (opens) {
+          float k, v;
+          fetch_scales(lead, k, v);
+          auto ref = [](float s, float& back) {  // its power of two, 1 for what is not positive and normal
+            const uint32_t bits = __float_as_uint(s) - (1u << 23) < 0x7f000000u ? __float_as_uint(s) & 0x7f800000u : 127u << 23;
+            back = __uint_as_float((254u << 23) - bits);
+            return __uint_as_float(bits);
+          };
+          kref = ref(k, kback);
+          vref = ref(v, vback);
+        }
+        // the tile after this one
+        bool more = true;
+        int next = tile + 1;
+        opens = next >= c.end;
+        int page = -1, first_page = -1;
+        if (opens) {
+          more = advance();
+          next = c.tile;
+          if (more) first_page = lookup(next, 0);
+        }
+        if (more) page = lookup(next, run * 16);
+        float rest_k, rest_v;
+        const bool held = here != kNowhere;
+        const uint32_t fk = split(held ? ks * kback : 1.f, rest_k), fv = split(held ? vs * vback : 1.f, rest_v);
+        if (!warp_wait(&bars->k_empty[st], parity, bars)) break;
+        // the softmax has done with tile j - 3
+        if (opened && lane == 0) bars->ref[item & 3] = make_float2(kref, vref);
+        if (speaks) {
+          const bool left_over = rest_k != 1.f || rest_v != 1.f;
+          bars->block[j & 3][run] = left_over ? make_float4(rest_k, e4m3::log2_of(rest_v), __fdividef(1.0f, rest_v), 0.f)
+                                              : make_float4(1.f, 0.f, 1.f, 0.f);
+          reinterpret_cast<uint8_t*>(&bars->flags[j & 3])[run] = left_over | (held ? 0 : 2);
+        }
+        convert(smem + C::kOffK + st * C::kTileB, wk, false, fk);
+        if (lane == 0) mbar_arrive(&bars->k_full[st]);
+        if (more) {
+          here = place(next, run * 16, c.h, page);
+          if (opens) lead = place(next, 0, c.h, first_page);
+          fetch_keys(here);
+          fetch_scales(here, ks, vs);
+        }
+        if (!warp_wait(&bars->v_empty[st], parity, bars)) break;
+        convert(smem + C::kOffV + st * C::kTileB, wv, true, fv);
+        if (lane == 0) mbar_arrive(&bars->v_full[st]);
+        if (!more) break;
+        if (opens) {
+          ++item;
+          minvis = c.minvis;
+          maxvis = c.maxvis;
+        }
+        tile = next;
+      }
+    } else if (F == kE2M1 && warp < 8 + kConvert) {
       // ================================================== codes to fp16 tiles
       const int tid = threadIdx.x - 256;
       uint32_t half = 0, tiles = 0, items = 0;  // half tiles, tiles and items so far
@@ -655,56 +858,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
       while (go && !bars->abort) {
         for (int tile = c.tile; tile < c.end && !bars->abort; ++tile, ++tiles) {
           const bool edge = (tile + 1) * kKeys > c.minvis;
-#pragma unroll 1
-          for (int ku = 0; ku < 2 * C::kUnits; ++ku, ++half) {
-            const int kv = ku / C::kUnits, unit = ku % C::kUnits;
+          for (int kv = 0; kv < 2; ++kv, ++half) {
             const uint32_t rs = half % kRaw, st = tiles & 1;
             if (!warp_wait(&bars->raw_full[rs], (half / kRaw) & 1, bars)) break;
-            if (unit == 0 && !warp_wait(kv ? &bars->v_empty[st] : &bars->k_empty[st], ((tiles >> 1) & 1) ^ 1, bars)) break;
+            if (!warp_wait(kv ? &bars->v_empty[st] : &bars->k_empty[st], ((tiles >> 1) & 1) ^ 1, bars)) break;
             const uint32_t valid = bars->raw_valid[tiles & 3];
             const uint8_t* raw = smem + C::kOffRaw + rs * C::kHalf;
             uint8_t* dst = smem + (kv ? C::kOffV : C::kOffK) + st * C::kTileB;
-            constexpr int PPR = C::kCode / 16;  // 16-byte pieces of a row's codes: 32 elements each, 16 of E4M3
-            if constexpr (F == kE4M3) {
-              constexpr int kPieces = C::kUnitKeys * PPR;
-#pragma unroll
-              for (int i = 0; i < (kPieces + kConvert * 32 - 1) / (kConvert * 32); ++i) {
-                const int ch = i * kConvert * 32 + tid, part = ch % PPR, r = unit * C::kUnitKeys + ch / PPR;
-                if (kPieces % (kConvert * 32) && ch >= kPieces) break;
-                uint4 w4 = *reinterpret_cast<const uint4*>(raw + ch * 16);
-                const bool ok = (valid >> (r >> 4)) & 1;
-                if (edge || !ok) {
-                  // a key that nobody sees, or one without a page, must weigh nothing; a NaN of V in a
-                  // tile that some rows see in part is dealt out by the epilogue
-                  if (!ok || tile * kKeys + r >= c.maxvis) {
-                    w4 = make_uint4(0, 0, 0, 0);
-                  } else if (kv) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                      uint32_t& wq = q == 0 ? w4.x : q == 1 ? w4.y : q == 2 ? w4.z : w4.w;
-                      const uint32_t nan = __vcmpeq4(wq & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                      wq &= ~nan;
-#pragma unroll 1
-                      for (int e = 0; nan && e < 4; ++e)
-                        if ((nan >> (8 * e)) & 1) {
-                          atomicMax(&bars->nan_key[items & 3][part * 16 + q * 4 + e],
-                                    ((unsigned long long)(items + 1) << 32) | ~(uint32_t)(tile * kKeys + r));
-                          bars->nan_item[items & 3] = items + 1;
-                        }
-                    }
-                  }
-                }
-                // The pieces of a row's upper half write their words in the other order, so that the
-                // eight lanes of one phase of a store hit eight different bank groups.
-                const bool flip = PPR == 8 && part >= 4;
-                const uint32_t w[4] = {flip ? w4.z : w4.x, flip ? w4.w : w4.y, flip ? w4.x : w4.z, flip ? w4.y : w4.w};
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-                  *reinterpret_cast<uint4*>(dst + swz(r, part * 2 + (flip ? 1 - k : k))) =
-                      make_uint4(e4m3::lo_to_h2(w[2 * k]), e4m3::hi_to_h2(w[2 * k]), e4m3::lo_to_h2(w[2 * k + 1]),
-                                 e4m3::hi_to_h2(w[2 * k + 1]));
-              }
-            } else {
+            constexpr int PPR = D / 32;  // 16-byte pieces of a row's codes: 32 elements each
 #pragma unroll
             for (int i = 0; i < (kKeys * PPR + kConvert * 32 - 1) / (kConvert * 32); ++i) {
               const int ch = i * kConvert * 32 + tid, r = ch / PPR, part = ch % PPR;
@@ -748,12 +909,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                     make_uint4(x[0], x[1], x[2], x[3]);
               }
             }
-            }
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
               mbar_arrive(&bars->raw_empty[rs]);
-              if (unit == C::kUnits - 1) mbar_arrive(kv ? &bars->v_full[st] : &bars->k_full[st]);
+              mbar_arrive(kv ? &bars->v_full[st] : &bars->k_full[st]);
             }
           }
         }
@@ -849,28 +1009,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         if (one) tc::mma_commit(&bars->drain);
         mbar_wait_drain(&bars->drain, 0);
       }
-     } else if (warp == 9 + kConvert) {
+     } else if (F == kE2M1 && warp == 9 + kConvert) {
       // ================================================================= loader
       uint32_t half = 0, tiles = 0;
-      // lanes 0 .. 15: a run of 16 keys to two of them, E2M1's codes and scales, E4M3's K scale (and codes) and V scale
       const int sub = (lane >> 1) & 7, scales = lane & 1;
-      const int row_bytes = F == kE2M1 && scales ? e2m1::scale_bytes(D) : C::kCode, bytes = 16 * row_bytes;
-      const size_t off = F == kE2M1 && scales ? (size_t)e2m1::code_bytes(D) << p.page_shift : 0;
-      const int dst = (F == kE2M1 && scales ? C::kCodes : 0) + sub % (8 / C::kUnits) * bytes;
-      auto find = [&](int tile) {  // the page of this lane's run of a tile of the piece; -1: none
+      const int bytes = 16 * (scales ? e2m1::scale_bytes(D) : e2m1::code_bytes(D));
+      const int row_bytes = scales ? e2m1::scale_bytes(D) : e2m1::code_bytes(D);
+      const size_t off = scales ? (size_t)e2m1::code_bytes(D) << p.page_shift : 0;
+      const int dst = (scales ? C::kCodes : 0) + sub * bytes;
+      auto find = [&](int b, int kv, int tile) {
         const int t = tile * kKeys + sub * 16;
-        return lane < 16 && tile < c.end && t < c.kv
-                   ? __ldg(p.table + (size_t)c.b * p.max_pages + (t >> p.page_shift)) : -1;
+        return lane < 16 && t < kv ? __ldg(p.table + (size_t)b * p.max_pages + (t >> p.page_shift)) : -1;
       };
-      auto row_of = [&](int tile) { return (tile * kKeys + sub * 16) & ((1 << p.page_shift) - 1); };
-      auto scale_of = [&](int page, int tile) {  // of E4M3's block
-        if (F == kE2M1 || (uint32_t)page >= (uint32_t)p.num_pages) return 1.0f;
-        return __ldg((scales ? p.v_scales : p.k_scales) + (((size_t)page * p.Hkv + c.h) << (p.page_shift - 4)) +
-                     (row_of(tile) >> 4));
-      };
-      // pages are looked up two tiles ahead, the scales of their blocks one
-      int page = find(c.tile), page1 = find(c.tile + 1);
-      float scale = scale_of(page, c.tile);
+      int page = find(c.b, c.kv, c.tile);
       bool go = true;
       while (go && !bars->abort) {
         for (int tile = c.tile; tile < c.end && !bars->abort; ++tile, ++tiles) {
@@ -879,45 +1030,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           uint32_t valid = 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) valid |= ((runs >> (2 * i)) & 1) << i;
-          const size_t src = ((size_t)page * p.Hkv + c.h) * p.page_bytes + off + (size_t)row_of(tile) * row_bytes;
-          const int page2 = find(tile + 2);
-          const float scale1 = scale_of(page1, tile + 1);
-#pragma unroll 1
-          for (int ku = 0; ku < 2 * C::kUnits; ++ku, ++half) {
-            const int kv = ku / C::kUnits, unit = ku % C::kUnits;
+          const size_t src = ((size_t)page * p.Hkv + c.h) * p.page_bytes + off +
+                             (size_t)((tile * kKeys + sub * 16) & ((1 << p.page_shift) - 1)) * row_bytes;
+          const int next = tile + 1 < c.end ? find(c.b, c.kv, tile + 1) : -1;
+          for (int kv = 0; kv < 2; ++kv, ++half) {
             const uint32_t rs = half % kRaw;
             if (!warp_wait(&bars->raw_empty[rs], ((half / kRaw) & 1) ^ 1, bars)) break;
-            if (F == kE4M3 && ku == 0 && lane < 16) {
-              float* b = &bars->block[tiles & 3][sub].x;
-              if (scales) {
-                b[1] = e4m3::log2_of(scale);
-                b[2] = __fdividef(1.0f, scale);
-              } else {
-                b[0] = scale;
-              }
-            }
-            __syncwarp();
-            const uint32_t here = C::kUnits == 1 ? valid : (valid >> (4 * unit)) & 15;
             if (lane == 0) {
-              if (ku == 0) bars->raw_valid[tiles & 3] = valid;
+              if (kv == 0) bars->raw_valid[tiles & 3] = valid;
               tc::mbar_expect_tx(&bars->raw_full[rs],
-                                 __popc(here) * 16 * (C::kCode + (F == kE2M1 ? e2m1::scale_bytes(D) : 0)));
+                                 __popc(valid) * 16 * (e2m1::code_bytes(D) + e2m1::scale_bytes(D)));
             }
             __syncwarp();
-            if (ok && (F == kE2M1 || !scales) && (C::kUnits == 1 || sub / 4 == unit))
+            if (ok)
               bulk_load(smem + C::kOffRaw + rs * C::kHalf + dst, (kv ? p.v_pool : p.k_pool) + src, bytes,
                         &bars->raw_full[rs]);
           }
-          page = page1;
-          page1 = page2;
-          scale = scale1;
+          page = next;
         }
         go = advance();
-        if (go) {
-          page = find(c.tile);
-          page1 = find(c.tile + 1);
-          scale = scale_of(page, c.tile);
-        }
+        if (go) page = find(c.b, c.kv, c.tile);
       }
       if (bars->abort)
         for (int i = 0; i < kRaw; ++i) {
