@@ -628,7 +628,8 @@ dkv_status dkv_paged_attend_debug_withhold(int enable);
  * so far, and one whose scale is not a positive finite number neither.  The block's scale becomes s; if it grew, codes that are
  * there become e4m3(code * old / s); the rows' codes are e4m3(y / s), to nearest even.  A NaN or an infinity becomes a
  * NaN of its element alone, and does not count for the scale.
- * Rows of one block must be consecutive rows of the call (as dkv_step_plan deals them), and no two may have one slot;
+ * The rows of one block must lie within 16 consecutive rows of the call (dkv_step_plan deals them one after another), and no
+ * two may have one slot;
  * sequences that append to the same block must not share it (dkv_pages_fork sees to that).  So a
  * sequence that is cut back and appended to again keeps its block's scale, which is then larger than it has to be, until
  * the block begins anew.

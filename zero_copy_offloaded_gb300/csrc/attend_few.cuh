@@ -91,7 +91,10 @@ struct Cfg {
   static constexpr int kS = kSub * e2m1::scale_bytes(D);
   static constexpr int kSlot = 2 * kC + (F == kE2M1 ? 2 * kS : 16);
   static constexpr int kOffScale = 2 * kC;
-  static constexpr int kSteps = F == kE2M1 ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 4);  // steps in a warp's ring
+  // Steps in a warp's ring.  E4M3 of 64 with three and three CTAs an SM: 32 x 8192 keys of 8 heads for 16 rows 71 us, with
+  // four, of which two CTAs fit, 90 (24 rows of 48 ragged sequences 67 and 76).  Of 128 two and three CTAs for
+  // eight rows (8 x 32769 keys 96.7 us, 4 x 131073 183; three steps and two CTAs 98.2 and 180), two CTAs for more.
+  static constexpr int kSteps = F == kE2M1 ? (D == 128 ? 3 : 4) : (D == 128 ? 2 : 3);
   static constexpr int kRing = 2 * kSteps * kSlot;   // per warp
   static constexpr int kRound = F == kE2M1 || D == 64 ? 8 : 4;  // rows of a round of the join of the warps
   static constexpr int kMerge = kWarps * kRound * D * 4;       // one of every warp's O
@@ -104,9 +107,10 @@ struct Cfg {
   // 64: 48 sequences of up to 8193 keys of 32 heads take 139 us with four, 149 with three; but
   // 16 x 512 keys of 8 heads 11.6 and 10.4, so that the fourth stays out of short ranges.
   static constexpr int kPerSm = F == kE2M1 && NT == 1 && D == 64 ? 4 : NT == 1 || (NT <= 3 && D == 64) ? 3 : 2;
-  // subs in flight at once: 20 rows over 16 x 32768 keys of 8 heads of 128 take 214 us with two, 225
-  // with one; of 64 141 and 142; four groups of rows have no registers for it
-  static constexpr int kBoth = NT == 1 || (NT <= 3 && D == 128) ? 2 : 1;
+  // Subs in flight at once.  E2M1: 20 rows over 16 x 32768 keys of 8 heads of 128 take 214 us with two, 225
+  // with one; of 64 141 and 142; four groups of rows have no registers for it.  E4M3, which keeps no scales in
+  // registers: 32 rows of 64 over 32 x 8192 keys 102 us with two, 108 with one.
+  static constexpr int kBoth = NT == 1 || (NT <= 3 && D == 128) || (F == kE4M3 && D == 64) ? 2 : 1;
 };
 
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
