@@ -8,8 +8,11 @@
 // each, plain stores: all writers write 1), a scan over the marks in page order, and a pass over the table.
 //
 // What bounds them: the table's entries, read once to mark (a scattered byte store each) and once to be
-// rewritten, and latency.  The marks and the rewrite want the whole GPU, the scan one cluster; a small table
-// takes all three in one launch of that cluster (see kOneLaunch).
+// rewritten, and latency: clearing the marks, marking, counting, what follows from the counts and the rewrite wait for one
+// another.  Large tables and pools take a launch of the whole GPU for each, small ones one launch of a cluster with a
+// barrier between them.  In a graph: a fork of 512 sequences of up to 32768 rows takes 20 us (with a scan by one cluster 46), a
+// compaction of their 1 M pages 27 (110); of 64 sequences of up to 4096 rows in a cluster 14 and 17.  A copy of 8192 pages of
+// 2 x 32 KB and their scales runs at 6.6 TB/s, as fast as a plain copy.
 #include <stdio.h>
 
 #include <algorithm>
@@ -26,15 +29,18 @@ using namespace dkv;
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32, kCluster = 8, kSms = 152;
 constexpr int kSegment = 256;  // table entries of a warp at a time, eight to a lane
-// Table entries plus pages up to which one cluster does everything in one launch.
-constexpr long long kOneLaunch = 1 << 16;
+// Table entries plus pages up to which one cluster does everything in one launch.  64 sequences of up to 16384 rows,
+// 131000 in all, take 18 us to fork and 23 to compact so, 18 and 22 in five launches, whose calls take 9 us longer; 256
+// of up to 8192 rows, twice as many, 24 and 36, and 18 and 21.
+constexpr long long kOneLaunch = 1 << 17;
 
-enum Phase : int { kAll = -1, kClear = 0, kMark = 1, kScan = 2, kWrite = 3 };
+// One launch of a cluster runs them all, or each is a launch of its own.
+enum Phase : int { kAll = -1, kClear = 0, kMark = 1, kCount = 2, kEmit = 3, kWrite = 4 };
 
 struct Row {
   int source;  // old row that this one becomes a copy of; -1: none
   int shared;  // its entries that go on
-  int page;    // the entry behind them, or -1
+  int take;    // where the entry behind them, a copy of the source's, comes from, on the stack; -1: there is none
   int pad;
 };
 
@@ -54,10 +60,9 @@ struct PageParams {
   Row* rows;             // fork: [B]
   int* old;              // fork in place: [B][max_pages]
   int* rank;             // compact: [num_pages], of pages that move
-  int* sums;             // [4][kCluster], then a flag: the tables are rewritten
+  int* counts;           // marks that each CTA of the scan has counted [kSms], then pages from which entries move
   int B, max_pages, shift, num_pages, max_moves;
 };
-constexpr int kSums = 4 * kCluster + 1;
 
 __device__ __forceinline__ void cluster_sync() {
   __syncwarp();
@@ -77,32 +82,20 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
   __syncthreads();  // s_warp is free
   if (lane == 31) s_warp[warp] = x;
   __syncthreads();
-  if (warp == 0) {
-    int w = s_warp[lane];
-    for (int d = 1; d < 32; d <<= 1) {
-      const int o = __shfl_up_sync(~0u, w, d);
-      if (lane >= d) w += o;
-    }
-    s_warp[lane] = w;
-  }
-  __syncthreads();
-  total = s_warp[kWarps - 1];
-  return x - v + (warp ? s_warp[warp - 1] : 0);
+  // every warp adds up the warps' sums for itself
+  const int w = s_warp[lane];
+  total = __reduce_add_sync(~0u, w);
+  return x - v + __reduce_add_sync(~0u, lane < warp ? w : 0);
 }
 
-// The same over the cluster: what the CTAs before this one have, and `total`; slots: its kCluster words.
-__device__ __forceinline__ int cluster_base(int own, int* slots, int& total) {
-  if (threadIdx.x == 0) slots[blockIdx.x] = own;
-  cluster_sync();
-  int base = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kCluster; ++i) {
-    const int v = __ldcg(slots + i);
-    base += i < (int)blockIdx.x ? v : 0;
-    total += v;
-  }
-  return base;
+// The marks that CTAs before `upto` have counted, and those of all; the threads together.
+__device__ __forceinline__ int counted(const int* counts, int upto, int* s_warp, int& total) {
+  const int t = threadIdx.x;
+  const int v = t < (int)gridDim.x ? __ldcg(counts + t) : 0;
+  int before;
+  block_scan(t < upto ? v : 0, s_warp, before);
+  block_scan(v, s_warp, total);
+  return before;
 }
 
 __device__ __forceinline__ void clear(uint8_t* at, int bytes) {
@@ -135,56 +128,70 @@ __device__ __forceinline__ void mark(const PageParams& p, uint8_t* at, const int
     if ((uint32_t)page[i] < (uint32_t)p.num_pages) at[page[i]] = 1;
 }
 
-// This thread's pages of the scan: [first, first + 16 n).
-__device__ __forceinline__ void scan_range(const PageParams& p, long long& first, int& n) {
-  const long long words = (p.num_pages + 15LL) / 16, threads = (long long)kCluster * kThreads;
-  n = (int)((words + threads - 1) / threads);
-  const long long at = ((long long)blockIdx.x * kThreads + threadIdx.x) * n;
-  first = at * 16;
-  n = (int)max(0LL, min((long long)n, words - at));
+// The scan's words of four pages: a CTA has words [cta * per, (cta + 1) * per), a thread n of them from `first` on.
+struct Range {
+  int per, first, n;
+};
+__device__ __forceinline__ Range scan_range(const PageParams& p, int cta) {
+  const int words = (p.num_pages + 3) / 4, per = (words + gridDim.x - 1) / gridDim.x;
+  const int each = (per + kThreads - 1) / kThreads, at = min((int)threadIdx.x * each, per);
+  const int first = (int)min((long long)cta * per + at, (long long)words);
+  return {per, first, max(0, min(min(each, per - at), words - first))};
 }
 
-__device__ __forceinline__ int count_bytes(const uint4& w) {
-  return __popc(w.x | w.y << 1 | w.z << 2 | w.w << 3);  // bytes are 0 or 1
+// Marks are bytes of 0 or 1.
+__device__ __forceinline__ uint32_t load_marks(const uint8_t* at, int word) {
+  return __ldcg(reinterpret_cast<const uint32_t*>(at) + word);
 }
 
 // ---- fork -----------------------------------------------------------------------------------
 
 // What every CTA finds out about the batch for itself.
 struct Batch {
+  int len[kThreads];   // of the old rows, from 0 to what the table holds
+  Row rows[kThreads];  // of the new ones
   int heir[kThreads];  // of old row s: -1 itself, else the lowest row that goes on as it; INT_MAX: none
   int warp[kWarps];
   int longest;
 };
 
-__device__ void fork_phase(const PageParams& p, int phase, Batch& s) {
+__device__ __forceinline__ uint32_t load_freed(const PageParams& p, int word) {  // held, and not any more
+  return load_marks(p.dead, word) & ~load_marks(p.live, word);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, int phase) {
+  __shared__ Batch s;
+  griddep_wait();
+  griddep_launch_dependents();
   const int b = threadIdx.x, lane = b & 31;
   const bool all = phase == kAll;
+  const long long cap = (long long)p.max_pages << p.shift;
+  int src = -1, free_count = 0;
+  long long len = 0;
+  if (phase != kClear && phase != kWrite) {
+    src = b < p.B ? p.sources[b] : -1;
+    len = b < p.B ? max(p.len[b], 0) : 0;
+    free_count = min(max(*p.free_count, 0), p.num_pages);
+  }
   if (phase == kClear || all) {
     clear(p.live, p.num_pages);
     clear(p.dead, p.num_pages);
     if (!all) return;
-    cluster_sync();
   }
-  const long long cap = (long long)p.max_pages << p.shift;
   if (phase != kWrite) {
     s.heir[b] = 0x7fffffff;
+    s.len[b] = (int)min(len, cap);
     if (b == 0) s.longest = 0;
-    __syncthreads();
-    const int src = b < p.B ? p.sources[b] : -1;
-    long long len = b < p.B ? max(p.len[b], 0) : 0;
     const bool wrong = __syncthreads_or(src >= p.B), far = __syncthreads_or(len > cap);
-    if (far && len > cap) len = cap;  // nothing is forked then; marks stay inside the row
     if (src >= 0 && src < p.B) atomicMin(&s.heir[src], src == b ? -1 : b);
     __syncthreads();
-    const bool vanishes = len > 0 && s.heir[b] == 0x7fffffff;
-    const bool any = __syncthreads_or(vanishes);
+    const bool any = __syncthreads_or(len > 0 && s.heir[b] == 0x7fffffff);  // a row vanishes
     if (phase == kMark || all) {
+      if (all) cluster_sync();
       segments(p, [&](int r, int first) {
-        const int end = (int)pages_of(min((long long)max(p.len[r], 0), cap), p.shift);
+        const int end = (int)pages_of(s.len[r], p.shift);
         if (first >= end) return;
-        const int heir = s.heir[r];
-        const bool goes = heir != 0x7fffffff;
+        const bool goes = s.heir[r] != 0x7fffffff;
         // in place, a row that another one becomes is read again after it may have been written
         const bool keep = p.old && goes;
         if (!any && !keep) return;
@@ -200,72 +207,68 @@ __device__ void fork_phase(const PageParams& p, int phase, Batch& s) {
       if (!all) return;
       cluster_sync();
     }
-    // ---- scan: pages that go back, in page order
-    const bool on = src >= 0 && src < p.B;
-    const long long new_len = on ? min((long long)max(p.len[on ? src : 0], 0), cap) : 0;
-    const int held = (int)pages_of(new_len, p.shift);
-    const bool need = on && (new_len & ((1 << p.shift) - 1)) && s.heir[src] != (src == b ? -1 : b);
-    int needed, freed = 0, at = 0;
-    const int k = block_scan(need, s.warp, needed);
-    const int free_count = min(max(*p.free_count, 0), p.num_pages);
-    long long first = 0;
-    int n = 0, mine = 0;
-    if (any) {
-      scan_range(p, first, n);
-      for (int i = 0; i < n; ++i) {
-        const uint4 d = __ldcg(reinterpret_cast<const uint4*>(p.dead + first) + i);
-        const uint4 l = __ldcg(reinterpret_cast<const uint4*>(p.live + first) + i);
-        mine += count_bytes(make_uint4(d.x & ~l.x, d.y & ~l.y, d.z & ~l.z, d.w & ~l.w));
-      }
-      int own;
-      at = block_scan(mine, s.warp, own);
-      at += cluster_base(own, p.sums, freed);
+    // ---- pages that go back, in page order
+    const Range range = scan_range(p, blockIdx.x);
+    int mine = 0;
+    if (any)
+      for (int i = 0; i < range.n; ++i) mine += __popc(load_freed(p, range.first + i));
+    int own, freed = 0, at = 0;
+    if (any) at = block_scan(mine, s.warp, own);
+    if (phase == kCount || all) {
+      if (any && b == 0) p.counts[blockIdx.x] = own;
+      if (!all) return;
+      cluster_sync();
     }
+    if (any) at += counted(p.counts, blockIdx.x, s.warp, freed);
+    const bool on = src >= 0 && src < p.B;
+    const int new_len = on ? s.len[src] : 0, held = (int)pages_of(new_len, p.shift);
+    const bool need = on && (new_len & ((1 << p.shift) - 1)) && s.heir[src] != (src == b ? -1 : b);
+    int needed;
+    const int k = block_scan(need, s.warp, needed);
     const long long stack = (long long)free_count + freed;
     const bool ok = !wrong && !far && needed <= stack && stack <= p.num_pages;
-    if (any && ok && mine) {
+    if (ok && mine) {
       int* to = p.free_pages + free_count + at;
-      for (int i = 0; i < n; ++i) {
-        const uint4 d = __ldcg(reinterpret_cast<const uint4*>(p.dead + first) + i);
-        const uint4 l = __ldcg(reinterpret_cast<const uint4*>(p.live + first) + i);
-        const uint32_t w[4] = {d.x & ~l.x, d.y & ~l.y, d.z & ~l.z, d.w & ~l.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          for (uint32_t m = w[q]; m; m &= m - 1) *to++ = (int)(first + 16 * i + 4 * q) + (__ffs(m) - 1) / 8;
+      for (int i = 0; i < range.n; ++i) {
+        for (uint32_t m = load_freed(p, range.first + i); m; m &= m - 1)
+          *to++ = (range.first + i) * 4 + (__ffs(m) - 1) / 8;
       }
     }
-    // What the inputs say has been read; lengths may be written in place behind this.
-    cluster_sync();
-    if (blockIdx.x == 0) {
-      const int longest = (int)(ok ? new_len : min(len, cap));
-      atomicMax(&s.longest, b < p.B ? (far ? max(p.len[b], 0) : longest) : 0);
+    Row row = {ok ? (on ? src : -1) : b, ok ? held - need : (int)pages_of(s.len[b], p.shift), -1, 0};
+    if (ok && need) row.take = (int)(stack - 1 - k);
+    s.rows[b] = row;
+    // one CTA, where it cannot be the only one to read the inputs, leaves what it writes over them to the next phase
+    if (blockIdx.x == gridDim.x - 1) {
+      const int length = ok ? new_len : (int)len;
+      atomicMax(&s.longest, length);
       if (b < p.B) {
-        Row r = {ok ? (on ? src : -1) : b, ok ? held - need : (int)pages_of(len, p.shift), -1, 0};
-        int from = -1;
-        if (ok && need) {
-          r.page = __ldcg(p.free_pages + stack - 1 - k);
-          from = p.table[(size_t)src * p.max_pages + held - 1];
-        }
-        p.rows[b] = r;
-        reinterpret_cast<int2*>(p.pairs)[b] = make_int2(from, r.page);
+        if (row.take < 0) reinterpret_cast<int2*>(p.pairs)[b] = make_int2(-1, -1);
+        p.rows[b] = row;
+        p.counts[kSms + 1 + b] = length;
       }
       __syncthreads();
-      if (b < p.B) p.len_out[b] = ok ? (int)new_len : max(p.len[b], 0);
       if (b == 0) {
-        *p.free_left = ok ? (int)(stack - needed) : free_count;
         p.report[0] = ok ? DKV_OK : wrong ? DKV_ERR_INVALID_ARG : DKV_ERR_CAPACITY;
         p.report[1] = ok ? freed : 0;
         p.report[2] = ok ? needed : 0;
         p.report[3] = s.longest;
+        p.counts[kSms] = ok ? (int)(stack - needed) : free_count;
       }
     }
     if (!all) return;
     cluster_sync();
   }
   // ---- write the rows
+  if (blockIdx.x == 0) {
+    if (b < p.B) p.len_out[b] = __ldcg(p.counts + kSms + 1 + b);
+    if (b == 0) *p.free_left = __ldcg(p.counts + kSms);
+  }
   segments(p, [&](int r, int first) {
-    const int4 w = __ldcg(reinterpret_cast<const int4*>(p.rows + r));
-    const Row row = {w.x, w.y, w.z, 0};
+    Row row = s.rows[r];
+    if (!all) {
+      const int4 w = __ldcg(reinterpret_cast<const int4*>(p.rows + r));
+      row = {w.x, w.y, w.z, w.w};
+    }
     if (row.source < 0 || first >= row.shared + 1 || (p.old && row.source == r)) return;
     int page[8];
     load_segment((p.old ? p.old : p.table) + (size_t)row.source * p.max_pages, first, row.shared, page);
@@ -273,25 +276,31 @@ __device__ void fork_phase(const PageParams& p, int phase, Batch& s) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = first + lane + 32 * i;
-      if (c < row.shared) to[c] = page[i];
-      else if (c == row.shared && row.page >= 0) to[c] = row.page;
+      if (c < row.shared) {
+        to[c] = page[i];
+      } else if (c == row.shared && row.take >= 0) {
+        const int taken = __ldcg(p.free_pages + row.take);
+        const int from = __ldcg((p.old ? p.old : p.table) + (size_t)row.source * p.max_pages + c);
+        to[c] = taken;
+        reinterpret_cast<int2*>(p.pairs)[r] = make_int2(from, taken);
+      }
     }
   });
-}
-
-__global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, int phase) {
-  __shared__ Batch s;
-  fork_phase(p, phase, s);
 }
 
 // ---- compaction -----------------------------------------------------------------------------
 
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PageParams p, int phase) {
-  __shared__ int s_warp[kWarps], s_longest;
+  __shared__ int s_warp[kWarps], s_longest, s_len[kThreads];
+  griddep_wait();
+  griddep_launch_dependents();
   const bool all = phase == kAll;
   const int lane = threadIdx.x & 31, t = threadIdx.x;
   const long long cap = (long long)p.max_pages << p.shift;
-  auto end_of = [&](int r) { return (int)pages_of(min((long long)max(p.len[r], 0), cap), p.shift); };
+  const int len = phase != kClear && t < p.B ? max(p.len[t], 0) : 0;
+  s_len[t] = (int)min((long long)len, cap);
+  __syncthreads();
+  auto end_of = [&](int r) { return (int)pages_of(s_len[r], p.shift); };
   if (phase == kClear || all) {
     clear(p.live, p.num_pages);
     if (!all) return;
@@ -308,68 +317,73 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PageParams p
     if (!all) return;
     cluster_sync();
   }
-  if (phase == kScan || all) {
-    if (t == 0) s_longest = 0;
-    const int len = t < p.B ? max(p.len[t], 0) : 0;
-    const bool ok = !__syncthreads_or(len > cap);
-    atomicMax(&s_longest, len);
-    long long first;
-    int n, mine = 0, high = 0, own, live, moves;
-    scan_range(p, first, n);
-    const uint4* words = reinterpret_cast<const uint4*>(p.live + first);
-    for (int i = 0; i < n; ++i) mine += count_bytes(__ldcg(words + i));
+  int from = 0;
+  if (phase != kWrite) {
+    const Range range = scan_range(p, blockIdx.x);
+    int mine = 0, own;
+    for (int i = 0; i < range.n; ++i) mine += __popc(load_marks(p.live, range.first + i));
     int before = block_scan(mine, s_warp, own);  // pages named before this thread's
-    before += cluster_base(own, p.sums, live);
-    // f(page, named, pages named before it)
-    auto each = [&](auto&& f) {
-      int at = before;
-      for (int i = 0; i < n; ++i) {
-        const uint4 v = __ldcg(words + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll 1
-        for (int q = 0; q < 16; ++q) {
-          const uint32_t word = q < 8 ? (q < 4 ? w[0] : w[1]) : (q < 12 ? w[2] : w[3]);
-          const int on = (word >> (8 * (q & 3))) & 1;
-          const long long page = first + 16 * i + q;
-          if (page < p.num_pages) f((int)page, on, at);
-          at += on;
+    if (phase == kCount || all) {
+      if (t == 0) p.counts[blockIdx.x] = own;
+      if (!all) return;
+      cluster_sync();
+    }
+    int live;
+    before += counted(p.counts, blockIdx.x, s_warp, live);
+    // named pages below `live`, which stay: those of the CTAs before the one that has page `live`, and a part of its own
+    const int edge = live / 4 / range.per;
+    int ignore, part = 0, low;
+    low = counted(p.counts, edge, s_warp, ignore);
+    const Range other = scan_range(p, edge);
+    for (int i = 0; i < other.n; ++i) {
+      const int word = other.first + i, keep = live - word * 4;  // bytes of it below `live`
+      part += __popc(load_marks(p.live, word) & (keep >= 4 ? ~0u : keep <= 0 ? 0u : (1u << (8 * keep)) - 1));
+    }
+    block_scan(part, s_warp, part);
+    low += part;
+    const int moves = live - low;
+    if (t == 0) s_longest = 0;
+    const bool ok = !__syncthreads_or(len > cap);
+    if (ok) {
+      for (int i = 0; i < range.n; ++i) {
+        const uint32_t word = load_marks(p.live, range.first + i);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int named = (word >> (8 * q)) & 1, page = (range.first + i) * 4 + q;
+          if (page < live) {
+            if (!named) p.pairs[2 * (page - before) + 1] = page;
+          } else if (named) {
+            p.pairs[2 * (before - low)] = page;
+            p.rank[page] = before - low;
+          }
+          before += named;
         }
       }
-    };
-    if (first >= live) high = mine;
-    else if (first + 16LL * n > live) each([&](int page, int on, int) { high += on && page >= live; });
-    block_scan(high, s_warp, own);
-    cluster_base(own, p.sums + kCluster, moves);
-    if (ok) {
-      const int low = live - moves;  // pages named below `live`: they stay
-      each([&](int page, int on, int at) {
-        if (page < live) {
-          if (!on) p.pairs[2 * (page - at) + 1] = page;
-        } else if (on) {
-          p.pairs[2 * (at - low)] = page;
-          p.rank[page] = at - low;
-        }
-      });
     }
-    const int rest = ok ? moves : 0;
-    for (int i = rest + blockIdx.x * kThreads + t; i < p.max_moves; i += kCluster * kThreads)
+    const int rest = ok ? moves : 0, stride = gridDim.x * kThreads;
+    for (int i = rest + blockIdx.x * kThreads + t; i < p.max_moves; i += stride)
       reinterpret_cast<int2*>(p.pairs)[i] = make_int2(-1, -1);
     if (ok)
-      for (int i = blockIdx.x * kThreads + t; i < p.num_pages - live; i += kCluster * kThreads)
-        p.free_pages[i] = p.num_pages - 1 - i;
-    if (blockIdx.x == 0 && t == 0) {
-      if (ok) *p.free_left = p.num_pages - live;
-      p.report[0] = ok ? DKV_OK : DKV_ERR_CAPACITY;
-      p.report[1] = rest;
-      p.report[2] = ok ? live : 0;
-      p.report[3] = s_longest;
-      p.sums[4 * kCluster] = ok ? live : 0x7fffffff;
+      for (int i = blockIdx.x * kThreads + t; i < p.num_pages - live; i += stride) p.free_pages[i] = p.num_pages - 1 - i;
+    if (blockIdx.x == 0) {
+      atomicMax(&s_longest, len);
+      __syncthreads();
+      if (t == 0) {
+        if (ok) *p.free_left = p.num_pages - live;
+        p.report[0] = ok ? DKV_OK : DKV_ERR_CAPACITY;
+        p.report[1] = rest;
+        p.report[2] = ok ? live : 0;
+        p.report[3] = s_longest;
+        p.counts[kSms] = ok ? live : 0x7fffffff;
+      }
     }
+    from = ok ? live : 0x7fffffff;
     if (!all) return;
     cluster_sync();
   }
   // ---- the tables follow
-  const int live = __ldcg(p.sums + 4 * kCluster);  // entries from it on have moved
+  // entries from it on have moved
+  const int live = phase == kWrite ? __ldcg(p.counts + kSms) : from;
   segments(p, [&](int r, int first) {
     const int end = end_of(r);
     if (first >= end) return;
@@ -452,24 +466,29 @@ const char* bad_sizes(int batch, int max_pages, int page_tokens, int num_pages) 
   return nullptr;
 }
 
-// Workspace: sums | rows | marks | marks or ranks | the old table.
-size_t ws_rows() { return align256(kSums * sizeof(int)); }
+// Workspace: counts, the end of the stack, new lengths | rows | marks | marks or ranks | the old table.
+size_t ws_rows() { return align256((kSms + 1 + DKV_MAX_STEP_BATCH) * sizeof(int)); }
 size_t ws_live() { return ws_rows() + align256(DKV_MAX_STEP_BATCH * sizeof(Row)); }
 size_t ws_more(int num_pages) { return ws_live() + align256(num_pages); }
 size_t ws_old(int num_pages) { return ws_more(num_pages) + align256((size_t)num_pages * 4); }
 
 template <typename K>
-cudaError_t launch_one(K* kernel, const PageParams& p, int phase, int grid, bool cluster, cudaStream_t s) {
+cudaError_t launch_one(K* kernel, const PageParams& p, int phase, int grid, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kCluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  if (phase == kAll) {
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = kCluster;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  } else {  // a phase's CTAs may come to an SM while the last ones of the phase before finish
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+  }
   cfg.attrs = at;
-  cfg.numAttrs = cluster ? 1 : 0;
+  cfg.numAttrs = phase == kClear ? 0 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p, phase);
 }
 
@@ -477,15 +496,16 @@ template <typename K>
 dkv_status launch(K* kernel, const PageParams& p, cudaStream_t s) {
   cudaError_t e;
   if ((long long)p.B * p.max_pages + p.num_pages <= kOneLaunch) {
-    e = launch_one(kernel, p, kAll, kCluster, true, s);
+    e = launch_one(kernel, p, kAll, kCluster, s);
   } else {
     const long long parts = (long long)p.B * ((p.max_pages + kSegment - 1) / kSegment);
     const int grid = (int)std::min<long long>((parts + kWarps - 1) / kWarps, kSms);
-    const int wide = (int)std::min<long long>((p.num_pages / 16 + kThreads) / kThreads, kSms);
-    e = launch_one(kernel, p, kClear, wide, false, s);
-    if (e == cudaSuccess) e = launch_one(kernel, p, kMark, grid, false, s);
-    if (e == cudaSuccess) e = launch_one(kernel, p, kScan, kCluster, true, s);
-    if (e == cudaSuccess) e = launch_one(kernel, p, kWrite, grid, false, s);
+    const int scan = std::min((p.num_pages + 4 * kThreads - 1) / (4 * kThreads), kSms);
+    e = launch_one(kernel, p, kClear, scan, s);
+    if (e == cudaSuccess) e = launch_one(kernel, p, kMark, grid, s);
+    if (e == cudaSuccess) e = launch_one(kernel, p, kCount, scan, s);
+    if (e == cudaSuccess) e = launch_one(kernel, p, kEmit, scan, s);
+    if (e == cudaSuccess) e = launch_one(kernel, p, kWrite, grid, s);
   }
   if (e != cudaSuccess) cudaGetLastError();
   return e == cudaSuccess ? DKV_OK : refuse(DKV_ERR_CUDA, cudaGetErrorString(e));
@@ -493,7 +513,7 @@ dkv_status launch(K* kernel, const PageParams& p, cudaStream_t s) {
 
 void set_workspace(PageParams& p, void* workspace) {
   char* w = static_cast<char*>(workspace);
-  p.sums = reinterpret_cast<int*>(w);
+  p.counts = reinterpret_cast<int*>(w);
   p.rows = reinterpret_cast<Row*>(w + ws_rows());
   p.live = reinterpret_cast<uint8_t*>(w + ws_live());
   p.dead = reinterpret_cast<uint8_t*>(w + ws_more(p.num_pages));
