@@ -890,7 +890,10 @@ class PagedKVCache(KVCache):
 
     kv_format "e2m1": 4-bit pools ([num_pages, Hkv, page_tokens * D * 9 // 16] uint8) for
     ``append`` and ``attend``, whose lengths, page table and slots are device tensors
-    (dkv_step_plan); ``k_pool`` and ``v_pool`` are the pools as pinned torch tensors."""
+    (dkv_step_plan); ``k_pool`` and ``v_pool`` are the pools as pinned torch tensors.
+    kv_format "e4m3_block": the same with E4M3 pools ([num_pages, Hkv, page_tokens, D]) and block scales, ``k_scales`` and
+    ``v_scales`` ([num_pages, Hkv, page_tokens // 16] fp32), which are CUDA tensors: they are read with every block.
+    ``pools`` are the tensors that dkv_pages_copy moves for a page of either."""
 
     def __init__(self, batch, n_kv_heads, head_dim, page_tokens, num_pages, max_pages_per_seq,
                  dtype="bf16", kv_format="native"):
@@ -898,26 +901,58 @@ class PagedKVCache(KVCache):
         self.page_tokens, self.num_pages, self.max_pages = page_tokens, num_pages, max_pages_per_seq
         self.S_max = page_tokens * max_pages_per_seq
         self.dtype, self.kv_format = dtype, kv_format
-        self.h = dkv_cache_alloc_ex(batch, n_kv_heads, head_dim, 0, dtype, kv_format, 1,
-                                    page_tokens, num_pages, max_pages_per_seq)
-        if kv_format == "e2m1":
+        blocks = kv_format == "e4m3_block"
+        if blocks and page_tokens % 16:
+            raise ValueError(f"pages of {page_tokens} tokens: blocks are 16")
+        # (the library's E4M3 cache without scales, whose projecting calls are refused here, has no fp16)
+        self.h = dkv_cache_alloc_ex(batch, n_kv_heads, head_dim, 0, "bf16" if blocks else dtype,
+                                    "e4m3" if blocks else kv_format, 1, page_tokens, num_pages, max_pages_per_seq)
+        self.k_pool = self.v_pool = self.k_scales = self.v_scales = None
+        if blocks or kv_format == "e2m1":
             import torch
-            self._views((num_pages, n_kv_heads, page_tokens * head_dim * 9 // 16))
+            self._views((num_pages, n_kv_heads, page_tokens, head_dim) if blocks else
+                        (num_pages, n_kv_heads, page_tokens * head_dim * 9 // 16))
             self.k_pool, self.v_pool = torch.from_numpy(self.k_host), torch.from_numpy(self.v_host)
+            if blocks:
+                self.k_scales, self.v_scales = (torch.ones((num_pages, n_kv_heads, page_tokens // 16), device="cuda")
+                                                for _ in "kv")
         else:
             self._views((num_pages, n_kv_heads, page_tokens, head_dim))
         self.table = np.full((batch, max_pages_per_seq), -1, np.int32)
 
     def append(self, q, k, v, positions, slots, q_out, **more):
-        """dkv_qkv_append into this E2M1 cache."""
-        dkv_qkv_append(q, k, v, positions, slots, self.k_pool, self.v_pool, q_out, **more)
+        """dkv_qkv_append into this E2M1 cache, dkv_block_append into one with block scales."""
+        if self.k_scales is not None:
+            dkv_block_append(q, k, v, positions, slots, self.k_pool, self.v_pool, self.k_scales, self.v_scales, q_out, **more)
+        else:
+            dkv_qkv_append(q, k, v, positions, slots, self.k_pool, self.v_pool, q_out, **more)
 
     def attend(self, q, page_table, kv_len, out, **more):
-        """dkv_paged_attend over this E2M1 cache."""
-        dkv_paged_attend(q, self.k_pool, self.v_pool, page_table, kv_len, out, **more)
+        """dkv_paged_attend over this E2M1 cache, dkv_block_attend over one with block scales."""
+        if self.k_scales is not None:
+            dkv_block_attend(q, self.k_pool, self.v_pool, self.k_scales, self.v_scales, page_table, kv_len, out, **more)
+        else:
+            dkv_paged_attend(q, self.k_pool, self.v_pool, page_table, kv_len, out, **more)
+
+    @property
+    def pools(self):
+        """What a page of this cache consists of, for dkv_pages_copy."""
+        return [t for t in (self.k_pool, self.v_pool, self.k_scales, self.v_scales) if t is not None]
+
+    def decode(self, *args, **more):
+        self._projects()
+        super().decode(*args, **more)
+
+    def prefill(self, *args, **more):
+        self._projects()
+        super().prefill(*args, **more)
+
+    def _projects(self):
+        if self.k_scales is not None:
+            raise DkvError(2, "PagedKVCache", "a cache with block scales is served by append and attend")
 
     def free(self):
-        self.k_pool = self.v_pool = None
+        self.k_pool = self.v_pool = self.k_scales = self.v_scales = None
         super().free()
 
     def set_page_table(self, table):
