@@ -738,7 +738,7 @@ dkv_status dkv_pages_compact(const int32_t* page_table, const int32_t* kv_len, i
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /* Page `to` of each pool's dst takes the bytes of page `from` of its src, for every {from, to} of pairs
- * [n_pairs][2] (device memory).  A pair with an index outside the pool is skipped.  src and dst may be one
+ * [n_pairs][2] (device memory; n_pairs may be 0).  A pair with an index outside the pool is skipped.  src and dst may be one
  * pool, or two of different sizes, in HBM or in pinned host memory (pages leave for the host, or come back).
  * No page may be `to` of two pairs, nor `to` of one and `from` of another in the same pool.
  * pools is host memory; up to 64 pools of one alignment go in one launch.

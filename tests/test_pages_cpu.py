@@ -99,7 +99,7 @@ def test_compact_refuses(L, change):
 
 
 @pytest.mark.parametrize("pairs,n,pools,count", [
-    (None, 4, (4096, 4096, 64, 8, 8), 1), (4096, 0, (4096, 4096, 64, 8, 8), 1), (4100, 4, (4096, 4096, 64, 8, 8), 1),
+    (None, 4, (4096, 4096, 64, 8, 8), 1), (4096, -1, (4096, 4096, 64, 8, 8), 1), (4100, 4, (4096, 4096, 64, 8, 8), 1),
     (4096, 4, None, 1), (4096, 4, (4096, 4096, 64, 8, 8), 0), (4096, 4, (0, 4096, 64, 8, 8), 1),
     (4096, 4, (4096, 0, 64, 8, 8), 1), (4096, 4, (4096, 4096, 0, 8, 8), 1), (4096, 4, (4096, 4096, 66, 8, 8), 1),
     (4096, 4, (4097, 4096, 64, 8, 8), 1), (4096, 4, (4096, 4098, 64, 8, 8), 1), (4096, 4, (4096, 4096, 64, 0, 8), 1),
@@ -108,6 +108,11 @@ def test_copy_refuses(L, pairs, n, pools, count):
     packed = ctypes.create_string_buffer(dkv._PAGE_POOL.pack(*pools)) if pools else None
     n = n if n < 1 << 31 else -(1 << 31)
     assert L.dkv_pages_copy(pairs, n, ctypes.addressof(packed) if packed else None, count, None) == 1
+
+
+def test_no_pairs_are_nothing_to_do(L):
+    packed = ctypes.create_string_buffer(dkv._PAGE_POOL.pack(4096, 4096, 64, 8, 8))
+    assert L.dkv_pages_copy(None, 0, ctypes.addressof(packed), 1, None) == 0
 
 
 def test_workspace(L):

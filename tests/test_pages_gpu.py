@@ -272,6 +272,47 @@ def test_captured_and_replayed_in_place():
             assert all(np.array_equal(rows(b, table, lengths), had[b]) for b in range(B))
 
 
+@pytest.mark.parametrize("op_name", ["fork", "compact"])
+def test_large_tables_in_a_graph(op_name):
+    """The launches of a large table captured, and replayed on inputs that change, workspace from the allocator."""
+    B, P, pages = 300, 16, 120_000
+    cases = [batch(s, B, P, 12_000, spare=400) for s in range(3)]
+    max_pages = cases[0][1].shape[1]
+    d = dict(table=i32(np.zeros((B, max_pages))), len=i32(np.zeros(B)), src=i32(np.zeros(B)), free=i32(np.full(pages, -1)),
+             count=i32([0]), out=i32(np.zeros((B, max_pages))), lo=i32(np.zeros(B)), left=i32([0]), copies=i32(np.zeros((B, 2))),
+             moves=i32(np.zeros((pages // 2, 2))), report=i32([0] * 4))
+
+    def call():
+        if op_name == "fork":
+            dkv.dkv_pages_fork(d["table"], d["len"], d["src"], d["free"], d["count"], P, d["out"], d["lo"], d["left"],
+                               d["copies"], d["report"])
+        else:
+            dkv.dkv_pages_compact(d["table"], d["len"], P, d["out"], d["free"], d["left"], d["moves"], d["report"])
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for s in (0, 1, 2, 0):
+        length, table, free, count = cases[s]
+        assert len(free) <= pages
+        src = sources(s, B, "mixed")
+        stack = np.full(pages, -1, np.int32)
+        stack[:count] = free[:count]
+        for k, v in (("table", table), ("len", length), ("src", src), ("free", stack), ("count", [count]), ("out", np.full_like(table, 77))):
+            d[k].copy_(i32(v))
+        graph.replay()
+        got = host(d)
+        if op_name == "fork":
+            want = op.fork(table, length, src, stack, count, P, np.full_like(table, 77))
+            assert np.array_equal(got["lo"], want["lengths"]) and np.array_equal(got["copies"], want["copies"])
+        else:
+            want = op.compact(table, length, pages, P, pages // 2, np.full_like(table, 77), stack)
+            assert np.array_equal(got["moves"], want["moves"])
+        assert np.array_equal(got["out"], want["table"]) and np.array_equal(got["free"], want["free"])
+        assert np.array_equal(got["report"], want["report"]) and got["left"][0] == want["free_left"]
+
+
 def test_streams_and_workspaces_from_the_allocator():
     """Many calls at once on two streams, workspaces from torch's allocator: each gives what it gives alone."""
     cases = [batch(s, 200, 16, 4000, spare=300) for s in range(4)]

@@ -580,8 +580,8 @@ extern "C" dkv_status dkv_pages_compact(const int32_t* page_table, const int32_t
 
 extern "C" dkv_status dkv_pages_copy(const int32_t* pairs, int n_pairs, const dkv_page_pool_t* pools, int n_pools,
                                      void* stream) {
-  if (!pairs || !pools) return refuse(DKV_ERR_INVALID_ARG, "null pointer argument");
-  if (n_pairs <= 0 || n_pairs > (1 << 30)) return refuse(DKV_ERR_INVALID_ARG, "pairs outside [1, 2^30]");
+  if ((!pairs && n_pairs) || !pools) return refuse(DKV_ERR_INVALID_ARG, "null pointer argument");
+  if (n_pairs < 0 || n_pairs > (1 << 30)) return refuse(DKV_ERR_INVALID_ARG, "pairs outside [0, 2^30]");
   if (n_pools <= 0 || n_pools > 65536) return refuse(DKV_ERR_INVALID_ARG, "pools outside [1, 65536]");
   if (reinterpret_cast<uintptr_t>(pairs) & 7) return refuse(DKV_ERR_INVALID_ARG, "the pairs must start on an 8-byte boundary");
   for (int i = 0; i < n_pools; ++i) {
@@ -593,6 +593,7 @@ extern "C" dkv_status dkv_pages_copy(const int32_t* pairs, int n_pairs, const dk
     if ((reinterpret_cast<uintptr_t>(a.src) | reinterpret_cast<uintptr_t>(a.dst)) & 3)
       return refuse(DKV_ERR_INVALID_ARG, "pools must start on 4-byte boundaries");
   }
+  if (!n_pairs) return DKV_OK;
   // Pages in words of 16 bytes first, then those that only have words of 4.
   for (int wide = 1; wide >= 0; --wide) {
     CopyParams p;
