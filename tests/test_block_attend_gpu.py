@@ -223,16 +223,27 @@ def test_masked_nan_does_not_leak(rows, D):
     check(c, out, lse)
 
 
-def test_nan_scales_of_later_tokens_do_not_leak():
-    """Blocks that the later rows of a chunk see and the earlier ones do not: their NaN scales reach the later ones alone."""
-    for rows, G in ((20, 1), (100, 2)):
-        c = case(12, [200], [rows], G, 1, 64, "fp16", 16)
-        clean, _ = run(c)
-        c["pools"][0][1][c["table"][0, 12]] = np.nan  # tokens 192 .. 199
-        got, want = host(run(c)[0]), host(clean)
-        first = 192 - (200 - rows)  # the first row that sees one
-        assert np.isnan(got[first:rows]).all()
-        assert np.array_equal(got[:first], want[:first])
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -1.0, 0.0])
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("rows,G,D", [(20, 1, 64), (12, 2, 128), (100, 2, 64), (70, 1, 128)])
+def test_scales_of_later_tokens_do_not_leak(rows, G, D, which, bad):
+    """Blocks that the later rows of a chunk see and the earlier ones do not: the earlier ones take nothing from their
+    scales, and a NaN reaches all the later ones.  (More than 32 packed rows: a tile with such a scale adds its weights up
+    block by block, so fp32 sums of at most 200 weights in another order, 200 * 2^-23 of lse; an output's quotient then
+    rounds to the same fp16 number or the one beside it, a step of 2^-10.)"""
+    c = case(12, [200], [rows], G, 1, D, "fp16", 16)
+    clean, low = run(c)
+    c["pools"][which][1][c["table"][0, 12]] = bad  # tokens 192 .. 199
+    got, lse = run(c)
+    first = 192 - (200 - rows)  # the first row that sees one
+    if np.isnan(bad):
+        assert torch.isnan(got[first:rows].float()).all()
+    if rows * G <= 32:
+        assert torch.equal(got[:first], clean[:first]) and torch.equal(lse[:first], low[:first])
+    else:
+        a, b = host(got)[:first], host(clean)[:first]
+        assert np.all(np.abs(a - b) <= 2.0 ** -10 * np.abs(b) + 2.0 ** -24)
+        assert np.all(np.abs(host(lse)[:first] - host(low)[:first]) <= 200 * 2.0 ** -23)
 
 
 @pytest.mark.parametrize("which,dim", [(0, 5), (1, 0), (1, 63), (1, 101)])
@@ -380,3 +391,20 @@ def test_offsets_past_32_bits():
             s[pages - n:] = dev(sc)
         moved = dict(c, table=c["table"] + np.int32(pages - n))
         check(c, *run(moved, pools=[*big, *scales]))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_waits_that_run_out(D):
+    """Outputs that are never signalled (a test hook): every wait of the many-row kernel ends, the rows and their lse are NaN,
+    and the next call is right."""
+    c = case(17, [700, 300], [90, 300], 4, 2, D, "bf16", 16)
+    want = run(c)
+    dkv.dkv_paged_attend_debug_withhold(True)
+    try:
+        out, lse = run(c)
+        torch.cuda.synchronize()
+    finally:
+        dkv.dkv_paged_attend_debug_withhold(False)
+    assert torch.isnan(out[:390].float()).all() and torch.isnan(lse[:390]).all() and (out[390:] == 7).all()
+    again = run(c)
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])

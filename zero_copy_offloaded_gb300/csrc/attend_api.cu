@@ -104,6 +104,8 @@ static dkv_status attend(const dkv_attend_t* a, Format format, const float* k_sc
     return refuse(DKV_ERR_INVALID_ARG, "num_pages must be positive, num_pages * page_tokens at most 2^30");
   if (a->max_pages <= 0 || (long long)a->max_pages * a->page_tokens > (1LL << 30))
     return refuse(DKV_ERR_INVALID_ARG, "max_pages must be positive, max_pages * page_tokens at most 2^30");
+  if (format == kE4M3 && (long long)a->num_pages * a->page_tokens / e4m3::kBlock * a->n_kv_heads >= 0xFFFFFFFFLL)
+    return refuse(DKV_ERR_INVALID_ARG, "a pool has fewer than 2^32 - 1 blocks");
   if (!aligned16(a->q) || !aligned16(a->k_pool) || !aligned16(a->v_pool) || !aligned16(a->out) ||
       (reinterpret_cast<uintptr_t>(a->workspace) & 255))
     return refuse(DKV_ERR_INVALID_ARG, "tensors must start on 16-byte boundaries, the workspace on 256");

@@ -606,8 +606,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<F, D, NT>::kPerSm) attend_kernel
         for (int nt = 0; nt < NT; ++nt) {
           const float p0 = tc::ex2_approx(s[nt][0] - m[nt][0]), p1 = tc::ex2_approx(s[nt][1] - m[nt][1]);
           const float p2 = tc::ex2_approx(s[nt][2] - m[nt][0]), p3 = tc::ex2_approx(s[nt][3] - m[nt][1]);
-          l[nt][0] = fmaf(p0 + p2, rvs, l[nt][0]);
-          l[nt][1] = fmaf(p1 + p3, rvs, l[nt][1]);
+          // (a row that sees nothing of the block takes nothing from its scale, whatever that is)
+          l[nt][0] = edge && p0 + p2 == 0.f ? l[nt][0] : fmaf(p0 + p2, rvs, l[nt][0]);
+          l[nt][1] = edge && p1 + p3 == 0.f ? l[nt][1] : fmaf(p1 + p3, rvs, l[nt][1]);
           pb[nt][0] = transpose8x8(tc::pack2<__half>(p0, p1));
           pb[nt][1] = transpose8x8(tc::pack2<__half>(p2, p3));
         }
