@@ -1,4 +1,4 @@
-// The paged attention over the 8-bit cache, few query rows.
+// The paged attention over the 8-bit cache with block scales, few query rows.
 #include "attend_few.cuh"
 
 namespace dkv {

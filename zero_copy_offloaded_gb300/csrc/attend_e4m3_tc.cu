@@ -1,4 +1,4 @@
-// The paged attention over the 8-bit cache, many query rows.
+// The paged attention over the 8-bit cache with block scales, many query rows.
 #include "attend_many.cuh"
 
 namespace dkv {

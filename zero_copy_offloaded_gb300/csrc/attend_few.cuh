@@ -1,5 +1,5 @@
-// dkv_paged_attend: softmax attention of ragged query rows over a paged cache
-// held in 4 bits (E2M1 codes, an E4M3 scale per 16 elements).
+// dkv_paged_attend and dkv_block_attend, few rows: softmax attention of ragged query rows over a paged cache held
+// in 4 bits (E2M1 codes, an E4M3 scale per 16 elements) or in 8 (E4M3 codes, a scale per 16 tokens and head).
 //
 // For query row i of sequence b (n_b rows, len_b cached keys, the rows' own keys
 // among them), query head h:
@@ -29,9 +29,16 @@
 // operand must be 16 bits: 2^-11 of a weight, and 2^-32 of the row's largest for
 // weights below 2^-21 of it (kBias); scores, references, sums and outputs stay in fp32.
 //
+// E4M3: the 16 keys of an MMA are one block, so its codes go to the tensor cores as they are (E4M3 in fp16, exact)
+// and its two scales are two numbers.  K's multiplies the fp32 scores.  V's joins the exponent: with
+//   x_j = s_j log2(e) + log2 vs_j,  o = sum 2^(x_j - m) c_j / sum 2^(x_j - m) / vs_j   (c_j the codes of V)
+// the fp16 weight is what the key adds to the outputs, whose bits it keeps whatever the scales are, and only the sum
+// takes the scale out again, in fp32.  A block costs no multiplication of its elements, where E2M1's scales are a half2
+// multiply for each pair.
+//
 // Why mma.sync here: tcgen05 takes at least 128 rows (or columns) a tile and its operands from
 // shared memory, so the converted keys would be written and read there once more.  Sixteen
-// rows of 32/8 heads over 16 x 8192 keys take 111 us in attend_e2m1_tc.cu's kernel, 58 here;
+// rows of 32/8 heads over 16 x 8192 keys take 111 us in attend_many.cuh's kernel, 58 here;
 // 32 rows 111 and 84 (heads of 64: 98 and 57); 33 rows and more, for whose outputs there
 // are no registers here, go there.
 //
@@ -45,6 +52,9 @@
 // a scheduler, 96 of them a warp's 32 keys at 24 rows, a quarter of the time that two
 // warps a scheduler need (20 rows over 16 x 8192 keys: 69 us); and a piece has a fixed cost, queries,
 // join of the warps and of the CTAs, of about 10000 cycles, near three of its tiles of 128 keys.
+// E4M3 reads 1 byte an element: the same 8 x 32769 keys (537 MB) take 97 to 100 us, 5.5 TB/s of 6.7, 4 x 131073 keys 183
+// (5.9); issue slots are 36 % busy, so that the warps mostly wait for copies that two steps a warp do not cover
+// (three steps leave room for two CTAs an SM: 98).
 #pragma once
 
 #include <float.h>

@@ -1,4 +1,4 @@
-// The 4-bit paged attention for many query rows, on the 5th-generation tensor cores.
+// dkv_paged_attend and dkv_block_attend, many rows: the same attention on the 5th-generation tensor cores.
 //
 // An item is (sequence, KV head, 256 query rows of that head's group, counted
 // token-major over the G heads): two tiles of 128 rows whose Q stays in shared memory
@@ -12,7 +12,7 @@
 // Warps (512 threads, one CTA per SM): two softmax groups of four warps, one per Q tile,
 // a thread to a row; six warps that turn codes into fp16 tiles (1.64 ms against 1.67 with four);
 // one that issues every MMA; one that fetches the codes (bulk copies, a run of 16 keys
-// each).  The MMA order per key tile is P.V and the next Q.K^T of tile 0, then of tile 1,
+// each; of E4M3 a seventh that converts, each with its own loads).  The MMA order per key tile is P.V and the next Q.K^T of tile 0, then of tile 1,
 // so one tile's softmax runs under the other tile's MMAs, and a finished Q.K^T also says
 // that the P.V before it is finished: O may be rescaled then without a barrier of its own.
 //
@@ -35,6 +35,15 @@
 // (192 KB a key tile) and the converted tiles (64 KB) share.  Tensor memory is full (S and O of two
 // tiles), which rules out a third tile and a Q in tensor memory.  Exponentials as degree-4 polynomials
 // on the FMA pipe do not help (five of sixteen: 2.20 ms against 1.86).
+//
+// E4M3: a tile's blocks have scales of their own, and the MMAs see one tile.  So each is split: what the append
+// writes are powers of two, and the ratio of a block's scale to that of its piece's first block goes into the converted
+// codes (fp16 holds a code times 2^-15 .. 2^7 exactly), while the first block's own multiplies the scores or the outputs.
+// A ratio outside, or no power of two, stays with the block: the softmax of a tile that has one multiplies its scores
+// by it, or adds log2 of it (V) to them and divides the sum.  With the blocks' scales in the softmax of every tile the
+// chunk above takes 2.15 ms, this way 1.63 to 1.68 (1250 TFLOP/s).  Codes come from memory into registers: a ring of 8-bit
+// tiles in shared memory leaves its bandwidth short (2.12 ms and more).  The conversion and its bookkeeping are about
+// a fifth of the instructions.
 //
 // Every item reads its keys, so a pool is read once for each 256 packed rows.  From HBM that is hidden;
 // a pool in host memory crosses the link as often (4096 rows of 32/8 heads over 28672 keys: 10.8 ms).
@@ -779,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         __syncwarp();
       };
       // The factor that codes are multiplied by, as an fp16 pair, and what is left of the scale: all of scale / ref
-      // where that is a power of two from 2^-15 to 2^7, which fp16 takes exactly (but for codes below 2^-24).
+      // where that is a power of two from 2^-15 to 2^7, which fp16 takes exactly (codes are multiples of 2^-9 up to 448).
       auto split = [](float ratio, float& rest) {
         const uint32_t bits = __float_as_uint(ratio);
         const int up = (int)(bits >> 23) - 127;
