@@ -109,6 +109,41 @@ def test_append(lens, Hq, Hkv, D, dtype, P, rot, inter, norm):
     check(q, k, v, slot, pos, table, filled(4, pages, Hkv, P, D), inter, norm, dtype=dtype)
 
 
+@pytest.mark.parametrize("Hkv,D,dtype,norm", [(1, 128, "bf16", True), (3, 128, "fp16", True), (3, 64, "bf16", False)])
+@pytest.mark.parametrize("mix", ["single", "few", "all"])
+def test_long_calls_of_short_blocks(mix, Hkv, D, dtype, norm):
+    """4096 rows and more, in blocks of one row, of a few, of all counts beside one another."""
+    rng = np.random.default_rng(21)
+    lens = {"single": [1] * 4200, "few": list(rng.integers(1, 9, 1000)),
+            "all": list(rng.permutation([1] * 600 + [5, 6, 7, 8] * 90 + [16, 17, 40] * 9 + [900]))}[mix]
+    slot, pages = slots_of(22, [int(n) for n in lens], 16)
+    N = len(slot)
+    assert N >= 4096
+    _, k, v = rows_of(23, N, 1, Hkv, D, dtype)
+    pos = rng.integers(0, 500, N).astype(np.int32)
+    table = dkv.rope_table(500, 32, device="cpu").numpy()
+    check(None, k, v, slot, pos, table, filled(24, pages, Hkv, 16, D), norm=norm, dtype=dtype, outs=mix == "all")
+
+
+@pytest.mark.parametrize("D,dtype,norm", [(64, "bf16", False), (64, "fp16", True), (128, "bf16", True)])
+def test_every_operation_rounds_once(D, dtype, norm):
+    """Millions of keys, each row a block of its own: one rounding more or less on the way moves some code across a border."""
+    N, Hkv = 4200, 33
+    _, k, v = rows_of(25, N, 1, Hkv, D, dtype, spread=0.3)
+    pos = np.random.default_rng(26).integers(0, 500, N).astype(np.int32)
+    table = dkv.rope_table(500, D, device="cpu").numpy()
+    gk = torch.from_numpy((1 + 0.2 * np.random.default_rng(9).standard_normal(D)).astype(np.float32)).to(k.dtype).cuda() if norm else None
+    code = [torch.zeros((N, Hkv, 16, D), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    sc = [torch.zeros((N, Hkv, 1), device="cuda") for _ in "kv"]
+    slot = 16 * np.arange(N, dtype=np.int32)
+    dkv.dkv_block_append(None, k, v, i32(pos), i32(slot), *code, *sc, k_gamma=gk, eps=2.0 ** -20, cos_sin=dev(table))
+    f = lambda t: None if t is None else t.float().cpu().numpy()  # noqa: E731
+    for c, s, y in zip(code, sc, (step.turn(f(k), f(gk), 2.0 ** -20, table, pos, False)[0], f(v))):
+        want = bs.scale_for(np.abs(y).max(-1))
+        assert np.array_equal(s.cpu().numpy()[..., 0], want.astype(np.float32))
+        assert np.array_equal(c[:, :, 0].cpu().numpy(), bs.encode(y / want[..., None]))
+
+
 @pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "fp16")])
 def test_token_by_token_is_the_chunk(D, dtype):
     """40 tokens one call each, into blocks that grow: with powers of two the same bytes as the oracle's at every call, and

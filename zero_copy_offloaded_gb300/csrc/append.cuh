@@ -85,13 +85,45 @@ __device__ __forceinline__ uint2 pack4(const float* x) {
   return make_uint2(tc::pack2<T>(x[0], x[1]), tc::pack2<T>(x[2], x[3]));
 }
 
+// Two fp32 operations an instruction: a - b, and two_sum, of which b may be a product that is exact in fp32.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 f2_sub(f32x2 a, f32x2 b) { return tc::f2_fma(b, tc::f2_pack(-1.f, -1.f), a); }
+__device__ __forceinline__ void two_sum2(f32x2& s, f32x2& e, f32x2 b) {
+  const f32x2 t = tc::f2_add(s, b), z = f2_sub(t, s);
+  e = tc::f2_add(e, tc::f2_add(f2_sub(s, f2_sub(t, z)), f2_sub(b, z)));
+  s = t;
+}
+
+// How a row's squares are added up: in fp32, in two words, in two words for each half of the elements.
+enum Sum : int { kPlain, kExact, kExactPairs };
+
 // x (8 elements of a row held by LPR lanes) times the row's 1 / rms and the norm weights.
-template <int LPR, bool EXACT>
+template <int LPR, Sum SUM>
 __device__ __forceinline__ void norm_row(float (&x)[8], const float (&g)[8], float eps) {
+  constexpr bool EXACT = SUM != kPlain;
   float hi = 0.f, lo = 0.f;
   if constexpr (EXACT) {
+    if constexpr (SUM == kExactPairs) {
+      f32x2 s, e;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) two_sum(hi, lo, __fmul_rn(x[e], x[e]));
+      for (int i = 0; i < 4; ++i) {
+        const f32x2 v = tc::f2_pack(x[2 * i], x[2 * i + 1]), sq = tc::f2_mul(v, v);
+        if (i) {
+          two_sum2(s, e, sq);
+        } else {
+          s = sq;
+          e = 0;
+        }
+      }
+      float oh, ol;
+      tc::f2_unpack(s, hi, oh);
+      tc::f2_unpack(e, lo, ol);
+      two_sum(hi, lo, oh);
+      lo = __fadd_rn(lo, ol);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) two_sum(hi, lo, __fmul_rn(x[e], x[e]));
+    }
 #pragma unroll
     for (int d = 1; d < LPR; d <<= 1) {
       const float oh = __shfl_xor_sync(~0u, hi, d), ol = __shfl_xor_sync(~0u, lo, d);
@@ -115,8 +147,41 @@ __device__ __forceinline__ void norm_row(float (&x)[8], const float (&g)[8], flo
     const float wide = inv_rms_wide<LPR>(x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7], eps);
     if (r == 0.f) r = wide;
   }
+  const f32x2 r2 = tc::f2_pack(r, r);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = __fmul_rn(__fmul_rn(x[e], r), g[e]);
+  for (int e = 0; e < 8; e += 2)
+    tc::f2_unpack(tc::f2_mul(tc::f2_mul(tc::f2_pack(x[e], x[e + 1]), r2), tc::f2_pack(g[e], g[e + 1])), x[e], x[e + 1]);
+}
+
+// (a, b) <- (a c - b s, b c + a s) of four pairs: elements e and 4 + e, or (INTER) 2 e and 2 e + 1.  The products take two
+// elements an instruction; an add.rn.f32x2 of them becomes an FMA, whose product is not rounded (a quarter of the sums
+// differ), so that the sums take one.
+template <bool INTER>
+__device__ __forceinline__ void rotate(float (&x)[8], const float* c, const float* s) {
+  if constexpr (INTER) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float &a = x[2 * e], &b = x[2 * e + 1];
+      const float ra = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
+      b = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
+      a = ra;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const f32x2 a = tc::f2_pack(x[e], x[e + 1]), b = tc::f2_pack(x[4 + e], x[5 + e]);
+      const f32x2 c2 = tc::f2_pack(c[e], c[e + 1]), s2 = tc::f2_pack(s[e], s[e + 1]);
+      float u[2], v[2];
+      tc::f2_unpack(tc::f2_mul(a, c2), u[0], u[1]);
+      tc::f2_unpack(tc::f2_mul(b, s2), v[0], v[1]);
+      x[e] = __fsub_rn(u[0], v[0]);
+      x[e + 1] = __fsub_rn(u[1], v[1]);
+      tc::f2_unpack(tc::f2_mul(b, c2), u[0], u[1]);
+      tc::f2_unpack(tc::f2_mul(a, s2), v[0], v[1]);
+      x[4 + e] = __fadd_rn(u[0], v[0]);
+      x[5 + e] = __fadd_rn(u[1], v[1]);
+    }
+  }
 }
 
 // y / s for s whose correctly rounded reciprocal is r: the quotient's residual is exact in one fused
@@ -243,7 +308,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int h
       float x[8];
       unpack4<T>(w[i][0], x);
       unpack4<T>(w[i][1], x + 4);
-      if (norm) norm_row<LPR, KIND == kKey>(x, g, p.eps);
+      if (norm) norm_row<LPR, KIND == kKey ? kExact : kPlain>(x, g, p.eps);
       if constexpr (KIND == kKey && !INTER) {
         if (p.pos) {
 #pragma unroll
@@ -254,15 +319,7 @@ __device__ __forceinline__ void append_rows(const AppendParams& p, int h0, int h
           }
         }
       } else if constexpr (KIND != kValue) {
-        if (turn) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float &a = INTER ? x[2 * e] : x[e], &b = INTER ? x[2 * e + 1] : x[4 + e];
-            const float ra = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
-            b = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
-            a = ra;
-          }
-        }
+        if (turn) rotate<INTER>(x, c, s);
       }
       if (KIND != kValue && far) {
 #pragma unroll

@@ -7,15 +7,15 @@
 // are brought to the new scale, code <- e4m3(code * old / s); new rows are e4m3(y / s).  Scales are powers of two so that
 // the quotients are exact: a code rounds once, and again only in E4M3's subnormals when its block's scale grows.
 //
-// One or two warps take the rows of one block and head together (16 at most, all loads in flight, their fp32 values in
+// One to four warps take the rows of one block and head together (16 at most, all loads in flight, their fp32 values in
 // registers until the largest of them is known), so that the scale needs no second pass and no atomics; blocks that a
 // call gives few rows go to a warp of several heads.  The rows of a block lie within 16 consecutive rows of the call; a
 // warp looks at 16 tokens and takes the blocks whose rows begin there.
 //
-// What bounds it: 20 KB a row of 32/8 heads of 128, 4096 of them 14 us at the measured copy rate; they take 27.6, of which
-// queries alone 18.  Neither memory nor a pipe is full: the warps wait for chains of scalar fp32 (the keys' exact sums of
-// squares, the 32 values a lane that have to live until the block's largest is known) and for instructions, of
-// which the unrolled rows have many.
+// What bounds it: 23 KB a row of 32/8 heads of 128, 4096 of them 14 us at the measured copy rate; they take 26.6, of which
+// queries alone 17.4, keys and values alone 16.8.  Neither memory nor a pipe is full: the warps wait for chains of fp32 (the keys'
+// exact sums of squares, the values that have to live until the block's largest is known) and for instructions, of
+// which the unrolled rows have many.  Sums, norms and rotations take two elements an instruction where they can.
 #include "append.cuh"
 #include "e4m3.cuh"
 
@@ -25,13 +25,13 @@ using namespace dkv;
 
 constexpr int kThreads = kAppendThreads, kWarps = kThreads / 32;
 
-constexpr int kUnit = 16;    // tokens that a warp of a long call looks at for blocks that begin there
-// Blocks that a call gives at most kShort rows go to warps that take one token of several heads (append_tokens), the others to
-// warps that take all of a block's rows (append_blocks).  Which is which is seen on the device, so both are launched,
-// but for calls of kLong rows and more, whose sequences (at most DKV_MAX_STEP_BATCH from one plan) have four
-// rows or more on average: there the second take them all.
-// 64 sequences' five rows each: 7.6 us with 6, 16.8 with 4; 512 single rows 8 us so, 55 by block; one sequence's 1024
-// rows 11.4 us by block, 27 by token.
+constexpr int kUnit = 16;    // tokens that append_blocks' warps look at together for blocks that begin there
+constexpr int kLook = kWarps * e4m3::kBlock;  // and a CTA of append_tokens in long calls
+// Blocks that a call gives at most kShort rows go to warps that take one block of several heads (append_tokens), the others to
+// warps that take all of a block's rows (append_blocks).  Which is which is seen on the device, so both are launched.
+// 64 sequences' five rows each: 7.6 us with 6, 16.8 with 4; 512 single rows 9 us so, 55 by block; one sequence's 1024
+// rows 11.4 us by block, 27 by token.  Calls of kLong rows and more look for short blocks with a warp for 16 tokens, not
+// one for each: 4096 rows of one sequence 26.6 us, about 35 with a warp each; 4096 single rows 39 us, by block 179.
 constexpr int kShort = 6, kLong = 4096;
 
 struct BlockParams {
@@ -40,8 +40,8 @@ struct BlockParams {
   float* v_scales;
   // CTAs of keys, and of values: by block, by token; of queries
   int block_ctas, token_ctas, q_ctas;
-  int least;  // rows of a block that append_blocks takes
-  int heads;  // of a unit of its
+  int heads;  // of a unit of append_blocks
+  int span;   // groups of heads of a unit of append_tokens, 0: short calls, whose units are a token and a group
 };
 
 // The block of a slot; -1: padding.
@@ -49,10 +49,10 @@ __device__ __forceinline__ int block_of(const AppendParams& p, int slot) {
   return slot < 0 || slot >= p.slots ? -1 : slot / e4m3::kBlock;
 }
 
-// max(|a|, |b|), NaN if either is one.
-__device__ __forceinline__ float max_abs(float a, float b) {
+// max(|a|, |b|, |c|), NaN if one of them is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
   float r;
-  asm("{\n\t.reg .f32 a, b;\n\tabs.f32 a, %1;\n\tabs.f32 b, %2;\n\tmax.NaN.f32 %0, a, b;\n\t}" : "=f"(r) : "f"(a), "f"(b));
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(fabsf(a)), "f"(fabsf(b)), "f"(fabsf(c)));
   return r;
 }
 // NaN for what is not finite (an infinity too: E4M3 has none), and the largest size of what is.
@@ -89,10 +89,11 @@ __device__ __forceinline__ void store_row(uint8_t* to, T* out, uint2 c, float s,
   *reinterpret_cast<uint2*>(out + off1) = pack4<T>(y + 4);
 }
 
-// Warps that share a run: with heads of 128 two of eight rows each, so that a lane holds 32 fp32 values (with one warp, 64
-// values and two CTAs an SM instead of three, 4096 rows of 32/8 heads take 38.7 us).
+// Warps that share a run: with heads of 128 four of four rows each, so that a lane holds 16 fp32 values (4096 rows of 32/8 heads
+// 26.6 us; with two warps 27 to 28, with one and two CTAs an SM instead of three 38.7).  Of 64 one (16384 rows of 32 heads
+// 88 us, 103 with two: what a warp does once for a run counts more).
 template <int D>
-constexpr int kShare = D == 128 ? 2 : 1;
+constexpr int kShare = D == 128 ? 4 : 1;
 
 // The rows t0 .. t0 + 15 of heads h0 .. h1 - 1 that lie in block `block` of the pool, row t0 among them.  The warps that
 // share it come here together; `turn` alternates between the heads that they take.  (Loading the next head's rows
@@ -102,7 +103,7 @@ __device__ __forceinline__ void append_run(const BlockParams& bp, int h0, int h1
   constexpr int LPR = D / 8, RPW = 32 / LPR, SH = kShare<D>, ITER = e4m3::kBlock / RPW / SH;
   constexpr bool PAIRED = KIND == kKey && !INTER;  // a lane holds both partners of its pairs
   const AppendParams& p = bp.a;
-  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR, part = SH == 2 ? (threadIdx.x >> 5) & 1 : 0;
+  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR, part = (threadIdx.x >> 5) % SH;
   const float nan = __int_as_float(0x7fc00000);
   const int half = p.rot / 2;
   const bool in_rot = KIND == kKey && p.pos && l * 8 < p.rot;
@@ -112,7 +113,7 @@ __device__ __forceinline__ void append_run(const BlockParams& bp, int h0, int h1
   const bool in = lane < e4m3::kBlock && t0 + lane < p.N;
   const int slot_l = in ? __ldg(p.slot + t0 + lane) : -1, pos_l = KIND == kKey && p.pos && in ? __ldg(p.pos + t0 + lane) : 0;
   const uint32_t members = __ballot_sync(~0u, in && block_of(p, slot_l) == block);
-  if (__popc(members) < bp.least) return;
+  if (__popc(members) <= kShort) return;
   auto member = [&](int i) { return (members >> row_of(i)) & 1; };
   // the block's rows that this run writes
   const uint32_t rows = __reduce_or_sync(~0u, (members >> lane) & 1 ? 1u << (slot_l & (e4m3::kBlock - 1)) : 0u);
@@ -184,23 +185,15 @@ __device__ __forceinline__ void append_run(const BlockParams& bp, int h0, int h1
         const float s[4] = {ahead[1].x, ahead[1].y, ahead[1].z, ahead[1].w};
         const bool far = ahead_far;
         if (p.pos && i + 1 < ITER) angles(i + 1);
-        if (gam) norm_row<LPR, true>(x[i], g, p.eps);
-        if (in_rot) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float &a = INTER ? x[i][2 * e] : x[i][e], &b = INTER ? x[i][2 * e + 1] : x[i][4 + e];
-            const float ra = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
-            b = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
-            a = ra;
-          }
-        }
+        if (gam) norm_row<LPR, kExactPairs>(x[i], g, p.eps);
+        if (in_rot) rotate<INTER>(x[i], c, s);
         if (far) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[i][e] = nan;
         }
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) most = max_abs(most, x[i][e]);
+      for (int e = 0; e < 8; e += 2) most = max_abs(most, x[i][e], x[i][e + 1]);
     }
     if (__any_sync(~0u, !(most <= FLT_MAX))) {
       most = 0.f;
@@ -209,11 +202,13 @@ __device__ __forceinline__ void append_run(const BlockParams& bp, int h0, int h1
     }
     uint32_t top = __float_as_uint(most);
     top = __reduce_max_sync(~0u, top);
-    if constexpr (SH == 2) {  // of the two, who also have both read `old` behind this
-      uint32_t* mine = s_top + 2 * ((threadIdx.x >> 6) * 2 + turn);
+    if constexpr (SH > 1) {  // of all of them, who also have read `old` behind this
+      const int team = threadIdx.x / (32 * SH);
+      uint32_t* mine = s_top + SH * (team * 2 + turn);
       if (lane == 0) mine[part] = top;
-      named_bar_sync(1 + (threadIdx.x >> 6), 64);
-      top = max(mine[0], mine[1]);
+      named_bar_sync(1 + team, 32 * SH);
+#pragma unroll
+      for (int i = 0; i < SH; ++i) top = max(top, mine[i]);
     }
     const float need = e4m3::scale_for(top), s = fmaxf(need, had);
     if (s > had && had > 0.f) {  // the rows already there, to the new scale
@@ -264,6 +259,142 @@ __device__ __forceinline__ void append_run(const BlockParams& bp, int h0, int h1
   }
 }
 
+// The rows of the block that begins at token t, where they are kShort at most, of as many heads from h0 on (below h1) as a warp has
+// groups of D / 8 lanes, one to a group: it goes over the rows twice (once for one row).
+template <typename T, int D, bool INTER, int KIND>
+__device__ __forceinline__ void append_few(const BlockParams& bp, int t, int h0, int h1) {
+  constexpr int LPR = D / 8;
+  constexpr bool PAIRED = KIND == kKey && !INTER;
+  const AppendParams& p = bp.a;
+  const int lane = threadIdx.x & 31, l = lane % LPR, h = h0 + lane / LPR;
+  const bool active = h < h1;
+  const float nan = __int_as_float(0x7fc00000);
+  const int half = p.rot / 2;
+  const bool in_rot = KIND == kKey && p.pos && l * 8 < p.rot;
+  const int off0 = PAIRED && in_rot ? 4 * l : 8 * l, off1 = PAIRED && in_rot ? half + 4 * l : 8 * l + 4;
+  const T* gam = static_cast<const T*>(KIND == kKey ? p.k_gamma : nullptr);
+  const long long stride = KIND == kKey ? p.ks : p.vs;
+  const int per_page = 1 << (p.page_shift - 4);
+  T* out = static_cast<T*>(KIND == kKey ? p.k_out : p.v_out);
+  float g[8];
+  if (KIND == kKey && gam) {
+    unpack4<T>(__ldg(reinterpret_cast<const uint2*>(gam + off0)), g);
+    unpack4<T>(__ldg(reinterpret_cast<const uint2*>(gam + off1)), g + 4);
+  }
+  // lane i: slot and position of token t + i, from 16 on of token t - 31 + i
+  const int token = lane < e4m3::kBlock ? t + lane : t - 31 + lane;
+  const bool in = token >= 0 && token < p.N && lane < 31;
+  const int slot_l = in ? __ldg(p.slot + token) : -1, pos_l = KIND == kKey && p.pos && in ? __ldg(p.pos + token) : 0;
+  const T* src = static_cast<const T*>(KIND == kKey ? p.k : p.v) + (size_t)t * stride + (size_t)h * D;
+  uint2 w[2];
+  auto load = [&](int r) {
+    w[0] = w[1] = make_uint2(0, 0);
+    if (!active) return;
+    const T* row = src + (size_t)r * stride;
+    if constexpr (PAIRED) {
+      w[0] = *reinterpret_cast<const uint2*>(row + off0);
+      w[1] = *reinterpret_cast<const uint2*>(row + off1);
+    } else {
+      const uint4 v = *reinterpret_cast<const uint4*>(row + l * 8);
+      w[0] = make_uint2(v.x, v.y);
+      w[1] = make_uint2(v.z, v.w);
+    }
+  };
+  load(0);
+  const int block = block_of(p, __shfl_sync(~0u, slot_l, 0));
+  const uint32_t same = __ballot_sync(~0u, in && block_of(p, slot_l) == block);
+  // padding, or the block's rows began before, or there are too many
+  if (block < 0 || same >> e4m3::kBlock || __popc(same) > kShort) return;
+  const uint32_t rows = __reduce_or_sync(~0u, (same >> lane) & 1 ? 1u << (slot_l & (e4m3::kBlock - 1)) : 0u);
+  const int page = block >> (p.page_shift - 4);
+  const size_t head = (size_t)page * p.Hkv + (active ? h : 0);
+  float* scale = (KIND == kKey ? bp.k_scales : bp.v_scales) + head * per_page + (block & (per_page - 1));
+  uint8_t* codes = (KIND == kKey ? p.k_pool : p.v_pool) +
+                   ((head << p.page_shift) + (block & (per_page - 1)) * e4m3::kBlock) * D;
+  float old = *scale;
+  if ((rows & 1) || !(old > 0.f && old <= FLT_MAX)) old = 0.f;
+  float x[8];
+  // Row r from w, and the row after it on its way into w.
+  auto row = [&](int r, int next) {
+    unpack4<T>(w[0], x);
+    unpack4<T>(w[1], x + 4);
+    const int pos = __shfl_sync(~0u, pos_l, r);
+    const bool far = KIND == kKey && p.pos && (pos < 0 || pos >= p.max_pos);
+    float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (in_rot && !far) {
+      const float* from = p.cos_sin + (size_t)pos * p.rot + 4 * l;
+      c4 = __ldg(reinterpret_cast<const float4*>(from));
+      s4 = __ldg(reinterpret_cast<const float4*>(from + half));
+    }
+    if (next >= 0) load(next);
+    if constexpr (KIND == kKey) {
+      if (gam) norm_row<LPR, kExactPairs>(x, g, p.eps);
+      if (in_rot) {
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+        rotate<INTER>(x, c, s);
+      }
+    }
+    if (far) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = nan;
+    }
+    float most = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) most = max_abs(most, x[e], x[e + 1]);
+    if (!(most <= FLT_MAX)) most = odd_values(x);
+    return __float_as_uint(most);
+  };
+  auto next_row = [&](int r) { return __ffs(same >> r >> 1) + r; };          // r: none (31 - clz below: -1)
+  auto previous_row = [&](int r) { return 31 - __clz(same & ((1u << r) - 1)); };
+  const int last = 31 - __clz(same);
+  uint32_t top = 0;
+#pragma unroll 1
+  for (int r = 0;; r = next_row(r)) {
+    top = max(top, row(r, r < last ? next_row(r) : previous_row(r)));
+    if (r == last) break;
+  }
+#pragma unroll
+  for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
+  const float s = fmaxf(e4m3::scale_for(top), old);
+  if (active && s > old && old > 0.f) {  // the rows already there, to the new scale
+    const float f = __fdiv_rn(old, s);
+#pragma unroll 1
+    for (int piece = l; piece < D; piece += LPR) {
+      if ((rows >> (piece * 16 / D)) & 1) continue;
+      uint32_t u4[4];
+      uint4* to = reinterpret_cast<uint4*>(codes) + piece;
+      *reinterpret_cast<uint4*>(u4) = *to;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t a2 = e4m3::lo_to_h2(u4[q]), b2 = e4m3::hi_to_h2(u4[q]);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&a2));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&b2));
+        u4[q] = e4m3::to_codes(__fmul_rn(a.x, f), __fmul_rn(a.y, f), __fmul_rn(b.x, f), __fmul_rn(b.y, f));
+      }
+      *to = *reinterpret_cast<const uint4*>(u4);
+    }
+  }
+  if (active && l == 0 && s != old) *scale = s;
+  const bool exact = !(__float_as_uint(s) & 0x7fffffu);
+  const float inv = __frcp_rn(s);
+#pragma unroll 1
+  for (int r = last; r >= 0; r = previous_row(r)) {  // the last row is at hand
+    if (r < last) row(r, previous_row(r));
+    const int slot = __shfl_sync(~0u, slot_l, r);
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(x[e], inv);
+    if (!exact) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = __fdiv_rn(x[e], s);
+    }
+    const uint2 c = make_uint2(e4m3::to_codes(y[0], y[1], y[2], y[3]), e4m3::to_codes(y[4], y[5], y[6], y[7]));
+    if (!active) continue;
+    store_row<T, D, PAIRED>(codes + (slot & (e4m3::kBlock - 1)) * D, out ? out + ((size_t)(t + r) * p.Hkv + h) * D : nullptr,
+                            c, s, off0, off1, l);
+  }
+}
+
 template <typename T, int D, bool INTER, int KIND>
 __device__ __forceinline__ void append_blocks(const BlockParams& bp, int cta, uint32_t* s_top) {
   constexpr int kTeams = kWarps / kShare<D>;
@@ -278,171 +409,69 @@ __device__ __forceinline__ void append_blocks(const BlockParams& bp, int cta, ui
     const int mine = token >= 0 && token < p.N ? block_of(p, __ldg(p.slot + token)) : -1;
     const uint32_t same = __match_any_sync(~0u, mine), before = ((1u << lane) - 1) & ~((1u << lane >> 15) - 1);
     uint32_t heads = __ballot_sync(~0u, mine >= 0 && !(same & before)) >> kUnit;
+    const int end = min(h + bp.heads, p.Hkv);
     while (heads) {
       const int at = __ffs(heads) - 1;
       heads &= heads - 1;
-      append_run<T, D, INTER, KIND>(bp, h, min(h + bp.heads, p.Hkv), first + at, __shfl_sync(~0u, mine, kUnit + at), s_top, turn);
+      append_run<T, D, INTER, KIND>(bp, h, end, first + at, __shfl_sync(~0u, mine, kUnit + at), s_top, turn);
     }
   }
 }
 
-// The same for short calls, where most blocks get one row or a few: a warp takes a token and as many heads as it has groups
-// of D / 8 lanes, one head to a group, and goes over the block's rows twice (once for one row).
+// All such blocks.  Short calls, where most are: a warp takes a token.  Long ones: the warps of a CTA look for them among kLook
+// tokens, 16 each, and share what they find.
 template <typename T, int D, bool INTER, int KIND>
-__device__ __forceinline__ void append_tokens(const BlockParams& bp, int cta) {
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  constexpr bool PAIRED = KIND == kKey && !INTER;
+__device__ __forceinline__ void append_tokens(const BlockParams& bp, int cta, uint32_t* s_todo) {
+  constexpr int RPW = 256 / D;
   const AppendParams& p = bp.a;
-  const int lane = threadIdx.x & 31, l = lane % LPR, sub = lane / LPR;
-  const float nan = __int_as_float(0x7fc00000);
-  const int half = p.rot / 2;
-  const bool in_rot = KIND == kKey && p.pos && l * 8 < p.rot;
-  const int off0 = PAIRED && in_rot ? 4 * l : 8 * l, off1 = PAIRED && in_rot ? half + 4 * l : 8 * l + 4;
-  const T* gam = static_cast<const T*>(KIND == kKey ? p.k_gamma : nullptr);
-  const long long stride = KIND == kKey ? p.ks : p.vs;
-  const int groups = (p.Hkv + RPW - 1) / RPW, per_page = 1 << (p.page_shift - 4);
-  T* out = static_cast<T*>(KIND == kKey ? p.k_out : p.v_out);
-  float g[8];
-  if (KIND == kKey && gam) {
-    unpack4<T>(__ldg(reinterpret_cast<const uint2*>(gam + off0)), g);
-    unpack4<T>(__ldg(reinterpret_cast<const uint2*>(gam + off1)), g + 4);
+  const int groups = (p.Hkv + RPW - 1) / RPW, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!bp.span) {
+    for (int u = cta * kWarps + warp; u < p.N * groups; u += bp.token_ctas * kWarps) {
+      const int t = u / groups;
+      append_few<T, D, INTER, KIND>(bp, t, (u - t * groups) * RPW, p.Hkv);
+    }
+    return;
   }
-  for (int u = cta * kWarps + (threadIdx.x >> 5); u < p.N * groups; u += bp.token_ctas * kWarps) {
-    const int t = u / groups, h = (u - t * groups) * RPW + sub;
-    const bool active = h < p.Hkv;
-    // lane i: slot and position of token t + i, from 16 on of token t - 31 + i
-    const int token = lane < e4m3::kBlock ? t + lane : t - 31 + lane;
-    const bool in = token >= 0 && token < p.N && lane < 31;
-    const int slot_l = in ? __ldg(p.slot + token) : -1, pos_l = KIND == kKey && p.pos && in ? __ldg(p.pos + token) : 0;
-    const T* src = static_cast<const T*>(KIND == kKey ? p.k : p.v) + (size_t)t * stride + (size_t)h * D;
-    uint2 w[2];
-    auto load = [&](int r) {
-      w[0] = w[1] = make_uint2(0, 0);
-      if (!active) return;
-      const T* row = src + (size_t)r * stride;
-      if constexpr (PAIRED) {
-        w[0] = *reinterpret_cast<const uint2*>(row + off0);
-        w[1] = *reinterpret_cast<const uint2*>(row + off1);
-      } else {
-        const uint4 v = *reinterpret_cast<const uint4*>(row + l * 8);
-        w[0] = make_uint2(v.x, v.y);
-        w[1] = make_uint2(v.z, v.w);
+  const int spans = (groups + bp.span - 1) / bp.span, units = (p.N + kLook - 1) / kLook * spans;
+  for (int u = cta; u < units; u += bp.token_ctas) {
+    const int first = u / spans * kLook, from = (u - u / spans * spans) * bp.span, n = min(bp.span, groups - from);
+    // lane i: the blocks of tokens at - 16 + i and at + i
+    const int at = first + warp * e4m3::kBlock, token = at + lane;
+    const int old = token >= e4m3::kBlock && token - e4m3::kBlock < p.N ? block_of(p, __ldg(p.slot + token - e4m3::kBlock)) : -1;
+    const int now = token < p.N ? block_of(p, __ldg(p.slot + token)) : -1;
+    const uint32_t same = __match_any_sync(~0u, old), before = ((1u << lane) - 1) & ~((1u << lane >> 15) - 1);
+    const uint32_t starts = __ballot_sync(~0u, old >= 0 && !(same & before)) >> e4m3::kBlock;
+    const uint32_t rows = __match_any_sync(~0u, now) & 0xffffu << lane;
+    const uint32_t todo = __ballot_sync(~0u, lane < e4m3::kBlock && (starts >> lane & 1) && __popc(rows) <= kShort);
+    if (lane == 0) s_todo[warp] = todo;
+    __syncthreads();
+    int turn = warp;
+    for (int w = 0; w < kWarps; ++w) {
+      const uint32_t found = s_todo[w];
+      const int items = __popc(found) * n;
+      for (; turn < items; turn += kWarps) {
+        uint32_t rest = found;
+        for (int k = turn / n; k; --k) rest &= rest - 1;
+        append_few<T, D, INTER, KIND>(bp, first + w * e4m3::kBlock + __ffs(rest) - 1, (from + turn % n) * RPW, p.Hkv);
       }
-    };
-    load(0);
-    const int block = block_of(p, __shfl_sync(~0u, slot_l, 0));
-    const uint32_t same = __ballot_sync(~0u, in && block_of(p, slot_l) == block);
-    // padding, or the block's rows began before, or there are too many
-    if (block < 0 || same >> e4m3::kBlock || __popc(same) > kShort) continue;
-    const uint32_t rows = __reduce_or_sync(~0u, (same >> lane) & 1 ? 1u << (slot_l & (e4m3::kBlock - 1)) : 0u);
-    const int page = block >> (p.page_shift - 4);
-    const size_t head = (size_t)page * p.Hkv + (active ? h : 0);
-    float* scale = (KIND == kKey ? bp.k_scales : bp.v_scales) + head * per_page + (block & (per_page - 1));
-    uint8_t* codes = (KIND == kKey ? p.k_pool : p.v_pool) +
-                     ((head << p.page_shift) + (block & (per_page - 1)) * e4m3::kBlock) * D;
-    float old = *scale;
-    if ((rows & 1) || !(old > 0.f && old <= FLT_MAX)) old = 0.f;
-    float x[8];
-    // Row r from w, and the row after it on its way into w.
-    auto row = [&](int r, int next) {
-      unpack4<T>(w[0], x);
-      unpack4<T>(w[1], x + 4);
-      const int pos = __shfl_sync(~0u, pos_l, r);
-      const bool far = KIND == kKey && p.pos && (pos < 0 || pos >= p.max_pos);
-      float4 c4 = make_float4(1.f, 1.f, 1.f, 1.f), s4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (in_rot && !far) {
-        const float* from = p.cos_sin + (size_t)pos * p.rot + 4 * l;
-        c4 = __ldg(reinterpret_cast<const float4*>(from));
-        s4 = __ldg(reinterpret_cast<const float4*>(from + half));
-      }
-      if (next >= 0) load(next);
-      if constexpr (KIND == kKey) {
-        if (gam) norm_row<LPR, true>(x, g, p.eps);
-        if (in_rot) {
-          const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float &a = INTER ? x[2 * e] : x[e], &b = INTER ? x[2 * e + 1] : x[4 + e];
-            const float ra = __fsub_rn(__fmul_rn(a, c[e]), __fmul_rn(b, s[e]));
-            b = __fadd_rn(__fmul_rn(b, c[e]), __fmul_rn(a, s[e]));
-            a = ra;
-          }
-        }
-      }
-      if (far) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = nan;
-      }
-      float most = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) most = max_abs(most, x[e]);
-      if (!(most <= FLT_MAX)) most = odd_values(x);
-      return __float_as_uint(most);
-    };
-    auto next_row = [&](int r) { return __ffs(same >> r >> 1) + r; };          // r: none (31 - clz below: -1)
-    auto previous_row = [&](int r) { return 31 - __clz(same & ((1u << r) - 1)); };
-    const int last = 31 - __clz(same);
-    uint32_t top = 0;
-#pragma unroll 1
-    for (int r = 0;; r = next_row(r)) {
-      top = max(top, row(r, r < last ? next_row(r) : previous_row(r)));
-      if (r == last) break;
+      turn -= items;
     }
-#pragma unroll
-    for (int d = 1; d < LPR; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
-    const float s = fmaxf(e4m3::scale_for(top), old);
-    if (active && s > old && old > 0.f) {  // the rows already there, to the new scale
-      const float f = __fdiv_rn(old, s);
-#pragma unroll 1
-      for (int piece = l; piece < D; piece += LPR) {
-        if ((rows >> (piece * 16 / D)) & 1) continue;
-        uint32_t u4[4];
-        uint4* to = reinterpret_cast<uint4*>(codes) + piece;
-        *reinterpret_cast<uint4*>(u4) = *to;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t a2 = e4m3::lo_to_h2(u4[q]), b2 = e4m3::hi_to_h2(u4[q]);
-          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&a2));
-          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&b2));
-          u4[q] = e4m3::to_codes(__fmul_rn(a.x, f), __fmul_rn(a.y, f), __fmul_rn(b.x, f), __fmul_rn(b.y, f));
-        }
-        *to = *reinterpret_cast<const uint4*>(u4);
-      }
-    }
-    if (active && l == 0 && s != old) *scale = s;
-    const bool exact = !(__float_as_uint(s) & 0x7fffffu);
-    const float inv = __frcp_rn(s);
-#pragma unroll 1
-    for (int r = last; r >= 0; r = previous_row(r)) {  // the last row is at hand
-      if (r < last) row(r, previous_row(r));
-      const int slot = __shfl_sync(~0u, slot_l, r);
-      float y[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(x[e], inv);
-      if (!exact) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = __fdiv_rn(x[e], s);
-      }
-      const uint2 c = make_uint2(e4m3::to_codes(y[0], y[1], y[2], y[3]), e4m3::to_codes(y[4], y[5], y[6], y[7]));
-      if (!active) continue;
-      store_row<T, D, PAIRED>(codes + (slot & (e4m3::kBlock - 1)) * D, out ? out + ((size_t)(t + r) * p.Hkv + h) * D : nullptr,
-                              c, s, off0, off1, l);
-    }
+    __syncthreads();
   }
 }
 
 // Keys first (they take longest), then values, then queries.
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3) append_block_kernel(const __grid_constant__ BlockParams p) {
-  __shared__ uint32_t s_top[2 * kWarps];  // by team and turn, of its two warps
+  __shared__ uint32_t s_top[2 * kWarps];  // by team and turn, of its warps; or what they found
   const int kv_ctas = p.block_ctas + p.token_ctas;
   int cta = blockIdx.x;
   if (cta < kv_ctas) {
     if (cta < p.block_ctas) append_blocks<T, D, INTER, kKey>(p, cta, s_top);
-    else append_tokens<T, D, INTER, kKey>(p, cta - p.block_ctas);
+    else append_tokens<T, D, INTER, kKey>(p, cta - p.block_ctas, s_top);
   } else if ((cta -= kv_ctas) < kv_ctas) {
     if (cta < p.block_ctas) append_blocks<T, D, INTER, kValue>(p, cta, s_top);
-    else append_tokens<T, D, INTER, kValue>(p, cta - p.block_ctas);
+    else append_tokens<T, D, INTER, kValue>(p, cta - p.block_ctas, s_top);
   } else {
     constexpr int GROUPQ = kIterQ * 32 / (D / 8);
     cta -= kv_ctas;
@@ -467,15 +496,18 @@ void launch(BlockParams& p, cudaStream_t s) {
     return (int)(c < kMost ? c : kMost);
   };
   const bool all = p.a.N >= kLong;
-  p.least = all ? 1 : kShort + 1;
   const long long chunks = (p.a.N + kUnit - 1) / kUnit;
   p.heads = 1;
   // What a warp finds out about its tokens serves up to four heads, while 2048 warps are left to do so: 4096 rows of 8
-  // heads 27.6 us with two, 31.2 with one, 40 with four; 16384 rows of 32 heads of 64 86 us with four, 113 with one;
+  // heads 26.6 us with two, 29 with one, 40 with four; 16384 rows of 32 heads of 64 88 us with four, 113 with one;
   // 1024 rows 11.4 us with one, 14 with two.
   while (p.heads < 4 && chunks * p.a.Hkv / (2 * p.heads) * kShare<D> >= 2048) p.heads *= 2;
   p.block_ctas = ctas(chunks * ((p.a.Hkv + p.heads - 1) / p.heads), kWarps / kShare<D>);
-  p.token_ctas = all ? 0 : ctas((long long)p.a.N * ((p.a.Hkv + 256 / D - 1) / (256 / D)), kWarps);
+  const long long groups = (p.a.Hkv + 256 / D - 1) / (256 / D), looks = (p.a.N + kLook - 1) / kLook;
+  // groups of heads that share a look, while 128 CTAs are left (16384 rows of 32 heads of 64: 88 us; with a look for each 100)
+  p.span = all ? 1 : 0;
+  while (all && p.span < groups && looks * groups / (2 * p.span) >= 128) p.span *= 2;
+  p.token_ctas = all ? ctas(looks * ((groups + p.span - 1) / p.span), 1) : ctas(p.a.N * groups, kWarps);
   const long long tokens = (p.a.N + kWarps - 1) / kWarps;
   const long long per = p.a.q_items ? (kMost + p.a.q_items - 1) / p.a.q_items : 0;
   p.q_ctas = (int)(tokens < per ? tokens : per) * p.a.q_items;
