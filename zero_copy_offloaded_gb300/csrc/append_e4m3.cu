@@ -30,9 +30,11 @@ constexpr int kLook = kWarps * e4m3::kBlock;  // and a CTA of append_tokens in l
 // Blocks that a call gives at most kShort rows go to warps that take one block of several heads (append_tokens), the others to
 // warps that take all of a block's rows (append_blocks).  Which is which is seen on the device, so both are launched.
 // 64 sequences' five rows each: 7.6 us with 6, 16.8 with 4; 512 single rows 9 us so, 55 by block; one sequence's 1024
-// rows 11.4 us by block, 27 by token.  Calls of kLong rows and more look for short blocks with a warp for 16 tokens, not
-// one for each: 4096 rows of one sequence 26.6 us, about 35 with a warp each; 4096 single rows 39 us, by block 179.
-constexpr int kShort = 6, kLong = 4096;
+// rows 10.3 us by block, 27 by token.  Calls of kLong rows and more look for
+// short blocks with a warp for 16 tokens, not one for each (4096 rows of one sequence 26.6 us, about 35 with a warp each; 2048
+// 17.8 and 21.2; 512 8.3 and 7.6), and about kLookCtas CTAs share what there is: 4096 single rows 42 us, by block 179; 1024
+// 16.1, 15.4 with a warp each.  (256 CTAs: 4096 rows of one sequence 28.6, single ones 40.7.)
+constexpr int kShort = 6, kLong = 1024, kLookCtas = 128;
 
 struct BlockParams {
   AppendParams a;
@@ -41,6 +43,7 @@ struct BlockParams {
   // CTAs of keys, and of values: by block, by token; of queries
   int block_ctas, token_ctas, q_ctas;
   int heads;  // of a unit of append_blocks
+  int parts;  // CTAs that share what a look of append_tokens finds, in long calls
   int span;   // groups of heads of a unit of append_tokens, 0: short calls, whose units are a token and a group
 };
 
@@ -419,7 +422,7 @@ __device__ __forceinline__ void append_blocks(const BlockParams& bp, int cta, ui
 }
 
 // All such blocks.  Short calls, where most are: a warp takes a token.  Long ones: the warps of a CTA look for them among kLook
-// tokens, 16 each, and share what they find.
+// tokens, 16 each, and share what they find, with other CTAs that look at the same.
 template <typename T, int D, bool INTER, int KIND>
 __device__ __forceinline__ void append_tokens(const BlockParams& bp, int cta, uint32_t* s_todo) {
   constexpr int RPW = 256 / D;
@@ -432,9 +435,10 @@ __device__ __forceinline__ void append_tokens(const BlockParams& bp, int cta, ui
     }
     return;
   }
-  const int spans = (groups + bp.span - 1) / bp.span, units = (p.N + kLook - 1) / kLook * spans;
+  const int spans = (groups + bp.span - 1) / bp.span, units = (p.N + kLook - 1) / kLook * spans * bp.parts;
   for (int u = cta; u < units; u += bp.token_ctas) {
-    const int first = u / spans * kLook, from = (u - u / spans * spans) * bp.span, n = min(bp.span, groups - from);
+    const int part = u % bp.parts, look = u / bp.parts / spans, from = (u / bp.parts - look * spans) * bp.span;
+    const int first = look * kLook, n = min(bp.span, groups - from);
     // lane i: the blocks of tokens at - 16 + i and at + i
     const int at = first + warp * e4m3::kBlock, token = at + lane;
     const int old = token >= e4m3::kBlock && token - e4m3::kBlock < p.N ? block_of(p, __ldg(p.slot + token - e4m3::kBlock)) : -1;
@@ -445,11 +449,11 @@ __device__ __forceinline__ void append_tokens(const BlockParams& bp, int cta, ui
     const uint32_t todo = __ballot_sync(~0u, lane < e4m3::kBlock && (starts >> lane & 1) && __popc(rows) <= kShort);
     if (lane == 0) s_todo[warp] = todo;
     __syncthreads();
-    int turn = warp;
+    int turn = part * kWarps + warp;
     for (int w = 0; w < kWarps; ++w) {
       const uint32_t found = s_todo[w];
       const int items = __popc(found) * n;
-      for (; turn < items; turn += kWarps) {
+      for (; turn < items; turn += kWarps * bp.parts) {
         uint32_t rest = found;
         for (int k = turn / n; k; --k) rest &= rest - 1;
         append_few<T, D, INTER, KIND>(bp, first + w * e4m3::kBlock + __ffs(rest) - 1, (from + turn % n) * RPW, p.Hkv);
@@ -500,14 +504,15 @@ void launch(BlockParams& p, cudaStream_t s) {
   p.heads = 1;
   // What a warp finds out about its tokens serves up to four heads, while 2048 warps are left to do so: 4096 rows of 8
   // heads 26.6 us with two, 29 with one, 40 with four; 16384 rows of 32 heads of 64 88 us with four, 113 with one;
-  // 1024 rows 11.4 us with one, 14 with two.
+  // 1024 rows 10.3 us with one, 14 with two.
   while (p.heads < 4 && chunks * p.a.Hkv / (2 * p.heads) * kShare<D> >= 2048) p.heads *= 2;
   p.block_ctas = ctas(chunks * ((p.a.Hkv + p.heads - 1) / p.heads), kWarps / kShare<D>);
   const long long groups = (p.a.Hkv + 256 / D - 1) / (256 / D), looks = (p.a.N + kLook - 1) / kLook;
-  // groups of heads that share a look, while 128 CTAs are left (16384 rows of 32 heads of 64: 88 us; with a look for each 100)
+  // groups of heads that share a look, while kLookCtas are left (16384 rows of 32 heads of 64: 88 us; with a look for each 100)
   p.span = all ? 1 : 0;
-  while (all && p.span < groups && looks * groups / (2 * p.span) >= 128) p.span *= 2;
-  p.token_ctas = all ? ctas(looks * ((groups + p.span - 1) / p.span), 1) : ctas(p.a.N * groups, kWarps);
+  while (all && p.span < groups && looks * groups / (2 * p.span) >= kLookCtas) p.span *= 2;
+  for (p.parts = 1; p.parts < 16 && looks * groups / p.span * p.parts < kLookCtas;) p.parts *= 2;
+  p.token_ctas = all ? ctas(looks * ((groups + p.span - 1) / p.span) * p.parts, 1) : ctas(p.a.N * groups, kWarps);
   const long long tokens = (p.a.N + kWarps - 1) / kWarps;
   const long long per = p.a.q_items ? (kMost + p.a.q_items - 1) / p.a.q_items : 0;
   p.q_ctas = (int)(tokens < per ? tokens : per) * p.a.q_items;
