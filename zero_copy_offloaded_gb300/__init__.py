@@ -822,15 +822,14 @@ def dkv_pages_copy(pairs, pools, into=None, stream=None):
         raise ValueError(f"{len(pools)} pools into {len(into)}")
     packed = bytearray()
     for i, (a, b) in enumerate(zip(pools, into)):
-        if a.dtype != b.dtype or a.dim() < 2 or a.shape[1:] != b.shape[1:]:
+        shape = a.shape
+        if len(shape) < 2 or a is not b and (a.dtype != b.dtype or shape[1:] != b.shape[1:]):
             raise ValueError(f"pool {i}: {a.dtype} {tuple(a.shape)} does not go into {b.dtype} {tuple(b.shape)}")
-        for t in (a,) if a is b else (a, b):
-            if not t.is_contiguous():
-                raise ValueError(f"pool {i} must be contiguous")
-            if t.get_device() != dev and not (t.get_device() < 0 and t.is_pinned()):
-                raise ValueError(f"pool {i} is neither with the pairs nor in pinned host memory")
-        n = a.shape[0]
-        packed += _PAGE_POOL.pack(a.data_ptr(), b.data_ptr(), a.numel() // n * a.element_size() if n else 0, n, b.shape[0])
+        to = at = _near(a, f"pool {i}", dev)
+        count = n = shape[0]
+        if a is not b:
+            to, count = _near(b, f"pool {i}", dev), b.shape[0]
+        packed += _PAGE_POOL.pack(at, to, a.nbytes // n if n else 0, n, count)
     n = pairs.shape[0]
     st = lib().dkv_pages_copy(_arg(pairs, "pairs", torch.int32, dev), n,
                               ctypes.addressof(ctypes.c_char.from_buffer(packed)) if packed else None, len(pools),
