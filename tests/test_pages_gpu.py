@@ -147,6 +147,19 @@ def test_compact_edges():
 
 # ---- copy ---------------------------------------------------------------------------------
 
+@pytest.mark.parametrize("size", [64, 127, 4096, 1 << 15, 1 << 17, 1 << 18])
+@pytest.mark.parametrize("off", [-1, 0, 1, 37])
+def test_pools_of_all_sizes(size, off):
+    """A few sequences in pools around powers of two, with those that just fit one launch and just do not among them."""
+    B, P, max_len = 4, 16, 120
+    used = len(batch(5, B, P, max_len, spare=0)[2])
+    entries = B * (-(-max_len // P) + 1)
+    length, table, free, count = batch(5, B, P, max_len, spare=max(8, size - entries - used + off))
+    for kind in ("mixed", "end", "one"):
+        assert check_fork(length, table, sources(6, B, kind), free, count, P)["report"][0] == 0
+    check_compact(length, table, len(free), P, inplace=bool(off & 1))
+
+
 def pools_of(seed, pages, shapes, pin=False):
     g = torch.Generator().manual_seed(seed)
     made = []

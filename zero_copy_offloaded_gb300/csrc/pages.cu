@@ -11,13 +11,15 @@
 // rewritten, and latency: clearing the marks, marking, counting, what follows from the counts and the rewrite wait for one
 // another.  Large tables and pools take a launch of the whole GPU for each, small ones one launch of a cluster with a
 // barrier between them.  In a graph: a fork of 512 sequences of up to 32768 rows takes 20 us (with a scan by one cluster 46), a
-// compaction of their 1 M pages 27 (110); of 64 sequences of up to 4096 rows in a cluster 14 and 17.  A copy of 8192 pages of
+// compaction of their 1 M pages 27 (110); of 64 sequences of up to 4096 rows in a cluster, whose shared memory holds the marks, 10.3
+// and 14.9 (with marks in memory 14 and 17).  A copy of 8192 pages of
 // 2 x 32 KB and their scales runs at 6.6 TB/s, as fast as a plain copy.
 #include <stdio.h>
 
 #include <algorithm>
 
 #include "dkv_internal.cuh"
+#include "per_device.h"
 
 namespace dkv {
 void set_last_error(dkv_status s, const char* msg);
@@ -30,11 +32,11 @@ using namespace dkv;
 constexpr int kThreads = 1024, kWarps = kThreads / 32, kCluster = 8, kSms = 152;
 constexpr int kSegment = 256;  // table entries of a warp at a time, eight to a lane
 // Table entries plus pages up to which one cluster does everything in one launch.  64 sequences of up to 16384 rows,
-// 131000 in all, take 18 us to fork and 23 to compact so, 18 and 22 in five launches, whose calls take 9 us longer; 256
-// of up to 8192 rows, twice as many, 24 and 36, and 18 and 21.
-constexpr long long kOneLaunch = 1 << 17;
+// 131000 in all, take 13.2 us to fork and 34 to compact so, 17.3 and 21.4 in five launches, whose calls take 9 us longer; with half
+// of that compactions too are faster in one.
+constexpr long long kForkInOne = 1 << 18, kCompactInOne = 1 << 17;
 
-// One launch of a cluster runs them all, or each is a launch of its own.
+// Each is a launch of its own, or one launch of a cluster runs them all.
 enum Phase : int { kAll = -1, kClear = 0, kMark = 1, kCount = 2, kEmit = 3, kWrite = 4 };
 
 struct Row {
@@ -62,6 +64,7 @@ struct PageParams {
   int* rank;             // compact: [num_pages], of pages that move
   int* counts;           // marks that each CTA of the scan has counted [kSms], then pages from which entries move
   int B, max_pages, shift, num_pages, max_moves;
+  int mark_shift;        // one launch: log2 of the marks' words of a CTA
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -88,20 +91,66 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int& total) {
   return x - v + __reduce_add_sync(~0u, lane < warp ? w : 0);
 }
 
+// Marks of the pool's pages, bytes of 0 or 1 in words of four: in the workspace, or (one launch) in the cluster's shared
+// memory, CTA c the words [c << shift, (c + 1) << shift), where clearing, marking and scanning wait for no memory.
+template <bool ONE>
+struct Marks {
+  uint8_t* global;
+  uint32_t shared;  // its address there, the same in every CTA
+  int shift;
+  __device__ __forceinline__ uint32_t at(int word) const {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(shared + (word & ((1 << shift) - 1)) * 4), "r"(word >> shift));
+    return a;
+  }
+  __device__ __forceinline__ void set(int page) const {
+    if constexpr (!ONE) global[page] = 1;
+    else asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(at(page >> 2) + (page & 3)), "r"(1) : "memory");
+  }
+  __device__ __forceinline__ uint32_t load(int word) const {
+    if constexpr (!ONE) return __ldcg(reinterpret_cast<const uint32_t*>(global) + word);
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at(word)) : "memory");
+    return v;
+  }
+  __device__ __forceinline__ void clear(int num_pages) const {
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if constexpr (!ONE) {
+      for (int i = blockIdx.x * kThreads + threadIdx.x; i < (num_pages + 15) / 16; i += gridDim.x * kThreads)
+        reinterpret_cast<uint4*>(global)[i] = zero;
+    } else {
+      for (int i = threadIdx.x; i < 1 << shift; i += kThreads)
+        asm volatile("st.shared.u32 [%0], %1;" ::"r"(shared + i * 4), "r"(0) : "memory");
+    }
+  }
+};
+
+// The marks that each CTA has counted: in the workspace, or in every CTA's shared memory.
+template <bool ONE>
+struct Counts {
+  int* global;
+  int* shared;
+  __device__ __forceinline__ void put(int own) const {  // the threads together
+    if constexpr (!ONE) {
+      if (threadIdx.x == 0) global[blockIdx.x] = own;
+    } else if (threadIdx.x < kCluster) {
+      uint32_t a;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(shared + blockIdx.x)), "r"(threadIdx.x));
+      asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(own) : "memory");
+    }
+  }
+  __device__ __forceinline__ int get(int cta) const { return ONE ? *(volatile int*)(shared + cta) : __ldcg(global + cta); }
+};
+
 // The marks that CTAs before `upto` have counted, and those of all; the threads together.
-__device__ __forceinline__ int counted(const int* counts, int upto, int* s_warp, int& total) {
+template <bool ONE>
+__device__ __forceinline__ int counted(const Counts<ONE>& counts, int upto, int* s_warp, int& total) {
   const int t = threadIdx.x;
-  const int v = t < (int)gridDim.x ? __ldcg(counts + t) : 0;
+  const int v = t < (int)gridDim.x ? counts.get(t) : 0;
   int before;
   block_scan(t < upto ? v : 0, s_warp, before);
   block_scan(v, s_warp, total);
   return before;
-}
-
-__device__ __forceinline__ void clear(uint8_t* at, int bytes) {
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < (bytes + 15) / 16;
-       i += (long long)gridDim.x * kThreads)
-    reinterpret_cast<uint4*>(at)[i] = make_uint4(0, 0, 0, 0);
 }
 
 // f(row, first entry) for each segment of the rows, a warp at a time.
@@ -122,26 +171,22 @@ __device__ __forceinline__ void load_segment(const int* row, int first, int end,
   for (int i = 0; i < 8; ++i) page[i] = at + 32 * i < end ? __ldcg(row + at + 32 * i) : -1;
 }
 
-__device__ __forceinline__ void mark(const PageParams& p, uint8_t* at, const int (&page)[8]) {
+template <bool ONE>
+__device__ __forceinline__ void mark(const PageParams& p, const Marks<ONE>& at, const int (&page)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    if ((uint32_t)page[i] < (uint32_t)p.num_pages) at[page[i]] = 1;
+    if ((uint32_t)page[i] < (uint32_t)p.num_pages) at.set(page[i]);
 }
 
 // The scan's words of four pages: a CTA has words [cta * per, (cta + 1) * per), a thread n of them from `first` on.
 struct Range {
   int per, first, n;
 };
-__device__ __forceinline__ Range scan_range(const PageParams& p, int cta) {
-  const int words = (p.num_pages + 3) / 4, per = (words + gridDim.x - 1) / gridDim.x;
+__device__ __forceinline__ Range scan_range(const PageParams& p, int cta, bool all) {
+  const int words = (p.num_pages + 3) / 4, per = all ? 1 << p.mark_shift : (words + gridDim.x - 1) / gridDim.x;
   const int each = (per + kThreads - 1) / kThreads, at = min((int)threadIdx.x * each, per);
   const int first = (int)min((long long)cta * per + at, (long long)words);
   return {per, first, max(0, min(min(each, per - at), words - first))};
-}
-
-// Marks are bytes of 0 or 1.
-__device__ __forceinline__ uint32_t load_marks(const uint8_t* at, int word) {
-  return __ldcg(reinterpret_cast<const uint32_t*>(at) + word);
 }
 
 // ---- fork -----------------------------------------------------------------------------------
@@ -151,20 +196,22 @@ struct Batch {
   int len[kThreads];   // of the old rows, from 0 to what the table holds
   Row rows[kThreads];  // of the new ones
   int heir[kThreads];  // of old row s: -1 itself, else the lowest row that goes on as it; INT_MAX: none
-  int warp[kWarps];
+  int warp[kWarps], counts[kCluster];
   int longest;
 };
 
-__device__ __forceinline__ uint32_t load_freed(const PageParams& p, int word) {  // held, and not any more
-  return load_marks(p.dead, word) & ~load_marks(p.live, word);
-}
-
+template <bool ALL>
 __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, int phase) {
   __shared__ Batch s;
+  extern __shared__ uint4 s_marks[];
+  const Marks<ALL> live = {p.live, smem_u32(s_marks), p.mark_shift};
+  const Marks<ALL> dead = {p.dead, smem_u32(s_marks) + (4 << p.mark_shift), p.mark_shift};
+  const Counts<ALL> counts = {p.counts, s.counts};
+  auto load_freed = [&](int word) { return dead.load(word) & ~live.load(word); };  // held, and not any more
   griddep_wait();
   griddep_launch_dependents();
   const int b = threadIdx.x, lane = b & 31;
-  const bool all = phase == kAll;
+  constexpr bool all = ALL;  // phases
   const long long cap = (long long)p.max_pages << p.shift;
   int src = -1, free_count = 0;
   long long len = 0;
@@ -174,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, i
     free_count = min(max(*p.free_count, 0), p.num_pages);
   }
   if (phase == kClear || all) {
-    clear(p.live, p.num_pages);
-    clear(p.dead, p.num_pages);
+    live.clear(p.num_pages);
+    dead.clear(p.num_pages);
     if (!all) return;
   }
   if (phase != kWrite) {
@@ -197,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, i
         if (!any && !keep) return;
         int page[8];
         load_segment(p.table + (size_t)r * p.max_pages, first, end, page);
-        if (any) mark(p, goes ? p.live : p.dead, page);
+        if (any) mark(p, goes ? live : dead, page);
         if (keep) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -208,18 +255,18 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, i
       cluster_sync();
     }
     // ---- pages that go back, in page order
-    const Range range = scan_range(p, blockIdx.x);
+    const Range range = scan_range(p, blockIdx.x, all);
     int mine = 0;
     if (any)
-      for (int i = 0; i < range.n; ++i) mine += __popc(load_freed(p, range.first + i));
+      for (int i = 0; i < range.n; ++i) mine += __popc(load_freed(range.first + i));
     int own, freed = 0, at = 0;
     if (any) at = block_scan(mine, s.warp, own);
     if (phase == kCount || all) {
-      if (any && b == 0) p.counts[blockIdx.x] = own;
+      if (any) counts.put(own);
       if (!all) return;
       cluster_sync();
     }
-    if (any) at += counted(p.counts, blockIdx.x, s.warp, freed);
+    if (any) at += counted(counts, blockIdx.x, s.warp, freed);
     const bool on = src >= 0 && src < p.B;
     const int new_len = on ? s.len[src] : 0, held = (int)pages_of(new_len, p.shift);
     const bool need = on && (new_len & ((1 << p.shift) - 1)) && s.heir[src] != (src == b ? -1 : b);
@@ -230,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, i
     if (ok && mine) {
       int* to = p.free_pages + free_count + at;
       for (int i = 0; i < range.n; ++i) {
-        for (uint32_t m = load_freed(p, range.first + i); m; m &= m - 1)
+        for (uint32_t m = load_freed(range.first + i); m; m &= m - 1)
           *to++ = (range.first + i) * 4 + (__ffs(m) - 1) / 8;
       }
     }
@@ -290,11 +337,15 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, i
 
 // ---- compaction -----------------------------------------------------------------------------
 
+template <bool ALL>
 __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PageParams p, int phase) {
-  __shared__ int s_warp[kWarps], s_longest, s_len[kThreads];
+  __shared__ int s_warp[kWarps], s_longest, s_len[kThreads], s_counts[kCluster];
+  extern __shared__ uint4 s_marks[];
+  const Marks<ALL> marks = {p.live, smem_u32(s_marks), p.mark_shift};
+  const Counts<ALL> counts = {p.counts, s_counts};
   griddep_wait();
   griddep_launch_dependents();
-  const bool all = phase == kAll;
+  constexpr bool all = ALL;  // phases
   const int lane = threadIdx.x & 31, t = threadIdx.x;
   const long long cap = (long long)p.max_pages << p.shift;
   const int len = phase != kClear && t < p.B ? max(p.len[t], 0) : 0;
@@ -302,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PageParams p
   __syncthreads();
   auto end_of = [&](int r) { return (int)pages_of(s_len[r], p.shift); };
   if (phase == kClear || all) {
-    clear(p.live, p.num_pages);
+    marks.clear(p.num_pages);
     if (!all) return;
     cluster_sync();
   }
@@ -312,32 +363,32 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PageParams p
       if (first >= end) return;
       int page[8];
       load_segment(p.table + (size_t)r * p.max_pages, first, end, page);
-      mark(p, p.live, page);
+      mark(p, marks, page);
     });
     if (!all) return;
     cluster_sync();
   }
   int from = 0;
   if (phase != kWrite) {
-    const Range range = scan_range(p, blockIdx.x);
+    const Range range = scan_range(p, blockIdx.x, all);
     int mine = 0, own;
-    for (int i = 0; i < range.n; ++i) mine += __popc(load_marks(p.live, range.first + i));
+    for (int i = 0; i < range.n; ++i) mine += __popc(marks.load(range.first + i));
     int before = block_scan(mine, s_warp, own);  // pages named before this thread's
     if (phase == kCount || all) {
-      if (t == 0) p.counts[blockIdx.x] = own;
+      counts.put(own);
       if (!all) return;
       cluster_sync();
     }
     int live;
-    before += counted(p.counts, blockIdx.x, s_warp, live);
+    before += counted(counts, blockIdx.x, s_warp, live);
     // named pages below `live`, which stay: those of the CTAs before the one that has page `live`, and a part of its own
     const int edge = live / 4 / range.per;
     int ignore, part = 0, low;
-    low = counted(p.counts, edge, s_warp, ignore);
-    const Range other = scan_range(p, edge);
+    low = counted(counts, edge, s_warp, ignore);
+    const Range other = scan_range(p, edge, all);
     for (int i = 0; i < other.n; ++i) {
       const int word = other.first + i, keep = live - word * 4;  // bytes of it below `live`
-      part += __popc(load_marks(p.live, word) & (keep >= 4 ? ~0u : keep <= 0 ? 0u : (1u << (8 * keep)) - 1));
+      part += __popc(marks.load(word) & (keep >= 4 ? ~0u : keep <= 0 ? 0u : (1u << (8 * keep)) - 1));
     }
     block_scan(part, s_warp, part);
     low += part;
@@ -346,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) compact_kernel(const PageParams p
     const bool ok = !__syncthreads_or(len > cap);
     if (ok) {
       for (int i = 0; i < range.n; ++i) {
-        const uint32_t word = load_marks(p.live, range.first + i);
+        const uint32_t word = marks.load(range.first + i);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int named = (word >> (8 * q)) & 1, page = (range.first + i) * 4 + q;
@@ -473,10 +524,11 @@ size_t ws_more(int num_pages) { return ws_live() + align256(num_pages); }
 size_t ws_old(int num_pages) { return ws_more(num_pages) + align256((size_t)num_pages * 4); }
 
 template <typename K>
-cudaError_t launch_one(K* kernel, const PageParams& p, int phase, int grid, cudaStream_t s) {
+cudaError_t launch_one(K* kernel, const PageParams& p, int phase, int grid, cudaStream_t s, int smem = 0) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   if (phase == kAll) {
@@ -492,11 +544,19 @@ cudaError_t launch_one(K* kernel, const PageParams& p, int phase, int grid, cuda
   return cudaLaunchKernelEx(&cfg, kernel, p, phase);
 }
 
+// `one` for up to `most` entries and pages, with so many maps of marks.
 template <typename K>
-dkv_status launch(K* kernel, const PageParams& p, cudaStream_t s) {
+dkv_status launch(K* one, long long most, int maps, K* kernel, PageParams& p, PerDevice& room, cudaStream_t s) {
   cudaError_t e;
-  if ((long long)p.B * p.max_pages + p.num_pages <= kOneLaunch) {
-    e = launch_one(kernel, p, kAll, kCluster, s);
+  if ((long long)p.B * p.max_pages + p.num_pages <= most) {
+    const int words = ((p.num_pages + 3) / 4 + kCluster - 1) / kCluster;
+    p.mark_shift = 2;
+    while ((1 << p.mark_shift) < words) ++p.mark_shift;
+    int device = 0;
+    e = cudaGetDevice(&device);
+    if (e == cudaSuccess)
+      e = room(device, [&] { return cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(maps * most / kCluster)); });
+    if (e == cudaSuccess) e = launch_one(one, p, kAll, kCluster, s, maps * (4 << p.mark_shift));
   } else {
     const long long parts = (long long)p.B * ((p.max_pages + kSegment - 1) / kSegment);
     const int grid = (int)std::min<long long>((parts + kWarps - 1) / kWarps, kSms);
@@ -553,7 +613,8 @@ extern "C" dkv_status dkv_pages_fork(const int32_t* page_table, const int32_t* k
   p.B = batch; p.max_pages = max_pages; p.num_pages = num_pages; p.shift = shift_of(page_tokens);
   set_workspace(p, workspace);
   if (table_out != page_table) p.old = nullptr;
-  return launch(fork_kernel, p, static_cast<cudaStream_t>(stream));
+  static PerDevice room;
+  return launch(fork_kernel<true>, kForkInOne, 2, fork_kernel<false>, p, room, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" dkv_status dkv_pages_compact(const int32_t* page_table, const int32_t* kv_len, int batch, int max_pages,
@@ -575,7 +636,8 @@ extern "C" dkv_status dkv_pages_compact(const int32_t* page_table, const int32_t
   p.B = batch; p.max_pages = max_pages; p.num_pages = num_pages; p.shift = shift_of(page_tokens);
   p.max_moves = moves ? max_moves : 0;
   set_workspace(p, workspace);
-  return launch(compact_kernel, p, static_cast<cudaStream_t>(stream));
+  static PerDevice room;
+  return launch(compact_kernel<true>, kCompactInOne, 1, compact_kernel<false>, p, room, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" dkv_status dkv_pages_copy(const int32_t* pairs, int n_pairs, const dkv_page_pool_t* pools, int n_pools,
