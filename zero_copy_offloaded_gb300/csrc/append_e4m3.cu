@@ -17,6 +17,7 @@
 // exact sums of squares, the values that have to live until the block's largest is known) and for instructions, of
 // which the unrolled rows have many.  Sums, norms and rotations take two elements an instruction where they can.
 #include "append.cuh"
+#include "append_geometry.h"
 #include "e4m3.cuh"
 
 namespace {
@@ -24,27 +25,19 @@ namespace {
 using namespace dkv;
 
 constexpr int kThreads = kAppendThreads, kWarps = kThreads / 32;
+static_assert(kWarps == kAppendWarps && kLook == kWarps * e4m3::kBlock && kIterQ == kAppendIterQ, "append_geometry.h");
 
-constexpr int kUnit = 16;    // tokens that append_blocks' warps look at together for blocks that begin there
-constexpr int kLook = kWarps * e4m3::kBlock;  // and a CTA of append_tokens in long calls
 // Blocks that a call gives at most kShort rows go to warps that take one block of several heads (append_tokens), the others to
 // warps that take all of a block's rows (append_blocks).  Which is which is seen on the device, so both are launched.
 // 64 sequences' five rows each: 7.6 us with 6, 16.8 with 4; 512 single rows 9 us so, 55 by block; one sequence's 1024
-// rows 10.3 us by block, 27 by token.  Calls of kLong rows and more look for
-// short blocks with a warp for 16 tokens, not one for each (4096 rows of one sequence 26.6 us, about 35 with a warp each; 2048
-// 17.8 and 21.2; 512 8.3 and 7.6), and about kLookCtas CTAs share what there is: 4096 single rows 42 us, by block 179; 1024
-// 16.1, 15.4 with a warp each.  (256 CTAs: 4096 rows of one sequence 28.6, single ones 40.7.)
-constexpr int kShort = 6, kLong = 1024, kLookCtas = 128;
+// rows 10.3 us by block, 27 by token.
+constexpr int kShort = 6;
 
 struct BlockParams {
   AppendParams a;
   float* k_scales;
   float* v_scales;
-  // CTAs of keys, and of values: by block, by token; of queries
-  int block_ctas, token_ctas, q_ctas;
-  int heads;  // of a unit of append_blocks
-  int parts;  // CTAs that share what a look of append_tokens finds, in long calls
-  int span;   // groups of heads of a unit of append_tokens, 0: short calls, whose units are a token and a group
+  AppendGeometry g;
 };
 
 // The block of a slot; -1: padding.
@@ -92,11 +85,9 @@ __device__ __forceinline__ void store_row(uint8_t* to, T* out, uint2 c, float s,
   *reinterpret_cast<uint2*>(out + off1) = pack4<T>(y + 4);
 }
 
-// Warps that share a run: with heads of 128 four of four rows each, so that a lane holds 16 fp32 values (4096 rows of 32/8 heads
-// 26.6 us; with two warps 27 to 28, with one and two CTAs an SM instead of three 38.7).  Of 64 one (16384 rows of 32 heads
-// 88 us, 103 with two: what a warp does once for a run counts more).
+// Warps that share a run.
 template <int D>
-constexpr int kShare = D == 128 ? 4 : 1;
+constexpr int kShare = append_share(D);
 
 // The rows t0 .. t0 + 15 of heads h0 .. h1 - 1 that lie in block `block` of the pool, row t0 among them.  The warps that
 // share it come here together; `turn` alternates between the heads that they take.  (Loading the next head's rows
@@ -403,16 +394,16 @@ __device__ __forceinline__ void append_blocks(const BlockParams& bp, int cta, ui
   constexpr int kTeams = kWarps / kShare<D>;
   const AppendParams& p = bp.a;
   const int lane = threadIdx.x & 31;
-  const int groups = (p.Hkv + bp.heads - 1) / bp.heads, units = (p.N + kUnit - 1) / kUnit * groups;
+  const int groups = (p.Hkv + bp.g.heads - 1) / bp.g.heads, units = (p.N + kUnit - 1) / kUnit * groups;
   int turn = 0;
-  for (int u = cta * kTeams + (threadIdx.x >> 5) / kShare<D>; u < units; u += bp.block_ctas * kTeams) {
-    const int chunk = u / groups, h = (u - chunk * groups) * bp.heads, first = chunk * kUnit;
+  for (int u = cta * kTeams + (threadIdx.x >> 5) / kShare<D>; u < units; u += bp.g.block_ctas * kTeams) {
+    const int chunk = u / groups, h = (u - chunk * groups) * bp.g.heads, first = chunk * kUnit;
     // lane i: the block of token first - 16 + i
     const int token = first - kUnit + lane;
     const int mine = token >= 0 && token < p.N ? block_of(p, __ldg(p.slot + token)) : -1;
     const uint32_t same = __match_any_sync(~0u, mine), before = ((1u << lane) - 1) & ~((1u << lane >> 15) - 1);
     uint32_t heads = __ballot_sync(~0u, mine >= 0 && !(same & before)) >> kUnit;
-    const int end = min(h + bp.heads, p.Hkv);
+    const int end = min(h + bp.g.heads, p.Hkv);
     while (heads) {
       const int at = __ffs(heads) - 1;
       heads &= heads - 1;
@@ -428,17 +419,17 @@ __device__ __forceinline__ void append_tokens(const BlockParams& bp, int cta, ui
   constexpr int RPW = 256 / D;
   const AppendParams& p = bp.a;
   const int groups = (p.Hkv + RPW - 1) / RPW, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (!bp.span) {
-    for (int u = cta * kWarps + warp; u < p.N * groups; u += bp.token_ctas * kWarps) {
+  if (!bp.g.span) {
+    for (int u = cta * kWarps + warp; u < p.N * groups; u += bp.g.token_ctas * kWarps) {
       const int t = u / groups;
       append_few<T, D, INTER, KIND>(bp, t, (u - t * groups) * RPW, p.Hkv);
     }
     return;
   }
-  const int spans = (groups + bp.span - 1) / bp.span, units = (p.N + kLook - 1) / kLook * spans * bp.parts;
-  for (int u = cta; u < units; u += bp.token_ctas) {
-    const int part = u % bp.parts, look = u / bp.parts / spans, from = (u / bp.parts - look * spans) * bp.span;
-    const int first = look * kLook, n = min(bp.span, groups - from);
+  const int spans = (groups + bp.g.span - 1) / bp.g.span, units = (p.N + kLook - 1) / kLook * spans * bp.g.parts;
+  for (int u = cta; u < units; u += bp.g.token_ctas) {
+    const int part = u % bp.g.parts, look = u / bp.g.parts / spans, from = (u / bp.g.parts - look * spans) * bp.g.span;
+    const int first = look * kLook, n = min(bp.g.span, groups - from);
     // lane i: the blocks of tokens at - 16 + i and at + i
     const int at = first + warp * e4m3::kBlock, token = at + lane;
     const int old = token >= e4m3::kBlock && token - e4m3::kBlock < p.N ? block_of(p, __ldg(p.slot + token - e4m3::kBlock)) : -1;
@@ -453,7 +444,7 @@ __device__ __forceinline__ void append_tokens(const BlockParams& bp, int cta, ui
     for (int w = 0; w < kWarps; ++w) {
       const uint32_t found = s_todo[w];
       const int items = __popc(found) * n;
-      for (; turn < items; turn += kWarps * bp.parts) {
+      for (; turn < items; turn += kWarps * bp.g.parts) {
         uint32_t rest = found;
         for (int k = turn / n; k; --k) rest &= rest - 1;
         append_few<T, D, INTER, KIND>(bp, first + w * e4m3::kBlock + __ffs(rest) - 1, (from + turn % n) * RPW, p.Hkv);
@@ -468,18 +459,18 @@ __device__ __forceinline__ void append_tokens(const BlockParams& bp, int cta, ui
 template <typename T, int D, bool INTER>
 __global__ void __launch_bounds__(kThreads, 3) append_block_kernel(const __grid_constant__ BlockParams p) {
   __shared__ uint32_t s_top[2 * kWarps];  // by team and turn, of its warps; or what they found
-  const int kv_ctas = p.block_ctas + p.token_ctas;
+  const int kv_ctas = p.g.block_ctas + p.g.token_ctas;
   int cta = blockIdx.x;
   if (cta < kv_ctas) {
-    if (cta < p.block_ctas) append_blocks<T, D, INTER, kKey>(p, cta, s_top);
-    else append_tokens<T, D, INTER, kKey>(p, cta - p.block_ctas, s_top);
+    if (cta < p.g.block_ctas) append_blocks<T, D, INTER, kKey>(p, cta, s_top);
+    else append_tokens<T, D, INTER, kKey>(p, cta - p.g.block_ctas, s_top);
   } else if ((cta -= kv_ctas) < kv_ctas) {
-    if (cta < p.block_ctas) append_blocks<T, D, INTER, kValue>(p, cta, s_top);
-    else append_tokens<T, D, INTER, kValue>(p, cta - p.block_ctas, s_top);
+    if (cta < p.g.block_ctas) append_blocks<T, D, INTER, kValue>(p, cta, s_top);
+    else append_tokens<T, D, INTER, kValue>(p, cta - p.g.block_ctas, s_top);
   } else {
     constexpr int GROUPQ = kIterQ * 32 / (D / 8);
     cta -= kv_ctas;
-    const int j = cta % p.a.q_items, per = p.q_ctas / p.a.q_items;
+    const int j = cta % p.a.q_items, per = p.g.q_ctas / p.a.q_items;
     append_rows<T, D, INTER, kQuery>(p.a, j * GROUPQ, min(GROUPQ, p.a.Hq - j * GROUPQ),
                                      cta / p.a.q_items * kWarps + (threadIdx.x >> 5), per * kWarps);
   }
@@ -492,33 +483,10 @@ dkv_status refuse(dkv_status s, const char* msg) {
 
 template <typename T, int D>
 void launch(BlockParams& p, cudaStream_t s) {
-  constexpr int GROUPQ = kIterQ * 32 / (D / 8);
-  constexpr long long kMost = 16 * 3 * 152;  // CTAs of a kind
-  p.a.q_items = p.a.q ? (p.a.Hq + GROUPQ - 1) / GROUPQ : 0;
-  auto ctas = [&](long long units, int each) {
-    const long long c = (units + each - 1) / each;
-    return (int)(c < kMost ? c : kMost);
-  };
-  const bool all = p.a.N >= kLong;
-  const long long chunks = (p.a.N + kUnit - 1) / kUnit;
-  p.heads = 1;
-  // What a warp finds out about its tokens serves up to four heads, while 2048 warps are left to do so: 4096 rows of 8
-  // heads 26.6 us with two, 29 with one, 40 with four; 16384 rows of 32 heads of 64 88 us with four, 113 with one;
-  // 1024 rows 10.3 us with one, 14 with two.
-  while (p.heads < 4 && chunks * p.a.Hkv / (2 * p.heads) * kShare<D> >= 2048) p.heads *= 2;
-  p.block_ctas = ctas(chunks * ((p.a.Hkv + p.heads - 1) / p.heads), kWarps / kShare<D>);
-  const long long groups = (p.a.Hkv + 256 / D - 1) / (256 / D), looks = (p.a.N + kLook - 1) / kLook;
-  // groups of heads that share a look, while kLookCtas are left (16384 rows of 32 heads of 64: 88 us; with a look for each 100)
-  p.span = all ? 1 : 0;
-  while (all && p.span < groups && looks * groups / (2 * p.span) >= kLookCtas) p.span *= 2;
-  for (p.parts = 1; p.parts < 16 && looks * groups / p.span * p.parts < kLookCtas;) p.parts *= 2;
-  p.token_ctas = all ? ctas(looks * ((groups + p.span - 1) / p.span) * p.parts, 1) : ctas(p.a.N * groups, kWarps);
-  const long long tokens = (p.a.N + kWarps - 1) / kWarps;
-  const long long per = p.a.q_items ? (kMost + p.a.q_items - 1) / p.a.q_items : 0;
-  p.q_ctas = (int)(tokens < per ? tokens : per) * p.a.q_items;
-  const int grid = 2 * (p.block_ctas + p.token_ctas) + p.q_ctas;
-  if (p.a.inter) append_block_kernel<T, D, true><<<grid, kThreads, 0, s>>>(p);
-  else append_block_kernel<T, D, false><<<grid, kThreads, 0, s>>>(p);
+  p.g = append_geometry(p.a.N, p.a.q ? p.a.Hq : 0, p.a.Hkv, D);
+  p.a.q_items = p.g.q_items;
+  if (p.a.inter) append_block_kernel<T, D, true><<<p.g.grid, kThreads, 0, s>>>(p);
+  else append_block_kernel<T, D, false><<<p.g.grid, kThreads, 0, s>>>(p);
 }
 
 }  // namespace
