@@ -1,0 +1,59 @@
+"""Attention over an 8-bit cache whose scales, or whose queries' sizes, lie far apart: against the fp64 oracle, with the
+bounds that test_block_attend_gpu.check derives."""
+import numpy as np
+import pytest
+
+from tests.test_block_attend_gpu import case, check, run
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+def far_keys(c, scale, every, seed=0):
+    """The first block of every sequence, and one in `every` of the others, has K scale `scale` (zero codes where that would
+    make scores of another size), the others 2^-7."""
+    (k, ks), v = c["pools"]
+    k, ks = k.copy(), np.full_like(ks, 2.0 ** -7)
+    far = np.random.default_rng(seed).random(ks.shape) < 1 / every
+    far[c["table"][:, 0], :, 0] = True
+    ks[far] = scale
+    if scale > 1:
+        k = np.where(np.repeat(far, 16, -1)[..., None], 0, k).astype(k.dtype)
+    return dict(c, pools=[(k, ks), v])
+
+
+@pytest.mark.parametrize("rows", [1, 3, 60])
+@pytest.mark.parametrize("D,dtype", [(64, "bf16"), (128, "bf16"), (128, "fp16")])
+@pytest.mark.parametrize("exponent", [-126, -112, -64, 60, 100, 126])
+def test_k_scales_far_from_the_first(rows, D, dtype, exponent):
+    c = far_keys(case(41, [500, 900, 40], [rows, rows, 1], 4, 2, D, dtype, 16), 2.0 ** exponent, 20)
+    check(c, *run(c))
+    # the other way round: the far scale in every block but the first of each sequence and some others
+    (k, ks), v = c["pools"]
+    if exponent < 0:
+        other = np.where(ks == 2.0 ** -7, np.float32(2.0 ** exponent), np.float32(2.0 ** -7))
+        check(d := dict(c, pools=[(k, other), v]), *run(d))
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_k_scales_of_every_size(rows):
+    """Blocks from 2^-126 to 2^-7 side by side, powers of two and not, over sequences that CTAs share."""
+    c = case(42, [5000, 700], [rows, rows], 4, 2, 128, "bf16", 16)
+    (k, ks), v = c["pools"]
+    rng = np.random.default_rng(1)
+    for x in (np.exp2(rng.integers(-126, -6, ks.shape)), np.exp2(rng.uniform(-126, -7, ks.shape)), np.exp2(rng.integers(-40, -6, ks.shape))):
+        d = dict(c, pools=[(k, x.astype(np.float32)), v])
+        check(d, *run(d))
+
+
+@pytest.mark.parametrize("bad", [np.nan, 2.0 ** -64])
+def test_a_nan_scale_reaches_the_rows_that_see_it(bad):
+    """Beside a first block whose scale is far away, more than 32 packed rows."""
+    c = far_keys(case(43, [300], [100], 2, 1, 128, "bf16", 16), 2.0 ** -112, 1000)
+    c["pools"][0][1][c["table"][0, 17]] = bad  # tokens 272 .. 287, seen from row 72 on
+    out, lse = run(c)
+    if np.isnan(bad):
+        assert torch.isnan(out[72:100].float()).all() and torch.isnan(lse[72:100]).all()
+        assert torch.isfinite(out[:72].float()).all() and torch.isfinite(lse[:72]).all()
+    else:
+        check(c, out, lse)

@@ -110,11 +110,12 @@ struct Bars {
   unsigned long long nan_key[4][kNan];
   uint32_t nan_item[4];   // E4M3: item + 1 of one that has any
   // E4M3.  By item & 3: the powers of two that K's and V's tiles of a piece are converted by.  By tile & 3, for each
-  // run of 16 keys: 1 where a scale is left over, 2 where there is no page; K's scale that is left over, log2 of V's and
-  // its inverse.
+  // run of 16 keys: 1 where a scale is left over, 2 where there is no page; K's scale, whole, where it is left over (the fourth
+  // is 1 then), log2 of what is left of V's and its inverse.  By row: the scale of its scores but for K's.
   float2 ref[4];
   uint2 flags[4];
   float4 block[F == kE2M1 ? 1 : 4][8];
+  float sl[F == kE2M1 ? 1 : 2 * kRows];
 };
 
 // Where a role is on the line: an item, and the key tiles [tile, end) of it here.
@@ -461,8 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->q_ready[t]);
-        return fminf(fmaxf(fabsf(p.scale_log2) * unscale, 1e-37f), FLT_MAX);
+        // positive and finite, so that a masked -infinity stays one; E4M3's is so once it has K's scale
+        return fminf(fmaxf(fabsf(p.scale_log2) * unscale, F == kE2M1 ? 1e-37f : 0.f), FLT_MAX);
       };
+      // (a NaN stays one)
+      auto positive = [](float x) { return x < 1e-37f ? 1e-37f : x > FLT_MAX ? FLT_MAX : x; };
       auto active = [&]() { return c.last >= c.qt * 2 * kRows + t * kRows; };
       bool go = true;
       float sl = 1.f;
@@ -499,7 +503,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
                 // bit 1 of four bytes side by side
                 valid ^= (f.x >> 1 & 0x01010101u) * 0x10204080u >> 28 | ((f.y >> 1 & 0x01010101u) * 0x10204080u >> 28) << 4;
               }
-              if (tile == tile0) sl = fminf(fmaxf(sl * bars->ref[items & 3].x, 1e-37f), FLT_MAX);
+              if (tile == tile0) {
+                bars->sl[t * kRows + row] = sl;  // this thread alone reads it
+                sl = positive(sl * bars->ref[items & 3].x);
+              }
             }
             const bool edge = k0 + kKeys > minvis || valid != 0xFFu;
             const int nvis = vis - k0;  // keys [0, nvis) of the tile are seen, where on a page
@@ -509,7 +516,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
               if constexpr (scaled) {
                 const float4 b0 = bars->block[place][2 * pc], b1 = bars->block[place][2 * pc + 1];
                 const bool see0 = nvis - pc * 32 > 0, see1 = nvis - pc * 32 > 16;
-                bsl = make_float2(see0 ? sl * b0.x : 1.f, see1 ? sl * b1.x : 1.f);
+                // (from K's own scale: its ratio to the piece's can leave fp32's range, and `sl` is held inside it)
+                auto scale_of = [&](const float4& b) { return b.w != 0.f ? positive(bars->sl[t * kRows + row] * b.x) : sl; };
+                bsl = make_float2(see0 ? scale_of(b0) : 1.f, see1 ? scale_of(b1) : 1.f);
                 blv = make_float2(see0 ? b0.y : 0.f, see1 ? b1.y : 0.f);
                 brv = make_float2(see0 ? b0.z : 1.f, see1 ? b1.z : 1.f);
               }
@@ -836,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         if (opened && lane == 0) bars->ref[item & 3] = make_float2(kref, vref);
         if (speaks) {
           const bool left_over = rest_k != 1.f || rest_v != 1.f;
-          bars->block[j & 3][run] = left_over ? make_float4(rest_k, e4m3::log2_of(rest_v), __fdividef(1.0f, rest_v), 0.f)
+          bars->block[j & 3][run] = left_over ? make_float4(ks, e4m3::log2_of(rest_v), __fdividef(1.0f, rest_v), rest_k != 1.f)
                                               : make_float4(1.f, 0.f, 1.f, 0.f);
           reinterpret_cast<uint8_t*>(&bars->flags[j & 3])[run] = left_over | (held ? 0 : 2);
         }
