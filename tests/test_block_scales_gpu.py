@@ -57,3 +57,35 @@ def test_a_nan_scale_reaches_the_rows_that_see_it(bad):
         assert torch.isfinite(out[:72].float()).all() and torch.isfinite(lse[:72]).all()
     else:
         check(c, out, lse)
+
+
+@pytest.mark.parametrize("rows", [1, 3, 5, 8, 60])
+@pytest.mark.parametrize("D", [64, 128])
+def test_small_queries_over_large_keys(rows, D):
+    """Queries near 2^-112 over K scales near 2^105: their products are of ordinary size."""
+    c = case(44, [500, 900, 40], [rows, rows, 1], 4, 1, D, "bf16", 16)
+    (k, ks), v = c["pools"]
+    c["q"] = (c["q"].float() * 2.0 ** -112).to(torch.bfloat16)
+    d = dict(c, pools=[(k, np.full_like(ks, 2.0 ** 105)), v])
+    check(d, *run(d))
+    first = np.full_like(ks, 2.0 ** 105)
+    first[c["table"][:, 0]] = 2.0 ** 20
+    d = dict(c, pools=[(k, first), v])
+    check(d, *run(d))
+
+
+@pytest.mark.parametrize("rows", [1, 3, 5, 8, 60])
+@pytest.mark.parametrize("D", [64, 128])
+def test_zero_codes_beside_large_scales_and_queries(rows, D):
+    """Dims of 2^90 in the queries meet zero codes of blocks with a scale of 2^60, and the other way round: scores of 0."""
+    c = case(45, [500, 900, 40], [rows, rows, 1], 4, 1, D, "bf16", 16)
+    (k, ks), v = c["pools"]
+    q = torch.zeros_like(c["q"])
+    q[..., :8] = 2.0 ** 90
+    c["q"] = q
+    k = k.copy()
+    k[..., :8] = 0
+    for scales in (np.full_like(ks, 2.0 ** 60), np.where(np.arange(len(ks))[:, None, None] % 3, 2.0 ** 60, 2.0 ** -7)):
+        d = dict(c, pools=[(k, scales.astype(np.float32)), v])
+        ref = check(d, *run(d))
+        assert np.all(ref["smax"] == 0)

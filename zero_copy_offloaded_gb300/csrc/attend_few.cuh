@@ -151,6 +151,13 @@ __device__ __forceinline__ void cp_async4_u32(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 
+// min(a, b), NaN if one of them is.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 template <int V>
 __device__ __forceinline__ void store_vec(float* to, const float (&x)[V]) {
   if constexpr (V == 4) *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
@@ -443,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<F, D, NT>::kPerSm) attend_kernel
 #pragma unroll
         for (int i = 0; i < 2 * J; ++i) f[i] ^= 0x80008000u;
       }
-      // positive and finite, so that a masked -infinity stays one
-      return fminf(fmaxf(fabsf(p.scale_log2) * unscale, 1e-37f), FLT_MAX);
+      // positive and finite, so that a masked -infinity stays one; E4M3, whose K scale has yet to come, masks behind it
+      return fminf(fmaxf(fabsf(p.scale_log2) * unscale, F == kE2M1 ? 1e-37f : 0.f), FLT_MAX);
     };
     if constexpr (QS) {
       for (int nt = warp; nt < NT; nt += kWarps) {
@@ -529,7 +536,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<F, D, NT>::kPerSm) attend_kernel
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float2 sl = scales(nt);
-          const float fx = sl.x * block.x, fy = sl.y * block.x;
+          // (finite, as zero codes of a block with a large scale are zeros; a NaN stays one)
+          const float fx = min_nan(sl.x * block.x, FLT_MAX), fy = min_nan(sl.y * block.x, FLT_MAX);
           s[nt][0] = fmaf(s[nt][0], fx, lv);
           s[nt][1] = fmaf(s[nt][1], fy, lv);
           s[nt][2] = fmaf(s[nt][2], fx, lv);
