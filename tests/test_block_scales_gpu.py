@@ -89,3 +89,36 @@ def test_zero_codes_beside_large_scales_and_queries(rows, D):
         d = dict(c, pools=[(k, scales.astype(np.float32)), v])
         ref = check(d, *run(d))
         assert np.all(ref["smax"] == 0)
+
+
+@pytest.mark.parametrize("rows,keys", [(1, 9000), (16, 9000), (40, 700), (40, 9000), (300, 2000)])
+@pytest.mark.parametrize("exponent", [-64, -30, 30, 90, 112])
+def test_v_scales_of_every_size(rows, keys, exponent):
+    """All of V near 2^exponent: outputs of pieces that CTAs share, up to bf16's range."""
+    c = case(46, [keys, 40], [rows, min(rows, 40)], 2, 1, 128, "bf16", 16, levels=3.0)
+    k, (v, vs) = c["pools"]
+    base = 2.0 ** (exponent + 7)  # codes reach 448: scales lie near 2^-7
+    d = dict(c, pools=[k, (v, (vs * base).astype(np.float32))])
+    check(d, *run(d))
+    # no powers of two
+    rng = np.random.default_rng(2)
+    odd = (vs * base * rng.uniform(1.0, 1.9, vs.shape)).astype(np.float32)
+    check(d := dict(c, pools=[k, (v, odd)]), *run(d))
+
+
+@pytest.mark.parametrize("rows", [1, 16, 40])
+@pytest.mark.parametrize("low,high", [(-64, 16), (-20, 60), (20, 100)])
+@pytest.mark.parametrize("first", [0, 1])
+def test_v_scales_that_one_row_sees(rows, low, high, first):
+    """Blocks 2^80 apart, side by side and in halves, the small ones first or last, over sequences that CTAs share."""
+    c = case(47, [6000, 300], [rows, rows], 2, 1, 128, "bf16", 16)
+    k, (v, vs) = c["pools"]
+    pages = len(vs)
+    order = np.zeros(pages, int)
+    for row in c["table"]:
+        order[row] = np.arange(len(row))
+    half = order < 200
+    for small in ((order + first) % 2 == 0, half if first else ~half):
+        x = np.where(small, 2.0 ** low, 2.0 ** high).astype(np.float32)[:, None, None]
+        d = dict(c, pools=[k, (v, np.broadcast_to(x, vs.shape).copy())])
+        check(d, *run(d))

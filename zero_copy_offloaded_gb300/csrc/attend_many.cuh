@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
           if (m == kNone && l == l) l = 0.f;  // no key of the piece is seen
           if (dead) l = bad;  // the wait for O may be the one that gave up: no lse beside outputs that are NaN
           const float vs = F == kE4M3 ? bars->ref[item & 3].y : p.v_scale;
-          const float inv = dead ? bad : whole ? (l == 0.f ? 0.f : vs / l) : F == kE4M3 ? vs : 1.0f;
+          const float inv = dead ? bad : whole ? (l == 0.f ? 0.f : vs / l) : 1.0f;
           const int tok = pr / G;
           const size_t orow = (size_t)(row0 + tok) * p.Hq + h * G + (pr - tok * G);
           T* out = static_cast<T*>(p.out) + orow * D;
@@ -679,7 +679,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
               if (p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
             } else {
               float2* ml = reinterpret_cast<float2*>(p.part_ml) + (size_t)slot * 2 * kRows + t * kRows + row;
-              *ml = make_float2(m, l);
+              // E4M3: pieces have V scales of their own, which join the exponents: times O they could pass fp32
+              *ml = F == kE4M3 ? make_float2(m + e4m3::log2_of(vs), l * (1.0f / vs)) : make_float2(m, l);
             }
           }
           tc::fence_before_sync();
