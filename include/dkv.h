@@ -656,8 +656,10 @@ dkv_status dkv_block_append(const dkv_block_append_t* args, void* stream);
 /* dkv_paged_attend over such a pool, with its arguments, kernels and limits (v_scale aside, which the blocks' scales
  * take the place of):
  *   o = softmax(scale * q . k) . v,  k and v the codes times their blocks' scales.
- * Scales of blocks that a row sees lie between 2^-126 and 2^126; those of V that one row sees
- * within 2^100 of one another.  |scale * q . k| up to 2^21 is served.  A weight is rounded to fp16, by 2^-11 of it, or by
+ * Scales of blocks that a row sees are K's from 2^-126 to 2^126, V's from 2^-64 (dkv_block_append writes none below; the sum
+ * of the weights, in fp32, counts their inverses) to 2^126, and those of V that one row sees within 2^80 of one another.
+ * |scale * q . k| up to 2^21 is served; scores of a row whose largest |scale * q| is below 2^-113 lose bits.
+ * A weight is rounded to fp16, by 2^-11 of it, or by
  * 2^-32 of the row's largest where it is below 2^-21 of that.  Up to 32 packed rows (max_rows times heads per KV head), and
  * above in tiles with a scale that is not a power of two from 2^-15 to 2^7 times its piece's first, weights count times
  * their V scale there.
