@@ -630,7 +630,7 @@ dkv_status dkv_paged_attend_debug_withhold(int enable);
  * NaN of its element alone, and does not count for the scale.
  * The rows of one block must lie within 16 consecutive rows of the call (dkv_step_plan deals them one after another), and no
  * two may have one slot;
- * sequences that append to the same block must not share it (dkv_pages_fork sees to that).  So a
+ * sequences that append to the same block must not share it (dkv_pages_fork sees to that, after a cut too).  A
  * sequence that is cut back and appended to again keeps its block's scale, which is then larger than it has to be, until
  * the block begins anew.
  * k_out, v_out [rows][n_kv_heads][head_dim] or null: the values that the cache now holds, rounded to `dtype` (an
@@ -686,7 +686,10 @@ dkv_status dkv_block_attend(const dkv_block_attend_t* args, void* stream);
 /* Sequences share, move and give back pages on the GPU.  A pool's pages have no counters: the page
  * table says who holds what (the ceil(kv_len / page_tokens) first entries of a sequence's row), and a page that no
  * sequence holds is free.  Several rows may name one page; dkv_step_plan appends to a sequence's last,
- * partly filled page only, which dkv_pages_fork never shares.  A sequence that may share pages ends by
+ * partly filled page only, which dkv_pages_fork leaves to one row alone.  A sequence that is cut back (a smaller
+ * kv_len) into a page that others hold goes through dkv_pages_fork, itself as its source, before anything is appended to
+ * it: the fork sees the shorter length and gives it a copy.  The pages behind its new end are on no stack until
+ * dkv_pages_compact.  A sequence that may share pages ends by
  * dkv_pages_fork (source -1): dkv_step_plan's release would put a shared page on the stack while others
  * hold it.  A table that serves several pools (layers; keys, values and their scales) takes one fork or
  * compaction and one dkv_pages_copy over all of them:
@@ -706,8 +709,9 @@ size_t dkv_pages_workspace(int batch, int max_pages, int num_pages);
  *   page_table [batch][max_pages], kv_len [batch]  before the call
  *   sources    [batch]  0 .. batch - 1, or below 0
  *   free_pages [num_pages], free_count [1]  the stack of dkv_step_plan
- * Full pages are shared.  Where the last page of a sequence is filled in part, one of the rows that go on as it keeps
- * that page (the sequence itself if sources[b] = b, else the lowest such b); every other one takes a page from
+ * Full pages are shared.  Of the rows that go on with the same last page, filled in part, one keeps it (the lowest with
+ * sources[b] = b, else the lowest), and none where a row that goes on has it as a full page (the others were cut back);
+ * every other one takes a page from
  * the stack, in order of b, the k-th from the top, and has copies[b] = {the source's page, its own}.  Pages that were
  * held before and are not any more are pushed first, in ascending order.
  * Written: table_out [batch][max_pages] (the entries of pages held; others are left as they were), len_out [batch],
@@ -715,7 +719,7 @@ size_t dkv_pages_workspace(int batch, int max_pages, int num_pages);
  * taken, longest len_out}.
  * All or nothing: where the stack does not hold enough (or would hold more than num_pages), or a length is above
  * max_pages * page_tokens, report[0] is DKV_ERR_CAPACITY, and with a source of batch or more
- * DKV_ERR_INVALID_ARG; nothing is copied, and table_out, len_out and free_left are what came in.
+ * DKV_ERR_INVALID_ARG; nothing is copied, and table_out, len_out (0 for a length below 0) and free_left are what came in.
  * A page index outside [0, num_pages) is handed on and never released.  Lengths below 0 count as 0.
  * table_out may be page_table, len_out kv_len and free_left free_count (in place); other buffers
  * must not overlap.  Errors: INVALID_ARG, CUDA. */

@@ -31,11 +31,18 @@ def fork(table, lengths, sources, free, free_count, P, table_out=None):
     before = {int(p) for b in range(B) for p in table[b, :held(lengths[b], P)]}
     new_len = [lengths[s] if s >= 0 else 0 for s in sources]
     rows = [list(map(int, table[s, :held(lengths[s], P)])) if s >= 0 else [] for s in sources]
+    # A page that a row fills in part is appended to: of the rows that go on with it one keeps it (one that stays itself, else
+    # any; the lowest), and none where a row that goes on has it as a full page.
+    full = {int(p) for s in sources if s >= 0 for p in table[s, :lengths[s] // P] if 0 <= p < pages}
+    parts = {}
+    for b in range(B):
+        if new_len[b] % P:
+            page = rows[b][-1]
+            parts.setdefault((page,) if 0 <= page < pages else (page, int(sources[b])), []).append(b)
     need = []
-    for s in range(B):
-        heirs = [b for b in range(B) if sources[b] == s]
-        if lengths[s] % P and heirs:
-            need += [b for b in heirs if b != (s if s in heirs else heirs[0])]
+    for key, held_by in parts.items():
+        keeper = None if key[0] in full else min(held_by, key=lambda b: (sources[b] != b, b))
+        need += [b for b in held_by if b != keeper]
     need.sort()
     after = {p for b in range(B) for p in (rows[b][:-1] if b in need else rows[b])}
     back = sorted(p for p in before - after if 0 <= p < pages)

@@ -28,3 +28,15 @@ def batch(seed, B, P, max_len, spare, share=0.3, extra=0):
     free = np.full(pages, -1, np.int32)
     free[:spare] = number[pool[at:at + spare]]
     return length, table, free, spare
+
+
+def cut_batch(seed, B, P, max_len, spare):
+    """The same after a fork in which many rows became copies of others, and with half of the rows then cut back to any
+    length: partly filled pages that other rows hold in full, or in part."""
+    rng = np.random.default_rng(seed + 7)
+    length, table, free, count = batch(seed, B, P, max_len, spare + 2 * B)
+    r = op.fork(table, length, rng.integers(0, max(1, B // 3), B), free, count, P)
+    assert r["report"][0] == 0
+    n = r["lengths"]
+    n = np.where(rng.random(B) < 0.5, rng.integers(0, n + 1), n).astype(np.int32)
+    return n, r["table"], r["free"], r["free_left"]

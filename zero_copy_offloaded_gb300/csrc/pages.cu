@@ -3,15 +3,18 @@
 // No page carries a count of its holders: the page table says who holds what.  Old sequence s holds the
 // ceil(len_s / P) first pages of its row.  A fork lets new sequence b be old sequence src_b: it is every old row's
 // fate to go on (some b has src_b = s) or to vanish, and the pages that go back are those that a vanished
-// row names and no row that goes on does.  A compaction needs the pages that any row names; with L of them the
-// i-th page named from L on moves to the i-th page not named below L.  Both are a mark of the pool's pages (a byte
+// row names and no row that goes on does.  A page that is some row's last, filled in part, is appended to, so one row alone may
+// keep it, and none where a row that goes on has it as a full page (a sequence that was cut back shares such a page); the
+// others take copies.  Whether a row has the page in full is a mark; who keeps it is found in a table of the
+// at most 1024 such pages by page, in shared memory.  A compaction needs the pages that any row names; with L of them the
+// i-th page named from L on moves to the i-th page not named below L.  Both are marks of the pool's pages (a byte
 // each, plain stores: all writers write 1), a scan over the marks in page order, and a pass over the table.
 //
 // What bounds them: the table's entries, read once to mark (a scattered byte store each) and once to be
 // rewritten, and latency: clearing the marks, marking, counting, what follows from the counts and the rewrite wait for one
 // another.  Large tables and pools take a launch of the whole GPU for each, small ones one launch of a cluster with a
-// barrier between them.  In a graph: a fork of 512 sequences of up to 32768 rows takes 20 us (with a scan by one cluster 46), a
-// compaction of their 1 M pages 27 (110); of 64 sequences of up to 4096 rows in a cluster, whose shared memory holds the marks, 10.3
+// barrier between them.  In a graph: a fork of 512 sequences of up to 32768 rows takes 21.4 us (with a scan by one cluster 46), a
+// compaction of their 1 M pages 27 (110); of 64 sequences of up to 4096 rows in a cluster, whose shared memory holds the marks, 10.5
 // and 14.9 (with marks in memory 14 and 17).  A copy of 8192 pages of
 // 2 x 32 KB and their scales runs at 6.6 TB/s, as fast as a plain copy.
 #include <stdio.h>
@@ -32,7 +35,7 @@ using namespace dkv;
 constexpr int kThreads = 1024, kWarps = kThreads / 32, kCluster = 8, kSms = 152;
 constexpr int kSegment = 256;  // table entries of a warp at a time, eight to a lane
 // Table entries plus pages up to which one cluster does everything in one launch.  64 sequences of up to 16384 rows,
-// 131000 in all, take 13.2 us to fork and 34 to compact so, 17.3 and 21.4 in five launches, whose calls take 9 us longer; with half
+// 131000 in all, take 14.3 us to fork and 34 to compact so, 18 and 21.4 in five launches, whose calls take 9 us longer; with half
 // of that compactions too are faster in one.
 constexpr long long kForkInOne = 1 << 18, kCompactInOne = 1 << 17;
 
@@ -58,6 +61,7 @@ struct PageParams {
   int* pairs;            // copies [B][2] or moves [max_moves][2]
   int* report;
   uint8_t* live;         // [num_pages, rounded up to 16]
+  uint8_t* tails;        // fork: the same
   uint8_t* dead;         // fork: the same
   Row* rows;             // fork: [B]
   int* old;              // fork in place: [B][max_pages]
@@ -106,6 +110,12 @@ struct Marks {
   __device__ __forceinline__ void set(int page) const {
     if constexpr (!ONE) global[page] = 1;
     else asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(at(page >> 2) + (page & 3)), "r"(1) : "memory");
+  }
+  __device__ __forceinline__ bool get(int page) const {
+    if constexpr (!ONE) return __ldcg(global + page);
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u8 %0, [%1];" : "=r"(v) : "r"(at(page >> 2) + (page & 3)) : "memory");
+    return v;
   }
   __device__ __forceinline__ uint32_t load(int word) const {
     if constexpr (!ONE) return __ldcg(reinterpret_cast<const uint32_t*>(global) + word);
@@ -192,22 +202,39 @@ __device__ __forceinline__ Range scan_range(const PageParams& p, int cta, bool a
 // ---- fork -----------------------------------------------------------------------------------
 
 // What every CTA finds out about the batch for itself.
+constexpr int kPlaces = 2 * kThreads;
 struct Batch {
   int len[kThreads];   // of the old rows, from 0 to what the table holds
   Row rows[kThreads];  // of the new ones
-  int heir[kThreads];  // of old row s: -1 itself, else the lowest row that goes on as it; INT_MAX: none
+  int goes[kThreads];  // old row s goes on
+  // The pages filled in part of rows that go on (outside the pool: num_pages + the row), at the place that their hash gives or the
+  // next one free, -1: free; and who keeps each: the lowest new row that is its old self, else 1024 + the lowest.
+  int page[kPlaces], keeper[kPlaces];
   int warp[kWarps], counts[kCluster];
   int longest;
+  // a source is not there; a length is beyond the table; a row vanishes; one that goes on fills a page in part
+  int wrong, far, any, some;
+
+  __device__ __forceinline__ int place_of(int key) {
+    int at = (uint32_t)key * 2654435761u >> 21;  // (Knuth, The Art of Computer Programming, volume 3, section 6.4)
+    static_assert(kPlaces == 1 << 11, "21 bits of the hash are left out");
+    for (;; at = (at + 1) & (kPlaces - 1)) {  // at most 1024 of 2048 places are taken
+      const int was = atomicCAS(page + at, -1, key);
+      if (was == -1 || was == key) return at;
+    }
+  }
 };
 
 template <bool ALL>
 __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, int phase) {
   __shared__ Batch s;
   extern __shared__ uint4 s_marks[];
+  // full pages of rows that go on, pages that these fill in part, pages of the others
   const Marks<ALL> live = {p.live, smem_u32(s_marks), p.mark_shift};
-  const Marks<ALL> dead = {p.dead, smem_u32(s_marks) + (4 << p.mark_shift), p.mark_shift};
+  const Marks<ALL> tails = {p.tails, smem_u32(s_marks) + (4 << p.mark_shift), p.mark_shift};
+  const Marks<ALL> dead = {p.dead, smem_u32(s_marks) + (8 << p.mark_shift), p.mark_shift};
   const Counts<ALL> counts = {p.counts, s.counts};
-  auto load_freed = [&](int word) { return dead.load(word) & ~live.load(word); };  // held, and not any more
+  auto load_freed = [&](int word) { return dead.load(word) & ~(live.load(word) | tails.load(word)); };  // held, and not any more
   griddep_wait();
   griddep_launch_dependents();
   const int b = threadIdx.x, lane = b & 31;
@@ -222,29 +249,50 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, i
   }
   if (phase == kClear || all) {
     live.clear(p.num_pages);
+    tails.clear(p.num_pages);
     dead.clear(p.num_pages);
     if (!all) return;
   }
   if (phase != kWrite) {
-    s.heir[b] = 0x7fffffff;
+    const int part = (1 << p.shift) - 1;
+    s.goes[b] = 0;
     s.len[b] = (int)min(len, cap);
-    if (b == 0) s.longest = 0;
-    const bool wrong = __syncthreads_or(src >= p.B), far = __syncthreads_or(len > cap);
-    if (src >= 0 && src < p.B) atomicMin(&s.heir[src], src == b ? -1 : b);
+    if (phase == kEmit || all) {
+      s.page[b] = s.page[b + kThreads] = -1;
+      s.keeper[b] = s.keeper[b + kThreads] = 0x7fffffff;
+    }
+    if (b == 0) s.longest = s.wrong = s.far = s.any = s.some = 0;
     __syncthreads();
-    const bool any = __syncthreads_or(len > 0 && s.heir[b] == 0x7fffffff);  // a row vanishes
+    const bool on = src >= 0 && src < p.B;
+    if (on) s.goes[src] = 1;
+    if (src >= p.B) s.wrong = 1;
+    if (len > cap) s.far = 1;
+    const int new_len = on ? s.len[src] : 0, held = (int)pages_of(new_len, p.shift);
+    const bool fills = new_len & part;
+    if (fills) s.some = 1;
+    __syncthreads();
+    if (len > 0 && !s.goes[b]) s.any = 1;
+    __syncthreads();
+    const bool any = s.any, some = s.some;
+    int tail = -1;
+    if (fills && (phase == kEmit || all)) tail = __ldcg(p.table + (size_t)src * p.max_pages + held - 1);
     if (phase == kMark || all) {
       if (all) cluster_sync();
       segments(p, [&](int r, int first) {
-        const int end = (int)pages_of(s.len[r], p.shift);
+        const int end = (int)pages_of(s.len[r], p.shift), full = s.len[r] >> p.shift;
         if (first >= end) return;
-        const bool goes = s.heir[r] != 0x7fffffff;
+        const bool goes = s.goes[r];
         // in place, a row that another one becomes is read again after it may have been written
         const bool keep = p.old && goes;
-        if (!any && !keep) return;
+        if (!any && !some && !keep) return;
         int page[8];
         load_segment(p.table + (size_t)r * p.max_pages, first, end, page);
-        if (any) mark(p, goes ? live : dead, page);
+        if (any || some) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            if ((uint32_t)page[i] < (uint32_t)p.num_pages)
+              (!goes ? dead : first + lane + 32 * i < full ? live : tails).set(page[i]);
+        }
         if (keep) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -252,8 +300,17 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, i
         }
       });
       if (!all) return;
-      cluster_sync();
     }
+    // who keeps a page that is filled in part
+    const bool in_pool = (uint32_t)tail < (uint32_t)p.num_pages;
+    const int rank = src == b ? b : kThreads + b;
+    int place = 0;
+    if (fills && (phase == kEmit || all)) {
+      place = s.place_of(in_pool ? tail : p.num_pages + src);
+      atomicMin(&s.keeper[place], rank);
+    }
+    if (all) cluster_sync();
+    const bool whole = in_pool && live.get(tail);  // some row that goes on has it as a full page
     // ---- pages that go back, in page order
     const Range range = scan_range(p, blockIdx.x, all);
     int mine = 0;
@@ -267,13 +324,12 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, i
       cluster_sync();
     }
     if (any) at += counted(counts, blockIdx.x, s.warp, freed);
-    const bool on = src >= 0 && src < p.B;
-    const int new_len = on ? s.len[src] : 0, held = (int)pages_of(new_len, p.shift);
-    const bool need = on && (new_len & ((1 << p.shift) - 1)) && s.heir[src] != (src == b ? -1 : b);
+    if (!all) __syncthreads();
+    const bool need = fills && (s.keeper[place] != rank || whole);
     int needed;
     const int k = block_scan(need, s.warp, needed);
     const long long stack = (long long)free_count + freed;
-    const bool ok = !wrong && !far && needed <= stack && stack <= p.num_pages;
+    const bool ok = !s.wrong && !s.far && needed <= stack && stack <= p.num_pages;
     if (ok && mine) {
       int* to = p.free_pages + free_count + at;
       for (int i = 0; i < range.n; ++i) {
@@ -295,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, i
       }
       __syncthreads();
       if (b == 0) {
-        p.report[0] = ok ? DKV_OK : wrong ? DKV_ERR_INVALID_ARG : DKV_ERR_CAPACITY;
+        p.report[0] = ok ? DKV_OK : s.wrong ? DKV_ERR_INVALID_ARG : DKV_ERR_CAPACITY;
         p.report[1] = ok ? freed : 0;
         p.report[2] = ok ? needed : 0;
         p.report[3] = s.longest;
@@ -316,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1) fork_kernel(const PageParams p, i
       const int4 w = __ldcg(reinterpret_cast<const int4*>(p.rows + r));
       row = {w.x, w.y, w.z, w.w};
     }
-    if (row.source < 0 || first >= row.shared + 1 || (p.old && row.source == r)) return;
+    if (row.source < 0 || first >= row.shared + 1 || (p.old && row.source == r && row.take < 0)) return;
     int page[8];
     load_segment((p.old ? p.old : p.table) + (size_t)row.source * p.max_pages, first, row.shared, page);
     int* to = p.table_out + (size_t)r * p.max_pages;
@@ -517,7 +573,7 @@ const char* bad_sizes(int batch, int max_pages, int page_tokens, int num_pages) 
   return nullptr;
 }
 
-// Workspace: counts, the end of the stack, new lengths | rows | marks | marks or ranks | the old table.
+// Workspace: counts, the end of the stack, new lengths | rows | marks | two more, or ranks | the old table.
 size_t ws_rows() { return align256((kSms + 1 + DKV_MAX_STEP_BATCH) * sizeof(int)); }
 size_t ws_live() { return ws_rows() + align256(DKV_MAX_STEP_BATCH * sizeof(Row)); }
 size_t ws_more(int num_pages) { return ws_live() + align256(num_pages); }
@@ -576,7 +632,8 @@ void set_workspace(PageParams& p, void* workspace) {
   p.counts = reinterpret_cast<int*>(w);
   p.rows = reinterpret_cast<Row*>(w + ws_rows());
   p.live = reinterpret_cast<uint8_t*>(w + ws_live());
-  p.dead = reinterpret_cast<uint8_t*>(w + ws_more(p.num_pages));
+  p.tails = reinterpret_cast<uint8_t*>(w + ws_more(p.num_pages));  // (the ranks' room holds both: twice num_pages + 15 bytes)
+  p.dead = p.tails + ((size_t)p.num_pages + 15) / 16 * 16;
   p.rank = reinterpret_cast<int*>(w + ws_more(p.num_pages));
   p.old = reinterpret_cast<int*>(w + ws_old(p.num_pages));
 }
@@ -614,7 +671,7 @@ extern "C" dkv_status dkv_pages_fork(const int32_t* page_table, const int32_t* k
   set_workspace(p, workspace);
   if (table_out != page_table) p.old = nullptr;
   static PerDevice room;
-  return launch(fork_kernel<true>, kForkInOne, 2, fork_kernel<false>, p, room, static_cast<cudaStream_t>(stream));
+  return launch(fork_kernel<true>, kForkInOne, 3, fork_kernel<false>, p, room, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" dkv_status dkv_pages_compact(const int32_t* page_table, const int32_t* kv_len, int batch, int max_pages,
