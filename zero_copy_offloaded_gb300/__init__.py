@@ -543,8 +543,8 @@ def _dtype_of(t):
 
 
 def _append_args(q, k, v, positions, slots, q_out, k_out, v_out, q_gamma, k_gamma, cos_sin):
-    """What the appends check alike: (device index, head_dim, KV heads) and the fields of dkv_append_t up to slots, the
-    three outputs, and the numbers from rows to max_positions."""
+    """What the appends check alike: the device index, the fields of dkv_append_t but the pools and what comes behind
+    max_positions, in their order.  (One flat tuple: nested ones cost the smallest calls a microsecond of their ten.)"""
     import torch
     some = q if q is not None else k
     if some is None:
@@ -576,8 +576,8 @@ def _append_args(q, k, v, positions, slots, q_out, k_out, v_out, q_gamma, k_gamm
         pcs = _arg(cos_sin, "cos_sin", f32, dev)
         max_positions, rotary_dim = cos_sin.shape
         pp = _arg(positions, "positions", i32, dev, (n,))
-    return ((dev, D, hkv), (pq, pk, pv, sq, sk, sv, pqg, pkg, pcs, pp, _arg(slots, "slots", i32, dev, (n,))),
-            (pqo, pko, pvo), (n, hq, hkv, D, code, rotary_dim, max_positions))
+    return (dev, pq, pk, pv, sq, sk, sv, pqg, pkg, pcs, pp, _arg(slots, "slots", i32, dev, (n,)), pqo, pko, pvo,
+            n, hq, hkv, D, code, rotary_dim, max_positions)
 
 
 def dkv_qkv_append(q, k, v, positions=None, slots=None, k_pool=None, v_pool=None, q_out=None,
@@ -586,8 +586,8 @@ def dkv_qkv_append(q, k, v, positions=None, slots=None, k_pool=None, v_pool=None
     """Head norms and rotation of q and k, append of k and v to an E2M1 pool (see include/dkv.h).
     q [rows, n_q_heads, D] and k, v [rows, n_kv_heads, D] may be slices of one projection's output."""
     import torch
-    (dev, D, hkv), rows, outs, numbers = _append_args(q, k, v, positions, slots, q_out, k_out, v_out, q_gamma,
-                                                      k_gamma, cos_sin)
+    (dev, pq, pk, pv, sq, sk, sv, pqg, pkg, pcs, pp, ps, pqo, pko, pvo, n, hq, hkv, D, code, rotary_dim,
+     max_positions) = _append_args(q, k, v, positions, slots, q_out, k_out, v_out, q_gamma, k_gamma, cos_sin)
     pkp = pvp = pages = page_tokens = 0
     if k_pool is not None:
         if v_pool is None or k is None:
@@ -598,7 +598,8 @@ def dkv_qkv_append(q, k, v, positions=None, slots=None, k_pool=None, v_pool=None
             raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens) for {hkv} heads")
         pages, page_tokens = shape[0], shape[2]
     st = lib().dkv_qkv_append(
-        _APPEND.pack(*rows, pkp, pvp, *outs, *numbers, bool(interleaved), page_tokens, pages, eps, k_scale, v_scale),
+        _APPEND.pack(pq, pk, pv, sq, sk, sv, pqg, pkg, pcs, pp, ps, pkp, pvp, pqo, pko, pvo, n, hq, hkv, D, code,
+                     rotary_dim, max_positions, bool(interleaved), page_tokens, pages, eps, k_scale, v_scale),
         _launch(dev, stream))
     if st:
         _check(st, "dkv_qkv_append")
@@ -614,7 +615,7 @@ def _near(t, what, index):
 
 
 def _block_pools(k_pool, v_pool, k_scales, v_scales, index, D):
-    """Addresses of the pools and scales of an 8-bit cache, and (num_pages, n_kv_heads, page_tokens)."""
+    """Addresses of the pools and scales of an 8-bit cache, num_pages, n_kv_heads and page_tokens."""
     import torch
     shape = k_pool.shape
     if len(shape) != 4 or shape[3] != D or v_pool.shape != shape:
@@ -627,7 +628,7 @@ def _block_pools(k_pool, v_pool, k_scales, v_scales, index, D):
         if t.dtype != torch.float32 or page_tokens % 16 or t.shape != (pages, heads, page_tokens // 16):
             raise ValueError(f"{what} is {t.dtype} {tuple(t.shape)}: float32 [{pages}, {heads}, {page_tokens} / 16] is wanted")
     return (_near(k_pool, "k_pool", index), _near(v_pool, "v_pool", index), _near(k_scales, "k_scales", index),
-            _near(v_scales, "v_scales", index)), (pages, heads, page_tokens)
+            _near(v_scales, "v_scales", index), pages, heads, page_tokens)
 
 
 def dkv_block_append(q, k, v, positions, slots, k_pool, v_pool, k_scales, v_scales, q_out=None, k_out=None, v_out=None,
@@ -635,13 +636,14 @@ def dkv_block_append(q, k, v, positions, slots, k_pool, v_pool, k_scales, v_scal
     """dkv_qkv_append into an 8-bit pool with block scales (see include/dkv.h): k_pool, v_pool float8_e4m3fn
     [num_pages, n_kv_heads, page_tokens, D], k_scales, v_scales fp32 [num_pages, n_kv_heads, page_tokens // 16].  q may
     be None."""
-    (dev, D, hkv), rows, outs, numbers = _append_args(q, k, v, positions, slots, q_out, k_out, v_out, q_gamma,
-                                                      k_gamma, cos_sin)
-    pools, shape = _block_pools(k_pool, v_pool, k_scales, v_scales, dev, D)
-    if k is None or shape[1] != hkv:
-        raise ValueError(f"pools of {shape} (pages, heads, page_tokens) for {hkv} heads")
+    (dev, pq, pk, pv, sq, sk, sv, pqg, pkg, pcs, pp, ps, pqo, pko, pvo, n, hq, hkv, D, code, rotary_dim,
+     max_positions) = _append_args(q, k, v, positions, slots, q_out, k_out, v_out, q_gamma, k_gamma, cos_sin)
+    pkp, pvp, pks, pvs, pages, heads, page_tokens = _block_pools(k_pool, v_pool, k_scales, v_scales, dev, D)
+    if k is None or heads != hkv:
+        raise ValueError(f"pools of {(pages, heads, page_tokens)} (pages, heads, page_tokens) for {hkv} heads")
     st = lib().dkv_block_append(
-        _BLOCK_APPEND.pack(*rows, *pools, *outs, *numbers, bool(interleaved), shape[2], shape[0], eps),
+        _BLOCK_APPEND.pack(pq, pk, pv, sq, sk, sv, pqg, pkg, pcs, pp, ps, pkp, pvp, pks, pvs, pqo, pko, pvo, n, hq, hkv,
+                           D, code, rotary_dim, max_positions, bool(interleaved), page_tokens, pages, eps),
         _launch(dev, stream))
     if st:
         _check(st, "dkv_block_append")
@@ -665,27 +667,22 @@ def _kept_for_graph(address):
     return False
 
 
-def _workspace(workspace, wanted, dev, s):
-    """Address and size of the caller's workspace, or of one taken from torch's allocator, whose address comes last and
-    which the caller releases once the call is enqueued."""
-    if workspace is not None:
-        import torch
-        return _arg(workspace, "workspace", torch.uint8, dev), workspace.numel(), 0
-    # The allocator's own call: a tensor around the bytes costs 3 us of the smallest calls' 13.
-    # The bytes are the launching stream's, so that they are not handed out again before it ran.
-    size = max(1, wanted())
+def _take(size, s):
+    """Address of a workspace from torch's allocator, which the caller releases once the call is enqueued.  The
+    allocator's own call: a tensor around the bytes costs 3 us of the smallest calls' 13.  The bytes are the launching
+    stream's, so that they are not handed out again before it ran."""
     _, _, allocate, release = _torch_calls()
-    taken = allocate(size, s)
+    taken = allocate(max(1, size), s)
     if lib().dkv_stream_capturing(s) == 1 and not _kept_for_graph(taken):
         # the allocator would hand the bytes out again while the graph lives
         release(taken)
         raise ValueError("a stream capture that torch does not know needs a workspace of its own")
-    return taken, size, taken
+    return taken
 
 
 def _attend_args(q, page_table, kv_len, out, row_start, lse, stream):
-    """What the attentions check alike: (device index, stream, rows, query heads, head_dim, dtype code, batch,
-    max_pages) and the addresses of q with its stride, of page_table, kv_len and row_start, and of out and lse."""
+    """What the attentions check alike: device index, stream, address of q and its stride, addresses of page_table, kv_len,
+    row_start, out and lse, batch, rows, query heads, head_dim, dtype code and max_pages."""
     import torch
     shape, i32 = q.shape, torch.int32
     if len(shape) != 3 or page_table.dim() != 2:
@@ -696,10 +693,9 @@ def _attend_args(q, page_table, kv_len, out, row_start, lse, stream):
     n, _, D = shape
     pq, hq, sq = _rows(q, "q", dt, dev, n, D)
     B, max_pages = page_table.shape
-    pt, pkl = _arg(page_table, "page_table", i32, dev), _arg(kv_len, "kv_len", i32, dev, (B,))
-    prs, po = _arg(row_start, "row_start", i32, dev, (B + 1,)), _arg(out, "out", dt, dev, (n, hq, D))
-    pl = _arg(lse, "lse", torch.float32, dev, (n, hq))
-    return (dev, s, n, hq, D, code, B, max_pages), (pq, sq), (pt, pkl, prs), (po, pl)
+    return (dev, s, pq, sq, _arg(page_table, "page_table", i32, dev), _arg(kv_len, "kv_len", i32, dev, (B,)),
+            _arg(row_start, "row_start", i32, dev, (B + 1,)), _arg(out, "out", dt, dev, (n, hq, D)),
+            _arg(lse, "lse", torch.float32, dev, (n, hq)), B, n, hq, D, code, max_pages)
 
 
 def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None, max_rows=1,
@@ -709,20 +705,25 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
     torch's caching allocator, on the launching stream; under a stream capture that is not torch's
     own (torch.cuda.graph) the call needs one, which the graph's owner keeps."""
     import torch
-    (dev, s, n, hq, D, code, B, max_pages), qs, tables, outs = _attend_args(q, page_table, kv_len, out, row_start, lse, stream)
+    dev, s, pq, sq, pt, pkl, prs, po, pl, B, n, hq, D, code, max_pages = _attend_args(
+        q, page_table, kv_len, out, row_start, lse, stream)
     pkp, shape = _pool(k_pool, "k_pool", torch.uint8, dev, D)
     pvp, other = _pool(v_pool, "v_pool", torch.uint8, dev, D)
     if shape != other:
         raise ValueError(f"pools of {shape} and {other} (pages, heads, page_tokens)")
     pages, hkv, page_tokens = shape
-    pw, size, taken = _workspace(workspace, lambda: dkv_paged_attend_workspace(B, hq, hkv, D, max_rows), dev, s)
+    if workspace is None:
+        size = dkv_paged_attend_workspace(B, hq, hkv, D, max_rows)
+        pw = _take(size, s)
+    else:
+        pw, size = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
     try:
         st = lib().dkv_paged_attend(
-            _ATTEND.pack(*qs, pkp, pvp, *tables, *outs, pw, size, B, n, max_rows, hq, hkv, D, code,
+            _ATTEND.pack(pq, sq, pkp, pvp, pt, pkl, prs, po, pl, pw, size, B, n, max_rows, hq, hkv, D, code,
                          page_tokens, pages, max_pages, D ** -0.5 if scale is None else scale, v_scale), s)
     finally:
-        if taken:
-            _torch_calls()[3](taken)
+        if workspace is None:
+            _torch_calls()[3](pw)
     if st:
         _check(st, "dkv_paged_attend")
 
@@ -730,16 +731,22 @@ def dkv_paged_attend(q, k_pool, v_pool, page_table, kv_len, out, row_start=None,
 def dkv_block_attend(q, k_pool, v_pool, k_scales, v_scales, page_table, kv_len, out, row_start=None, max_rows=1,
                      scale=None, lse=None, workspace=None, stream=None):
     """dkv_paged_attend over an 8-bit pool with block scales (see include/dkv.h), as dkv_block_append fills it."""
-    (dev, s, n, hq, D, code, B, max_pages), qs, tables, outs = _attend_args(q, page_table, kv_len, out, row_start, lse, stream)
-    pools, (pages, hkv, page_tokens) = _block_pools(k_pool, v_pool, k_scales, v_scales, dev, D)
-    pw, size, taken = _workspace(workspace, lambda: dkv_paged_attend_workspace(B, hq, hkv, D, max_rows), dev, s)
+    import torch
+    dev, s, pq, sq, pt, pkl, prs, po, pl, B, n, hq, D, code, max_pages = _attend_args(
+        q, page_table, kv_len, out, row_start, lse, stream)
+    pkp, pvp, pks, pvs, pages, hkv, page_tokens = _block_pools(k_pool, v_pool, k_scales, v_scales, dev, D)
+    if workspace is None:
+        size = dkv_paged_attend_workspace(B, hq, hkv, D, max_rows)
+        pw = _take(size, s)
+    else:
+        pw, size = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
     try:
         st = lib().dkv_block_attend(
-            _BLOCK_ATTEND.pack(*qs, *pools, *tables, *outs, pw, size, B, n, max_rows, hq, hkv, D, code,
-                               page_tokens, pages, max_pages, D ** -0.5 if scale is None else scale), s)
+            _BLOCK_ATTEND.pack(pq, sq, pkp, pvp, pks, pvs, pt, pkl, prs, po, pl, pw, size, B, n, max_rows, hq, hkv, D,
+                               code, page_tokens, pages, max_pages, D ** -0.5 if scale is None else scale), s)
     finally:
-        if taken:
-            _torch_calls()[3](taken)
+        if workspace is None:
+            _torch_calls()[3](pw)
     if st:
         _check(st, "dkv_block_attend")
 
@@ -774,12 +781,16 @@ def dkv_pages_fork(page_table, kv_len, sources, free_pages, free_count, page_tok
             _arg(table_out, "table_out", i32, dev, (B, max_pages)), _arg(len_out, "len_out", i32, dev, each),
             _arg(free_left, "free_left", i32, dev, one), _arg(copies, "copies", i32, dev, (B, 2)),
             _arg(report, "report", i32, dev, (4,)))
-    pw, size, taken = _workspace(workspace, lambda: dkv_pages_workspace(B, max_pages, pages), dev, s)
+    if workspace is None:
+        size = dkv_pages_workspace(B, max_pages, pages)
+        pw = _take(size, s)
+    else:
+        pw, size = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
     try:
         st = lib().dkv_pages_fork(*args, pw, size, s)
     finally:
-        if taken:
-            _torch_calls()[3](taken)
+        if workspace is None:
+            _torch_calls()[3](pw)
     if st:
         _check(st, "dkv_pages_fork")
 
@@ -799,12 +810,16 @@ def dkv_pages_compact(page_table, kv_len, page_tokens, table_out, free_pages, fr
             page_tokens, pages, _arg(table_out, "table_out", i32, dev, (B, max_pages)),
             _arg(free_pages, "free_pages", i32, dev), _arg(free_left, "free_left", i32, dev, (1,)),
             _arg(moves, "moves", i32, dev), moves.shape[0], _arg(report, "report", i32, dev, (4,)))
-    pw, size, taken = _workspace(workspace, lambda: dkv_pages_workspace(B, max_pages, pages), dev, s)
+    if workspace is None:
+        size = dkv_pages_workspace(B, max_pages, pages)
+        pw = _take(size, s)
+    else:
+        pw, size = _arg(workspace, "workspace", torch.uint8, dev), workspace.numel()
     try:
         st = lib().dkv_pages_compact(*args, pw, size, s)
     finally:
-        if taken:
-            _torch_calls()[3](taken)
+        if workspace is None:
+            _torch_calls()[3](pw)
     if st:
         _check(st, "dkv_pages_compact")
 
