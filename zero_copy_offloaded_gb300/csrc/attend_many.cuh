@@ -41,12 +41,13 @@
 // codes (fp16 holds a code times 2^-15 .. 2^7 exactly), while the first block's own multiplies the scores or the outputs.
 // A ratio outside, or no power of two, stays with the block: the softmax of a tile that has one multiplies its scores
 // by it, or adds log2 of it (V) to them and divides the sum.  With the blocks' scales in the softmax of every tile the
-// chunk above takes 2.15 ms, this way 1.63 to 1.68 (1250 TFLOP/s).  Codes come from memory into registers: a ring of 8-bit
-// tiles in shared memory leaves its bandwidth short (2.12 ms and more).  The conversion and its bookkeeping are about
-// a fifth of the instructions.
+// chunk above takes 2.11 ms, this way 1.63 to 1.66 (1250 TFLOP/s).  The first is what a pool takes whose first block's scale
+// lies 2^8 or more below the others' (2.11), or in which one V block of eight has a scale that is no power of two (2.10).
+// Codes come from memory into registers: a ring of 8-bit tiles in shared memory leaves its bandwidth short (2.12 ms and more).
+// The conversion and its bookkeeping are about a fifth of the instructions.
 //
 // Every item reads its keys, so a pool is read once for each 256 packed rows.  From HBM that is hidden;
-// a pool in host memory crosses the link as often (4096 rows of 32/8 heads over 28672 keys: 10.8 ms).
+// a pool in host memory crosses the link as often (4096 rows of 32/8 heads over 28672 keys: 10.8 ms, of E4M3 19.1).
 #pragma once
 
 #include <float.h>
@@ -110,8 +111,9 @@ struct Bars {
   unsigned long long nan_key[4][kNan];
   uint32_t nan_item[4];   // E4M3: item + 1 of one that has any
   // E4M3.  By item & 3: the powers of two that K's and V's tiles of a piece are converted by.  By tile & 3, for each
-  // run of 16 keys: 1 where a scale is left over, 2 where there is no page; K's scale, whole, where it is left over (the fourth
-  // is 1 then), log2 of what is left of V's and its inverse.  By row: the scale of its scores but for K's.
+  // run of 16 keys: 1 where a scale is left over, 2 where there is no page; what K's codes still have to be multiplied by (the
+  // whole scale where it is left over, else the piece's power of two), log2 of what is left of V's and its inverse.  By
+  // row: the scale of its scores but for K's.
   float2 ref[4];
   uint2 flags[4];
   float4 block[F == kE2M1 ? 1 : 4][8];
@@ -465,8 +467,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         // positive and finite, so that a masked -infinity stays one; E4M3's is so once it has K's scale
         return fminf(fmaxf(fabsf(p.scale_log2) * unscale, F == kE2M1 ? 1e-37f : 0.f), FLT_MAX);
       };
-      // (a NaN stays one)
-      auto positive = [](float x) { return x < 1e-37f ? 1e-37f : x > FLT_MAX ? FLT_MAX : x; };
+      auto positive = [](float x) {  // (a NaN stays one)
+        float r;
+        asm("max.NaN.f32 %0, %1, %2;\n\tmin.NaN.f32 %0, %0, %3;" : "=&f"(r) : "f"(x), "f"(1e-37f), "f"(FLT_MAX));
+        return r;
+      };
       auto active = [&]() { return c.last >= c.qt * 2 * kRows + t * kRows; };
       bool go = true;
       float sl = 1.f;
@@ -516,9 +521,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
               if constexpr (scaled) {
                 const float4 b0 = bars->block[place][2 * pc], b1 = bars->block[place][2 * pc + 1];
                 const bool see0 = nvis - pc * 32 > 0, see1 = nvis - pc * 32 > 16;
-                // (from K's own scale: its ratio to the piece's can leave fp32's range, and `sl` is held inside it)
-                auto scale_of = [&](const float4& b) { return b.w != 0.f ? positive(bars->sl[t * kRows + row] * b.x) : sl; };
-                bsl = make_float2(see0 ? scale_of(b0) : 1.f, see1 ? scale_of(b1) : 1.f);
+                // (not from `sl`, which is held inside fp32's range, and a ratio, which can leave it)
+                const float raw = bars->sl[t * kRows + row];
+                bsl = make_float2(see0 ? positive(raw * b0.x) : 1.f, see1 ? positive(raw * b1.x) : 1.f);
                 blv = make_float2(see0 ? b0.y : 0.f, see1 ? b1.y : 0.f);
                 brv = make_float2(see0 ? b0.z : 1.f, see1 ? b1.z : 1.f);
               }
@@ -846,8 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tc_kernel(const AttendPara
         if (opened && lane == 0) bars->ref[item & 3] = make_float2(kref, vref);
         if (speaks) {
           const bool left_over = rest_k != 1.f || rest_v != 1.f;
-          bars->block[j & 3][run] = left_over ? make_float4(ks, e4m3::log2_of(rest_v), __fdividef(1.0f, rest_v), rest_k != 1.f)
-                                              : make_float4(1.f, 0.f, 1.f, 0.f);
+          bars->block[j & 3][run] = left_over ? make_float4(rest_k != 1.f ? ks : kref, e4m3::log2_of(rest_v), __fdividef(1.0f, rest_v), 0.f)
+                                              : make_float4(kref, 0.f, 1.f, 0.f);
           reinterpret_cast<uint8_t*>(&bars->flags[j & 3])[run] = left_over | (held ? 0 : 2);
         }
         convert(smem + C::kOffK + st * C::kTileB, wk, false, fk);
