@@ -16,11 +16,11 @@
 // rounded to 16 bits, use a plain fp32 sum.
 //
 // What bounds it: each byte once through memory, 26 KB a row of 32/8 heads of 128.  4096 such rows
-// take 29 us (3.7 TB/s of 6.8 measured), 16384 rows of 32/32 fp16 heads of 64, rotated in half
-// and without norms, 86 us (5.1 TB/s).  In the first neither memory nor a pipe is full: its warps wait for
-// their own chains of scalar fp32 (norms, exact sums, quantisation; about 60 % of the issue slots), and queries
-// alone (15 us) and keys and values alone (14) add up.  A pool in host memory takes 53 us for them: the codes
-// cross the link in stores of 4 bytes a lane, the scales of 1.
+// take 26.8 us in a graph (4.0 TB/s of 6.7 measured; 28.8 a call), 16384 rows of 32/32 fp16 heads of 64, rotated in half
+// and without norms, 85.4 us (87.3).  In the first neither memory nor a pipe is full: its warps wait for
+// their own chains of fp32 (norms, exact sums, quantisation; about 60 % of the issue slots; products two elements an
+// instruction where they can), and queries alone (17.7 us) and keys and values alone (10.8) add up.  A pool in host
+// memory takes 51 us for them: the codes cross the link in stores of 4 bytes a lane, the scales of 1.
 #include "append.cuh"
 
 namespace {

@@ -12,8 +12,8 @@
 // call gives few rows go to a warp of several heads.  The rows of a block lie within 16 consecutive rows of the call; a
 // warp looks at 16 tokens and takes the blocks whose rows begin there.
 //
-// What bounds it: 23 KB a row of 32/8 heads of 128, 4096 of them 14 us at the measured copy rate; they take 26.6, of which
-// queries alone 17.4, keys and values alone 16.8.  Neither memory nor a pipe is full: the warps wait for chains of fp32 (the keys'
+// What bounds it: 23 KB a row of 32/8 heads of 128, 4096 of them 14 us at the measured copy rate; they take 26.8, of which
+// queries alone 17.5, keys and values alone 17.1.  Neither memory nor a pipe is full: the warps wait for chains of fp32 (the keys'
 // exact sums of squares, the values that have to live until the block's largest is known) and for instructions, of
 // which the unrolled rows have many.  Sums, norms and rotations take two elements an instruction where they can.
 #include "append.cuh"
@@ -29,8 +29,9 @@ static_assert(kWarps == kAppendWarps && kLook == kWarps * e4m3::kBlock && kIterQ
 
 // Blocks that a call gives at most kShort rows go to warps that take one block of several heads (append_tokens), the others to
 // warps that take all of a block's rows (append_blocks).  Which is which is seen on the device, so both are launched.
-// 64 sequences' five rows each: 7.6 us with 6, 16.8 with 4; 512 single rows 9 us so, 55 by block; one sequence's 1024
-// rows 10.3 us by block, 27 by token.
+// 64 sequences' five rows each: 7.8 us with 6, 16.8 with 4; 512 single rows 9.1 us so, 55 by block; one sequence's 1024
+// rows 10.3 us by block, 27 by token.  Four rows of 1024 sequences, 39.8 us for 14 us of memory traffic: append_few goes over the
+// rows of a block twice, norm and rotation included, with one of them in flight.
 constexpr int kShort = 6;
 
 struct BlockParams {

@@ -7,14 +7,14 @@ constexpr int kAppendWarps = 8;  // of a CTA
 constexpr int kAppendIterQ = 8;  // query rows of a lane group for one token
 constexpr int kUnit = 16;        // tokens that append_blocks' warps look at together for blocks that begin there
 constexpr int kLook = kAppendWarps * 16;  // and a CTA of append_tokens in long calls
-// Calls of kLong rows and more look for short blocks with a warp for 16 tokens, not one for each (4096 rows of one sequence
-// 26.6 us, about 35 with a warp each; 2048 17.8 and 21.2; 512 8.3 and 7.6), and about kLookCtas CTAs share what there is: 4096
-// single rows 42 us, by block 179; 1024 16.1, 15.4 with a warp each.  (256 CTAs: 4096 rows of one sequence 28.6, single
-// ones 40.7.)
+// Calls of kLong rows and more look for short blocks with a warp for 16 tokens, not one for each: 4096 rows of one sequence
+// 26.8 us, 35.8 with a warp each; 2048 18.1 and 21.4; 1024 10.3 and 11.4; 512 8.4 and 7.5.  About kLookCtas CTAs share
+// what there is: 4096 single rows 42 us, 41 with a warp each, by block 179; 1024 16.1 and 15.5; 512 11.1 and 9.1.  (256 CTAs:
+// 4096 rows of one sequence 28.6, single ones 40.7.)
 constexpr int kLong = 1024, kLookCtas = 128;
 
 // Warps that share a run: with heads of 128 four of four rows each, so that a lane holds 16 fp32 values (4096 rows of 32/8 heads
-// 26.6 us; with two warps 27 to 28, with one and two CTAs an SM instead of three 38.7).  Of 64 one (16384 rows of 32 heads
+// 26.8 us; with two warps 27 to 28, with one and two CTAs an SM instead of three 38.7).  Of 64 one (16384 rows of 32 heads
 // 88 us, 103 with two: what a warp does once for a run counts more).
 constexpr int append_share(int head_dim) { return head_dim == 128 ? 4 : 1; }
 
@@ -40,9 +40,10 @@ inline AppendGeometry append_geometry(int rows, int q_heads, int kv_heads, int h
   const bool all = rows >= kLong;
   const long long chunks = (rows + kUnit - 1) / kUnit;
   a.heads = 1;
-  // What a warp finds out about its tokens serves up to four heads, while 2048 warps are left to do so: 4096 rows of 8
-  // heads 26.6 us with two, 29 with one, 40 with four; 16384 rows of 32 heads of 64 88 us with four, 113 with one;
-  // 1024 rows 10.3 us with one, 14 with two.
+  // What a warp finds out about its tokens serves up to four heads, while 2048 warps are left to do so.  In us with one, two and
+  // four: 4096 rows of 8 heads of 128 33.8, 29.4, 26.5 (the rule takes four), 2048 rows 19.7, 18.0, 21.2 (two), 1024
+  // rows 10.1, 9.3, 12.9 (one), 4096 rows of 2 heads 11.1, 11.6, 11.5 (one); 16384 rows of 32 heads of 64 115, 98, 87
+  // (four), 8192 rows of 8 33, 29, 40 (two).
   while (a.heads < 4 && chunks * kv_heads / (2 * a.heads) * share >= 2048) a.heads *= 2;
   a.block_ctas = ctas(chunks * ((kv_heads + a.heads - 1) / a.heads), kAppendWarps / share);
   const long long groups = (kv_heads + 256 / head_dim - 1) / (256 / head_dim), looks = (rows + kLook - 1) / kLook;
