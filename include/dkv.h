@@ -617,7 +617,7 @@ dkv_status dkv_paged_attend_debug_withhold(int enable);
 /* A pool of E4M3 codes [num_pages][n_kv_heads][page_tokens][head_dim] (one byte an element, the layout of a
  * paged DKV_KV_E4M3 cache) with fp32 scales [num_pages][n_kv_heads][page_tokens / 16]: an element is its
  * code times the scale of its block, 16 consecutive tokens of a page and head.  Pages hold 16 to 4096 tokens.
- * Three significant bits more than E2M1's two, for twice the bytes; dkv_step_plan plans it, dkv_pages_* share and move
+ * Four significant bits where E2M1 has two, for less than twice the bytes; dkv_step_plan plans it, dkv_pages_* share and move
  * its pages (codes and scales are pools of one table).  Pools may be HBM or the mapped alias of pinned host
  * memory, scales too. */
 
